@@ -82,6 +82,11 @@ enum spec_head { SPEC_HEAD_MARKOV = 0, SPEC_HEAD_RNN = 1 };
 #define SPEC_STATUS_TIMEOUT 0x10u     /* an internal pipeline wait gave up after
                                          2 s (never expected): the call's
                                          outputs are invalid                     */
+#define SPEC_STATUS_BAD_LEN 0x20u     /* a length, row offset or page count was
+                                         outside its range                       */
+#define SPEC_STATUS_NO_PAGES 0x40u    /* no free page left, or a page table full */
+#define SPEC_STATUS_BAD_PAGE 0x80u    /* a page id or slot was outside the cache */
+#define SPEC_STATUS_BAD_POSITION 0x100u /* a position was outside [0, 2^24)      */
 
 /* ------------------------------------------------------------------ draft -
  * DSpark summary, "第二阶段：轻量顺序头" (sequential Markov head) and the
@@ -430,6 +435,180 @@ typedef struct spec_round_host_args {
 } spec_round_host_args;
 
 int spec_round_host(const spec_round_host_args *args, uint64_t seed, spec_stream_t stream);
+
+/* -------------------------------------------------- cache tables of a round -
+ * The target model's keys and values live in a paged cache: n_pages pages of
+ * page_size tokens, a page table [R, max_pages] per request, and a ring of the
+ * ids of the free pages.  A round adds n_r = row_off[r + 1] - row_off[r] tokens
+ * to request r (1 + l_r of them with spec_schedule's row_off: the last emitted
+ * token and the scheduled draft) and keeps some of them after verification.
+ * Both calls run on the device alone; the host never needs a length.
+ *
+ * spec_cache_reserve, with P = page_size and kv_r = kv_len[r]:
+ *   have_r = ceil(kv_r / P), want_r = ceil((kv_r + n_r) / P),
+ *   off_r = sum over i < r of want_i - have_i;
+ *   block_table[r][have_r + i] = ring[(head + off_r + i) mod n_pages] for
+ *   i < want_r - have_r, and new_len[r] = kv_r + n_r;
+ *   packed row b = row_off[r] + j, j < n_r, at place p = kv_r + j:
+ *   position[b] = pos_base[r] + p, request[b] = r,
+ *   slot[b] = block_table[r][p / P] * P + p mod P;
+ *   rows from row_off[R] to `rows` (the capacity of the three arrays, which a
+ *   captured graph keeps fixed) get -1 in all three.
+ * A request whose pages do not fit, in the ring (off_r + want_r - have_r >
+ * tail - head, and it needs any) or in its page table (want_r > max_pages), gets
+ * none: SPEC_STATUS_NO_PAGES, its rows get -1 and new_len[r] = max(kv_r, 0).  The same
+ * holds, with SPEC_STATUS_BAD_LEN, for a request with kv_r < 0 or with rows
+ * outside [0, rows] or in descending order.  A page id outside [0, n_pages)
+ * gives slot -1 and SPEC_STATUS_BAD_PAGE.
+ *
+ * spec_cache_commit, after the verification (keep = spec_verify's n_out: the
+ * token before the draft and the accepted ones have their keys in the cache):
+ *   kept_r = min(kv_r + keep[r], new_len[r]), or 0 where keep[r] < 0 (the request
+ *   has ended); kv_out[r] = kept_r; the pages block_table[r][ceil(kept_r / P) ..
+ *   ceil(new_len[r] / P)) go to the ring from its tail on, in request order.
+ *   Table entries past the kept ones keep their old values and mean nothing.
+ *
+ *   ring_pos  [2] int64 {head, tail}: pages ring[head mod n_pages ..) up to tail
+ *             are free, 0 <= tail - head <= n_pages.  ring_out receives it after
+ *             the call; reserve moves the head, commit the tail, so two words
+ *             pairs that take turns serve a whole run.
+ * ring_out is not ring_pos, and new_len and kv_out are none of the inputs'
+ * arrays (SPEC_ERR_INVALID_ARG for equal pointers): blocks of the same launch
+ * still read the inputs.  Repeating a call with the same inputs repeats its
+ * outputs.  Sizes: 0 <= R <= 65535, page_size >= 1, 1 <= max_pages,
+ * n_pages * page_size < 2^31, 0 <= rows < 2^31; positions stay below 2^31.
+ */
+typedef struct spec_cache_reserve_args {
+  int R, rows, page_size, n_pages, max_pages;
+  const int32_t *kv_len;   /* [R]                                     */
+  const int32_t *row_off;  /* [R + 1]                                 */
+  const int32_t *pos_base; /* [R], nullable: 0                        */
+  int32_t *block_table;    /* [R, max_pages], in and out              */
+  const int32_t *ring;     /* [n_pages]                               */
+  const int64_t *ring_pos; /* [2]                                     */
+  int64_t *ring_out;       /* [2]                                     */
+  int32_t *new_len;        /* [R]                                     */
+  int32_t *position, *request, *slot; /* [rows]                       */
+  uint32_t *status;
+} spec_cache_reserve_args;
+
+int spec_cache_reserve(const spec_cache_reserve_args *args, spec_stream_t stream);
+
+typedef struct spec_cache_commit_args {
+  int R, page_size, n_pages, max_pages;
+  const int32_t *kv_len;      /* [R], as given to spec_cache_reserve  */
+  const int32_t *new_len;     /* [R], from it                         */
+  const int32_t *keep;        /* [R]                                  */
+  const int32_t *block_table; /* [R, max_pages]                       */
+  int32_t *ring;              /* [n_pages], in and out                */
+  const int64_t *ring_pos;    /* [2]                                  */
+  int64_t *ring_out;          /* [2]                                  */
+  int32_t *kv_out;            /* [R]                                  */
+  uint32_t *status;
+} spec_cache_commit_args;
+
+int spec_cache_commit(const spec_cache_commit_args *args, spec_stream_t stream);
+
+/* ------------------------------------------------------- rotary positions -
+ * Rotary positions on a round's queries and keys, with the keys and values
+ * written to their slots of the paged cache, in one pass.  Pair i < rot / 2 of a
+ * head, (x, y), turns by the angle t = position * freq[i]:
+ *   x' = scale * (x cos t - y sin t),  y' = scale * (y cos t + x sin t),
+ * in fp32 from the stored values, rounded once; (x, y) are elements (i, i +
+ * rot / 2) for SPEC_ROPE_HALF and (2 i, 2 i + 1) for SPEC_ROPE_INTERLEAVED.
+ * Elements rot .. D - 1 are copied.  The angle is exact to fp32 accuracy of its
+ * remainder at every position (no loss at far ones).  freq holds whatever a
+ * long-context scaling makes of the frequencies, scale its attention factor.
+ *   q  [rows, Hq, D], k, v [rows, Hk, D] (dtype), element strides *_row and
+ *      *_head, the last dimension dense: parts of one projection's output will do
+ *   q_out  [rows, Hq, D] by q_out_row / q_out_head; may be q itself
+ *   k_cache, v_cache  [n_slots, Hk, D] dense (n_slots = pages * page size)
+ *   freq [rot / 2] f64 radians per position;  position, slot [rows] int32
+ * position < 0: the row is left out (q_out not written).  position >= 2^24:
+ * taken as 2^24 - 1, SPEC_STATUS_BAD_POSITION.  slot < 0: keys and values of the
+ * row are not written.  slot >= n_slots: the same, SPEC_STATUS_BAD_PAGE.  Rows
+ * with equal slots leave either's values.  Hk = 0 turns queries alone (k, v, the
+ * caches and slot are ignored), Hq = 0 keys alone.
+ * Sizes: rows >= 0, 0 <= Hq, Hk <= 1024, 1 <= D <= 512, rot even, 0 <= rot <= D.
+ */
+enum spec_rope_layout { SPEC_ROPE_HALF = 0, SPEC_ROPE_INTERLEAVED = 1 };
+
+typedef struct spec_rope_cache_args {
+  int rows, Hq, Hk, D, rot;
+  int dtype;  /* spec_dtype of q, k, v, q_out and the caches */
+  int layout; /* spec_rope_layout                            */
+  float scale;
+  const void *q, *k, *v;
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head;
+  void *q_out;
+  int64_t q_out_row, q_out_head;
+  void *k_cache, *v_cache;
+  int64_t n_slots;
+  const double *freq;
+  const int32_t *position, *slot;
+  uint32_t *status;
+} spec_rope_cache_args;
+
+int spec_rope_cache(const spec_rope_cache_args *args, spec_stream_t stream);
+
+/* ------------------------------------------------------ logit adjustments -
+ * Penalties for repeated tokens, biases and grammar masks on packed rows of
+ * logits, ahead of spec_verify (rows 1 + l_r of a request, spec_schedule's
+ * row_off) or of a draft (gamma rows a request).  For entry v of row j of
+ * request r, in fp32 and rounded once:
+ *   c    = how often v is among tokens[r][prompt_len[r] .. length[r]) and
+ *          x[r][0 .. j) (the drafted tokens that the row's position follows)
+ *   seen = c > 0 or v is among tokens[r][0 .. min(prompt_len[r], length[r]))
+ *   z <- z > 0 ? z / repetition[r] : z * repetition[r]   where seen
+ *   z <- z - frequency[r] * c - presence[r]              where c > 0
+ *   z <- z + bias of v in the request's list (a token's last entry counts)
+ *   z <- -inf where bit v mod 32 of word v / 32 of the row's mask is 0
+ * Entries that no rule names keep their bits.  A mask that allows nothing leaves a
+ * row of -inf; NaN or an infinity under a mask becomes -inf.
+ *   logits, out  [rows, V] (dtype), row strides ld, out_ld >= V; out may be
+ *            logits (with out_ld = ld): entries that no rule names are then not
+ *            written.  Otherwise they do not overlap.
+ *   row_off  [R + 1], nullable: row r * rows_per_request + j then.  Rows outside
+ *            every request's are neither read nor written.
+ *   tokens   [R, tokens_ld], tokens_cols tokens each, with prompt_len (nullable: 0)
+ *            and length [R];  x [R, x_ld] (nullable), x_cols tokens each: read where a
+ *            penalty is given
+ *   repetition, frequency, presence [R] f32, each nullable (1, 0, 0)
+ *   bias_off [R + 1], bias_tok, bias_val [n_bias]: nullable together
+ *   mask     [n_masks, mask_ld] 32-bit words, mask_ld >= ceil(V / 32); mask_row
+ *            [rows] names each row's mask, negative: none; NULL: row b has mask b
+ *            (rows past n_masks - 1: none, SPEC_STATUS_BAD_ROW)
+ * Tokens outside [0, V) count for nothing (SPEC_STATUS_BAD_TOKEN); lengths, row
+ * offsets and list offsets are cut to their ranges (SPEC_STATUS_BAD_LEN); a mask
+ * index past the last mask is none (SPEC_STATUS_BAD_ROW).  The result does not
+ * depend on the order of any atomic operation.
+ * Sizes: 0 <= R <= 65535, 1 <= V < 2^30, x_cols <= 64, rows * ld < 2^62 elements.
+ */
+typedef struct spec_logits_args {
+  int R, V, rows, rows_per_request;
+  int dtype; /* spec_dtype of logits and out */
+  const void *logits;
+  int64_t ld;
+  void *out;
+  int64_t out_ld;
+  const int32_t *row_off;
+  const int32_t *tokens;
+  int64_t tokens_ld;
+  const int32_t *prompt_len, *length;
+  const int32_t *x;
+  int64_t x_ld;
+  int tokens_cols, x_cols, n_bias;
+  const float *repetition, *frequency, *presence;
+  const int32_t *bias_off, *bias_tok;
+  const float *bias_val;
+  const int32_t *mask;
+  int64_t mask_ld;
+  const int32_t *mask_row;
+  int n_masks;
+  uint32_t *status;
+} spec_logits_args;
+
+int spec_adjust_logits(const spec_logits_args *args, spec_stream_t stream);
 
 /* ------------------------------------------------------------ stream ----
  * The library's random stream, as the kernels draw it (see "Randomness" above):

@@ -33,6 +33,7 @@ STAGE_DRAFT, STAGE_SCHEDULE, STAGE_VERIFY = 0, 1, 2
 HEAD_MARKOV, HEAD_RNN = 0, 1
 STATUS_BAD_TOKEN, STATUS_BAD_ELL, STATUS_BAD_SURVIVAL, STATUS_BAD_ROW = 0x1, 0x2, 0x4, 0x8
 STATUS_TIMEOUT = 0x10
+STATUS_BAD_LEN, STATUS_NO_PAGES, STATUS_BAD_PAGE, STATUS_BAD_POSITION = 0x20, 0x40, 0x80, 0x100
 
 _P = ctypes.c_void_p
 
@@ -124,6 +125,7 @@ def lib() -> ctypes.CDLL:
         L.spec_stream_uniforms.argtypes = [ctypes.c_uint64, ctypes.c_uint32, ctypes.c_uint32,
                                            ctypes.c_uint32, ctypes.c_int, _P, _P, _P]
         L.spec_stream_uniforms.restype = ctypes.c_int
+        target._bind(L)
         _lib = L
     return _lib
 
@@ -531,3 +533,9 @@ def run_round_host(draft_in: DraftInputs, tgt: torch.Tensor, tgt_row_off: torch.
            "spec_round_host")
     del keep
     return {"draft": d_outs, "sched": s_outs, "verify": v_outs}
+
+
+# the operators around the target model's forward pass
+from . import target  # noqa: E402
+from .target import (adjust_logits, cache_commit, cache_reserve, cache_tables,  # noqa: E402,F401
+                     rope_cache, rope_frequencies)

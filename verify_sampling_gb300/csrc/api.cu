@@ -3,6 +3,7 @@
 // launched; no call synchronises the host or allocates device memory.
 #include <cstdint>
 
+#include "checks.cuh"
 #include "draft.cuh"
 #include "draft_run.cuh"
 #include "draft_tc.cuh"
@@ -17,12 +18,6 @@ namespace {
 using namespace spec;
 
 constexpr int kMaxGridY = 65535;
-
-size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
-
-bool valid_dtype(int d) { return d == SPEC_F32 || d == SPEC_BF16; }
-size_t dtype_size(int d) { return d == SPEC_F32 ? 4 : 2; }
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 // Partials: the larger of the generic kernel's [R, nsplit] and the fused
 // kernel's two slots of [R, splits <= kMaxDeviceSms] (positions alternate, so
@@ -45,13 +40,6 @@ bool draft_sizes_ok(int R, int gamma, int V, int r) {
 bool verify_sizes_ok(int R, int gamma, int V) {
   return R >= 1 && R <= kMaxGridY && gamma >= 1 && gamma + 1 <= kMaxGridY && V >= 1 &&
          V < (1 << 30) && (double)R * (gamma + 1) * V < 1099511627776.0;
-}
-
-int check_workspace(void* ws, size_t have, size_t need) {
-  if (need == 0) return SPEC_OK;
-  if (!ws || have < need) return SPEC_ERR_WORKSPACE;
-  if (!aligned(ws, 256)) return SPEC_ERR_ALIGNMENT;
-  return SPEC_OK;
 }
 
 }  // namespace

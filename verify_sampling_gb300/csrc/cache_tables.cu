@@ -1,0 +1,240 @@
+// Paged-cache bookkeeping of a round: the rows' positions, requests and slots
+// from the requests' lengths, pages taken from the ring of free ones, and pages
+// given back after the verification.
+//
+// Mathematics: an exclusive scan over the requests of the pages each needs (or
+// gives back); everything else is one division per row.
+//
+// Layout: no block waits for another.  Every block scans the lengths of all
+// requests itself (8 bytes a request, from L2 after the first block) and keeps
+// the part it needs: reserve the requests whose rows meet its kChunk packed rows,
+// commit the kOwn requests whose pages it returns.  One launch each, where a
+// scan kernel followed by a map kernel would be two.  Rows are dealt out, not
+// requests, so one prompt of thousands of tokens spreads over the GPU like
+// thousands of requests of one token.
+#include "cache_tables.cuh"
+
+#include <algorithm>
+#include <climits>
+
+namespace spec {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kChunk = 1024;  // packed rows of a reserve block
+constexpr int kOwn = 64;      // requests of a commit block
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return a / b + (a % b > 0); }
+
+// Exclusive prefix of `v` over the block; `total` is the block's sum.
+__device__ __forceinline__ unsigned long long block_scan(unsigned long long v,
+                                                         unsigned long long* warp_sum,
+                                                         unsigned long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned long long inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long t = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += t;
+  }
+  __syncthreads();  // the previous round's readers of warp_sum are done
+  if (lane == 31) warp_sum[warp] = inc;
+  __syncthreads();
+  unsigned long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const unsigned long long t = warp_sum[w];
+    before += w < warp ? t : 0ull;
+    all += t;
+  }
+  *total = all;
+  return before + inc - v;
+}
+
+// One request that has rows in the block's chunk.
+struct Entry {
+  int r, row0, n, kv, have, base;
+  unsigned off;  // its first page's place in the ring, counted from the head
+};
+
+__global__ void __launch_bounds__(kThreads) reserve_kernel(spec_cache_reserve_args a) {
+  __shared__ Entry list[kChunk];
+  __shared__ unsigned long long warp_sum[kWarps];
+  __shared__ unsigned taken_s;
+  const int tid = threadIdx.x, P = a.page_size;
+  const int b0 = blockIdx.x * kChunk, b1 = min(b0 + kChunk, a.rows);
+  const bool first = blockIdx.x == 0;
+  const long long head = a.ring_pos[0], tail = a.ring_pos[1];
+  const long long avail = min(max(tail - head, 0ll), (long long)a.n_pages);
+  long long hm = head % a.n_pages;
+  if (hm < 0) hm += a.n_pages;
+  uint32_t bad = (tail - head != avail) ? SPEC_STATUS_BAD_LEN : 0u;
+  if (tid == 0) taken_s = 0u;
+
+  // scan of the needs (high word) and of the requests met here (low word)
+  unsigned long long carry = 0;
+  for (int r0 = 0; r0 < a.R; r0 += kThreads) {
+    const int r = r0 + tid;
+    int kv = 0, row0 = 0, n = 0, have = 0, need = 0;
+    bool ok = false;
+    if (r < a.R) {
+      kv = a.kv_len[r];
+      row0 = a.row_off[r];
+      const int row1 = a.row_off[r + 1];
+      ok = kv >= 0 && row0 >= 0 && row1 >= row0 && row1 <= a.rows && kv <= INT_MAX - (row1 - row0);
+      if (!ok) bad |= SPEC_STATUS_BAD_LEN;
+      if (ok) {
+        n = row1 - row0;
+        have = ceil_div(kv, P);
+        const int want = ceil_div(kv + n, P);
+        need = want - have;
+        if (want > a.max_pages) {
+          bad |= SPEC_STATUS_NO_PAGES;
+          ok = false;
+          need = 0;
+        }
+      }
+    }
+    const bool met = ok && n > 0 && row0 < b1 && row0 + n > b0;
+    unsigned long long all;
+    const unsigned long long at =
+        carry + block_scan(((unsigned long long)need << 32) | (met ? 1u : 0u), warp_sum, &all);
+    carry += all;
+    const unsigned off = (unsigned)(at >> 32), place = (unsigned)at;
+    const bool granted = ok && (need == 0 || (long long)off + need <= avail);
+    if (ok && !granted) bad |= SPEC_STATUS_NO_PAGES;
+    if (met && place < kChunk)
+      list[place] = Entry{r, row0, granted ? n : 0, kv, have,
+                          a.pos_base ? a.pos_base[r] : 0, off};
+    if (first && r < a.R) {
+      a.new_len[r] = granted ? kv + n : max(kv, 0);
+      if (granted && need > 0) atomicMax(&taken_s, off + (unsigned)need);
+    }
+  }
+  __syncthreads();
+  if (first && tid == 0) {
+    a.ring_out[0] = head + taken_s;
+    a.ring_out[1] = tail;
+  }
+
+  const int n_list = min((int)(unsigned)carry, kChunk);
+  for (int b = b0 + tid; b < b1; b += kThreads) {
+    int lo = 0, hi = n_list;  // the last entry that starts at or before row b
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (list[mid].row0 <= b) lo = mid;
+      else hi = mid;
+    }
+    int position = -1, request = -1, slot = -1;
+    if (n_list > 0) {
+      const Entry e = list[lo];
+      const int j = b - e.row0;
+      if (j >= 0 && j < e.n) {
+        const int p = e.kv + j, pi = p / P, in = p - pi * P;
+        int32_t* entry = a.block_table + (size_t)e.r * a.max_pages + pi;
+        int page;
+        if (pi < e.have) {
+          page = *entry;
+        } else {
+          long long q = hm + e.off + (pi - e.have);
+          if (q >= a.n_pages) q -= a.n_pages;
+          page = a.ring[q];
+          if (in == 0) *entry = page;  // the page's first row: the one writer of the entry
+        }
+        request = e.r;
+        position = e.base + p;
+        if (page >= 0 && page < a.n_pages) slot = page * P + in;
+        else bad |= SPEC_STATUS_BAD_PAGE;
+      }
+    }
+    a.position[b] = position;
+    a.request[b] = request;
+    a.slot[b] = slot;
+  }
+  if (bad) set_status(a.status, bad);
+}
+
+__global__ void __launch_bounds__(kThreads) commit_kernel(spec_cache_commit_args a) {
+  __shared__ unsigned long long warp_sum[kWarps];
+  __shared__ int stay_s[kOwn];
+  __shared__ unsigned at_s[kOwn + 1];
+  const int tid = threadIdx.x, P = a.page_size;
+  const int own0 = blockIdx.x * kOwn, own1 = min(own0 + kOwn, a.R);
+  const bool first = blockIdx.x == 0;
+  const long long head = a.ring_pos[0], tail = a.ring_pos[1];
+  uint32_t bad = 0;
+
+  unsigned long long carry = 0;
+  const int upto = first ? a.R : own1;  // block 0 also needs the total
+  for (int r0 = 0; r0 < upto; r0 += kThreads) {
+    const int r = r0 + tid;
+    int kept = 0, stay = 0, back = 0;
+    if (r < upto) {
+      const int kv = a.kv_len[r], len = a.new_len[r], keep = a.keep[r];
+      const bool ok = kv >= 0 && len >= kv && ceil_div(len, P) <= a.max_pages;
+      if (ok) {
+        kept = keep < 0 ? 0 : (keep < len - kv ? kv + keep : len);
+        stay = ceil_div(kept, P);
+        back = ceil_div(len, P) - stay;
+      } else {
+        bad |= SPEC_STATUS_BAD_LEN;
+        kept = max(kv, 0);
+      }
+    }
+    unsigned long long all;
+    const unsigned at = (unsigned)(carry + block_scan((unsigned long long)back, warp_sum, &all));
+    carry += all;
+    if (r >= own0 && r < own1) {
+      stay_s[r - own0] = stay;
+      at_s[r - own0] = at;
+      if (r == own1 - 1) at_s[own1 - own0] = at + back;
+      a.kv_out[r] = kept;
+    }
+  }
+  __syncthreads();
+  // the ring has room for n_pages ids: more than that can only come from bad lengths
+  const long long room = max(0ll, a.n_pages - max(tail - head, 0ll));
+  if (first && tid == 0) {
+    const long long total = (long long)carry;
+    if (total > room) bad |= SPEC_STATUS_BAD_LEN;
+    a.ring_out[0] = head;
+    a.ring_out[1] = tail + min(total, room);
+  }
+  const int n_own = own1 - own0;
+  if (n_own > 0) {
+    long long tm = tail % a.n_pages;
+    if (tm < 0) tm += a.n_pages;
+    const unsigned end = at_s[n_own];
+    for (unsigned i = at_s[0] + tid; i < end; i += kThreads) {
+      if ((long long)i >= room) break;
+      int lo = 0, hi = n_own;  // the last request whose pages start at or before i
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (at_s[mid] <= i) lo = mid;
+        else hi = mid;
+      }
+      const int page = a.block_table[(size_t)(own0 + lo) * a.max_pages + stay_s[lo] + (i - at_s[lo])];
+      if (page < 0 || page >= a.n_pages) bad |= SPEC_STATUS_BAD_PAGE;
+      a.ring[(tm + i) % a.n_pages] = page;
+    }
+  }
+  if (bad) set_status(a.status, bad);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_reserve(const spec_cache_reserve_args& a, cudaStream_t stream) {
+  const int blocks = std::max(1, (int)(((long long)a.rows + kChunk - 1) / kChunk));
+  reserve_kernel<<<blocks, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_commit(const spec_cache_commit_args& a, cudaStream_t stream) {
+  const int blocks = std::max(1, (a.R + kOwn - 1) / kOwn);
+  commit_kernel<<<blocks, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace spec

@@ -1,0 +1,262 @@
+// Penalties for repeated tokens, biases and grammar masks on packed rows of logits.
+//
+// Mathematics (all in fp32, rounded once): with c = how often v is among the
+// request's generated tokens and the row's drafted ones, and seen = c > 0 or v in
+// the prompt,
+//   z <- z > 0 ? z / repetition : z * repetition   where seen
+//   z <- z - frequency * c - presence * [c > 0]
+//   z <- z + bias[v],   z <- -inf where the row's mask bit is 0.
+//
+// Layout: a block takes a slice of the vocabulary of one request for all its
+// rows.  It reads the request's tokens once, counts those of its slice in shared
+// memory and marks them (and the biased and drafted ones) in a bitmap; then the
+// rows stream through, and a 16-byte vector without a marked or masked entry goes
+// out as it came in.  The history costs 4 bytes a token and slice from L2, where
+// a table of counts over the vocabulary would cost 4 bytes an entry and request
+// from HBM, and has to be kept up between rounds.  Rows share the counts: a row's
+// drafted tokens are compared only at marked entries.
+// Bound by memory: each logit is read and written once.
+#include "logits.cuh"
+
+#include <algorithm>
+
+namespace spec {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxSlice = 4096;  // 33 KB of tables: six blocks an SM
+constexpr int kMinSlice = 1024;
+constexpr int kUnroll = 4;
+constexpr int kMaxDraft = 64;
+constexpr uint32_t kPrompt = 0x80000000u;
+
+template <typename T, int VEC>
+struct RawVec;
+template <>
+struct RawVec<float, 4> {
+  using type = uint4;
+};
+template <>
+struct RawVec<__nv_bfloat16, 8> {
+  using type = uint4;
+};
+template <>
+struct RawVec<float, 1> {
+  using type = uint32_t;
+};
+template <>
+struct RawVec<__nv_bfloat16, 1> {
+  using type = uint16_t;
+};
+
+template <typename T, int VEC>
+union Vec {
+  typename RawVec<T, VEC>::type raw;
+  T e[VEC];
+  __device__ Vec() {}
+};
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_f(float v, float* o) { *o = v; }
+__device__ __forceinline__ void from_f(float v, __nv_bfloat16* o) { *o = __float2bfloat16_rn(v); }
+
+// Bits [at, at + n) of a bitmap, n <= 8, without touching a word they do not reach.
+__device__ __forceinline__ uint32_t bits_at(const uint32_t* w, int at, int n) {
+  const int i = at >> 5, sh = at & 31;
+  uint32_t b = w[i] >> sh;
+  if (sh + n > 32) b |= w[i + 1] << (32 - sh);
+  return b & ((1u << n) - 1u);
+}
+
+// What a block knows of its slice.
+struct Tables {
+  uint32_t* count;   // [slice + 8]: output tokens, kPrompt where the prompt has it
+  int32_t* bias;     // [slice + 8]: entry of the bias list + 1
+  uint32_t* marked;  // bitmap of the entries that any rule touches
+};
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kThreads) adjust_kernel(spec_logits_args p, int slice) {
+  extern __shared__ uint32_t smem[];
+  __shared__ int32_t draft_s[kMaxDraft];
+  const int span = slice + 8;  // a vector that starts in the slice may end 7 entries past it
+  const Tables tab{smem, reinterpret_cast<int32_t*>(smem + span), smem + 2 * span};
+  const int words = (span + 31) / 32;
+  const int tid = threadIdx.x, r = blockIdx.y;
+  const int s0 = blockIdx.x * slice, s1 = min(s0 + slice, p.V);
+  const bool counts = p.repetition || p.frequency || p.presence;
+  uint32_t bad = 0;
+
+  int row0 = p.row_off ? p.row_off[r] : r * p.rows_per_request;
+  int row1 = p.row_off ? p.row_off[r + 1] : row0 + p.rows_per_request;
+  if (row0 < 0 || row1 < row0 || row1 > p.rows) {
+    bad |= SPEC_STATUS_BAD_LEN;
+    row0 = min(max(row0, 0), p.rows);
+    row1 = min(max(row1, row0), p.rows);
+  }
+  const int n = row1 - row0;
+  const int per = (n + gridDim.z - 1) / gridDim.z;  // rows of this block
+  const int j0 = min((int)blockIdx.z * per, n), j1 = min(j0 + per, n);
+  const int n_draft = counts && p.x ? min(max(j1 - 1, 0), p.x_cols) : 0;
+
+  if (j0 < j1) {
+    for (int i = tid; i < 2 * span + words + 1; i += kThreads) smem[i] = 0u;
+    __syncthreads();
+    auto mark = [&](int d) { atomicOr(&tab.marked[d >> 5], 1u << (d & 31)); };
+    if (counts) {
+      const int32_t* tok = p.tokens + (size_t)r * p.tokens_ld;
+      int len = p.length[r];
+      if (len < 0 || len > p.tokens_cols) {
+        bad |= SPEC_STATUS_BAD_LEN;
+        len = min(max(len, 0), p.tokens_cols);
+      }
+      const int prompt = p.prompt_len ? p.prompt_len[r] : 0;
+      for (int i = tid; i < len; i += kThreads * kUnroll) {
+        int t[kUnroll];
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) t[k] = i + k * kThreads < len ? tok[i + k * kThreads] : s0 - 1;
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+          const int at = i + k * kThreads;
+          if (at < len && (unsigned)t[k] >= (unsigned)p.V) bad |= SPEC_STATUS_BAD_TOKEN;
+          const unsigned d = (unsigned)t[k] - (unsigned)s0;
+          if (d < (unsigned)span && (unsigned)t[k] < (unsigned)p.V) {
+            if (at < prompt) atomicOr(&tab.count[d], kPrompt);
+            else atomicAdd(&tab.count[d], 1u);
+            mark(d);
+          }
+        }
+      }
+      for (int i = tid; i < n_draft; i += kThreads) {
+        const int t = p.x[(size_t)r * p.x_ld + i];
+        draft_s[i] = t;
+        if ((unsigned)t >= (unsigned)p.V) bad |= SPEC_STATUS_BAD_TOKEN;
+        const unsigned d = (unsigned)t - (unsigned)s0;
+        if (d < (unsigned)span && (unsigned)t < (unsigned)p.V) mark(d);
+      }
+    }
+    if (p.bias_off) {
+      int b0 = p.bias_off[r], b1 = p.bias_off[r + 1];
+      if (b0 < 0 || b1 < b0 || b1 > p.n_bias) {
+        bad |= SPEC_STATUS_BAD_LEN;
+        b0 = min(max(b0, 0), p.n_bias);
+        b1 = min(max(b1, b0), p.n_bias);
+      }
+      for (int i = b0 + tid; i < b1; i += kThreads) {
+        const int t = p.bias_tok[i];
+        if ((unsigned)t >= (unsigned)p.V) bad |= SPEC_STATUS_BAD_TOKEN;
+        const unsigned d = (unsigned)t - (unsigned)s0;
+        if (d < (unsigned)span && (unsigned)t < (unsigned)p.V) {
+          atomicMax(&tab.bias[d], i + 1);  // a token's last entry counts
+          mark(d);
+        }
+      }
+    }
+    __syncthreads();
+
+    const float rep = p.repetition ? p.repetition[r] : 1.f, freq = p.frequency ? p.frequency[r] : 0.f,
+                pres = p.presence ? p.presence[r] : 0.f;
+    const bool same = p.out == p.logits && p.out_ld == p.ld;
+    for (int j = j0; j < j1; ++j) {
+      const size_t b = (size_t)(row0 + j);
+      const T* in = (const T*)p.logits + b * p.ld;
+      T* out = (T*)p.out + b * p.out_ld;
+      const uint32_t* mask = nullptr;
+      if (p.mask) {
+        const int m = p.mask_row ? p.mask_row[b] : (int)b;
+        if (m >= p.n_masks) bad |= SPEC_STATUS_BAD_ROW;
+        else if (m >= 0) mask = reinterpret_cast<const uint32_t*>(p.mask) + (size_t)m * p.mask_ld;
+      }
+      auto adjust = [&](T& e, int v, bool is_marked, bool allowed) {
+        if (!allowed) {
+          from_f(-CUDART_INF_F, &e);
+          return;
+        }
+        if (!is_marked) return;
+        const int d = v - s0;
+        float z = to_f(e);
+        if (counts) {
+          const uint32_t w = tab.count[d];
+          uint32_t c = w & ~kPrompt;
+          const int upto = min(j, n_draft);
+          for (int i = 0; i < upto; ++i) c += draft_s[i] == v;
+          if (c > 0 || (w & kPrompt)) z = z > 0.f ? z / rep : z * rep;
+          if (c > 0) z = z - freq * (float)c - pres;
+        }
+        const int bi = tab.bias[d];
+        if (bi > 0) z += p.bias_val[bi - 1];
+        from_f(z, &e);
+      };
+      // Vectors lie on 16 bytes of memory, so a row that starts off them begins
+      // with a partial vector: entry v of vector i is i * VEC - lead + its place.
+      const int lead = VEC == 1 ? 0 : (int)(((uintptr_t)in / sizeof(T)) & (VEC - 1));
+      const int i_begin = s0 == 0 ? 0 : (s0 + lead + VEC - 1) / VEC, i_end = (s1 + lead + VEC - 1) / VEC;
+      using V = Vec<T, VEC>;
+      using R = decltype(V().raw);
+      for (int i = i_begin + tid; i < i_end; i += kThreads * kUnroll) {
+        V x[kUnroll];
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+          const int v = (i + k * kThreads) * VEC - lead;
+          if (i + k * kThreads < i_end && v >= 0 && v + VEC <= p.V)
+            x[k].raw = *reinterpret_cast<const R*>(in + v);
+        }
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+          if (i + k * kThreads >= i_end) break;
+          const int v = (i + k * kThreads) * VEC - lead;
+          if (v >= 0 && v + VEC <= p.V) {
+            const uint32_t mk = bits_at(tab.marked, v - s0, VEC);
+            const uint32_t al = mask ? bits_at(mask, v, VEC) : (1u << VEC) - 1u;
+            const bool changed = mk != 0u || al != (1u << VEC) - 1u;
+            if (changed) {
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) adjust(x[k].e[e], v + e, mk >> e & 1u, al >> e & 1u);
+            }
+            if (changed || !same) *reinterpret_cast<R*>(out + v) = x[k].raw;
+          } else {  // the row's first or last entries
+            for (int e = 0; e < VEC; ++e) {
+              const int w = v + e;
+              if (w < 0 || w >= p.V) continue;
+              T z = in[w];
+              adjust(z, w, bits_at(tab.marked, w - s0, 1), mask ? bits_at(mask, w, 1) : 1u);
+              out[w] = z;
+            }
+          }
+        }
+      }
+    }
+  }
+  if (bad) set_status(p.status, bad);
+}
+
+template <typename T, int VEC>
+cudaError_t launch(const spec_logits_args& a, cudaStream_t stream) {
+  // Few rows: small slices, so that one row of a large vocabulary spreads over
+  // the SMs; otherwise the largest, whose blocks read the history least often.
+  const long long blocks = (long long)a.R * ((a.V + kMaxSlice - 1) / kMaxSlice);
+  const int slice = blocks < 304 ? kMinSlice : kMaxSlice;
+  // A request with many rows is split over blocks of about 16.
+  const int parts = (int)std::min<long long>(64, std::max<long long>(1, (long long)a.rows / (16ll * a.R)));
+  const int span = slice + 8;
+  const size_t smem = (size_t)(2 * span + (span + 31) / 32 + 1) * 4;
+  const dim3 grid((a.V + slice - 1) / slice, a.R, parts);
+  adjust_kernel<T, VEC><<<grid, kThreads, smem, stream>>>(a, slice);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_adjust_logits(const spec_logits_args& a, cudaStream_t stream) {
+  if (a.R == 0 || a.rows == 0) return cudaSuccess;
+  const size_t es = a.dtype == SPEC_F32 ? 4 : 2;
+  // 16-byte vectors wherever a row lies on the same offset from 16 bytes in both arrays
+  const bool wide = ((uintptr_t)a.logits - (uintptr_t)a.out) % 16 == 0 &&
+                    ((a.ld - a.out_ld) * (int64_t)es) % 16 == 0;
+  if (a.dtype == SPEC_F32) return wide ? launch<float, 4>(a, stream) : launch<float, 1>(a, stream);
+  return wide ? launch<__nv_bfloat16, 8>(a, stream) : launch<__nv_bfloat16, 1>(a, stream);
+}
+
+}  // namespace spec

@@ -1,0 +1,317 @@
+"""The operators around the target model's forward pass: cache tables, rotary
+positions with the cache write, shared-prefix attention and logit adjustments.
+
+Like the rest of the binding these functions only marshal arguments; layouts,
+rules and status bits are in ``include/spec.h``.  Tensors that a call makes for
+itself belong to the stream it runs on.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import math
+from typing import Optional
+
+import torch
+
+from . import _check, _dev, _dtype_code, _P, lib
+
+_I, _L, _F = ctypes.c_int, ctypes.c_int64, ctypes.c_float
+
+
+class CacheReserveArgs(ctypes.Structure):
+    _fields_ = [("R", _I), ("rows", _I), ("page_size", _I), ("n_pages", _I), ("max_pages", _I),
+                ("kv_len", _P), ("row_off", _P), ("pos_base", _P), ("block_table", _P), ("ring", _P),
+                ("ring_pos", _P), ("ring_out", _P), ("new_len", _P), ("position", _P),
+                ("request", _P), ("slot", _P), ("status", _P)]
+
+
+class CacheCommitArgs(ctypes.Structure):
+    _fields_ = [("R", _I), ("page_size", _I), ("n_pages", _I), ("max_pages", _I), ("kv_len", _P),
+                ("new_len", _P), ("keep", _P), ("block_table", _P), ("ring", _P), ("ring_pos", _P),
+                ("ring_out", _P), ("kv_out", _P), ("status", _P)]
+
+
+class RopeCacheArgs(ctypes.Structure):
+    _fields_ = [("rows", _I), ("Hq", _I), ("Hk", _I), ("D", _I), ("rot", _I), ("dtype", _I),
+                ("layout", _I), ("scale", _F), ("q", _P), ("k", _P), ("v", _P), ("q_row", _L),
+                ("q_head", _L), ("k_row", _L), ("k_head", _L), ("v_row", _L), ("v_head", _L),
+                ("q_out", _P), ("q_out_row", _L), ("q_out_head", _L), ("k_cache", _P),
+                ("v_cache", _P), ("n_slots", _L), ("freq", _P), ("position", _P), ("slot", _P),
+                ("status", _P)]
+
+
+class LogitsArgs(ctypes.Structure):
+    _fields_ = [("R", _I), ("V", _I), ("rows", _I), ("rows_per_request", _I), ("dtype", _I),
+                ("logits", _P), ("ld", _L), ("out", _P), ("out_ld", _L), ("row_off", _P),
+                ("tokens", _P), ("tokens_ld", _L), ("prompt_len", _P), ("length", _P), ("x", _P),
+                ("x_ld", _L), ("tokens_cols", _I), ("x_cols", _I), ("n_bias", _I), ("repetition", _P), ("frequency", _P),
+                ("presence", _P), ("bias_off", _P), ("bias_tok", _P), ("bias_val", _P),
+                ("mask", _P), ("mask_ld", _L), ("mask_row", _P), ("n_masks", _I), ("status", _P)]
+
+
+def _bind(L: ctypes.CDLL) -> None:
+    """Prototypes of this module's entry points (called once by ``lib``)."""
+    for name, cls in (("spec_cache_reserve", CacheReserveArgs),
+                      ("spec_cache_commit", CacheCommitArgs),
+                      ("spec_rope_cache", RopeCacheArgs),
+                      ("spec_adjust_logits", LogitsArgs)):
+        f = getattr(L, name)
+        f.argtypes, f.restype = [ctypes.POINTER(cls), _P], ctypes.c_int
+
+
+def _t(t: torch.Tensor, name: str, dtype: torch.dtype, numel: int = -1) -> int:
+    """Address of a contiguous device tensor of this dtype (and at least numel entries)."""
+    if _dev(t, name).dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.numel() < numel:
+        raise ValueError(f"{name} must have {numel} entries")
+    return t.data_ptr()
+
+
+def _opt(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, numel: int = -1) -> Optional[int]:
+    return None if t is None else _t(t, name, dtype, numel)
+
+
+def _on(stream) -> int:
+    """Handle of the stream to launch on."""
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _made_on(stream):
+    """Context in which the call's own tensors are allocated: memory of the stream it runs on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+# ------------------------------------------------------------- cache tables --
+def cache_tables(R: int, n_pages: int, page_size: int, max_pages: int, device="cuda") -> dict:
+    """An empty cache's bookkeeping: lengths 0, every page free.  Keys: "kv_len" [R],
+    "block_table" [R, max_pages], "ring" [n_pages] int32, "ring_pos" [2] int64 and "page_size"."""
+    return {"kv_len": torch.zeros(R, dtype=torch.int32, device=device),
+            "block_table": torch.full((R, max_pages), -1, dtype=torch.int32, device=device),
+            "ring": torch.arange(n_pages, dtype=torch.int32, device=device),
+            "ring_pos": torch.tensor([0, n_pages], dtype=torch.int64, device=device),
+            "page_size": page_size}
+
+
+def cache_reserve(cache: dict, row_off: torch.Tensor, rows: int, *,
+                  pos_base: Optional[torch.Tensor] = None, out: Optional[dict] = None,
+                  status: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """spec_cache_reserve: pages, positions and slots for row_off[R] new tokens.
+
+    ``cache`` is the dict of ``cache_tables``; its "block_table" gets the new pages.  ``rows`` is
+    the capacity of the row arrays (row_off[R] at least; the rest is -1).  Returns {"new_len" [R],
+    "position", "request", "slot" [rows] int32, "ring_pos" [2] int64}, which ``cache_commit`` takes."""
+    table, ring = cache["block_table"], cache["ring"]
+    R, width = table.shape
+    if out is None:
+        dev = table.device
+        with _made_on(stream):
+            position, request, slot = torch.empty(3, rows, dtype=torch.int32, device=dev).unbind(0)
+            out = {"new_len": torch.empty(R, dtype=torch.int32, device=dev), "position": position,
+                   "request": request, "slot": slot,
+                   "ring_pos": torch.empty(2, dtype=torch.int64, device=dev)}
+    i32, i64 = torch.int32, torch.int64
+    a = CacheReserveArgs(
+        R, rows, cache["page_size"], ring.numel(), width, _t(cache["kv_len"], "kv_len", i32, R),
+        _t(row_off, "row_off", i32, R + 1), _opt(pos_base, "pos_base", i32, R),
+        _t(table, "block_table", i32), _t(ring, "ring", i32),
+        _t(cache["ring_pos"], "ring_pos", i64, 2), _t(out["ring_pos"], "out ring_pos", i64, 2),
+        _t(out["new_len"], "new_len", i32, R), _t(out["position"], "position", i32, rows),
+        _t(out["request"], "request", i32, rows), _t(out["slot"], "slot", i32, rows),
+        _opt(status, "status", i32, 1))
+    _check(lib().spec_cache_reserve(ctypes.byref(a), _on(stream)), "spec_cache_reserve")
+    return out
+
+
+def cache_commit(cache: dict, reserved: dict, keep: torch.Tensor, *, out: Optional[dict] = None,
+                 status: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """spec_cache_commit: keep the first keep[r] new tokens of each request (verify's n_out; a
+    negative entry ends the request) and give the other pages back to cache["ring"].
+
+    Returns {"kv_len" [R], "ring_pos" [2]}; ``cache.update(...)`` with it makes it the next
+    round's state (both rounds' dicts can serve in turn as ``out``)."""
+    table, ring = cache["block_table"], cache["ring"]
+    R, width = table.shape
+    if out is None:
+        with _made_on(stream):
+            out = {"kv_len": torch.empty(R, dtype=torch.int32, device=table.device),
+                   "ring_pos": torch.empty(2, dtype=torch.int64, device=table.device)}
+    i32, i64 = torch.int32, torch.int64
+    a = CacheCommitArgs(
+        R, cache["page_size"], ring.numel(), width, _t(cache["kv_len"], "kv_len", i32, R),
+        _t(reserved["new_len"], "new_len", i32, R), _t(keep, "keep", i32, R),
+        _t(table, "block_table", i32), _t(ring, "ring", i32),
+        _t(reserved["ring_pos"], "ring_pos", i64, 2), _t(out["ring_pos"], "out ring_pos", i64, 2),
+        _t(out["kv_len"], "out kv_len", i32, R), _opt(status, "status", i32, 1))
+    _check(lib().spec_cache_commit(ctypes.byref(a), _on(stream)), "spec_cache_commit")
+    return out
+
+
+# --------------------------------------------------------- rotary positions --
+def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
+                     trained: int = 0, low: float = 1.0, high: float = 32.0, device="cuda"):
+    """Frequencies [rot / 2] float64 (radians per position) and the attention factor for ``rope_cache``.
+
+    f_i = base^(-2 i / rot), then for contexts ``factor`` times as long as the trained ones:
+      "none"    as they are
+      "linear"  f_i / factor (positions interpolated)
+      "base"    base * factor^(rot / (rot - 2)): the highest frequency kept, the lowest divided by factor
+      "ramp"    f_i where a head turns more than ``high`` times over ``trained`` positions, f_i / factor
+                where it turns less than ``low`` times, linear in the turns' pair index between; attention
+                factor 0.1 ln(factor) + 1
+      "band"    the same two ends, linear in the number of turns between; attention factor 1
+    """
+    if rot < 2 or rot % 2:
+        raise ValueError("rot must be even and positive")
+    if not factor >= 1.0 or (scaling in ("ramp", "band") and (trained < 1 or not 0 < low < high)):
+        raise ValueError("factor must be 1 or more; ramp and band need trained > 0 and 0 < low < high")
+    i = torch.arange(0, rot, 2, dtype=torch.float64)
+    if scaling == "base":
+        if rot < 4:
+            raise ValueError("base scaling needs rot >= 4")
+        base = base * factor ** (rot / (rot - 2))
+    f = base ** (-i / rot)
+    scale = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling in ("ramp", "band"):
+        if scaling == "band":
+            share = (trained * f / (2 * math.pi) - low) / (high - low)
+        else:
+            at = [rot * math.log(trained / (2 * math.pi * t)) / (2 * math.log(base)) for t in (high, low)]
+            first, last = max(0, math.floor(at[0])), min(rot - 1, math.ceil(at[1]))
+            share = 1 - (i / 2 - first) / max(last - first, 1e-3)
+            scale = 0.1 * math.log(factor) + 1.0
+        share = share.clamp(0, 1)
+        f = f * share + f / factor * (1 - share)
+    elif scaling not in ("none", "base"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return f.to(device), scale
+
+
+def _strided(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) -> tuple:
+    """Address and the row and head strides of [rows, heads, D] whose last dimension is dense."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    row, head, one = t.stride()
+    if one != 1 and shape[2] > 1:
+        raise ValueError(f"{name}'s last dimension must be dense")
+    return t.data_ptr(), row, head
+
+
+def rope_cache(q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Tensor],
+               freq: torch.Tensor, position: torch.Tensor, slot: Optional[torch.Tensor],
+               k_cache: Optional[torch.Tensor], v_cache: Optional[torch.Tensor], *,
+               interleaved: bool = False, scale: float = 1.0, q_out: Optional[torch.Tensor] = None,
+               status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """spec_rope_cache: turn q [rows, Hq, D] and k [rows, Hk, D] by their positions, write k and v
+    to their slots of the caches [pages, page_size, Hk, D]; returns the turned queries (``q_out``,
+    which may be ``q`` itself).  2 * freq.numel() elements of each head turn.  q, k and v may be
+    parts of one wider tensor; with k None only the queries turn."""
+    rows, Hq, D = q.shape
+    dt = q.dtype
+    if q_out is None:
+        with _made_on(stream):
+            q_out = torch.empty((rows, Hq, D), dtype=dt, device=q.device)
+    qp, qr, qh = _strided(q, "q", dt, (rows, Hq, D))
+    op, orow, oh = _strided(q_out, "q_out", dt, (rows, Hq, D))
+    if k is None:
+        Hk, n_slots, kv, sp, kc, vc = 0, 0, (None, None, 0, 0, 0, 0), None, None, None
+    else:
+        Hk = k.shape[1]
+        kp, kr, kh = _strided(k, "k", dt, (rows, Hk, D))
+        vp, vr, vh = _strided(v, "v", dt, (rows, Hk, D))
+        kv = (kp, vp, kr, kh, vr, vh)
+        if k_cache.dim() != 4 or k_cache.shape[2:] != (Hk, D) or v_cache.shape != k_cache.shape:
+            raise ValueError("k_cache and v_cache must both be [pages, page_size, Hk, D]")
+        kc, vc = _t(k_cache, "k_cache", dt), _t(v_cache, "v_cache", dt)
+        n_slots, sp = k_cache.shape[0] * k_cache.shape[1], _t(slot, "slot", torch.int32, rows)
+    a = RopeCacheArgs(rows, Hq, Hk, D, 2 * freq.numel(), _dtype_code(q), int(interleaved), scale, qp,
+                      kv[0], kv[1], qr, qh, *kv[2:], op, orow, oh, kc, vc, n_slots,
+                      _t(freq, "freq", torch.float64), _t(position, "position", torch.int32, rows), sp,
+                      _opt(status, "status", torch.int32, 1))
+    _check(lib().spec_rope_cache(ctypes.byref(a), _on(stream)), "spec_rope_cache")
+    return q_out
+
+
+# -------------------------------------------------------- logit adjustments --
+def _matrix(t: torch.Tensor, name: str, dtype: torch.dtype) -> tuple:
+    """Address and row stride of a device matrix with dense rows."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a matrix with dense rows")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+
+def adjust_logits(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None,
+                  prompt_len: Optional[torch.Tensor] = None, length: Optional[torch.Tensor] = None, *,
+                  row_off: Optional[torch.Tensor] = None, rows_per_request: int = 1,
+                  x: Optional[torch.Tensor] = None, repetition: Optional[torch.Tensor] = None,
+                  frequency: Optional[torch.Tensor] = None, presence: Optional[torch.Tensor] = None,
+                  bias: Optional[tuple] = None, mask: Optional[torch.Tensor] = None,
+                  mask_row: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """spec_adjust_logits: penalties, biases and grammar masks on the rows of ``logits`` [rows, V].
+
+    ``row_off`` [R + 1] int32 packs the rows (schedule's row_off); without it each request has
+    ``rows_per_request``.  ``tokens`` [R, n] int32 are each request's prompt and output so far
+    (``length`` [R] of them, the first ``prompt_len`` [R] the prompt); row j counts the first j
+    drafted tokens of ``x`` [R, gamma] too.  ``bias`` = (offsets [R + 1], tokens, values),
+    ``mask`` [n, ceil(V / 32)] int32 bits with ``mask_row`` [rows] (negative: no mask).
+    ``out`` may be ``logits``.  Rows outside every request's are left as they are in ``out``."""
+    i32, f32 = torch.int32, torch.float32
+    dt = logits.dtype
+    lp, ld = _matrix(logits, "logits", dt)
+    rows, V = logits.shape
+    if out is None:
+        with _made_on(stream):
+            out = torch.empty((rows, V), dtype=dt, device=logits.device)
+        op, old = out.data_ptr(), V
+    else:
+        op, old = _matrix(out, "out", dt)
+        if out.shape != logits.shape:
+            raise ValueError("out must have the shape of logits")
+    if row_off is not None:
+        R = row_off.numel() - 1
+    else:
+        R = length.numel() if length is not None else rows // max(rows_per_request, 1)
+    tp, tl, tc = None, 0, 0
+    if tokens is not None:
+        tp, tl = _matrix(tokens, "tokens", i32)
+        tc = tokens.shape[1]
+        if tokens.shape[0] < R:
+            raise ValueError("tokens must have a row for each request")
+    xp, xl, xc = None, 0, 0
+    if x is not None:
+        xp, xl = _matrix(x, "x", i32)
+        xc = x.shape[1]
+        if x.shape[0] < R:
+            raise ValueError("x must have a row for each request")
+    bo = bt = bv = None
+    nb = 0
+    if bias is not None and bias[1].numel() > 0:
+        nb = bias[1].numel()
+        bo, bt, bv = (_t(bias[0], "bias offsets", i32, R + 1), _t(bias[1], "bias tokens", i32),
+                      _t(bias[2], "bias values", f32, nb))
+    mp, ml, nm = None, 0, 0
+    if mask is not None:
+        mp, ml = _matrix(mask, "mask", i32)
+        nm = mask.shape[0]
+        if mask.shape[1] * 32 < V:
+            raise ValueError("mask rows must have ceil(V / 32) words")
+    a = LogitsArgs(
+        R, V, rows, rows_per_request, _dtype_code(logits), lp, ld, op, old,
+        _opt(row_off, "row_off", i32, 1), tp, tl, _opt(prompt_len, "prompt_len", i32, R),
+        _opt(length, "length", i32, R), xp, xl, tc, xc, nb, _opt(repetition, "repetition", f32, R),
+        _opt(frequency, "frequency", f32, R), _opt(presence, "presence", f32, R), bo, bt, bv, mp, ml,
+        _opt(mask_row, "mask_row", i32, rows), nm, _opt(status, "status", i32, 1))
+    _check(lib().spec_adjust_logits(ctypes.byref(a), _on(stream)), "spec_adjust_logits")
+    return out
