@@ -551,6 +551,58 @@ typedef struct spec_rope_cache_args {
 
 int spec_rope_cache(const spec_rope_cache_args *args, spec_stream_t stream);
 
+/* ------------------------------------------------- shared-prefix attention -
+ * Attention of a round's packed rows over a paged cache, for a batch whose
+ * requests share a long prefix: the prefix's keys are read once for all rows of a
+ * group, each request's own keys once for its rows.  Row j of request r (packed
+ * row row_off[r] + j, n_r rows) attends to
+ *   - the prefix_len[g] keys of its group's prefix pages, if it is in a group g
+ *     (requests group_off[g] .. group_off[g + 1] - 1), and
+ *   - its own keys 0 .. kv_len[r] - n_r + j, in block_table's pages: kv_len counts
+ *     the rows' own tokens, which are in the cache (spec_cache_reserve's new_len,
+ *     spec_rope_cache); positions are the caller's.
+ *   out = sum_i softmax_i(scale * q . k_i) v_i, query head hq with key head
+ *   hq / (Hq / Hk); lse = ln sum_i exp(scale * q . k_i).
+ * Maxima, sums and values are kept in fp32; on the tensor-core path the softmax
+ * weights are rounded to bf16 for the product with the values.  A row without keys
+ * gets zeros and lse = -inf.  Rows outside every request's are not written.  What
+ * pages hold past a request's keys (NaN too) has no effect; the values of the keys
+ * themselves have to be finite.
+ *   q, out  [rows, Hq, D] by element strides; caches [n_pages, page_size, Hk, D]
+ *   kv_len [R], block_table [R, max_pages]; group_off [G + 1], prefix_len [G],
+ *   prefix_table [G, max_prefix_pages] (G = 0: no prefixes); lse [rows, Hq] nullable
+ *   workspace  spec_attention_workspace_bytes(rows, R, Hq, D) bytes
+ * bf16 with D 64 or 128, pages of 8, 16, 32, 64 or a multiple of 128 tokens and
+ * 16-byte rows take the tensor-core kernels; everything else the generic ones.
+ * A length past its page table is cut to it, a bad row or group range left out
+ * (SPEC_STATUS_BAD_LEN); a page id outside [0, n_pages) is taken as page 0
+ * (SPEC_STATUS_BAD_PAGE).
+ * Sizes: 0 <= R <= 65535, 0 <= G <= R, Hk divides Hq <= 1024, D <= 256, rows * Hq
+ * < 2^31, n_pages * page_size < 2^31, 0 < scale < 1e30.
+ */
+typedef struct spec_prefix_attention_args {
+  int R, rows, Hq, Hk, D;
+  int dtype; /* spec_dtype of q, out and the caches */
+  int page_size, n_pages, max_pages, G, max_prefix_pages;
+  float scale;
+  const void *q;
+  int64_t q_row, q_head;
+  const void *k_cache, *v_cache;
+  const int32_t *row_off, *kv_len, *block_table;
+  const int32_t *group_off, *prefix_len, *prefix_table;
+  void *out;
+  int64_t out_row, out_head;
+  float *lse;
+  void *workspace;
+  size_t workspace_bytes;
+  uint32_t *status;
+} spec_prefix_attention_args;
+
+int spec_prefix_attention(const spec_prefix_attention_args *args, spec_stream_t stream);
+
+/* Workspace of spec_prefix_attention (0 if the sizes are invalid). */
+size_t spec_attention_workspace_bytes(int rows, int R, int Hq, int D);
+
 /* ------------------------------------------------------ logit adjustments -
  * Penalties for repeated tokens, biases and grammar masks on packed rows of
  * logits, ahead of spec_verify (rows 1 + l_r of a request, spec_schedule's

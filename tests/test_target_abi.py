@@ -13,6 +13,7 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 STRUCTS = {"spec_cache_reserve_args": target.CacheReserveArgs,
            "spec_cache_commit_args": target.CacheCommitArgs,
            "spec_rope_cache_args": target.RopeCacheArgs,
+           "spec_prefix_attention_args": target.PrefixAttentionArgs,
            "spec_logits_args": target.LogitsArgs}
 
 
@@ -125,3 +126,21 @@ def test_logits_refuse(lib):
         ({"logits": 4098}, ALIGN), ({"dtype": 1, "out": 4097}, ALIGN), ({"tokens": 4097}, ALIGN), ({"mask": 4098}, ALIGN)])
     for none in ({"R": 0}, {"rows": 0}):
         assert lib.spec_adjust_logits(ctypes.byref(_filled(target.LogitsArgs, **{**sizes, **none})), None) == vs.SPEC_OK
+
+
+def test_attention_refuses(lib):
+    need = vs.attention_workspace_bytes(8, 4, 8, 64)
+    assert need > 0 and vs.attention_workspace_bytes(-1, 4, 8, 64) == 0 and vs.attention_workspace_bytes(8, 4, 8, 257) == 0
+    sizes = dict(R=4, rows=8, Hq=8, Hk=2, D=64, page_size=16, n_pages=20, max_pages=4, G=2, max_prefix_pages=3, scale=0.125,
+                 workspace_bytes=need)
+    _refusals(lib.spec_prefix_attention, target.PrefixAttentionArgs, sizes, [
+        ({"R": -1}, BAD), ({"R": 65536}, BAD), ({"rows": -1}, BAD), ({"Hq": 0}, BAD), ({"Hq": 7}, BAD), ({"Hk": 0}, BAD),
+        ({"Hq": 1026}, BAD), ({"D": 0}, BAD), ({"D": 257}, UNSUP), ({"dtype": 3}, BAD), ({"page_size": 0}, BAD), ({"n_pages": 0}, BAD),
+        ({"max_pages": 0}, BAD), ({"G": -1}, BAD), ({"G": 5}, BAD), ({"max_prefix_pages": 0}, BAD), ({"scale": 0.0}, BAD),
+        ({"scale": float("nan")}, BAD), ({"scale": float("inf")}, BAD), ({"q": None}, BAD), ({"k_cache": None}, BAD), ({"out": None}, BAD),
+        ({"row_off": None}, BAD), ({"kv_len": None}, BAD), ({"block_table": None}, BAD), ({"group_off": None}, BAD),
+        ({"prefix_table": None}, BAD), ({"rows": 1 << 30, "Hq": 2}, BAD), ({"q": 4098}, ALIGN), ({"lse": 4097}, ALIGN),
+        ({"prefix_len": 4098}, ALIGN), ({"workspace": None}, vs.SPEC_ERR_WORKSPACE), ({"workspace_bytes": need - 1}, vs.SPEC_ERR_WORKSPACE),
+        ({"workspace": 4096 + 128}, ALIGN)])
+    for none in ({"R": 0, "G": 0}, {"rows": 0}):
+        assert lib.spec_prefix_attention(ctypes.byref(_filled(target.PrefixAttentionArgs, **{**sizes, **none})), None) == vs.SPEC_OK

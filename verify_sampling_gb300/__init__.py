@@ -537,5 +537,6 @@ def run_round_host(draft_in: DraftInputs, tgt: torch.Tensor, tgt_row_off: torch.
 
 # the operators around the target model's forward pass
 from . import target  # noqa: E402
-from .target import (adjust_logits, cache_commit, cache_reserve, cache_tables,  # noqa: E402,F401
-                     rope_cache, rope_frequencies)
+from .target import (adjust_logits, attention_workspace_bytes, cache_commit,  # noqa: E402,F401
+                     cache_reserve, cache_tables, prefix_attention, rope_cache,
+                     rope_frequencies)

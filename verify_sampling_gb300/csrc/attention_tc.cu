@@ -1,0 +1,752 @@
+// Shared-prefix attention on the tensor cores (bf16, heads of 64 or 128): a
+// round's packed rows against the prefix pages that their group shares and each
+// request's own pages, every key read once for all the rows that need it.
+//
+// Mathematics: for a row with scaled scores z (log2 units) over a piece of its
+// keys, the piece keeps a reference m, l = sum 2^(z - m) and O = sum 2^(z - m) v;
+// pieces join as out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.  m follows the
+// running maximum only when it has grown by more than 8, so O is rescaled a few
+// times a row instead of once a tile; a weight is then at most 2^8 and fp32 sums
+// lose nothing by it.  Weights are rounded to bf16 for the second product (8 bits
+// of a weight are 8 bits of its share of the result); l adds them unrounded.
+//
+// Work: an item is up to 256 query rows (packed rows x the query heads of one
+// key head) of a group over its prefix, or of a request over its own keys.  The
+// items' tiles of 128 keys, laid end to end with a fixed cost an item, are cut
+// into equal lengths, one per block and one block per SM: blocks finish together
+// whatever the mix of one long prefix, many short requests or one request alone.
+// Lengths are device data, so each block computes the layout itself (one scan).
+// An item cut between blocks leaves several pieces; a second kernel joins every
+// row's pieces.
+//
+// Block: producer warp (TMA of key and value tiles, 64 x page boxes, into one
+// ring), MMA warp (S = Q K^T into TMEM, O += P V with P read from TMEM), and two
+// softmax warpgroups of 128 rows, one thread a row, so maxima and sums need no
+// shuffles.  An item of more than 128 rows uses both warpgroups on the same key
+// tile, one's softmax under the other's products; smaller items alternate
+// between them, and the next item's first product is issued before the
+// current one's last weights are ready.
+//
+// Every wait is bounded; on a timeout the block sets SPEC_STATUS_TIMEOUT, waits
+// for its copies and products in flight and frees its TMEM.
+#include <cuda.h>
+
+#include "attention.cuh"
+#include "fused_tc.cuh"
+#include "tc.cuh"
+
+namespace spec {
+
+namespace {
+
+using namespace attn;
+
+constexpr int kTile = 128;  // keys of a tile, rows of a warpgroup
+constexpr int kThreads = 320;
+constexpr int kProducer = 8, kMma = 9;  // warps 0-3 and 4-7 are the softmax warpgroups
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr float kSlack = 8.f;  // log2 units the maximum may grow by before O is rescaled
+// Costs, in units of about 400 clocks: a prefix tile (two warpgroups, bound by the
+// products), an own tile (bound by its 64 KB), and an item's start and end.
+constexpr int kCostPrefix = 2, kCostOwn = 3, kCostItem = 3;
+
+// ------------------------------------------------------------ work layout --
+struct Segment {  // a group's prefix or a request's own keys
+  int row0, n;    // packed rows
+  int keys;
+  int first_own;  // own index of row 0's last key + 1 (prefix: keys)
+  const int32_t* table;
+  bool prefix;
+};
+
+struct Item {
+  int row0, m0, rows;  // query rows m0 .. m0 + rows of the segment's n * heads-per-key-head
+  int h, lo, hi;       // key head, tiles
+  int keys;            // keys the item reads
+  int first_own;
+  bool prefix;
+  const int32_t* table;
+  size_t slot;  // partial row of its row m0
+};
+
+struct Layout {
+  int64_t per;  // cost of a block
+  int64_t x0, x1;
+  int k0;        // first segment and its position
+  int64_t s0;
+};
+
+__device__ __forceinline__ Segment segment(const spec_prefix_attention_args& a, int k, uint32_t* bad) {
+  Segment s;
+  if (k < a.G) {
+    const int2 in = group_requests(a, k, bad);
+    const Rows rows = rows_between(a, in.x, in.y, bad);
+    s = Segment{rows.row0, rows.n, prefix_keys(a, k, bad), 0,
+                a.prefix_table + (size_t)k * a.max_prefix_pages, true};
+    s.first_own = s.keys;
+  } else {
+    const int r = k - a.G;
+    const Rows rows = rows_between(a, r, r + 1, bad);
+    const int kv = own_keys(a, r, bad);
+    s = Segment{rows.row0, rows.n, kv, kv - rows.n + 1, a.block_table + (size_t)r * a.max_pages, false};
+  }
+  return s;
+}
+// Keys that the item of query rows [256 i, ..) needs: its last row's.
+__device__ __forceinline__ int item_keys(const Segment& s, int i, int per_head) {
+  if (s.prefix) return s.keys;
+  const int j = min(s.n - 1, (i * kItemRows + kItemRows - 1) / per_head);
+  return max(0, min(s.keys, s.first_own + j));
+}
+__device__ __forceinline__ int item_count(const Segment& s, int per_head) {
+  return (int)(((int64_t)s.n * per_head + kItemRows - 1) / kItemRows);
+}
+__device__ __forceinline__ int64_t item_cost(int keys, bool prefix) {
+  const int tiles = (keys + kTile - 1) / kTile;
+  return tiles ? kCostItem + (int64_t)tiles * (prefix ? kCostPrefix : kCostOwn) : 0;
+}
+__device__ __forceinline__ int64_t head_cost(const Segment& s, int per_head) {
+  const int n = item_count(s, per_head);
+  if (s.prefix) return n * item_cost(s.keys, true);
+  int64_t c = 0;
+  for (int i = 0; i < n; ++i) c += item_cost(item_keys(s, i, per_head), false);
+  return c;
+}
+
+// The block's items, in the order every warp role walks them.
+struct Walker {
+  const spec_prefix_attention_args& a;
+  int64_t pos, x0, x1;
+  int k, h, i, per_head, count;
+  Segment seg;
+  uint32_t bad;
+
+  __device__ Walker(const spec_prefix_attention_args& args, const Layout& lay)
+      : a(args), pos(lay.s0), x0(lay.x0), x1(lay.x1), k(lay.k0), h(0), i(0),
+        per_head(args.Hq / args.Hk), count(0), bad(0) {
+    if (x0 >= x1) return;
+    load();
+    const int64_t c = head_cost(seg, per_head);
+    if (c > 0) {
+      h = (int)((x0 - pos) / c);
+      pos += h * c;
+    }
+  }
+  __device__ void load() {
+    seg = segment(a, k, &bad);
+    count = item_count(seg, per_head);
+  }
+  __device__ bool next(Item& it) {
+    if (x0 >= x1) return false;
+    while (true) {
+      while (i >= count || h >= a.Hk) {  // next head, or next segment
+        i = 0;
+        if (count == 0 || ++h >= a.Hk) {
+          h = 0;
+          if (++k >= a.G + a.R) return false;
+          if (pos >= x1) return false;
+          load();
+        }
+      }
+      if (pos >= x1) return false;
+      const int keys = item_keys(seg, i, per_head);
+      const int64_t cost = item_cost(keys, seg.prefix), at = pos + kCostItem;
+      pos += cost;
+      const int mine = i++;
+      if (cost == 0 || pos <= x0) continue;
+      const int w = seg.prefix ? kCostPrefix : kCostOwn, tiles = (keys + kTile - 1) / kTile;
+      it.lo = x0 <= at ? 0 : (int)((x0 - at + w - 1) / w);
+      it.hi = x1 <= at ? 0 : (int)min((int64_t)tiles, (x1 - at + w - 1) / w);
+      if (it.lo >= it.hi) continue;
+      const int m = seg.n * per_head;
+      it.row0 = seg.row0;
+      it.m0 = mine * kItemRows;
+      it.rows = min(kItemRows, m - it.m0);
+      it.h = h;
+      it.keys = keys;
+      it.first_own = seg.first_own;
+      it.prefix = seg.prefix;
+      it.table = seg.table;
+      it.slot = (seg.prefix ? 0 : (size_t)a.rows * a.Hq) + (size_t)seg.row0 * a.Hq + (size_t)h * m +
+                it.m0 + (size_t)kItemRows * blockIdx.x;
+      return true;
+    }
+  }
+};
+
+// ------------------------------------------------------------- tcgen05 -----
+// MN-major operand in the 128-byte swizzle layout: rows of 64 elements, 8-row
+// groups 1024 bytes apart (stride offset), the next 64 elements `lead` bytes on.
+__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t lead) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// A from tensor memory.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// bf16x2 with `lo` in the low half
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <int D>
+struct Smem {
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr int kRing = 2 * kTileBytes;  // after the two query tiles
+  static constexpr int kBars = kRing + kStages * kTileBytes;
+  static constexpr int kBytes = kBars + 512 + 1024;  // barriers, and the base's alignment
+};
+
+struct Bars {
+  uint64_t full[10], empty[10];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                        const spec_prefix_attention_args a, float* part, float2* stat, int64_t* plan) {
+  using S = Smem<D>;
+  constexpr int kHalves = D / 64;
+  constexpr int kHalfBytes = kTile * 128;  // 64 elements of 128 keys
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+  Bars& bars = *reinterpret_cast<Bars*>(smem + S::kBars);
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+  __shared__ int64_t warp_sum[kThreads / 32];
+  __shared__ Layout lay;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per_head = a.Hq / a.Hk;
+
+  // ---- the work layout: every thread a run of segments, one scan
+  {
+    const int n_seg = a.G + a.R, run = (n_seg + kThreads - 1) / kThreads;
+    const int k0 = min(tid * run, n_seg), k1 = min(k0 + run, n_seg);
+    uint32_t bad = 0;
+    int64_t mine = 0;
+    for (int k = k0; k < k1; ++k) mine += a.Hk * head_cost(segment(a, k, &bad), per_head);
+    int64_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t t = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += t;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    if (tid == 0) {
+      abort_flag = 0;
+      lay = Layout{0, 0, 0, 0, 0};
+      for (int i = 0; i < S::kStages; ++i) {
+        tc::mbar_init(&bars.full[i], 1);
+        tc::mbar_init(&bars.empty[i], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        tc::mbar_init(&bars.q_full[i], 4);
+        tc::mbar_init(&bars.s_full[i], 1);
+        tc::mbar_init(&bars.p_full[i], 4);
+        tc::mbar_init(&bars.o_full[i], 1);
+      }
+      tc::mbar_init(&bars.drain, 1);
+      tc::fence_barrier_init();
+    }
+    if (warp == kMma) tc::tmem_alloc(&tmem_slot, 512);
+    if (warp == kProducer && lane == 0) {
+      tc::tma_prefetch_desc(&k_map);
+      tc::tma_prefetch_desc(&v_map);
+    }
+    __syncthreads();
+    int64_t before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      before += w < warp ? warp_sum[w] : 0;
+      total += warp_sum[w];
+    }
+    int64_t at = before + inc - mine;  // position of the thread's first segment
+    // at least one tile a block, so that every block of an item's range has one
+    const int64_t per = max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)max(kCostPrefix, kCostOwn));
+    const int64_t x0 = per * blockIdx.x, x1 = min(x0 + per, total);
+    const bool here = x0 < x1 && at <= x0 && x0 < at + mine;
+    if (here || blockIdx.x == 0) {
+      for (int k = k0; k < k1; ++k) {
+        const int64_t c = a.Hk * head_cost(segment(a, k, &bad), per_head);
+        if (blockIdx.x == 0) plan[1 + k] = at;
+        if (here && at <= x0 && x0 < at + c) lay = Layout{per, x0, x1, k, at};
+        at += c;
+      }
+    }
+    if (blockIdx.x == 0 && tid == 0) plan[0] = per;
+    if (bad && blockIdx.x == 0) set_status(a.status, bad);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+  }
+  const uint32_t tmem = tmem_slot;
+  auto fail = [&]() {
+    abort_flag = 1;
+    set_status(a.status, SPEC_STATUS_TIMEOUT);
+  };
+  // A wait of a whole warp: all of its lanes go on, or all give up.
+  auto warp_wait = [&](uint64_t* bar, uint32_t phase) {
+    const bool got = !abort_flag && tc::mbar_wait(bar, phase & 1u, kWaitNs);
+    if (__all_sync(0xffffffffu, got)) return true;
+    fail();
+    return false;
+  };
+
+  if (warp == kProducer) {
+    // ------------------------------------------------------------ producer --
+    Walker walk(a, lay);
+    Item it;
+    uint32_t seq = 0;  // ring positions used: keys and values in turn
+    bool ok = true;
+    const int box = min(a.page_size, kTile), boxes = kTile / box;  // keys of a box, boxes of a tile
+    while (ok && walk.next(it)) {
+      for (int i = it.lo; ok && i < it.hi; ++i) {
+        const int live = min(kTile, it.keys - i * kTile);
+        const int used = (live + box - 1) / box;  // pages (or parts of one) that have keys
+        int row = 0;
+        const int which = lane / kHalves;
+        if (which < used) {
+          const int key = i * kTile + which * box, pi = key / a.page_size;
+          row = page_of(a, it.table, pi, &walk.bad) * a.page_size + (key - pi * a.page_size);
+        }
+        for (int kv = 0; kv < 2; ++kv, ++seq) {
+          const int st = seq % S::kStages;
+          ok = warp_wait(&bars.empty[st], (seq / S::kStages) ^ 1u);
+          if (!ok) break;
+          if (lane == 0) tc::mbar_expect_tx(&bars.full[st], (uint32_t)(used * box * D * 2));
+          __syncwarp();
+          if (which < used && which < boxes) {
+            const int half = lane % kHalves;
+            tc::tma_load_3d(smem + S::kRing + st * S::kTileBytes + half * kHalfBytes + which * box * 128,
+                            kv ? &v_map : &k_map, &bars.full[st], half * 64, it.h, row);
+          }
+        }
+      }
+    }
+    if (!ok) {  // the copies in flight land before the block's memory goes
+      const uint32_t from = seq > (uint32_t)S::kStages ? seq - S::kStages : 0u;
+      for (uint32_t s = from; s < seq; ++s)
+        tc::mbar_wait(&bars.full[s % S::kStages], (s / S::kStages) & 1u, kWaitNs);
+    }
+    if (walk.bad) set_status(a.status, walk.bad);
+  } else if (warp == kMma) {
+    // ------------------------------------------------------------ products --
+    if (lane == 0) {
+      Walker walk(a, lay);
+      Item it, nx;
+      uint32_t seq = 0;  // ring position of the current tile's keys
+      uint32_t q_n[2] = {0, 0}, p_n[2] = {0, 0};
+      int turn = 0;      // warpgroup of the next small item
+      bool ok = true;
+      const uint32_t q_base = tc::smem_u32(smem), ring = tc::smem_u32(smem + S::kRing);
+      constexpr uint32_t kDescS = tc::bf16_idesc(128, kTile);
+      constexpr uint32_t kDescO = tc::bf16_idesc(128, D) | (1u << 16);  // values: keys down, head across
+      auto wait = [&](uint64_t* bar, uint32_t n) {
+        if (ok && (abort_flag || !tc::mbar_wait(bar, n & 1u, kWaitNs))) {
+          fail();
+          ok = false;
+        }
+      };
+      auto scores = [&](int t, uint32_t s) {  // S_t = Q_t K^T with the keys at ring position s
+        const uint32_t kb = ring + (s % S::kStages) * S::kTileBytes, qb = q_base + t * S::kTileBytes;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          const uint32_t off = (c >> 2) * kHalfBytes + (c & 3) * 32;
+          tc::mma_bf16(tmem + t * kTile, tc::sw128_desc(qb + off), tc::sw128_desc(kb + off), kDescS, c > 0);
+        }
+        tc::mma_commit(&bars.s_full[t]);
+      };
+      auto values = [&](int t, uint32_t s, bool first) {  // O_t (+)= P_t V
+        const uint32_t vb = ring + (s % S::kStages) * S::kTileBytes;
+#pragma unroll
+        for (int c = 0; c < kTile / 16; ++c)
+          mma_bf16_ts(tmem + 2 * kTile + t * kTile, tmem + t * kTile + c * 8,
+                      sw128_desc_mn(vb + c * 2048, kHalfBytes), kDescO, !first || c > 0);
+      };
+      auto begin = [&](const Item& x, int l0, int l1, uint32_t s) {  // an item's first scores
+        wait(&bars.full[s % S::kStages], s / S::kStages);
+        for (int t = l0; t <= l1 && ok; ++t) {
+          wait(&bars.q_full[t], q_n[t]++);
+          if (!ok) break;
+          tc::fence_after_sync();
+          scores(t, s);
+        }
+        if (ok) tc::mma_commit(&bars.empty[s % S::kStages]);
+      };
+      bool more = walk.next(it);
+      int l0 = 0, l1 = 0;
+      auto lanes = [&](const Item& x, int& p, int& q) {
+        if (x.rows > kTile) {
+          p = 0;
+          q = 1;
+        } else {
+          p = q = turn;
+          turn ^= 1;
+        }
+      };
+      if (more) {
+        lanes(it, l0, l1);
+        begin(it, l0, l1, seq);
+      }
+      while (more && ok) {
+        bool more_next = false, early = false;
+        int n0 = 0, n1 = 0;
+        for (int i = it.lo; i < it.hi && ok; ++i, seq += 2) {
+          const bool last = i + 1 == it.hi;
+          if (last) {
+            more_next = walk.next(nx);
+            if (more_next) {
+              lanes(nx, n0, n1);
+              early = l0 == l1 && n0 == n1 && n0 != l0;
+              if (early) begin(nx, n0, n1, seq + 2);
+            }
+          }
+          wait(&bars.full[(seq + 1) % S::kStages], (seq + 1) / S::kStages);
+          if (!last) wait(&bars.full[(seq + 2) % S::kStages], (seq + 2) / S::kStages);
+          for (int t = l0; t <= l1 && ok; ++t) {
+            wait(&bars.p_full[t], p_n[t]++);
+            if (!ok) break;
+            tc::fence_after_sync();
+            values(t, seq + 1, i == it.lo);
+            if (last) tc::mma_commit(&bars.o_full[t]);
+            else scores(t, seq + 2);
+          }
+          if (!ok) break;
+          tc::mma_commit(&bars.empty[(seq + 1) % S::kStages]);
+          if (!last) tc::mma_commit(&bars.empty[(seq + 2) % S::kStages]);
+        }
+        if (!ok) break;
+        more = more_next;
+        it = nx;
+        l0 = n0;
+        l1 = n1;
+        if (more && !early) begin(it, l0, l1, seq);
+      }
+      if (!ok) {  // the products in flight end before TMEM is freed
+        tc::mma_commit(&bars.drain);
+        tc::mbar_wait(&bars.drain, 0, kWaitNs);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------- softmax --
+    const int t = warp >> 2, tid_g = tid & 127;
+    const uint32_t lane_base = (uint32_t)(warp & 3) << 21;  // 32 TMEM lanes a warp, lanes in the high half
+    const uint32_t s_addr = tmem + lane_base + t * kTile, o_addr = tmem + lane_base + 2 * kTile + t * kTile;
+    const float sl = a.scale * kLog2e;
+    Walker walk(a, lay);
+    Item it;
+    uint32_t seq = 0, s_n = 0, o_n = 0;
+    int turn = 0;
+    bool ok = true;
+    while (ok && walk.next(it)) {
+      const bool both = it.rows > kTile;
+      const int mine = both ? t : turn;
+      if (!both) turn ^= 1;
+      const uint32_t seq0 = seq;
+      seq += 2u * (uint32_t)(it.hi - it.lo);
+      if (mine != t) continue;
+      const int m = (both ? t * kTile : 0) + tid_g;
+      const bool valid = m < it.rows;
+      const int qrow = it.m0 + m, j = qrow / per_head;
+      // the query row into its swizzled place
+      {
+        const __nv_bfloat16* q = (const __nv_bfloat16*)a.q + (size_t)(it.row0 + j) * a.q_row +
+                                 (size_t)(it.h * per_head + (qrow - j * per_head)) * a.q_head;
+        uint8_t* to = smem + t * S::kTileBytes + tid_g * 128;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (valid) x = *reinterpret_cast<const uint4*>(q + c * 8);
+          *reinterpret_cast<uint4*>(to + (c >> 3) * kHalfBytes + (((c & 7) ^ (tid_g & 7)) << 4)) = x;
+        }
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars.q_full[t]);
+      }
+      const int limit = it.prefix ? it.keys : min(it.keys, it.first_own + j);  // keys of this row
+      float ref = -CUDART_INF_F, l = 0.f;
+      for (int i = it.lo; i < it.hi; ++i) {
+        ok = warp_wait(&bars.s_full[t], s_n++);
+        if (!ok) break;
+        tc::fence_after_sync();
+        uint32_t s[kTile];
+#pragma unroll
+        for (int c = 0; c < kTile; c += 32) tmem_ld32(s_addr + c, s + c);
+        tc::tmem_ld_wait();
+        const int lim = limit - i * kTile;
+        if (__any_sync(0xffffffffu, lim < kTile)) {
+#pragma unroll
+          for (int c = 0; c < kTile; ++c)
+            if (c >= lim) s[c] = 0xff800000u;  // -inf
+        }
+        float m0 = -CUDART_INF_F, m1 = m0, m2 = m0, m3 = m0;
+#pragma unroll
+        for (int c = 0; c < kTile; c += 4) {
+          m0 = fmaxf(m0, __uint_as_float(s[c]));
+          m1 = fmaxf(m1, __uint_as_float(s[c + 1]));
+          m2 = fmaxf(m2, __uint_as_float(s[c + 2]));
+          m3 = fmaxf(m3, __uint_as_float(s[c + 3]));
+        }
+        const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sl;
+        if (__any_sync(0xffffffffu, top > ref + kSlack)) {
+          const float to = fmaxf(ref, top);
+          const float c = ref == -CUDART_INF_F ? 0.f : tc::ex2(ref - to);
+          ref = to;
+          l *= c;
+          if (i > it.lo) {
+#pragma unroll
+            for (int d = 0; d < D; d += 32) {
+              uint32_t o[32];
+              tmem_ld32(o_addr + d, o);
+              tc::tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * c);
+              tmem_st32(o_addr + d, o);
+            }
+          }
+        }
+        const float sub = ref == -CUDART_INF_F ? 0.f : ref;
+        float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+#pragma unroll
+        for (int c = 0; c < kTile; c += 64) {
+          uint32_t p[32];
+#pragma unroll
+          for (int e = 0; e < 64; e += 4) {
+            const float p0 = tc::ex2(fmaf(__uint_as_float(s[c + e]), sl, -sub));
+            const float p1 = tc::ex2(fmaf(__uint_as_float(s[c + e + 1]), sl, -sub));
+            const float p2 = tc::ex2(fmaf(__uint_as_float(s[c + e + 2]), sl, -sub));
+            const float p3 = tc::ex2(fmaf(__uint_as_float(s[c + e + 3]), sl, -sub));
+            a0 += p0;
+            a1 += p1;
+            a2 += p2;
+            a3 += p3;
+            p[e / 2] = pack_bf16(p0, p1);
+            p[e / 2 + 1] = pack_bf16(p2, p3);
+          }
+          tmem_st32(s_addr + c / 2, p);
+        }
+        l += (a0 + a1) + (a2 + a3);
+        // Values past the item's keys may be anything, NaN among them: zeros instead.
+        // (The first warpgroup of two does it, whose product is issued first.)
+        const int live = it.keys - i * kTile;
+        if (live < kTile && (!both || t == 0)) {
+          const uint32_t sv = seq0 + 2u * (uint32_t)(i - it.lo) + 1u;
+          ok = warp_wait(&bars.full[sv % S::kStages], sv / S::kStages);
+          if (!ok) break;
+          if (tid_g >= live) {
+            uint8_t* to = smem + S::kRing + (sv % S::kStages) * S::kTileBytes + tid_g * 128;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+              *reinterpret_cast<uint4*>(to + (c >> 3) * kHalfBytes + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+          }
+          tc::fence_proxy_async();
+        }
+        tmem_st_wait();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars.p_full[t]);
+      }
+      if (!ok) break;
+      ok = warp_wait(&bars.o_full[t], o_n++);
+      if (!ok) break;
+      tc::fence_after_sync();
+      const size_t slot = it.slot + m;
+#pragma unroll
+      for (int d = 0; d < D; d += 32) {
+        uint32_t o[32];
+        tmem_ld32(o_addr + d, o);
+        tc::tmem_ld_wait();
+        if (valid) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<uint4*>(part + slot * D + d + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+      }
+      tc::fence_before_sync();
+      if (valid) stat[slot] = make_float2(ref, l);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == kMma) tc::tmem_dealloc(tmem, 512);
+}
+
+// ----------------------------------------------------------------- join ----
+constexpr int kJoinThreads = 256;
+
+// Joins the pieces of every row: a block a packed row, a warp a query head.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads)
+    join_tc_kernel(const spec_prefix_attention_args a, const float* part, const float2* stat, const int64_t* plan) {
+  constexpr int kPer = D / 32;
+  const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per_head = a.Hq / a.Hk;
+  uint32_t bad = 0;
+  const int r = last_at_or_below(a.row_off, a.R, b);
+  const Rows rows = rows_between(a, r, r + 1, &bad);
+  if (b < rows.row0 || b >= rows.row0 + rows.n) return;
+  const int64_t per = plan[0];
+  int g = -1;
+  Segment pre{0, 0, 0, 0, nullptr, true};
+  if (a.G > 0) {
+    const int c = last_at_or_below(a.group_off, a.G, r);
+    const int2 in = group_requests(a, c, &bad);
+    if (r >= in.x && r < in.y) {
+      g = c;
+      pre = segment(a, c, &bad);
+    }
+  }
+  const Segment own = segment(a, a.G + r, &bad);
+  const int64_t pre_at = g >= 0 ? plan[1 + g] : 0, own_at = plan[1 + a.G + r];
+  const int64_t own_head = head_cost(own, per_head), pre_head = head_cost(pre, per_head);
+
+  for (int hq = warp; hq < a.Hq; hq += kJoinThreads / 32) {
+    const int h = hq / per_head, in_head = hq - h * per_head;
+    int first[2] = {0, 0}, count[2] = {0, 0};  // blocks that have a piece of this row
+    size_t slot[2] = {0, 0};                   // its partial row, without the block's offset
+    auto find = [&](int w, const Segment& s, int64_t at, int64_t per_h, size_t region) {
+      const int m = (b - s.row0) * per_head + in_head, i = m / kItemRows;
+      const int keys = item_keys(s, i, per_head), tiles = (keys + kTile - 1) / kTile;
+      if (tiles == 0) return;
+      at += h * per_h;
+      if (s.prefix) at += i * item_cost(keys, true);
+      else
+        for (int x = 0; x < i; ++x) at += item_cost(item_keys(s, x, per_head), false);
+      at += kCostItem;
+      first[w] = (int)(at / per);
+      count[w] = (int)((at + (int64_t)(tiles - 1) * (s.prefix ? kCostPrefix : kCostOwn)) / per) - first[w] + 1;
+      slot[w] = region + (size_t)s.row0 * a.Hq + (size_t)h * ((size_t)s.n * per_head) + m;
+    };
+    if (g >= 0) find(0, pre, pre_at, pre_head, 0);
+    find(1, own, own_at, own_head, (size_t)a.rows * a.Hq);
+    const int n = count[0] + count[1];
+    auto place = [&](int p) {
+      return p < count[0] ? slot[0] + (size_t)kItemRows * (first[0] + p)
+                          : slot[1] + (size_t)kItemRows * (first[1] + p - count[0]);
+    };
+    float top = -CUDART_INF_F, sum = 0.f, o[kPer];
+#pragma unroll
+    for (int d = 0; d < kPer; ++d) o[d] = 0.f;
+    for (int p0 = 0; p0 < n; p0 += 32) {
+      float2 st = make_float2(-CUDART_INF_F, 0.f);
+      if (p0 + lane < n) st = stat[place(p0 + lane)];
+      float m = st.x;
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+      m = fmaxf(m, top);
+      const float c = top == -CUDART_INF_F ? 0.f : tc::ex2(top - m);
+      const float w = st.x == -CUDART_INF_F ? 0.f : tc::ex2(st.x - m);
+      float l = st.y * w;
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+      sum = sum * c + l;
+#pragma unroll
+      for (int d = 0; d < kPer; ++d) o[d] *= c;
+      const int np = min(32, n - p0);
+#pragma unroll 4
+      for (int p = 0; p < np; ++p) {
+        const float wp = __shfl_sync(0xffffffffu, w, p);
+        const float* src = part + place(p0 + p) * D + lane * kPer;
+        float v[kPer];
+        if constexpr (kPer == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(src);
+          v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(src);
+          v[0] = x.x, v[1] = x.y;
+        }
+#pragma unroll
+        for (int d = 0; d < kPer; ++d) o[d] = fmaf(v[d], wp, o[d]);
+      }
+      top = m;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row without keys: zeros
+    __nv_bfloat16* out = (__nv_bfloat16*)a.out + (size_t)b * a.out_row + (size_t)hq * a.out_head + lane * kPer;
+#pragma unroll
+    for (int d = 0; d < kPer; d += 2) *reinterpret_cast<uint32_t*>(out + d) = pack_bf16(o[d] * inv, o[d + 1] * inv);
+    if (a.lse && lane == 0)
+      a.lse[(size_t)b * a.Hq + hq] = sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * kLn2;
+  }
+}
+
+template <int D>
+cudaError_t launch(const spec_prefix_attention_args& a, int sms, float* part, float2* stat, int64_t* plan,
+                   cudaStream_t stream) {
+  const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.Hk, (uint64_t)a.n_pages * a.page_size};
+  const uint32_t box[3] = {64, 1, (uint32_t)(a.page_size < kTile ? a.page_size : kTile)};
+  CUtensorMap km, vm;
+  if (!fused::encode_tiled(&km, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.k_cache, 3, dims, box) ||
+      !fused::encode_tiled(&vm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.v_cache, 3, dims, box))
+    return cudaErrorInvalidValue;
+  cudaError_t err = cudaFuncSetAttribute(attention_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Smem<D>::kBytes);
+  if (err != cudaSuccess) return err;
+  attention_tc_kernel<D><<<sms, kThreads, Smem<D>::kBytes, stream>>>(km, vm, a, part, stat, plan);
+  if ((err = cudaGetLastError()) != cudaSuccess) return err;
+  join_tc_kernel<D><<<a.rows, kJoinThreads, 0, stream>>>(a, part, stat, plan);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// bf16 heads of 64 or 128, pages that tile 128 keys in boxes of 8 rows or more,
+// 16-byte rows, an sm_100-family GPU.
+bool attn_tc_ok(const spec_prefix_attention_args& a, int* sms) {
+  if (a.dtype != SPEC_BF16 || (a.D != 64 && a.D != 128)) return false;
+  const int P = a.page_size;
+  if (P < 128 ? (P < 8 || 128 % P != 0) : P % 128 != 0) return false;
+  auto on = [](const void* p, size_t n) { return ((uintptr_t)p % n) == 0; };
+  if (!on(a.q, 16) || a.q_row % 8 != 0 || a.q_head % 8 != 0 || !on(a.k_cache, 16) || !on(a.v_cache, 16) ||
+      !on(a.out, 4) || a.out_row % 2 != 0 || a.out_head % 2 != 0)
+    return false;
+  int dev = 0, major = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return false;
+  return major == 10 && *sms >= 1 && *sms <= kMaxCtas;
+}
+
+cudaError_t launch_attention_tc(const spec_prefix_attention_args& a, int sms, float* part, float2* stat,
+                                int64_t* plan, cudaStream_t stream) {
+  return a.D == 128 ? launch<128>(a, sms, part, stat, plan, stream)
+                    : launch<64>(a, sms, part, stat, plan, stream);
+}
+
+}  // namespace spec

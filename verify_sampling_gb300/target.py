@@ -41,6 +41,16 @@ class RopeCacheArgs(ctypes.Structure):
                 ("status", _P)]
 
 
+class PrefixAttentionArgs(ctypes.Structure):
+    _fields_ = [("R", _I), ("rows", _I), ("Hq", _I), ("Hk", _I), ("D", _I), ("dtype", _I),
+                ("page_size", _I), ("n_pages", _I), ("max_pages", _I), ("G", _I),
+                ("max_prefix_pages", _I), ("scale", _F), ("q", _P), ("q_row", _L), ("q_head", _L),
+                ("k_cache", _P), ("v_cache", _P), ("row_off", _P), ("kv_len", _P),
+                ("block_table", _P), ("group_off", _P), ("prefix_len", _P), ("prefix_table", _P),
+                ("out", _P), ("out_row", _L), ("out_head", _L), ("lse", _P), ("workspace", _P),
+                ("workspace_bytes", ctypes.c_size_t), ("status", _P)]
+
+
 class LogitsArgs(ctypes.Structure):
     _fields_ = [("R", _I), ("V", _I), ("rows", _I), ("rows_per_request", _I), ("dtype", _I),
                 ("logits", _P), ("ld", _L), ("out", _P), ("out_ld", _L), ("row_off", _P),
@@ -55,9 +65,12 @@ def _bind(L: ctypes.CDLL) -> None:
     for name, cls in (("spec_cache_reserve", CacheReserveArgs),
                       ("spec_cache_commit", CacheCommitArgs),
                       ("spec_rope_cache", RopeCacheArgs),
+                      ("spec_prefix_attention", PrefixAttentionArgs),
                       ("spec_adjust_logits", LogitsArgs)):
         f = getattr(L, name)
         f.argtypes, f.restype = [ctypes.POINTER(cls), _P], ctypes.c_int
+    L.spec_attention_workspace_bytes.argtypes = [_I] * 4
+    L.spec_attention_workspace_bytes.restype = ctypes.c_size_t
 
 
 def _t(t: torch.Tensor, name: str, dtype: torch.dtype, numel: int = -1) -> int:
@@ -237,6 +250,59 @@ def rope_cache(q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Ten
                       _opt(status, "status", torch.int32, 1))
     _check(lib().spec_rope_cache(ctypes.byref(a), _on(stream)), "spec_rope_cache")
     return q_out
+
+
+# -------------------------------------------------- shared-prefix attention --
+def attention_workspace_bytes(rows: int, R: int, Hq: int, D: int) -> int:
+    """spec_attention_workspace_bytes: workspace of ``prefix_attention``."""
+    return int(lib().spec_attention_workspace_bytes(rows, R, Hq, D))
+
+
+def prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                     row_off: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Tensor, *,
+                     scale: Optional[float] = None, group_off: Optional[torch.Tensor] = None,
+                     prefix_len: Optional[torch.Tensor] = None,
+                     prefix_table: Optional[torch.Tensor] = None, want_lse: bool = False,
+                     out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None, stream=None):
+    """spec_prefix_attention: attention of the packed rows q [rows, Hq, D] over a paged cache
+    [pages, page_size, Hk, D]: each request's own ``kv_len`` keys in its ``block_table`` pages
+    (causal over its rows) and, for requests ``group_off[g]`` .. ``group_off[g + 1]``, the
+    ``prefix_len[g]`` keys in ``prefix_table[g]``.  ``scale`` defaults to D^-1/2.  Returns out
+    [rows, Hq, D], or (out, lse [rows, Hq]) with ``want_lse``."""
+    i32 = torch.int32
+    rows, Hq, D = q.shape
+    dt = q.dtype
+    if k_cache.dim() != 4 or k_cache.shape[3] != D or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must both be [pages, page_size, Hk, D]")
+    n_pages, P, Hk, _ = k_cache.shape
+    R, width = block_table.shape
+    G = 0 if prefix_len is None else prefix_len.numel()
+    if G and (group_off is None or prefix_table is None or prefix_table.dim() != 2 or
+              prefix_table.shape[0] != G):
+        raise ValueError("prefixes need group_off [G + 1], prefix_len [G] and prefix_table [G, pages]")
+    need = attention_workspace_bytes(rows, R, Hq, D)
+    with _made_on(stream):
+        if out is None:
+            out = torch.empty((rows, Hq, D), dtype=dt, device=q.device)
+        if want_lse and lse is None:
+            lse = torch.empty((rows, Hq), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    a = PrefixAttentionArgs(
+        R, rows, Hq, Hk, D, _dtype_code(q), P, n_pages, width, G, prefix_table.shape[1] if G else 0,
+        D ** -0.5 if scale is None else scale, *_strided(q, "q", dt, (rows, Hq, D)),
+        _t(k_cache, "k_cache", dt), _t(v_cache, "v_cache", dt), _t(row_off, "row_off", i32, R + 1),
+        _t(kv_len, "kv_len", i32, R), _t(block_table, "block_table", i32),
+        _t(group_off, "group_off", i32, G + 1) if G else None,
+        _t(prefix_len, "prefix_len", i32) if G else None,
+        _t(prefix_table, "prefix_table", i32) if G else None,
+        *_strided(out, "out", dt, (rows, Hq, D)), _opt(lse, "lse", torch.float32, rows * Hq),
+        _dev(workspace, "workspace").data_ptr(), workspace.numel() * workspace.element_size(),
+        _opt(status, "status", i32, 1))
+    _check(lib().spec_prefix_attention(ctypes.byref(a), _on(stream)), "spec_prefix_attention")
+    return (out, lse) if want_lse else out
 
 
 # -------------------------------------------------------- logit adjustments --
