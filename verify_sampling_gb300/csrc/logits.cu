@@ -9,12 +9,15 @@
 //
 // Layout: a block takes a slice of the vocabulary of one request for all its
 // rows.  It reads the request's tokens once, counts those of its slice in shared
-// memory and marks them (and the biased and drafted ones) in a bitmap; then the
-// rows stream through, and a 16-byte vector without a marked or masked entry goes
-// out as it came in.  The history costs 4 bytes a token and slice from L2, where
-// a table of counts over the vocabulary would cost 4 bytes an entry and request
-// from HBM, and has to be kept up between rounds.  Rows share the counts: a row's
-// drafted tokens are compared only at marked entries.
+// memory and lists each token that a rule names once.  The rows then stream
+// through as 16-byte vectors that only the mask can change; after that the listed
+// entries are computed from the inputs and written over, one thread each.  (With
+// the rules applied inside the stream a warp met a named entry in two of three
+// vectors and the round case below took 1390 us.)
+// The history costs 4 bytes a token and slice from L2, where a table of counts
+// over the vocabulary would cost 4 bytes an entry and request from HBM, and has to
+// be kept up between rounds.  Rows share the counts: a row's drafted tokens are
+// compared at listed entries only.
 // Bound by memory: each logit is read and written once.
 #include "logits.cuh"
 
@@ -25,7 +28,7 @@ namespace spec {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxSlice = 4096;  // 33 KB of tables: six blocks an SM
+constexpr int kMaxSlice = 4096;  // 41 KB of tables: five blocks an SM
 constexpr int kMinSlice = 1024;
 constexpr int kUnroll = 4;
 constexpr int kMaxDraft = 64;
@@ -70,20 +73,20 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t* w, int at, int n) {
   return b & ((1u << n) - 1u);
 }
 
-// What a block knows of its slice.
-struct Tables {
-  uint32_t* count;   // [slice + 8]: output tokens, kPrompt where the prompt has it
-  int32_t* bias;     // [slice + 8]: entry of the bias list + 1
-  uint32_t* marked;  // bitmap of the entries that any rule touches
-};
+__device__ __forceinline__ void hide(float& e) { e = -CUDART_INF_F; }
+__device__ __forceinline__ void hide(__nv_bfloat16& e) { e = __ushort_as_bfloat16(0xff80); }
 
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads) adjust_kernel(spec_logits_args p, int slice) {
-  extern __shared__ uint32_t smem[];
+  // tables of the slice: output tokens (kPrompt where the prompt has it), bias entry + 1, and the
+  // named tokens, each once
+  extern __shared__ __align__(16) uint32_t smem[];
+  uint32_t* count = smem;
+  int32_t* bias = reinterpret_cast<int32_t*>(smem + slice);
+  uint16_t* named = reinterpret_cast<uint16_t*>(smem + 2 * slice);
+  uint32_t* seen = smem + 2 * slice + slice / 2;  // bitmap of the named tokens
   __shared__ int32_t draft_s[kMaxDraft];
-  const int span = slice + 8;  // a vector that starts in the slice may end 7 entries past it
-  const Tables tab{smem, reinterpret_cast<int32_t*>(smem + span), smem + 2 * span};
-  const int words = (span + 31) / 32;
+  __shared__ int n_named;
   const int tid = threadIdx.x, r = blockIdx.y;
   const int s0 = blockIdx.x * slice, s1 = min(s0 + slice, p.V);
   const bool counts = p.repetition || p.frequency || p.presence;
@@ -102,9 +105,16 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(spec_logits_args p, in
   const int n_draft = counts && p.x ? min(max(j1 - 1, 0), p.x_cols) : 0;
 
   if (j0 < j1) {
-    for (int i = tid; i < 2 * span + words + 1; i += kThreads) smem[i] = 0u;
+    uint4* clear = reinterpret_cast<uint4*>(smem);
+    for (int i = tid; i < (2 * slice) / 4; i += kThreads) clear[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < slice / 32; i += kThreads) seen[i] = 0u;
+    if (tid == 0) n_named = 0;
     __syncthreads();
-    auto mark = [&](int d) { atomicOr(&tab.marked[d >> 5], 1u << (d & 31)); };
+    auto name = [&](int d) {
+      const uint32_t bit = 1u << (d & 31);
+      if (!(atomicOr(&seen[d >> 5], bit) & bit)) named[atomicAdd(&n_named, 1)] = (uint16_t)d;
+    };
+    auto inside = [&](int t) { return t >= s0 && t < s1; };
     if (counts) {
       const int32_t* tok = p.tokens + (size_t)r * p.tokens_ld;
       int len = p.length[r];
@@ -116,16 +126,16 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(spec_logits_args p, in
       for (int i = tid; i < len; i += kThreads * kUnroll) {
         int t[kUnroll];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) t[k] = i + k * kThreads < len ? tok[i + k * kThreads] : s0 - 1;
+        for (int k = 0; k < kUnroll; ++k) t[k] = i + k * kThreads < len ? tok[i + k * kThreads] : -1;
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k) {
           const int at = i + k * kThreads;
           if (at < len && (unsigned)t[k] >= (unsigned)p.V) bad |= SPEC_STATUS_BAD_TOKEN;
-          const unsigned d = (unsigned)t[k] - (unsigned)s0;
-          if (d < (unsigned)span && (unsigned)t[k] < (unsigned)p.V) {
-            if (at < prompt) atomicOr(&tab.count[d], kPrompt);
-            else atomicAdd(&tab.count[d], 1u);
-            mark(d);
+          if (inside(t[k])) {
+            const int d = t[k] - s0;
+            if (at < prompt) atomicOr(&count[d], kPrompt);
+            else atomicAdd(&count[d], 1u);
+            name(d);
           }
         }
       }
@@ -133,8 +143,7 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(spec_logits_args p, in
         const int t = p.x[(size_t)r * p.x_ld + i];
         draft_s[i] = t;
         if ((unsigned)t >= (unsigned)p.V) bad |= SPEC_STATUS_BAD_TOKEN;
-        const unsigned d = (unsigned)t - (unsigned)s0;
-        if (d < (unsigned)span && (unsigned)t < (unsigned)p.V) mark(d);
+        if (inside(t)) name(t - s0);
       }
     }
     if (p.bias_off) {
@@ -147,85 +156,91 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(spec_logits_args p, in
       for (int i = b0 + tid; i < b1; i += kThreads) {
         const int t = p.bias_tok[i];
         if ((unsigned)t >= (unsigned)p.V) bad |= SPEC_STATUS_BAD_TOKEN;
-        const unsigned d = (unsigned)t - (unsigned)s0;
-        if (d < (unsigned)span && (unsigned)t < (unsigned)p.V) {
-          atomicMax(&tab.bias[d], i + 1);  // a token's last entry counts
-          mark(d);
+        if (inside(t)) {
+          atomicMax(&bias[t - s0], i + 1);  // a token's last entry counts
+          name(t - s0);
         }
       }
     }
-    __syncthreads();
 
-    const float rep = p.repetition ? p.repetition[r] : 1.f, freq = p.frequency ? p.frequency[r] : 0.f,
-                pres = p.presence ? p.presence[r] : 0.f;
     const bool same = p.out == p.logits && p.out_ld == p.ld;
+    auto mask_of = [&](size_t b) -> const uint32_t* {
+      if (!p.mask) return nullptr;
+      const int m = p.mask_row ? p.mask_row[b] : (int)b;
+      if (m >= p.n_masks) bad |= SPEC_STATUS_BAD_ROW;
+      return m < 0 || m >= p.n_masks ? nullptr
+                                     : reinterpret_cast<const uint32_t*>(p.mask) + (size_t)m * p.mask_ld;
+    };
     for (int j = j0; j < j1; ++j) {
       const size_t b = (size_t)(row0 + j);
       const T* in = (const T*)p.logits + b * p.ld;
       T* out = (T*)p.out + b * p.out_ld;
-      const uint32_t* mask = nullptr;
-      if (p.mask) {
-        const int m = p.mask_row ? p.mask_row[b] : (int)b;
-        if (m >= p.n_masks) bad |= SPEC_STATUS_BAD_ROW;
-        else if (m >= 0) mask = reinterpret_cast<const uint32_t*>(p.mask) + (size_t)m * p.mask_ld;
-      }
-      auto adjust = [&](T& e, int v, bool is_marked, bool allowed) {
-        if (!allowed) {
-          from_f(-CUDART_INF_F, &e);
-          return;
-        }
-        if (!is_marked) return;
-        const int d = v - s0;
-        float z = to_f(e);
-        if (counts) {
-          const uint32_t w = tab.count[d];
-          uint32_t c = w & ~kPrompt;
-          const int upto = min(j, n_draft);
-          for (int i = 0; i < upto; ++i) c += draft_s[i] == v;
-          if (c > 0 || (w & kPrompt)) z = z > 0.f ? z / rep : z * rep;
-          if (c > 0) z = z - freq * (float)c - pres;
-        }
-        const int bi = tab.bias[d];
-        if (bi > 0) z += p.bias_val[bi - 1];
-        from_f(z, &e);
-      };
-      // Vectors lie on 16 bytes of memory, so a row that starts off them begins
-      // with a partial vector: entry v of vector i is i * VEC - lead + its place.
+      const uint32_t* mask = mask_of(b);
+      if (!mask && same) continue;
+      // Vectors lie on 16 bytes of memory: vector i starts at entry i * VEC - lead.
+      // One that reaches past the slice is taken entry by entry, so that no entry
+      // is written by two blocks.
       const int lead = VEC == 1 ? 0 : (int)(((uintptr_t)in / sizeof(T)) & (VEC - 1));
-      const int i_begin = s0 == 0 ? 0 : (s0 + lead + VEC - 1) / VEC, i_end = (s1 + lead + VEC - 1) / VEC;
+      const int i_begin = (s0 + lead) / VEC, i_end = (s1 + lead + VEC - 1) / VEC;
       using V = Vec<T, VEC>;
       using R = decltype(V().raw);
       for (int i = i_begin + tid; i < i_end; i += kThreads * kUnroll) {
         V x[kUnroll];
+        uint32_t al[kUnroll];
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k) {
           const int v = (i + k * kThreads) * VEC - lead;
-          if (i + k * kThreads < i_end && v >= 0 && v + VEC <= p.V)
+          al[k] = (1u << VEC) - 1u;
+          if (i + k * kThreads < i_end && v >= s0 && v + VEC <= s1) {
             x[k].raw = *reinterpret_cast<const R*>(in + v);
+            if (mask) al[k] = bits_at(mask, v, VEC);
+          }
         }
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k) {
           if (i + k * kThreads >= i_end) break;
           const int v = (i + k * kThreads) * VEC - lead;
-          if (v >= 0 && v + VEC <= p.V) {
-            const uint32_t mk = bits_at(tab.marked, v - s0, VEC);
-            const uint32_t al = mask ? bits_at(mask, v, VEC) : (1u << VEC) - 1u;
-            const bool changed = mk != 0u || al != (1u << VEC) - 1u;
-            if (changed) {
+          if (v >= s0 && v + VEC <= s1) {
 #pragma unroll
-              for (int e = 0; e < VEC; ++e) adjust(x[k].e[e], v + e, mk >> e & 1u, al >> e & 1u);
-            }
-            if (changed || !same) *reinterpret_cast<R*>(out + v) = x[k].raw;
-          } else {  // the row's first or last entries
+            for (int e = 0; e < VEC; ++e)
+              if (!(al[k] >> e & 1u)) hide(x[k].e[e]);
+            if (!same || al[k] != (1u << VEC) - 1u) *reinterpret_cast<R*>(out + v) = x[k].raw;
+          } else {
             for (int e = 0; e < VEC; ++e) {
               const int w = v + e;
-              if (w < 0 || w >= p.V) continue;
+              if (w < s0 || w >= s1) continue;
               T z = in[w];
-              adjust(z, w, bits_at(tab.marked, w - s0, 1), mask ? bits_at(mask, w, 1) : 1u);
+              if (mask && !bits_at(mask, w, 1)) hide(z);
               out[w] = z;
             }
           }
         }
+      }
+    }
+    __syncthreads();  // the stream is written, the lists are whole
+
+    const float rep = p.repetition ? p.repetition[r] : 1.f, freq = p.frequency ? p.frequency[r] : 0.f,
+                pres = p.presence ? p.presence[r] : 0.f;
+    const int listed = n_named;
+    for (int j = j0; j < j1; ++j) {
+      const size_t b = (size_t)(row0 + j);
+      const T* in = (const T*)p.logits + b * p.ld;
+      T* out = (T*)p.out + b * p.out_ld;
+      const uint32_t* mask = mask_of(b);
+      const int upto = min(j, n_draft);
+      for (int i = tid; i < listed; i += kThreads) {
+        const int d = named[i], v = s0 + d;
+        if (mask && !bits_at(mask, v, 1)) continue;
+        const uint32_t w = count[d];
+        const int bi = bias[d];
+        uint32_t c = w & ~kPrompt;
+        for (int k = 0; k < upto; ++k) c += draft_s[k] == v;
+        if (c == 0 && w == 0 && bi == 0) continue;  // drafted for a later row only
+        float z = to_f(in[v]);
+        if (c > 0 || w != 0) z = z > 0.f ? z / rep : z * rep;
+        if (c > 0) z = z - freq * (float)c - pres;
+        if (bi > 0) z += p.bias_val[bi - 1];
+        from_f(z, out + v);
       }
     }
   }
@@ -240,8 +255,7 @@ cudaError_t launch(const spec_logits_args& a, cudaStream_t stream) {
   const int slice = blocks < 304 ? kMinSlice : kMaxSlice;
   // A request with many rows is split over blocks of about 16.
   const int parts = (int)std::min<long long>(64, std::max<long long>(1, (long long)a.rows / (16ll * a.R)));
-  const int span = slice + 8;
-  const size_t smem = (size_t)(2 * span + (span + 31) / 32 + 1) * 4;
+  const size_t smem = (size_t)(2 * slice + slice / 2 + slice / 32) * 4;
   const dim3 grid((a.V + slice - 1) / slice, a.R, parts);
   adjust_kernel<T, VEC><<<grid, kThreads, smem, stream>>>(a, slice);
   return cudaGetLastError();

@@ -14,8 +14,11 @@
 // Layout: a block takes kRopeTokens or fewer tokens (or a part of one), computes
 // their cosines and sines once into shared memory for all heads, and moves units
 // of two 16-byte vectors: the two halves of a pair in the half layout, two
-// vectors next to each other otherwise.  Four units a thread are loaded before
-// the first is used.  Bound by memory: every element is read and written once.
+// vectors next to each other otherwise.  Either way unit u of a head takes the
+// frequencies [u VEC, (u + 1) VEC), which lie in shared memory as one float4 column
+// a unit, so that the units of a head read without bank conflicts.  Four units a
+// thread are loaded before the first is used.  Bound by memory: every element is
+// read and written once.
 #include "rope.cuh"
 
 #include <algorithm>
@@ -28,24 +31,9 @@ constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
 constexpr int kRopeTokens = 8;
 
-template <int BYTES>
-struct Raw;
-template <>
-struct Raw<16> {
-  using type = uint4;
-};
-template <>
-struct Raw<4> {
-  using type = uint32_t;
-};
-template <>
-struct Raw<2> {
-  using type = uint16_t;
-};
-
 template <typename T, int VEC>
 union Vec {
-  typename Raw<sizeof(T) * VEC>::type raw;
+  uint4 raw;
   T e[VEC];
   __device__ Vec() {}
 };
@@ -59,119 +47,190 @@ __device__ __forceinline__ void from_f(float v, __nv_bfloat16* o) { *o = __float
 template <typename T>
 __device__ __forceinline__ void turn(T& x, T& y, float2 cs) {
   const float a = to_f(x), b = to_f(y);
-  from_f(a * cs.x - b * cs.y, &x);
-  from_f(b * cs.x + a * cs.y, &y);
+  // spelled out, so that every kernel rounds alike
+  from_f(fmaf(a, cs.x, -__fmul_rn(b, cs.y)), &x);
+  from_f(fmaf(b, cs.x, __fmul_rn(a, cs.y)), &y);
 }
 
-// The two vectors of a unit: element offsets in the head (-1: none) and how they turn.
-struct Unit {
-  int a, b;
-  int kind;  // 0: copied, 1: a and b turn together, 2: pairs inside each vector
+// cos and sin, times the scale, of position x times the frequency (radians).
+__device__ __forceinline__ float2 cos_sin(float x, double freq, float scale) {
+  const double turns = freq * 0.15915494309189533577;  // 1 / (2 pi)
+  const float hi = (float)turns, lo = (float)(turns - (double)hi);
+  const float m = x * hi, e = fmaf(x, hi, -m);
+  const float frac = (m - rintf(m)) + fmaf(x, lo, e);
+  float s, c;
+  sincospif(2.f * frac, &s, &c);
+  return make_float2(c * scale, s * scale);
+}
+
+// Where a unit is read and written.
+template <typename T>
+struct Move {
+  const T* from;
+  T* to;  // null: nothing to do
 };
 
-template <int VEC, bool INTER>
-__device__ __forceinline__ Unit unit_of(int u, int D, int rot, bool rotated) {
-  const int half = rot >> 1;
-  if (rotated && (VEC == 1 || !INTER)) {
-    const int pairs = half / VEC;
-    if (u < pairs) return INTER ? Unit{2 * u, 2 * u + 1, 1} : Unit{u * VEC, half + u * VEC, 1};
-    const int a = rot + 2 * (u - pairs) * VEC;  // the part of the head that does not turn
-    return Unit{a < D ? a : -1, a + VEC < D ? a + VEC : -1, 0};
+template <typename T>
+__device__ __forceinline__ Move<T> head_of(const spec_rope_cache_args& p, size_t row, int h, int slot) {
+  if (h < p.Hq)
+    return Move<T>{(const T*)p.q + row * p.q_row + (size_t)h * p.q_head,
+                   (T*)p.q_out + row * p.q_out_row + (size_t)h * p.q_out_head};
+  if (slot < 0) return Move<T>{nullptr, nullptr};
+  const bool key = h < p.Hq + p.Hk;
+  const int hk = h - p.Hq - (key ? 0 : p.Hk);
+  return Move<T>{key ? (const T*)p.k + row * p.k_row + (size_t)hk * p.k_head
+                     : (const T*)p.v + row * p.v_row + (size_t)hk * p.v_head,
+                 (T*)(key ? p.k_cache : p.v_cache) + ((size_t)slot * p.Hk + hk) * p.D};
+}
+
+// Slot of each of the block's rows; -2 where the row is left out.
+__device__ __forceinline__ void read_slots(const spec_rope_cache_args& p, int row0, int nrow, int* slot_s) {
+  if ((int)threadIdx.x >= nrow) return;
+  const int pos = p.position[row0 + threadIdx.x];
+  int slot = p.slot ? max(p.slot[row0 + threadIdx.x], -1) : -1;
+  uint32_t bad = 0;
+  if (pos >= (1 << 24)) bad |= SPEC_STATUS_BAD_POSITION;
+  if (slot >= p.n_slots) {
+    bad |= SPEC_STATUS_BAD_PAGE;
+    slot = -1;
   }
-  const int a = 2 * u * VEC;
-  return Unit{a < D ? a : -1, a + VEC < D ? a + VEC : -1, rotated ? 2 : 0};
+  slot_s[threadIdx.x] = pos < 0 ? -2 : slot;
+  if (bad) set_status(p.status, bad);
+}
+__device__ __forceinline__ float position_of(const spec_rope_cache_args& p, int row) {
+  return (float)min(max(p.position[row], 0), (1 << 24) - 1);
 }
 
 template <typename T, int VEC, bool INTER>
 __global__ void __launch_bounds__(kThreads) rope_kernel(spec_rope_cache_args p, int tokens, int units,
                                                         int per_block) {
-  extern __shared__ float2 cs_s[];  // [tokens][rot / 2]
+  static_assert(VEC == 16 / (int)sizeof(T), "16-byte vectors");
+  constexpr int kCol = VEC / 4;  // float4s of a unit's cosines
+  extern __shared__ __align__(16) float4 cs_s[];  // a token: cosines [kCol][turning], then sines
   __shared__ int slot_s[kRopeTokens];
-  __shared__ bool live_s[kRopeTokens];
   using V = Vec<T, VEC>;
-  const int half = p.rot >> 1, heads = p.Hq + 2 * p.Hk;
+  const int half = p.rot >> 1, heads = p.Hq + 2 * p.Hk, turned = p.Hq + p.Hk;
+  const int turning = (half + VEC - 1) / VEC;  // units that turn
   const int row0 = blockIdx.x * tokens, nrow = min(tokens, p.rows - row0);
   const int begin = blockIdx.y * per_block, end = min(begin + per_block, nrow * heads * units);
 
-  uint32_t bad = 0;
   for (int i = threadIdx.x; i < nrow * half; i += kThreads) {
     const int t = i / half, f = i - t * half;
-    const int pos = min(max(p.position[row0 + t], 0), (1 << 24) - 1);
-    const double turns = p.freq[f] * 0.15915494309189533577;  // 1 / (2 pi)
-    const float hi = (float)turns, lo = (float)(turns - (double)hi), x = (float)pos;
-    const float m = x * hi, e = fmaf(x, hi, -m);
-    const float frac = (m - rintf(m)) + fmaf(x, lo, e);
-    float s, c;
-    sincospif(2.f * frac, &s, &c);
-    cs_s[i] = make_float2(c * p.scale, s * p.scale);
+    const float2 cs = cos_sin(position_of(p, row0 + t), p.freq[f], p.scale);
+    const int u = f / VEC, e = f % VEC;
+    float* col = reinterpret_cast<float*>(cs_s + (size_t)t * 2 * kCol * turning + (e / 4) * turning + u) + e % 4;
+    col[0] = cs.x;
+    col[4 * kCol * turning] = cs.y;
   }
-  if (threadIdx.x < nrow) {
-    const int pos = p.position[row0 + threadIdx.x];
-    int slot = p.slot ? p.slot[row0 + threadIdx.x] : -1;
-    if (pos >= (1 << 24)) bad |= SPEC_STATUS_BAD_POSITION;
-    if (slot >= p.n_slots) {
-      bad |= SPEC_STATUS_BAD_PAGE;
-      slot = -1;
-    }
-    slot_s[threadIdx.x] = slot;
-    live_s[threadIdx.x] = pos >= 0;
-  }
-  if (bad) set_status(p.status, bad);
+  read_slots(p, row0, nrow, slot_s);
   __syncthreads();
 
-  for (int i0 = begin + threadIdx.x; i0 < end; i0 += kThreads * kUnroll) {
+  // (token, head, unit) of the thread's next unit, stepped by the block's threads
+  int i = begin + threadIdx.x;
+  int h = i / units, u = i - h * units, t = h / heads;
+  h -= t * heads;
+  const int dh = kThreads / units, du = kThreads - dh * units;
+  while (i < end) {
     V va[kUnroll], vb[kUnroll];
-    Unit un[kUnroll];
-    T* to[kUnroll];
-    int tok[kUnroll];
+    Move<T> mv[kUnroll];
+    int tu[kUnroll], ea[kUnroll], eb[kUnroll];  // token and unit; element offsets, -1: none
+    bool rot[kUnroll];
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
-      const int i = i0 + k * kThreads;
-      to[k] = nullptr;
-      if (i >= end) continue;
-      const int hh = i / units, u = i - hh * units, t = hh / heads, h = hh - t * heads;
-      if (!live_s[t]) continue;
-      const size_t row = (size_t)(row0 + t);
-      const T* from;
-      if (h < p.Hq) {
-        from = (const T*)p.q + row * p.q_row + (size_t)h * p.q_head;
-        to[k] = (T*)p.q_out + row * p.q_out_row + (size_t)h * p.q_out_head;
-      } else {
-        const int s = slot_s[t];
-        if (s < 0) continue;
-        const bool key = h < p.Hq + p.Hk;
-        const int hk = h - p.Hq - (key ? 0 : p.Hk);
-        from = key ? (const T*)p.k + row * p.k_row + (size_t)hk * p.k_head
-                   : (const T*)p.v + row * p.v_row + (size_t)hk * p.v_head;
-        to[k] = (T*)(key ? p.k_cache : p.v_cache) + ((size_t)s * p.Hk + hk) * p.D;
+      mv[k].to = nullptr;
+      if (i < end) {
+        const int slot = slot_s[t];
+        if (slot > -2) mv[k] = head_of<T>(p, (size_t)(row0 + t), h, slot);
+        rot[k] = h < turned;
+        tu[k] = t * 2 * kCol * turning + u;
+        if (!INTER && rot[k] && u < turning) {
+          ea[k] = u * VEC;
+          eb[k] = half + u * VEC;
+        } else {  // two vectors next to each other, past the turning part where there is one
+          ea[k] = !INTER && rot[k] ? p.rot + 2 * (u - turning) * VEC : 2 * u * VEC;
+          eb[k] = ea[k] + VEC;
+          if (!INTER) rot[k] = false;
+        }
+        if (mv[k].to && ea[k] < p.D) va[k].raw = *reinterpret_cast<const uint4*>(mv[k].from + ea[k]);
+        if (mv[k].to && eb[k] < p.D) vb[k].raw = *reinterpret_cast<const uint4*>(mv[k].from + eb[k]);
       }
-      un[k] = unit_of<VEC, INTER>(u, p.D, p.rot, h < p.Hq + p.Hk);
-      tok[k] = t;
-      using R = decltype(va[k].raw);
-      if (un[k].a >= 0) va[k].raw = *reinterpret_cast<const R*>(from + un[k].a);
-      if (un[k].b >= 0) vb[k].raw = *reinterpret_cast<const R*>(from + un[k].b);
+      i += kThreads;
+      u += du;
+      h += dh;
+      if (u >= units) {
+        u -= units;
+        ++h;
+      }
+      while (h >= heads && i < end) {
+        h -= heads;
+        ++t;
+      }
     }
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
-      if (!to[k]) continue;
-      const float2* cs = cs_s + tok[k] * half;
-      if (un[k].kind == 1) {
-        const int f = INTER ? un[k].a >> 1 : un[k].a;
+      if (!mv[k].to) continue;
+      if (rot[k]) {
+        float4 c[kCol], s[kCol];
+        if (!INTER || ea[k] < p.rot) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) turn(va[k].e[j], vb[k].e[j], cs[f + j]);
-      } else if constexpr (VEC > 1 && INTER) {
-        if (un[k].kind == 2) {
+          for (int j = 0; j < kCol; ++j) {
+            c[j] = cs_s[tu[k] + j * turning];
+            s[j] = cs_s[tu[k] + (kCol + j) * turning];
+          }
+        }
+        const float* cf = reinterpret_cast<const float*>(c);
+        const float* sf = reinterpret_cast<const float*>(s);
+        if (!INTER) {
 #pragma unroll
-          for (int j = 0; j < VEC; j += 2) {
-            if (un[k].a < p.rot) turn(va[k].e[j], va[k].e[j + 1], cs[(un[k].a + j) >> 1]);
-            if (un[k].b >= 0 && un[k].b < p.rot)
-              turn(vb[k].e[j], vb[k].e[j + 1], cs[(un[k].b + j) >> 1]);
+          for (int e = 0; e < VEC; ++e) turn(va[k].e[e], vb[k].e[e], make_float2(cf[e], sf[e]));
+        } else {
+          if (ea[k] < p.rot) {
+#pragma unroll
+            for (int e = 0; e < VEC; e += 2) turn(va[k].e[e], va[k].e[e + 1], make_float2(cf[e / 2], sf[e / 2]));
+          }
+          if (eb[k] < p.rot) {
+#pragma unroll
+            for (int e = 0; e < VEC; e += 2)
+              turn(vb[k].e[e], vb[k].e[e + 1], make_float2(cf[VEC / 2 + e / 2], sf[VEC / 2 + e / 2]));
           }
         }
       }
-      using R = decltype(va[k].raw);
-      if (un[k].a >= 0) *reinterpret_cast<R*>(to[k] + un[k].a) = va[k].raw;
-      if (un[k].b >= 0) *reinterpret_cast<R*>(to[k] + un[k].b) = vb[k].raw;
+      if (ea[k] < p.D) *reinterpret_cast<uint4*>(mv[k].to + ea[k]) = va[k].raw;
+      if (eb[k] < p.D) *reinterpret_cast<uint4*>(mv[k].to + eb[k]) = vb[k].raw;
+    }
+  }
+}
+
+// The same, element by element: sizes, strides or addresses that are off 16 bytes.
+template <typename T, bool INTER>
+__global__ void __launch_bounds__(kThreads) rope_scalar_kernel(spec_rope_cache_args p, int tokens, int units,
+                                                               int per_block) {
+  extern __shared__ __align__(16) float2 cs2_s[];  // [tokens][rot / 2]
+  __shared__ int slot_s[kRopeTokens];
+  const int half = p.rot >> 1, heads = p.Hq + 2 * p.Hk;
+  const int row0 = blockIdx.x * tokens, nrow = min(tokens, p.rows - row0);
+  const int begin = blockIdx.y * per_block, end = min(begin + per_block, nrow * heads * units);
+  for (int i = threadIdx.x; i < nrow * half; i += kThreads) {
+    const int t = i / half;
+    cs2_s[i] = cos_sin(position_of(p, row0 + t), p.freq[i - t * half], p.scale);
+  }
+  read_slots(p, row0, nrow, slot_s);
+  __syncthreads();
+  for (int i = begin + threadIdx.x; i < end; i += kThreads) {
+    const int hh = i / units, u = i - hh * units, t = hh / heads, h = hh - t * heads;
+    if (slot_s[t] < -1) continue;
+    const Move<T> mv = head_of<T>(p, (size_t)(row0 + t), h, slot_s[t]);
+    if (!mv.to) continue;
+    if (h < p.Hq + p.Hk && u < half) {
+      const int a = INTER ? 2 * u : u, b = INTER ? a + 1 : half + u;
+      T x = mv.from[a], y = mv.from[b];
+      turn(x, y, cs2_s[t * half + u]);
+      mv.to[a] = x;
+      mv.to[b] = y;
+    } else {
+      const int a = h < p.Hq + p.Hk ? p.rot + 2 * (u - half) : 2 * u;
+      if (a < p.D) mv.to[a] = mv.from[a];
+      if (a + 1 < p.D) mv.to[a + 1] = mv.from[a + 1];
     }
   }
 }
@@ -192,9 +251,15 @@ cudaError_t launch(const spec_rope_cache_args& a, cudaStream_t stream) {
   const int per_block = a.rows < 304 ? kThreads : tokens == 1 ? deep : (int)(tokens * per_token);
   const int parts = (int)((tokens * per_token + per_block - 1) / per_block);
   const dim3 grid((a.rows + tokens - 1) / tokens, std::max(1, parts));
-  const size_t smem = (size_t)tokens * half * sizeof(float2);
-  if (inter) rope_kernel<T, VEC, true><<<grid, kThreads, smem, stream>>>(a, tokens, units, per_block);
-  else rope_kernel<T, VEC, false><<<grid, kThreads, smem, stream>>>(a, tokens, units, per_block);
+  if constexpr (VEC == 1) {
+    const size_t smem = (size_t)tokens * half * sizeof(float2);
+    if (inter) rope_scalar_kernel<T, true><<<grid, kThreads, smem, stream>>>(a, tokens, units, per_block);
+    else rope_scalar_kernel<T, false><<<grid, kThreads, smem, stream>>>(a, tokens, units, per_block);
+  } else {
+    const size_t smem = (size_t)tokens * 2 * ((half + VEC - 1) / VEC) * VEC * sizeof(float);
+    if (inter) rope_kernel<T, VEC, true><<<grid, kThreads, smem, stream>>>(a, tokens, units, per_block);
+    else rope_kernel<T, VEC, false><<<grid, kThreads, smem, stream>>>(a, tokens, units, per_block);
+  }
   return cudaGetLastError();
 }
 
