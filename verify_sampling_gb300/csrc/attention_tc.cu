@@ -19,8 +19,9 @@
 // An item cut between blocks leaves several pieces; a second kernel joins every
 // row's pieces.
 //
-// Block: producer warp (TMA of key and value tiles, 64 x page boxes, into one
-// ring), MMA warp (S = Q K^T into TMEM, O += P V with P read from TMEM), and two
+// Block: planner warp (walks the block's items and posts them in shared memory),
+// producer warp (TMA of key and value tiles, 64 x page boxes, into one ring), MMA
+// warp (S = Q K^T into TMEM, O += P V with P read from TMEM), and two
 // softmax warpgroups of 128 rows, one thread a row, so maxima and sums need no
 // shuffles.  An item of more than 128 rows uses both warpgroups on the same key
 // tile, one's softmax under the other's products; smaller items alternate
@@ -42,8 +43,13 @@ namespace {
 using namespace attn;
 
 constexpr int kTile = 128;  // keys of a tile, rows of a warpgroup
-constexpr int kThreads = 320;
-constexpr int kProducer = 8, kMma = 9;  // warps 0-3 and 4-7 are the softmax warpgroups
+constexpr int kThreads = 384;
+// Warps 0-3 and 4-7 are the softmax warpgroups.
+constexpr int kProducer = 8, kMma = 9, kPlanner = 10;
+constexpr int kItemSlots = 4, kItemReaders = 10;  // the producer, the MMA warp, eight softmax warps
+// Registers a thread after the split: a softmax thread holds a row of 128 scores.
+// 256 x 216 + 128 x 72 = 384 x 168, what the block was launched with.
+constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kSlack = 8.f;  // log2 units the maximum may grow by before O is rescaled
 // Costs, in units of about 400 clocks: a prefix tile (two warpgroups, bound by the
@@ -113,7 +119,7 @@ __device__ __forceinline__ int64_t head_cost(const Segment& s, int per_head) {
   return c;
 }
 
-// The block's items, in the order every warp role walks them.
+// The block's items in order.
 struct Walker {
   const spec_prefix_attention_args& a;
   int64_t pos, x0, x1;
@@ -215,6 +221,43 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+template <int N>
+__device__ __forceinline__ void regs_grow() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_shrink() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  return pair(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ float2 halves(uint64_t v) {
+  uint32_t lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // bf16x2 with `lo` in the low half
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
@@ -232,6 +275,7 @@ struct Smem {
 };
 
 struct Bars {
+  uint64_t item_full[kItemSlots], item_empty[kItemSlots];
   uint64_t full[10], empty[10];
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain;
 };
@@ -250,6 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ volatile int abort_flag;
   __shared__ int64_t warp_sum[kThreads / 32];
   __shared__ Layout lay;
+  __shared__ Item items[kItemSlots];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per_head = a.Hq / a.Hk;
 
@@ -281,6 +326,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::mbar_init(&bars.o_full[i], 1);
       }
       tc::mbar_init(&bars.drain, 1);
+      for (int i = 0; i < kItemSlots; ++i) {
+        tc::mbar_init(&bars.item_full[i], 1);
+        tc::mbar_init(&bars.item_empty[i], kItemReaders);
+      }
       tc::fence_barrier_init();
     }
     if (warp == kMma) tc::tmem_alloc(&tmem_slot, 512);
@@ -327,14 +376,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     return false;
   };
 
+  if (warp >= 8) regs_shrink<kRegsOther>();
   if (warp == kProducer) {
     // ------------------------------------------------------------ producer --
-    Walker walk(a, lay);
-    Item it;
     uint32_t seq = 0;  // ring positions used: keys and values in turn
+    uint32_t bad = 0;
     bool ok = true;
     const int box = min(a.page_size, kTile), boxes = kTile / box;  // keys of a box, boxes of a tile
-    while (ok && walk.next(it)) {
+    for (uint32_t n_item = 0;; ++n_item) {
+      const Item& posted = items[n_item % kItemSlots];
+      ok = warp_wait(&bars.item_full[n_item % kItemSlots], n_item / kItemSlots);
+      if (!ok || posted.rows == 0) break;
+      const Item it = posted;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars.item_empty[n_item % kItemSlots]);
       for (int i = it.lo; ok && i < it.hi; ++i) {
         const int live = min(kTile, it.keys - i * kTile);
         const int used = (live + box - 1) / box;  // pages (or parts of one) that have keys
@@ -342,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int which = lane / kHalves;
         if (which < used) {
           const int key = i * kTile + which * box, pi = key / a.page_size;
-          row = page_of(a, it.table, pi, &walk.bad) * a.page_size + (key - pi * a.page_size);
+          row = page_of(a, it.table, pi, &bad) * a.page_size + (key - pi * a.page_size);
         }
         for (int kv = 0; kv < 2; ++kv, ++seq) {
           const int st = seq % S::kStages;
@@ -357,18 +412,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      if (!ok) break;
     }
+    if (bad) set_status(a.status, bad);
     if (!ok) {  // the copies in flight land before the block's memory goes
       const uint32_t from = seq > (uint32_t)S::kStages ? seq - S::kStages : 0u;
       for (uint32_t s = from; s < seq; ++s)
         tc::mbar_wait(&bars.full[s % S::kStages], (s / S::kStages) & 1u, kWaitNs);
     }
-    if (walk.bad) set_status(a.status, walk.bad);
   } else if (warp == kMma) {
     // ------------------------------------------------------------ products --
     if (lane == 0) {
-      Walker walk(a, lay);
-      Item it, nx;
+      int rows = 0, tiles = 0, n_rows = 0, n_tiles = 0;  // of the current and the next item
+      uint32_t n_item = 0;
       uint32_t seq = 0;  // ring position of the current tile's keys
       uint32_t q_n[2] = {0, 0}, p_n[2] = {0, 0};
       int turn = 0;      // warpgroup of the next small item
@@ -398,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_bf16_ts(tmem + 2 * kTile + t * kTile, tmem + t * kTile + c * 8,
                       sw128_desc_mn(vb + c * 2048, kHalfBytes), kDescO, !first || c > 0);
       };
-      auto begin = [&](const Item& x, int l0, int l1, uint32_t s) {  // an item's first scores
+      auto begin = [&](int l0, int l1, uint32_t s) {  // an item's first scores
         wait(&bars.full[s % S::kStages], s / S::kStages);
         for (int t = l0; t <= l1 && ok; ++t) {
           wait(&bars.q_full[t], q_n[t]++);
@@ -408,10 +464,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok) tc::mma_commit(&bars.empty[s % S::kStages]);
       };
-      bool more = walk.next(it);
-      int l0 = 0, l1 = 0;
-      auto lanes = [&](const Item& x, int& p, int& q) {
-        if (x.rows > kTile) {
+      auto next = [&](int& r, int& n) {  // the next item's rows and tiles; false after the last
+        const uint32_t slot = n_item % kItemSlots;
+        wait(&bars.item_full[slot], n_item / kItemSlots);
+        ++n_item;
+        if (!ok) return false;
+        r = items[slot].rows;
+        n = items[slot].hi - items[slot].lo;
+        if (r == 0) return false;
+        tc::mbar_arrive(&bars.item_empty[slot]);
+        return true;
+      };
+      auto lanes = [&](int r, int& p, int& q) {  // the warpgroups of an item
+        if (r > kTile) {
           p = 0;
           q = 1;
         } else {
@@ -419,21 +484,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           turn ^= 1;
         }
       };
+      int l0 = 0, l1 = 0;
+      bool more = next(rows, tiles);
       if (more) {
-        lanes(it, l0, l1);
-        begin(it, l0, l1, seq);
+        lanes(rows, l0, l1);
+        begin(l0, l1, seq);
       }
       while (more && ok) {
         bool more_next = false, early = false;
         int n0 = 0, n1 = 0;
-        for (int i = it.lo; i < it.hi && ok; ++i, seq += 2) {
-          const bool last = i + 1 == it.hi;
+        for (int i = 0; i < tiles && ok; ++i, seq += 2) {
+          const bool last = i + 1 == tiles;
           if (last) {
-            more_next = walk.next(nx);
+            more_next = next(n_rows, n_tiles);
             if (more_next) {
-              lanes(nx, n0, n1);
+              lanes(n_rows, n0, n1);
               early = l0 == l1 && n0 == n1 && n0 != l0;
-              if (early) begin(nx, n0, n1, seq + 2);
+              if (early) begin(n0, n1, seq + 2);
             }
           }
           wait(&bars.full[(seq + 1) % S::kStages], (seq + 1) / S::kStages);
@@ -442,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait(&bars.p_full[t], p_n[t]++);
             if (!ok) break;
             tc::fence_after_sync();
-            values(t, seq + 1, i == it.lo);
+            values(t, seq + 1, i == 0);
             if (last) tc::mma_commit(&bars.o_full[t]);
             else scores(t, seq + 2);
           }
@@ -452,10 +519,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         more = more_next;
-        it = nx;
+        rows = n_rows;
+        tiles = n_tiles;
         l0 = n0;
         l1 = n1;
-        if (more && !early) begin(it, l0, l1, seq);
+        if (more && !early) begin(l0, l1, seq);
       }
       if (!ok) {  // the products in flight end before TMEM is freed
         tc::mma_commit(&bars.drain);
@@ -463,18 +531,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else {
+  } else if (warp == kPlanner) {
+    // ------------------------------------------------------------- planner --
+    Walker walk(a, lay);
+    Item it;
+    for (uint32_t n_item = 0;; ++n_item) {
+      if (!walk.next(it)) it.rows = 0;  // the end
+      const uint32_t slot = n_item % kItemSlots;
+      if (!warp_wait(&bars.item_empty[slot], (n_item / kItemSlots) ^ 1u)) break;
+      if (lane == 0) {
+        items[slot] = it;
+        tc::mbar_arrive(&bars.item_full[slot]);
+      }
+      if (it.rows == 0) break;
+    }
+  } else if (warp < 8) {
     // ------------------------------------------------------------- softmax --
+    regs_grow<kRegsSoftmax>();
     const int t = warp >> 2, tid_g = tid & 127;
     const uint32_t lane_base = (uint32_t)(warp & 3) << 21;  // 32 TMEM lanes a warp, lanes in the high half
     const uint32_t s_addr = tmem + lane_base + t * kTile, o_addr = tmem + lane_base + 2 * kTile + t * kTile;
     const float sl = a.scale * kLog2e;
-    Walker walk(a, lay);
-    Item it;
     uint32_t seq = 0, s_n = 0, o_n = 0;
     int turn = 0;
     bool ok = true;
-    while (ok && walk.next(it)) {
+    for (uint32_t n_item = 0;; ++n_item) {
+      const Item& posted = items[n_item % kItemSlots];
+      ok = warp_wait(&bars.item_full[n_item % kItemSlots], n_item / kItemSlots);
+      if (!ok || posted.rows == 0) break;
+      const Item it = posted;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars.item_empty[n_item % kItemSlots]);
       const bool both = it.rows > kTile;
       const int mine = both ? t : turn;
       if (!both) turn ^= 1;
@@ -517,11 +604,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float m0 = -CUDART_INF_F, m1 = m0, m2 = m0, m3 = m0;
 #pragma unroll
-        for (int c = 0; c < kTile; c += 4) {
-          m0 = fmaxf(m0, __uint_as_float(s[c]));
-          m1 = fmaxf(m1, __uint_as_float(s[c + 1]));
-          m2 = fmaxf(m2, __uint_as_float(s[c + 2]));
-          m3 = fmaxf(m3, __uint_as_float(s[c + 3]));
+        for (int c = 0; c < kTile; c += 8) {
+          m0 = max3(m0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+          m1 = max3(m1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+          m2 = max3(m2, __uint_as_float(s[c + 4]), __uint_as_float(s[c + 5]));
+          m3 = max3(m3, __uint_as_float(s[c + 6]), __uint_as_float(s[c + 7]));
         }
         const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sl;
         if (__any_sync(0xffffffffu, top > ref + kSlack)) {
@@ -542,26 +629,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float sub = ref == -CUDART_INF_F ? 0.f : ref;
-        float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+        const uint64_t sl2 = pair(sl, sl), sub2 = pair(-sub, -sub);
+        uint64_t a0 = 0, a1 = 0;
 #pragma unroll
         for (int c = 0; c < kTile; c += 64) {
           uint32_t p[32];
 #pragma unroll
           for (int e = 0; e < 64; e += 4) {
-            const float p0 = tc::ex2(fmaf(__uint_as_float(s[c + e]), sl, -sub));
-            const float p1 = tc::ex2(fmaf(__uint_as_float(s[c + e + 1]), sl, -sub));
-            const float p2 = tc::ex2(fmaf(__uint_as_float(s[c + e + 2]), sl, -sub));
-            const float p3 = tc::ex2(fmaf(__uint_as_float(s[c + e + 3]), sl, -sub));
-            a0 += p0;
-            a1 += p1;
-            a2 += p2;
-            a3 += p3;
+            const float2 z0 = halves(fma2(pair(s[c + e], s[c + e + 1]), sl2, sub2));
+            const float2 z1 = halves(fma2(pair(s[c + e + 2], s[c + e + 3]), sl2, sub2));
+            const float p0 = tc::ex2(z0.x), p1 = tc::ex2(z0.y), p2 = tc::ex2(z1.x), p3 = tc::ex2(z1.y);
+            a0 = add2(a0, pair(p0, p1));
+            a1 = add2(a1, pair(p2, p3));
             p[e / 2] = pack_bf16(p0, p1);
             p[e / 2 + 1] = pack_bf16(p2, p3);
           }
           tmem_st32(s_addr + c / 2, p);
         }
-        l += (a0 + a1) + (a2 + a3);
+        const float2 sum = halves(add2(a0, a1));
+        l += sum.x + sum.y;
         // Values past the item's keys may be anything, NaN among them: zeros instead.
         // (The first warpgroup of two does it, whose product is issued first.)
         const int live = it.keys - i * kTile;
