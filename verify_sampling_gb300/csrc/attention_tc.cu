@@ -20,8 +20,9 @@
 // row's pieces.
 //
 // Block: planner warp (walks the block's items and posts them in shared memory),
-// producer warp (TMA of key and value tiles, 64 x page boxes, into one ring), MMA
-// warp (S = Q K^T into TMEM, O += P V with P read from TMEM), and two
+// producer warp (TMA of key and value tiles, 64 x page boxes, into one ring), loader
+// warp (query rows: TMA where the heads of a key head divide a box, else 16-byte
+// copies into the swizzled places), MMA warp (S = Q K^T into TMEM, O += P V with P read from TMEM), and two
 // softmax warpgroups of 128 rows, one thread a row, so maxima and sums need no
 // shuffles.  An item of more than 128 rows uses both warpgroups on the same key
 // tile, one's softmax under the other's products; smaller items alternate
@@ -45,16 +46,14 @@ using namespace attn;
 constexpr int kTile = 128;  // keys of a tile, rows of a warpgroup
 constexpr int kThreads = 384;
 // Warps 0-3 and 4-7 are the softmax warpgroups.
-constexpr int kProducer = 8, kMma = 9, kPlanner = 10;
-constexpr int kItemSlots = 4, kItemReaders = 10;  // the producer, the MMA warp, eight softmax warps
-// Registers a thread after the split: a softmax thread holds a row of 128 scores.
-// 256 x 216 + 128 x 72 = 384 x 168, what the block was launched with.
-constexpr int kRegsSoftmax = 216, kRegsOther = 72;
+constexpr int kProducer = 8, kMma = 9, kPlanner = 10, kLoader = 11;
+constexpr int kItemSlots = 4, kItemReaders = 11;  // producer, MMA, loader, eight softmax warps
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kSlack = 8.f;  // log2 units the maximum may grow by before O is rescaled
-// Costs, in units of about 400 clocks: a prefix tile (two warpgroups, bound by the
-// products), an own tile (bound by its 64 KB), and an item's start and end.
-constexpr int kCostPrefix = 2, kCostOwn = 3, kCostItem = 3;
+// Costs, in units of 0.1 us, measured: a tile of an item of two warpgroups (bound
+// by the products), a tile of a smaller one (bound by its 64 KB), and an item's
+// start and end.
+constexpr int kCostPair = 22, kCostSingle = 15, kCostStartPair = 50, kCostStartSingle = 20;
 
 // ------------------------------------------------------------ work layout --
 struct Segment {  // a group's prefix or a request's own keys
@@ -71,6 +70,7 @@ struct Item {
   int keys;            // keys the item reads
   int first_own;
   bool prefix;
+  bool direct;  // the whole of its rows' keys: the result itself is written
   const int32_t* table;
   size_t slot;  // partial row of its row m0
 };
@@ -98,6 +98,17 @@ __device__ __forceinline__ Segment segment(const spec_prefix_attention_args& a, 
   }
   return s;
 }
+// The group that request r is in, or -1, and the keys of its prefix.
+__device__ __forceinline__ int group_of(const spec_prefix_attention_args& a, int r, uint32_t* bad) {
+  if (a.G == 0) return -1;
+  const int g = last_at_or_below(a.group_off, a.G, r);
+  const int2 in = group_requests(a, g, bad);
+  return r >= in.x && r < in.y ? g : -1;
+}
+__device__ __forceinline__ int shared_keys(const spec_prefix_attention_args& a, int r, uint32_t* bad) {
+  const int g = group_of(a, r, bad);
+  return g < 0 ? 0 : prefix_keys(a, g, bad);
+}
 // Keys that the item of query rows [256 i, ..) needs: its last row's.
 __device__ __forceinline__ int item_keys(const Segment& s, int i, int per_head) {
   if (s.prefix) return s.keys;
@@ -107,15 +118,23 @@ __device__ __forceinline__ int item_keys(const Segment& s, int i, int per_head) 
 __device__ __forceinline__ int item_count(const Segment& s, int per_head) {
   return (int)(((int64_t)s.n * per_head + kItemRows - 1) / kItemRows);
 }
-__device__ __forceinline__ int64_t item_cost(int keys, bool prefix) {
+__device__ __forceinline__ int tile_cost(int rows) { return rows > kTile ? kCostPair : kCostSingle; }
+__device__ __forceinline__ int start_cost(int rows) { return rows > kTile ? kCostStartPair : kCostStartSingle; }
+// Cost of an item of `rows` query rows (or more: 256 are its own).
+__device__ __forceinline__ int64_t item_cost(int keys, int rows) {
   const int tiles = (keys + kTile - 1) / kTile;
-  return tiles ? kCostItem + (int64_t)tiles * (prefix ? kCostPrefix : kCostOwn) : 0;
+  return tiles ? start_cost(rows) + (int64_t)tiles * tile_cost(rows) : 0;
 }
 __device__ __forceinline__ int64_t head_cost(const Segment& s, int per_head) {
   const int n = item_count(s, per_head);
-  if (s.prefix) return n * item_cost(s.keys, true);
   int64_t c = 0;
-  for (int i = 0; i < n; ++i) c += item_cost(item_keys(s, i, per_head), false);
+  if (s.prefix) {
+    if (n > 0)
+      c = (n - 1) * item_cost(s.keys, kItemRows) +
+          item_cost(s.keys, s.n * per_head - (n - 1) * kItemRows);
+    return c;
+  }
+  for (int i = 0; i < n; ++i) c += item_cost(item_keys(s, i, per_head), s.n * per_head - i * kItemRows);
   return c;
 }
 
@@ -125,11 +144,12 @@ struct Walker {
   int64_t pos, x0, x1;
   int k, h, i, per_head, count;
   Segment seg;
+  bool alone;  // a request without a prefix
   uint32_t bad;
 
   __device__ Walker(const spec_prefix_attention_args& args, const Layout& lay)
       : a(args), pos(lay.s0), x0(lay.x0), x1(lay.x1), k(lay.k0), h(0), i(0),
-        per_head(args.Hq / args.Hk), count(0), bad(0) {
+        per_head(args.Hq / args.Hk), count(0), alone(false), bad(0) {
     if (x0 >= x1) return;
     load();
     const int64_t c = head_cost(seg, per_head);
@@ -141,6 +161,7 @@ struct Walker {
   __device__ void load() {
     seg = segment(a, k, &bad);
     count = item_count(seg, per_head);
+    alone = k >= a.G && shared_keys(a, k - a.G, &bad) == 0;
   }
   __device__ bool next(Item& it) {
     if (x0 >= x1) return false;
@@ -156,11 +177,12 @@ struct Walker {
       }
       if (pos >= x1) return false;
       const int keys = item_keys(seg, i, per_head);
-      const int64_t cost = item_cost(keys, seg.prefix), at = pos + kCostItem;
+      const int left = seg.n * per_head - i * kItemRows;
+      const int64_t cost = item_cost(keys, left), at = pos + start_cost(left);
       pos += cost;
       const int mine = i++;
       if (cost == 0 || pos <= x0) continue;
-      const int w = seg.prefix ? kCostPrefix : kCostOwn, tiles = (keys + kTile - 1) / kTile;
+      const int w = tile_cost(left), tiles = (keys + kTile - 1) / kTile;
       it.lo = x0 <= at ? 0 : (int)((x0 - at + w - 1) / w);
       it.hi = x1 <= at ? 0 : (int)min((int64_t)tiles, (x1 - at + w - 1) / w);
       if (it.lo >= it.hi) continue;
@@ -172,6 +194,7 @@ struct Walker {
       it.keys = keys;
       it.first_own = seg.first_own;
       it.prefix = seg.prefix;
+      it.direct = alone && it.lo == 0 && it.hi == tiles;
       it.table = seg.table;
       it.slot = (seg.prefix ? 0 : (size_t)a.rows * a.Hq) + (size_t)seg.row0 * a.Hq + (size_t)h * m +
                 it.m0 + (size_t)kItemRows * blockIdx.x;
@@ -181,19 +204,33 @@ struct Walker {
 };
 
 // ------------------------------------------------------------- tcgen05 -----
-// MN-major operand in the 128-byte swizzle layout: rows of 64 elements, 8-row
-// groups 1024 bytes apart (stride offset), the next 64 elements `lead` bytes on.
-__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t lead) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) |
-         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// Descriptors of the 128-byte swizzle layout (8-row groups 1024 bytes apart) differ
+// in their low words alone, so the issuing thread adds constants to 32-bit words:
+// it is one thread, and what it computes between products the tensor pipe waits for.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride, version, swizzle
+// K-major operand at a shared address
+__device__ __forceinline__ uint32_t desc_k(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
+// MN-major operand: rows of 64 elements, the next 64 elements `lead` bytes on
+__device__ __forceinline__ uint32_t desc_mn(uint32_t saddr, uint32_t lead) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n"
+      " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+      : "memory");
 }
 // A from tensor memory.
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                            uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.b32 p, %4, 0;\n"
+      " mov.b64 db, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
       : "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
@@ -218,16 +255,16 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void regs_grow() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_shrink() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
@@ -258,11 +295,35 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// 16 bytes to a shared address, without registers in between.
+__device__ __forceinline__ void copy16(uint32_t saddr, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(saddr), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// 32 bytes to a 32-byte address: one whole sector.
+__device__ __forceinline__ void store32(float* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 // bf16x2 with `lo` in the low half
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// The rest of a wait whose first look failed.  Gives up when the time limit passes or
+// another warp has given up.  (Out of line: the code of a role that a short item
+// runs once has to fit the instruction cache beside the others'.)
+__device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t phase, volatile int* abort_flag, uint32_t* status) {
+  for (int i = 0; i < 2000; ++i) {
+    if (tc::mbar_wait(bar, phase & 1u, kWaitNs / 2000)) return true;
+    if (*abort_flag) return false;
+  }
+  *abort_flag = 1;
+  set_status(status, SPEC_STATUS_TIMEOUT);
+  return false;
 }
 
 template <int D>
@@ -277,12 +338,13 @@ struct Smem {
 struct Bars {
   uint64_t item_full[kItemSlots], item_empty[kItemSlots];
   uint64_t full[10], empty[10];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain;
 };
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                        const __grid_constant__ CUtensorMap q_map, const int q_box,
                         const spec_prefix_attention_args a, float* part, float2* stat, int64_t* plan) {
   using S = Smem<D>;
   constexpr int kHalves = D / 64;
@@ -320,7 +382,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::mbar_init(&bars.empty[i], 1);
       }
       for (int i = 0; i < 2; ++i) {
-        tc::mbar_init(&bars.q_full[i], 4);
+        tc::mbar_init(&bars.q_full[i], 1);
+        tc::mbar_init(&bars.q_empty[i], 1);
         tc::mbar_init(&bars.s_full[i], 1);
         tc::mbar_init(&bars.p_full[i], 4);
         tc::mbar_init(&bars.o_full[i], 1);
@@ -336,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kProducer && lane == 0) {
       tc::tma_prefetch_desc(&k_map);
       tc::tma_prefetch_desc(&v_map);
+      if (q_box > 0) tc::tma_prefetch_desc(&q_map);
     }
     __syncthreads();
     int64_t before = 0, total = 0;
@@ -346,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     int64_t at = before + inc - mine;  // position of the thread's first segment
     // at least one tile a block, so that every block of an item's range has one
-    const int64_t per = max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)max(kCostPrefix, kCostOwn));
+    const int64_t per = max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)max(kCostPair, kCostSingle));
     const int64_t x0 = per * blockIdx.x, x1 = min(x0 + per, total);
     const bool here = x0 < x1 && at <= x0 && x0 < at + mine;
     if (here || blockIdx.x == 0) {
@@ -364,23 +428,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_after_sync();
   }
   const uint32_t tmem = tmem_slot;
-  auto fail = [&]() {
-    abort_flag = 1;
-    set_status(a.status, SPEC_STATUS_TIMEOUT);
-  };
   // A wait of a whole warp: all of its lanes go on, or all give up.
   auto warp_wait = [&](uint64_t* bar, uint32_t phase) {
-    const bool got = !abort_flag && tc::mbar_wait(bar, phase & 1u, kWaitNs);
-    if (__all_sync(0xffffffffu, got)) return true;
-    fail();
-    return false;
+    bool got = tc::mbar_try_wait(bar, phase & 1u);
+    if (!__all_sync(0xffffffffu, got)) {
+      got = slow_wait(bar, phase, &abort_flag, a.status);
+      got = __all_sync(0xffffffffu, got);
+    }
+    return got;
   };
-
-  if (warp >= 8) regs_shrink<kRegsOther>();
   if (warp == kProducer) {
     // ------------------------------------------------------------ producer --
     uint32_t seq = 0;  // ring positions used: keys and values in turn
-    uint32_t bad = 0;
+    uint32_t bad = 0, ph = 0;
+    int st = 0;
     bool ok = true;
     const int box = min(a.page_size, kTile), boxes = kTile / box;  // keys of a box, boxes of a tile
     for (uint32_t n_item = 0;; ++n_item) {
@@ -400,8 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           row = page_of(a, it.table, pi, &bad) * a.page_size + (key - pi * a.page_size);
         }
         for (int kv = 0; kv < 2; ++kv, ++seq) {
-          const int st = seq % S::kStages;
-          ok = warp_wait(&bars.empty[st], (seq / S::kStages) ^ 1u);
+          ok = warp_wait(&bars.empty[st], ph ^ 1u);
           if (!ok) break;
           if (lane == 0) tc::mbar_expect_tx(&bars.full[st], (uint32_t)(used * box * D * 2));
           __syncwarp();
@@ -409,6 +469,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int half = lane % kHalves;
             tc::tma_load_3d(smem + S::kRing + st * S::kTileBytes + half * kHalfBytes + which * box * 128,
                             kv ? &v_map : &k_map, &bars.full[st], half * 64, it.h, row);
+          }
+          if (++st == S::kStages) {
+            st = 0;
+            ph ^= 1u;
           }
         }
       }
@@ -425,44 +489,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       int rows = 0, tiles = 0, n_rows = 0, n_tiles = 0;  // of the current and the next item
       uint32_t n_item = 0;
-      uint32_t seq = 0;  // ring position of the current tile's keys
       uint32_t q_n[2] = {0, 0}, p_n[2] = {0, 0};
-      int turn = 0;      // warpgroup of the next small item
+      int turn = 0;  // warpgroup of the next small item
       bool ok = true;
-      const uint32_t q_base = tc::smem_u32(smem), ring = tc::smem_u32(smem + S::kRing);
       constexpr uint32_t kDescS = tc::bf16_idesc(128, kTile);
       constexpr uint32_t kDescO = tc::bf16_idesc(128, D) | (1u << 16);  // values: keys down, head across
-      auto wait = [&](uint64_t* bar, uint32_t n) {
-        if (ok && (abort_flag || !tc::mbar_wait(bar, n & 1u, kWaitNs))) {
-          fail();
-          ok = false;
+      const uint32_t q_lo = desc_k(tc::smem_u32(smem));
+      const uint32_t k_lo = desc_k(tc::smem_u32(smem + S::kRing));
+      const uint32_t v_lo = desc_mn(tc::smem_u32(smem + S::kRing), kHalfBytes);
+      struct Place {  // a ring position: its stage and the parity of its barriers
+        uint32_t stage, phase;
+        __device__ __forceinline__ Place next() const {
+          return stage + 1 == S::kStages ? Place{0, phase ^ 1u} : Place{stage + 1, phase};
         }
       };
-      auto scores = [&](int t, uint32_t s) {  // S_t = Q_t K^T with the keys at ring position s
-        const uint32_t kb = ring + (s % S::kStages) * S::kTileBytes, qb = q_base + t * S::kTileBytes;
+      auto wait = [&](uint64_t* bar, uint32_t phase) {
+        if (ok && !tc::mbar_try_wait(bar, phase & 1u)) ok = slow_wait(bar, phase, &abort_flag, a.status);
+      };
+      auto scores = [&](int t, const Place& k, bool last) {  // S_t = Q_t K^T
+        const uint32_t kb = k_lo + k.stage * (S::kTileBytes >> 4), qb = q_lo + t * (S::kTileBytes >> 4);
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
-          const uint32_t off = (c >> 2) * kHalfBytes + (c & 3) * 32;
-          tc::mma_bf16(tmem + t * kTile, tc::sw128_desc(qb + off), tc::sw128_desc(kb + off), kDescS, c > 0);
+          constexpr uint32_t kStep = 32 >> 4;
+          const uint32_t off = (c >> 2) * (kHalfBytes >> 4) + (c & 3) * kStep;
+          mma_ss(tmem + t * kTile, qb + off, kb + off, kDescS, c > 0);
         }
         tc::mma_commit(&bars.s_full[t]);
+        if (last) tc::mma_commit(&bars.q_empty[t]);
       };
-      auto values = [&](int t, uint32_t s, bool first) {  // O_t (+)= P_t V
-        const uint32_t vb = ring + (s % S::kStages) * S::kTileBytes;
+      auto values = [&](int t, const Place& v, bool first) {  // O_t (+)= P_t V
+        const uint32_t vb = v_lo + v.stage * (S::kTileBytes >> 4);
 #pragma unroll
         for (int c = 0; c < kTile / 16; ++c)
-          mma_bf16_ts(tmem + 2 * kTile + t * kTile, tmem + t * kTile + c * 8,
-                      sw128_desc_mn(vb + c * 2048, kHalfBytes), kDescO, !first || c > 0);
+          mma_ts(tmem + 2 * kTile + t * kTile, tmem + t * kTile + c * 8, vb + c * (2048 >> 4), kDescO,
+                 c > 0 || !first);
       };
-      auto begin = [&](int l0, int l1, uint32_t s) {  // an item's first scores
-        wait(&bars.full[s % S::kStages], s / S::kStages);
+      auto begin = [&](int l0, int l1, const Place& k, int tiles) {  // an item's first scores
+        wait(&bars.full[k.stage], k.phase);
         for (int t = l0; t <= l1 && ok; ++t) {
           wait(&bars.q_full[t], q_n[t]++);
           if (!ok) break;
           tc::fence_after_sync();
-          scores(t, s);
+          scores(t, k, tiles == 1);
         }
-        if (ok) tc::mma_commit(&bars.empty[s % S::kStages]);
+        if (ok) tc::mma_commit(&bars.empty[k.stage]);
       };
       auto next = [&](int& r, int& n) {  // the next item's rows and tiles; false after the last
         const uint32_t slot = n_item % kItemSlots;
@@ -485,37 +555,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       int l0 = 0, l1 = 0;
+      Place key{0, 0};  // the current tile's keys; its values follow
       bool more = next(rows, tiles);
       if (more) {
         lanes(rows, l0, l1);
-        begin(l0, l1, seq);
+        begin(l0, l1, key, tiles);
       }
       while (more && ok) {
         bool more_next = false, early = false;
         int n0 = 0, n1 = 0;
-        for (int i = 0; i < tiles && ok; ++i, seq += 2) {
+        for (int i = 0; i < tiles && ok; ++i) {
           const bool last = i + 1 == tiles;
+          const Place val = key.next(), then = val.next();
           if (last) {
             more_next = next(n_rows, n_tiles);
             if (more_next) {
               lanes(n_rows, n0, n1);
-              early = l0 == l1 && n0 == n1 && n0 != l0;
-              if (early) begin(n0, n1, seq + 2);
+              // ahead of the current item's last values, if all is there: the other
+              // warpgroup may still be busy with the item before
+              early = l0 == l1 && n0 == n1 && n0 != l0 && tc::mbar_try_wait(&bars.q_full[n0], q_n[n0] & 1u) &&
+                      tc::mbar_try_wait(&bars.full[then.stage], then.phase);
+              if (early) begin(n0, n1, then, n_tiles);
             }
           }
-          wait(&bars.full[(seq + 1) % S::kStages], (seq + 1) / S::kStages);
-          if (!last) wait(&bars.full[(seq + 2) % S::kStages], (seq + 2) / S::kStages);
+          wait(&bars.full[val.stage], val.phase);
+          if (!last) wait(&bars.full[then.stage], then.phase);
           for (int t = l0; t <= l1 && ok; ++t) {
             wait(&bars.p_full[t], p_n[t]++);
             if (!ok) break;
             tc::fence_after_sync();
-            values(t, seq + 1, i == 0);
+            values(t, val, i == 0);
             if (last) tc::mma_commit(&bars.o_full[t]);
-            else scores(t, seq + 2);
+            else scores(t, then, i + 2 == tiles);
           }
           if (!ok) break;
-          tc::mma_commit(&bars.empty[(seq + 1) % S::kStages]);
-          if (!last) tc::mma_commit(&bars.empty[(seq + 2) % S::kStages]);
+          tc::mma_commit(&bars.empty[val.stage]);
+          if (!last) tc::mma_commit(&bars.empty[then.stage]);
+          key = then;
         }
         if (!ok) break;
         more = more_next;
@@ -523,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tiles = n_tiles;
         l0 = n0;
         l1 = n1;
-        if (more && !early) begin(l0, l1, seq);
+        if (more && !early) begin(l0, l1, key, tiles);
       }
       if (!ok) {  // the products in flight end before TMEM is freed
         tc::mma_commit(&bars.drain);
@@ -545,79 +621,140 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (it.rows == 0) break;
     }
+  } else if (warp == kLoader) {
+    // -------------------------------------------------------------- loader --
+    uint32_t n[2] = {0, 0};  // query tiles taken
+    int turn = 0;
+    bool ok = true;
+    for (uint32_t n_item = 0; ok; ++n_item) {
+      const Item& posted = items[n_item % kItemSlots];
+      ok = warp_wait(&bars.item_full[n_item % kItemSlots], n_item / kItemSlots);
+      if (!ok || posted.rows == 0) break;
+      const int row0 = posted.row0, m0 = posted.m0, rows = posted.rows, h = posted.h;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars.item_empty[n_item % kItemSlots]);
+      const bool both = rows > kTile;
+      const int t0 = both ? 0 : turn, t1 = both ? 1 : turn;
+      if (!both) turn ^= 1;
+      for (int t = t0; ok && t <= t1; ++t) {
+        ok = warp_wait(&bars.q_empty[t], n[t] ^ 1u);
+        if (!ok) break;
+        ++n[t];
+        // rows past the item's keep what was there: their results are not read
+        const int first = both ? t * kTile : 0, live = min(kTile, rows - first);
+        if (q_box > 0) {  // boxes of q_box query rows: whole packed rows of one key head
+          const int boxes = (live + q_box - 1) / q_box;
+          if (lane == 0) tc::mbar_expect_tx(&bars.q_full[t], (uint32_t)(boxes * q_box * D * 2));
+          __syncwarp();
+          const int half = lane % kHalves, x = lane / kHalves;
+          if (x < boxes)
+            tc::tma_load_3d(smem + t * S::kTileBytes + half * kHalfBytes + x * q_box * 128, &q_map,
+                            &bars.q_full[t], half * 64, h * per_head, row0 + (m0 + first + x * q_box) / per_head);
+          continue;
+        }
+        const uint32_t to = tc::smem_u32(smem) + t * S::kTileBytes;
+        constexpr int kChunks = D / 8;  // 16-byte pieces of a row
+        const int c = lane % kChunks;
+        for (int r = lane / kChunks; r < live; r += 32 / kChunks) {
+          const int qrow = m0 + first + r, j = qrow / per_head;
+          const __nv_bfloat16* q = (const __nv_bfloat16*)a.q + (size_t)(row0 + j) * a.q_row +
+                                   (size_t)(h * per_head + (qrow - j * per_head)) * a.q_head + c * 8;
+          copy16(to + r * 128 + (c >> 3) * kHalfBytes + (((c & 7) ^ (r & 7)) << 4), q);
+        }
+      }
+      if (q_box > 0) continue;
+      copies_wait();
+      tc::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0 && ok)
+        for (int t = t0; t <= t1; ++t) tc::mbar_arrive(&bars.q_full[t]);
+    }
+    if (abort_flag && q_box > 0)
+      for (int t = 0; t < 2; ++t)
+        if (n[t] > 0) tc::mbar_wait(&bars.q_full[t], (n[t] - 1u) & 1u, kWaitNs);
   } else if (warp < 8) {
     // ------------------------------------------------------------- softmax --
-    regs_grow<kRegsSoftmax>();
     const int t = warp >> 2, tid_g = tid & 127;
     const uint32_t lane_base = (uint32_t)(warp & 3) << 21;  // 32 TMEM lanes a warp, lanes in the high half
     const uint32_t s_addr = tmem + lane_base + t * kTile, o_addr = tmem + lane_base + 2 * kTile + t * kTile;
     const float sl = a.scale * kLog2e;
-    uint32_t seq = 0, s_n = 0, o_n = 0;
+    const bool wide_out = ((uintptr_t)a.out & 15) == 0 && a.out_row % 8 == 0 && a.out_head % 8 == 0;
+    uint32_t seq = 0, n_item = 0, s_n = 0, o_n = 0;  // ring position, items seen, scores and results waited for
     int turn = 0;
     bool ok = true;
-    for (uint32_t n_item = 0;; ++n_item) {
-      const Item& posted = items[n_item % kItemSlots];
-      ok = warp_wait(&bars.item_full[n_item % kItemSlots], n_item / kItemSlots);
-      if (!ok || posted.rows == 0) break;
-      const Item it = posted;
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bars.item_empty[n_item % kItemSlots]);
+    // This warpgroup's next item and its ring position.
+    auto next = [&](Item& it, uint32_t& seq0) {
+      while (true) {
+        const Item& posted = items[n_item % kItemSlots];
+        ok = warp_wait(&bars.item_full[n_item % kItemSlots], n_item / kItemSlots);
+        if (!ok || posted.rows == 0) return false;
+        it = posted;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars.item_empty[n_item % kItemSlots]);
+        ++n_item;
+        const bool both = it.rows > kTile;
+        const int mine = both ? t : turn;
+        if (!both) turn ^= 1;
+        seq0 = seq;
+        seq += 2u * (uint32_t)(it.hi - it.lo);
+        if (mine == t) break;
+      }
+      return true;
+    };
+    Item it;
+    uint32_t seq0 = 0;
+    bool more = next(it, seq0);
+    while (more) {
       const bool both = it.rows > kTile;
-      const int mine = both ? t : turn;
-      if (!both) turn ^= 1;
-      const uint32_t seq0 = seq;
-      seq += 2u * (uint32_t)(it.hi - it.lo);
-      if (mine != t) continue;
       const int m = (both ? t * kTile : 0) + tid_g;
       const bool valid = m < it.rows;
       const int qrow = it.m0 + m, j = qrow / per_head;
-      // the query row into its swizzled place
-      {
-        const __nv_bfloat16* q = (const __nv_bfloat16*)a.q + (size_t)(it.row0 + j) * a.q_row +
-                                 (size_t)(it.h * per_head + (qrow - j * per_head)) * a.q_head;
-        uint8_t* to = smem + t * S::kTileBytes + tid_g * 128;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (valid) x = *reinterpret_cast<const uint4*>(q + c * 8);
-          *reinterpret_cast<uint4*>(to + (c >> 3) * kHalfBytes + (((c & 7) ^ (tid_g & 7)) << 4)) = x;
-        }
-        tc::fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bars.q_full[t]);
-      }
       const int limit = it.prefix ? it.keys : min(it.keys, it.first_own + j);  // keys of this row
       float ref = -CUDART_INF_F, l = 0.f;
       for (int i = it.lo; i < it.hi; ++i) {
         ok = warp_wait(&bars.s_full[t], s_n++);
         if (!ok) break;
         tc::fence_after_sync();
-        uint32_t s[kTile];
-#pragma unroll
-        for (int c = 0; c < kTile; c += 32) tmem_ld32(s_addr + c, s + c);
-        tc::tmem_ld_wait();
+        // Scores are read twice: a row's maximum, then its weights, in loops of few
+        // instructions.  Held in registers in between, or in one pass against the old
+        // reference, they cost straight-line code that the instruction cache does not
+        // feed to two warps a scheduler: both were slower, on long items too.
         const int lim = limit - i * kTile;
-        if (__any_sync(0xffffffffu, lim < kTile)) {
-#pragma unroll
-          for (int c = 0; c < kTile; ++c)
-            if (c >= lim) s[c] = 0xff800000u;  // -inf
-        }
+        const bool cut = __any_sync(0xffffffffu, lim < kTile);
         float m0 = -CUDART_INF_F, m1 = m0, m2 = m0, m3 = m0;
+#pragma unroll 1
+        for (int c = 0; c < kTile; c += 64) {
+          uint32_t s[64];
+          tmem_ld32(s_addr + c, s);
+          tmem_ld32(s_addr + c + 32, s + 32);
+          tc::tmem_ld_wait();
+          if (cut) {  // -inf past the row's keys, in place
 #pragma unroll
-        for (int c = 0; c < kTile; c += 8) {
-          m0 = max3(m0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-          m1 = max3(m1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-          m2 = max3(m2, __uint_as_float(s[c + 4]), __uint_as_float(s[c + 5]));
-          m3 = max3(m3, __uint_as_float(s[c + 6]), __uint_as_float(s[c + 7]));
+            for (int e = 0; e < 64; ++e)
+              if (c + e >= lim) s[e] = 0xff800000u;
+            tmem_st32(s_addr + c, s);
+            tmem_st32(s_addr + c + 32, s + 32);
+          }
+#pragma unroll
+          for (int e = 0; e < 64; e += 8) {
+            m0 = max3(m0, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+            m1 = max3(m1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+            m2 = max3(m2, __uint_as_float(s[e + 4]), __uint_as_float(s[e + 5]));
+            m3 = max3(m3, __uint_as_float(s[e + 6]), __uint_as_float(s[e + 7]));
+          }
         }
+        if (cut) tmem_st_wait();
+        uint32_t s[2][32];
+        tmem_ld32(s_addr, s[0]);
         const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sl;
         if (__any_sync(0xffffffffu, top > ref + kSlack)) {
-          const float to = fmaxf(ref, top);
-          const float c = ref == -CUDART_INF_F ? 0.f : tc::ex2(ref - to);
+          // each row by its own scores alone: its bits do not depend on its neighbours
+          const float to = top > ref + kSlack ? top : ref;
+          const float c = to == ref ? 1.f : tc::ex2(ref - to);  // 0 from -inf
           ref = to;
           l *= c;
           if (i > it.lo) {
-#pragma unroll
+#pragma unroll 1
             for (int d = 0; d < D; d += 32) {
               uint32_t o[32];
               tmem_ld32(o_addr + d, o);
@@ -631,20 +768,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sub = ref == -CUDART_INF_F ? 0.f : ref;
         const uint64_t sl2 = pair(sl, sl), sub2 = pair(-sub, -sub);
         uint64_t a0 = 0, a1 = 0;
+        // the weights of 32 scores take 16 columns: behind the reads
+        auto weights = [&](const uint32_t* x, int c) {
+          uint32_t p[16];
 #pragma unroll
-        for (int c = 0; c < kTile; c += 64) {
-          uint32_t p[32];
-#pragma unroll
-          for (int e = 0; e < 64; e += 4) {
-            const float2 z0 = halves(fma2(pair(s[c + e], s[c + e + 1]), sl2, sub2));
-            const float2 z1 = halves(fma2(pair(s[c + e + 2], s[c + e + 3]), sl2, sub2));
+          for (int e = 0; e < 32; e += 4) {
+            const float2 z0 = halves(fma2(pair(x[e], x[e + 1]), sl2, sub2));
+            const float2 z1 = halves(fma2(pair(x[e + 2], x[e + 3]), sl2, sub2));
             const float p0 = tc::ex2(z0.x), p1 = tc::ex2(z0.y), p2 = tc::ex2(z1.x), p3 = tc::ex2(z1.y);
             a0 = add2(a0, pair(p0, p1));
             a1 = add2(a1, pair(p2, p3));
             p[e / 2] = pack_bf16(p0, p1);
             p[e / 2 + 1] = pack_bf16(p2, p3);
           }
-          tmem_st32(s_addr + c / 2, p);
+          tmem_st16(s_addr + c / 2, p);
+        };
+#pragma unroll 1
+        for (int c = 0; c < kTile; c += 64) {
+          tc::tmem_ld_wait();
+          tmem_ld32(s_addr + c + 32, s[1]);
+          weights(s[0], c);
+          tc::tmem_ld_wait();
+          if (c == 0) tmem_ld32(s_addr + 64, s[0]);
+          weights(s[1], c + 32);
         }
         const float2 sum = halves(add2(a0, a1));
         l += sum.x + sum.y;
@@ -669,25 +815,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) tc::mbar_arrive(&bars.p_full[t]);
       }
       if (!ok) break;
+      const size_t slot = it.slot + m;
+      const bool direct = it.direct;
+      const int row = it.row0 + j, hq = it.h * per_head + (qrow - j * per_head);
       ok = warp_wait(&bars.o_full[t], o_n++);
       if (!ok) break;
       tc::fence_after_sync();
-      const size_t slot = it.slot + m;
-#pragma unroll
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // a row without keys: zeros
+#pragma unroll 1
       for (int d = 0; d < D; d += 32) {
         uint32_t o[32];
         tmem_ld32(o_addr + d, o);
         tc::tmem_ld_wait();
-        if (valid) {
+        if (!valid) continue;
+        if (!direct) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<uint4*>(part + slot * D + d + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          for (int e = 0; e < 32; e += 8) store32(part + slot * D + d + e, o + e);
+          continue;
+        }
+        uint32_t p[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          p[e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+        __nv_bfloat16* out = (__nv_bfloat16*)a.out + (size_t)row * a.out_row + (size_t)hq * a.out_head + d;
+        if (wide_out) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<uint4*>(out + 2 * e) = make_uint4(p[e], p[e + 1], p[e + 2], p[e + 3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) *reinterpret_cast<uint32_t*>(out + 2 * e) = p[e];
         }
       }
       tc::fence_before_sync();
-      if (valid) stat[slot] = make_float2(ref, l);
+      if (valid) {
+        if (!direct) stat[slot] = make_float2(ref, l);
+        else if (a.lse) a.lse[(size_t)row * a.Hq + hq] = l == 0.f ? -CUDART_INF_F : (ref + log2f(l)) * kLn2;
+      }
+      more = next(it, seq0);
     }
   }
+  tc::grid_dep_launch();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -696,98 +864,121 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ----------------------------------------------------------------- join ----
 constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 32;  // query rows (packed rows x heads of a key head) of a block at a time
 
-// Joins the pieces of every row: a block a packed row, a warp a query head.
+// Cost of a head's items before item `upto`, and of all of them; a warp adds them up.
+__device__ __forceinline__ void costs_of(const Segment& s, int per_head, int upto, int64_t* before, int64_t* all) {
+  const int n = item_count(s, per_head), lane = threadIdx.x & 31;
+  int64_t x = 0, y = 0;
+  for (int i = lane; i < n; i += 32) {
+    const int64_t c = item_cost(item_keys(s, i, per_head), s.n * per_head - i * kItemRows);
+    y += c;
+    if (i < upto) x += c;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    x += __shfl_xor_sync(0xffffffffu, x, o);
+    y += __shfl_xor_sync(0xffffffffu, y, o);
+  }
+  *before = x;
+  *all = y;
+}
+
+// Joins the pieces of every row that has more than one.  A block takes rows of one
+// request and key head, which share nearly all of what says where their pieces
+// are: that chain of dependent loads is paid once for up to 32 rows.  A warp a row.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads)
     join_tc_kernel(const spec_prefix_attention_args a, const float* part, const float2* stat, const int64_t* plan) {
-  constexpr int kPer = D / 32;
-  const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per_head = a.Hq / a.Hk;
+  constexpr int kPer = D / 32, kBatch = 4;
+  const int r = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, per_head = a.Hq / a.Hk;
   uint32_t bad = 0;
-  const int r = last_at_or_below(a.row_off, a.R, b);
-  const Rows rows = rows_between(a, r, r + 1, &bad);
-  if (b < rows.row0 || b >= rows.row0 + rows.n) return;
-  const int64_t per = plan[0];
-  int g = -1;
-  Segment pre{0, 0, 0, 0, nullptr, true};
-  if (a.G > 0) {
-    const int c = last_at_or_below(a.group_off, a.G, r);
-    const int2 in = group_requests(a, c, &bad);
-    if (r >= in.x && r < in.y) {
-      g = c;
-      pre = segment(a, c, &bad);
-    }
-  }
   const Segment own = segment(a, a.G + r, &bad);
-  const int64_t pre_at = g >= 0 ? plan[1 + g] : 0, own_at = plan[1 + a.G + r];
-  const int64_t own_head = head_cost(own, per_head), pre_head = head_cost(pre, per_head);
+  int g = group_of(a, r, &bad);
+  Segment pre{0, 0, 0, 0, nullptr, true};
+  if (g >= 0) pre = segment(a, g, &bad);
+  if (own.row0 < pre.row0 || own.row0 + own.n > pre.row0 + pre.n) g = -1;  // rows out of order
+  const int m_own = own.n * per_head;
+  const int m_off = (own.row0 - pre.row0) * per_head;  // the request's first row among the group's
+  tc::grid_dep_wait();  // all of the above is the caller's; the pieces and their layout are ready now
+  const int64_t per = plan[0];
+  const int64_t own_at = plan[1 + a.G + r], pre_at = g >= 0 ? plan[1 + g] : 0;
 
-  for (int hq = warp; hq < a.Hq; hq += kJoinThreads / 32) {
-    const int h = hq / per_head, in_head = hq - h * per_head;
-    int first[2] = {0, 0}, count[2] = {0, 0};  // blocks that have a piece of this row
-    size_t slot[2] = {0, 0};                   // its partial row, without the block's offset
-    auto find = [&](int w, const Segment& s, int64_t at, int64_t per_h, size_t region) {
-      const int m = (b - s.row0) * per_head + in_head, i = m / kItemRows;
-      const int keys = item_keys(s, i, per_head), tiles = (keys + kTile - 1) / kTile;
-      if (tiles == 0) return;
-      at += h * per_h;
-      if (s.prefix) at += i * item_cost(keys, true);
-      else
-        for (int x = 0; x < i; ++x) at += item_cost(item_keys(s, x, per_head), false);
-      at += kCostItem;
-      first[w] = (int)(at / per);
-      count[w] = (int)((at + (int64_t)(tiles - 1) * (s.prefix ? kCostPrefix : kCostOwn)) / per) - first[w] + 1;
-      slot[w] = region + (size_t)s.row0 * a.Hq + (size_t)h * ((size_t)s.n * per_head) + m;
-    };
-    if (g >= 0) find(0, pre, pre_at, pre_head, 0);
-    find(1, own, own_at, own_head, (size_t)a.rows * a.Hq);
-    const int n = count[0] + count[1];
-    auto place = [&](int p) {
-      return p < count[0] ? slot[0] + (size_t)kItemRows * (first[0] + p)
-                          : slot[1] + (size_t)kItemRows * (first[1] + p - count[0]);
-    };
-    float top = -CUDART_INF_F, sum = 0.f, o[kPer];
+  int item[2] = {-1, -1};  // own and prefix item whose pieces are known
+  int first[2] = {0, 0}, count[2] = {0, 0};
+  auto pieces = [&](int w, const Segment& s, int64_t at, int i) {  // blocks that have pieces of item i
+    if (i == item[w]) return;
+    item[w] = i;
+    const int tiles = (item_keys(s, i, per_head) + kTile - 1) / kTile;
+    count[w] = 0;
+    if (tiles == 0) return;
+    int64_t before, all;
+    costs_of(s, per_head, i, &before, &all);
+    const int rows = s.n * per_head - i * kItemRows;
+    at += h * all + before + start_cost(rows);
+    first[w] = (int)(at / per);
+    count[w] = (int)((at + (int64_t)(tiles - 1) * tile_cost(rows)) / per) - first[w] + 1;
+  };
+  const size_t own_slot = (size_t)a.rows * a.Hq + (size_t)own.row0 * a.Hq + (size_t)h * m_own;
+  const size_t pre_slot = (size_t)pre.row0 * a.Hq + (size_t)h * pre.n * per_head + m_off;
+
+  for (int m0 = blockIdx.z * kJoinRows; m0 < m_own; m0 += gridDim.z * kJoinRows) {
+    for (int m = m0 + (threadIdx.x >> 5); m < min(m0 + kJoinRows, m_own); m += kJoinThreads / 32) {
+      pieces(0, own, own_at, m / kItemRows);
+      if (g >= 0) pieces(1, pre, pre_at, (m_off + m) / kItemRows);
+      const int n = count[0] + count[1];
+      if (count[1] == 0 && n == 1) continue;  // written by its block
+      auto place = [&](int p) {
+        return p < count[0] ? own_slot + m + (size_t)kItemRows * (first[0] + p)
+                            : pre_slot + m + (size_t)kItemRows * (first[1] + p - count[0]);
+      };
+      float top = -CUDART_INF_F, sum = 0.f, o[kPer];
 #pragma unroll
-    for (int d = 0; d < kPer; ++d) o[d] = 0.f;
-    for (int p0 = 0; p0 < n; p0 += 32) {
-      float2 st = make_float2(-CUDART_INF_F, 0.f);
-      if (p0 + lane < n) st = stat[place(p0 + lane)];
-      float m = st.x;
+      for (int d = 0; d < kPer; ++d) o[d] = 0.f;
+      for (int p0 = 0; p0 < n; p0 += kBatch) {
+        float2 st[kBatch];
+        float v[kBatch][kPer];
 #pragma unroll
-      for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-      m = fmaxf(m, top);
-      const float c = top == -CUDART_INF_F ? 0.f : tc::ex2(top - m);
-      const float w = st.x == -CUDART_INF_F ? 0.f : tc::ex2(st.x - m);
-      float l = st.y * w;
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-      sum = sum * c + l;
-#pragma unroll
-      for (int d = 0; d < kPer; ++d) o[d] *= c;
-      const int np = min(32, n - p0);
-#pragma unroll 4
-      for (int p = 0; p < np; ++p) {
-        const float wp = __shfl_sync(0xffffffffu, w, p);
-        const float* src = part + place(p0 + p) * D + lane * kPer;
-        float v[kPer];
-        if constexpr (kPer == 4) {
-          const float4 x = *reinterpret_cast<const float4*>(src);
-          v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-        } else {
-          const float2 x = *reinterpret_cast<const float2*>(src);
-          v[0] = x.x, v[1] = x.y;
+        for (int p = 0; p < kBatch; ++p) {
+          st[p] = make_float2(-CUDART_INF_F, 0.f);
+          if (p0 + p < n) {
+            const size_t at = place(p0 + p);
+            st[p] = stat[at];
+            const float* src = part + at * D + lane * kPer;
+            if constexpr (kPer == 4) {
+              const float4 x = *reinterpret_cast<const float4*>(src);
+              v[p][0] = x.x, v[p][1] = x.y, v[p][2] = x.z, v[p][3] = x.w;
+            } else {
+              const float2 x = *reinterpret_cast<const float2*>(src);
+              v[p][0] = x.x, v[p][1] = x.y;
+            }
+          }
         }
+        float m_new = top;
 #pragma unroll
-        for (int d = 0; d < kPer; ++d) o[d] = fmaf(v[d], wp, o[d]);
+        for (int p = 0; p < kBatch; ++p) m_new = fmaxf(m_new, st[p].x);
+        const float c = top == -CUDART_INF_F ? 0.f : tc::ex2(top - m_new);
+        sum *= c;
+#pragma unroll
+        for (int d = 0; d < kPer; ++d) o[d] *= c;
+#pragma unroll
+        for (int p = 0; p < kBatch; ++p) {
+          if (p0 + p >= n) break;
+          const float w = st[p].x == -CUDART_INF_F ? 0.f : tc::ex2(st[p].x - m_new);
+          sum = fmaf(st[p].y, w, sum);
+#pragma unroll
+          for (int d = 0; d < kPer; ++d) o[d] = fmaf(v[p][d], w, o[d]);
+        }
+        top = m_new;
       }
-      top = m;
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row without keys: zeros
-    __nv_bfloat16* out = (__nv_bfloat16*)a.out + (size_t)b * a.out_row + (size_t)hq * a.out_head + lane * kPer;
+      const int b = own.row0 + m / per_head, hq = h * per_head + m % per_head;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row without keys: zeros
+      __nv_bfloat16* out = (__nv_bfloat16*)a.out + (size_t)b * a.out_row + (size_t)hq * a.out_head + lane * kPer;
 #pragma unroll
-    for (int d = 0; d < kPer; d += 2) *reinterpret_cast<uint32_t*>(out + d) = pack_bf16(o[d] * inv, o[d + 1] * inv);
-    if (a.lse && lane == 0)
-      a.lse[(size_t)b * a.Hq + hq] = sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * kLn2;
+      for (int d = 0; d < kPer; d += 2) *reinterpret_cast<uint32_t*>(out + d) = pack_bf16(o[d] * inv, o[d + 1] * inv);
+      if (a.lse && lane == 0)
+        a.lse[(size_t)b * a.Hq + hq] = sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * kLn2;
+    }
   }
 }
 
@@ -800,13 +991,36 @@ cudaError_t launch(const spec_prefix_attention_args& a, int sms, float* part, fl
   if (!fused::encode_tiled(&km, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.k_cache, 3, dims, box) ||
       !fused::encode_tiled(&vm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.v_cache, 3, dims, box))
     return cudaErrorInvalidValue;
+  // query boxes of 32 rows (a small item loads few), or of one packed row's heads
+  const int per_head = a.Hq / a.Hk;
+  int q_box = per_head > 32 ? per_head : 32;
+  CUtensorMap qm = km;
+  {
+    const uint64_t qdims[3] = {(uint64_t)D, (uint64_t)a.Hq, (uint64_t)a.rows};
+    const uint64_t qstrides[2] = {(uint64_t)a.q_head * 2, (uint64_t)a.q_row * 2};
+    const uint32_t qbox[3] = {64, (uint32_t)per_head, (uint32_t)(q_box / per_head)};
+    if (kTile % per_head != 0 || q_box % per_head != 0 || a.q_head < D || a.q_row < D ||
+        !fused::encode_tiled_strided(&qm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 3, qdims, qstrides, qbox))
+      q_box = 0;
+  }
   cudaError_t err = cudaFuncSetAttribute(attention_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Smem<D>::kBytes);
   if (err != cudaSuccess) return err;
-  attention_tc_kernel<D><<<sms, kThreads, Smem<D>::kBytes, stream>>>(km, vm, a, part, stat, plan);
+  attention_tc_kernel<D><<<sms, kThreads, Smem<D>::kBytes, stream>>>(km, vm, qm, q_box, a, part, stat, plan);
   if ((err = cudaGetLastError()) != cudaSuccess) return err;
-  join_tc_kernel<D><<<a.rows, kJoinThreads, 0, stream>>>(a, part, stat, plan);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  // blocks for the mean request's rows; a longer one's loop
+  const int64_t blocks = ((int64_t)a.rows * (a.Hq / a.Hk) + (int64_t)kJoinRows * a.R - 1) / ((int64_t)kJoinRows * a.R);
+  cfg.gridDim = dim3(a.R, a.Hk, (unsigned)(blocks < 1024 ? blocks : 1024));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_tc_kernel<D>, a, (const float*)part, (const float2*)stat,
+                            (const int64_t*)plan);
 }
 
 }  // namespace

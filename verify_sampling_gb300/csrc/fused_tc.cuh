@@ -156,6 +156,9 @@ struct Ring {
 // 128-byte swizzle (dims innermost first; `es` bytes per element).
 bool encode_tiled(CUtensorMap* map, CUtensorMapDataType dt, size_t es, const void* base, int rank,
                   const uint64_t* dims, const uint32_t* box);
+// The same with the byte strides of the outer dimensions given.
+bool encode_tiled_strided(CUtensorMap* map, CUtensorMapDataType dt, const void* base, int rank,
+                          const uint64_t* dims, const uint64_t* strides, const uint32_t* box);
 
 }  // namespace fused
 }  // namespace spec
