@@ -22,11 +22,13 @@
 // Block: planner warp (walks the block's items and posts them in shared memory),
 // producer warp (TMA of key and value tiles, 64 x page boxes, into one ring), loader
 // warp (query rows: TMA where the heads of a key head divide a box, else 16-byte
-// copies into the swizzled places), MMA warp (S = Q K^T into TMEM, O += P V with P read from TMEM), and two
-// softmax warpgroups of 128 rows, one thread a row, so maxima and sums need no
-// shuffles.  An item of more than 128 rows uses both warpgroups on the same key
-// tile, one's softmax under the other's products; smaller items alternate
-// between them, and the next item's first product is issued before the
+// copies into the swizzled places), MMA warp (S = Q K^T into TMEM, O += P V with P
+// read from TMEM), and two softmax groups of 128 rows.  A row has two threads, each
+// half of its columns, that meet once a tile for the maximum: with one thread a row
+// the time from scores to weights (1870 clocks) was most of the 3860 of a tile, and
+// the tensor pipe waited for it.  An item of more than 128 rows uses both groups on
+// the same key tile, one's softmax under the other's products; smaller items
+// alternate between them, and the next item's first product is issued before the
 // current one's last weights are ready.
 //
 // Every wait is bounded; on a timeout the block sets SPEC_STATUS_TIMEOUT, waits
@@ -44,16 +46,18 @@ namespace {
 using namespace attn;
 
 constexpr int kTile = 128;  // keys of a tile, rows of a warpgroup
-constexpr int kThreads = 384;
-// Warps 0-3 and 4-7 are the softmax warpgroups.
-constexpr int kProducer = 8, kMma = 9, kPlanner = 10, kLoader = 11;
-constexpr int kItemSlots = 4, kItemReaders = 11;  // producer, MMA, loader, eight softmax warps
+// Softmax warps: warpgroup pair t (rows 128 t ..) is warps 8 t .. 8 t + 7; warps w and
+// w + 4 of it take the same 32 rows (TMEM lanes go by the warp's number mod 4), the
+// first the even half of the columns, the second the odd half.
+constexpr int kSoftWarps = 16, kProducer = 16, kMma = 17, kPlanner = 18, kLoader = 19;
+constexpr int kThreads = 640;
+constexpr int kItemSlots = 4, kItemReaders = 3 + kSoftWarps;  // producer, MMA, loader, softmax warps
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kSlack = 8.f;  // log2 units the maximum may grow by before O is rescaled
 // Costs, in units of 0.1 us, measured: a tile of an item of two warpgroups (bound
 // by the products), a tile of a smaller one (bound by its 64 KB), and an item's
 // start and end.
-constexpr int kCostPair = 22, kCostSingle = 15, kCostStartPair = 50, kCostStartSingle = 20;
+constexpr int kCostPair = 17, kCostSingle = 15, kCostStartPair = 57, kCostStartSingle = 21;
 
 // ------------------------------------------------------------ work layout --
 struct Segment {  // a group's prefix or a request's own keys
@@ -205,8 +209,10 @@ struct Walker {
 
 // ------------------------------------------------------------- tcgen05 -----
 // Descriptors of the 128-byte swizzle layout (8-row groups 1024 bytes apart) differ
-// in their low words alone, so the issuing thread adds constants to 32-bit words:
-// it is one thread, and what it computes between products the tensor pipe waits for.
+// in their low words alone.  The products are issued by one lane through a predicate,
+// not inside a branch: the warp's control flow and addresses stay uniform, so they
+// live in uniform registers, which the instruction takes.  Issued from a one-lane
+// branch, the moves into them held the tensor pipe to 54% of its rate.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride, version, swizzle
 // K-major operand at a shared address
 __device__ __forceinline__ uint32_t desc_k(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
@@ -214,24 +220,38 @@ __device__ __forceinline__ uint32_t desc_k(uint32_t saddr) { return ((saddr & 0x
 __device__ __forceinline__ uint32_t desc_mn(uint32_t saddr, uint32_t lead) {
   return ((saddr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
-                                       uint32_t accumulate) {
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                       uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n"
+      "{\n .reg .pred p, q;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %6, 0;\n"
       " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi), "r"(lead)
       : "memory");
 }
 // A from tensor memory.
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
-                                       uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                       uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.b32 p, %4, 0;\n"
+      "{\n .reg .pred p, q;\n .reg .b64 db;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %6, 0;\n"
       " mov.b64 db, {%2, %5};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi), "r"(lead)
       : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+          tc::smem_u32(bar)),
+      "r"(lead)
+      : "memory");
+}
+// 1 in one lane of the warp.
+__device__ __forceinline__ uint32_t elected() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r;
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
   asm volatile(
@@ -326,19 +346,28 @@ __device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t phase, volatile i
   return false;
 }
 
+// Everything shared beside the tiles.
+struct Shared {
+  uint64_t item_full[kItemSlots], item_empty[kItemSlots];
+  uint64_t full[10], empty[10];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t both[2][4];  // the two warps of 32 rows
+  Item items[kItemSlots];
+  Layout lay;
+  int64_t warp_sum[kThreads / 32];
+  uint32_t tmem;
+  volatile int abort_flag;
+  float row[2][2][kTile];  // what the two threads of a row tell each other
+};
+
 template <int D>
 struct Smem {
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kStages = D == 128 ? 5 : 10;
   static constexpr int kRing = 2 * kTileBytes;  // after the two query tiles
-  static constexpr int kBars = kRing + kStages * kTileBytes;
-  static constexpr int kBytes = kBars + 512 + 1024;  // barriers, and the base's alignment
-};
-
-struct Bars {
-  uint64_t item_full[kItemSlots], item_empty[kItemSlots];
-  uint64_t full[10], empty[10];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain;
+  static constexpr int kShared = kRing + kStages * kTileBytes;
+  static constexpr int kBytes = kShared + (int)sizeof(Shared);
+  static_assert(kBytes <= 227 * 1024, "shared memory of a block");
 };
 
 template <int D>
@@ -349,15 +378,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   using S = Smem<D>;
   constexpr int kHalves = D / 64;
   constexpr int kHalfBytes = kTile * 128;  // 64 elements of 128 keys
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
-  Bars& bars = *reinterpret_cast<Bars*>(smem + S::kBars);
-  __shared__ uint32_t tmem_slot;
-  __shared__ volatile int abort_flag;
-  __shared__ int64_t warp_sum[kThreads / 32];
-  __shared__ Layout lay;
-  __shared__ Item items[kItemSlots];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // The tiles' swizzle needs 1024 bytes' alignment.  All shared memory is this one
+  // array, so it starts where the block's window does.
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Shared& bars = *reinterpret_cast<Shared*>(smem + S::kShared);
+  Item* items = bars.items;
+  Layout& lay = bars.lay;
+  int64_t* warp_sum = bars.warp_sum;
+  volatile int& abort_flag = bars.abort_flag;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be uniform
   const int per_head = a.Hq / a.Hk;
 
   // ---- the work layout: every thread a run of segments, one scan
@@ -385,7 +415,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::mbar_init(&bars.q_full[i], 1);
         tc::mbar_init(&bars.q_empty[i], 1);
         tc::mbar_init(&bars.s_full[i], 1);
-        tc::mbar_init(&bars.p_full[i], 4);
+        tc::mbar_init(&bars.p_full[i], 8);
+        for (int w = 0; w < 4; ++w) tc::mbar_init(&bars.both[i][w], 2);
         tc::mbar_init(&bars.o_full[i], 1);
       }
       tc::mbar_init(&bars.drain, 1);
@@ -395,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc::fence_barrier_init();
     }
-    if (warp == kMma) tc::tmem_alloc(&tmem_slot, 512);
+    if (warp == kMma) tc::tmem_alloc(&bars.tmem, 512);
     if (warp == kProducer && lane == 0) {
       tc::tma_prefetch_desc(&k_map);
       tc::tma_prefetch_desc(&v_map);
@@ -427,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc::fence_after_sync();
   }
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem, 0);
   // A wait of a whole warp: all of its lanes go on, or all give up.
   auto warp_wait = [&](uint64_t* bar, uint32_t phase) {
     bool got = tc::mbar_try_wait(bar, phase & 1u);
@@ -486,7 +517,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMma) {
     // ------------------------------------------------------------ products --
-    if (lane == 0) {
+    {
+      const uint32_t lead = elected();
       int rows = 0, tiles = 0, n_rows = 0, n_tiles = 0;  // of the current and the next item
       uint32_t n_item = 0;
       uint32_t q_n[2] = {0, 0}, p_n[2] = {0, 0};
@@ -504,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       auto wait = [&](uint64_t* bar, uint32_t phase) {
-        if (ok && !tc::mbar_try_wait(bar, phase & 1u)) ok = slow_wait(bar, phase, &abort_flag, a.status);
+        if (ok) ok = warp_wait(bar, phase);
       };
       auto scores = [&](int t, const Place& k, bool last) {  // S_t = Q_t K^T
         const uint32_t kb = k_lo + k.stage * (S::kTileBytes >> 4), qb = q_lo + t * (S::kTileBytes >> 4);
@@ -512,16 +544,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < D / 16; ++c) {
           constexpr uint32_t kStep = 32 >> 4;
           const uint32_t off = (c >> 2) * (kHalfBytes >> 4) + (c & 3) * kStep;
-          mma_ss(tmem + t * kTile, qb + off, kb + off, kDescS, c > 0);
+          mma_ss(lead, tmem + t * kTile, qb + off, kb + off, kDescS, c > 0);
         }
-        tc::mma_commit(&bars.s_full[t]);
-        if (last) tc::mma_commit(&bars.q_empty[t]);
+        commit_if(lead, &bars.s_full[t]);
+        if (last) commit_if(lead, &bars.q_empty[t]);
       };
       auto values = [&](int t, const Place& v, bool first) {  // O_t (+)= P_t V
         const uint32_t vb = v_lo + v.stage * (S::kTileBytes >> 4);
 #pragma unroll
         for (int c = 0; c < kTile / 16; ++c)
-          mma_ts(tmem + 2 * kTile + t * kTile, tmem + t * kTile + c * 8, vb + c * (2048 >> 4), kDescO,
+          mma_ts(lead, tmem + 2 * kTile + t * kTile, tmem + t * kTile + c * 8, vb + c * (2048 >> 4), kDescO,
                  c > 0 || !first);
       };
       auto begin = [&](int l0, int l1, const Place& k, int tiles) {  // an item's first scores
@@ -532,17 +564,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::fence_after_sync();
           scores(t, k, tiles == 1);
         }
-        if (ok) tc::mma_commit(&bars.empty[k.stage]);
+        if (ok) commit_if(lead, &bars.empty[k.stage]);
       };
       auto next = [&](int& r, int& n) {  // the next item's rows and tiles; false after the last
         const uint32_t slot = n_item % kItemSlots;
         wait(&bars.item_full[slot], n_item / kItemSlots);
         ++n_item;
         if (!ok) return false;
-        r = items[slot].rows;
-        n = items[slot].hi - items[slot].lo;
+        // (from one lane, so that what follows is uniform)
+        r = __shfl_sync(0xffffffffu, items[slot].rows, 0);
+        n = __shfl_sync(0xffffffffu, items[slot].hi - items[slot].lo, 0);
         if (r == 0) return false;
-        tc::mbar_arrive(&bars.item_empty[slot]);
+        if (lane == 0) tc::mbar_arrive(&bars.item_empty[slot]);
         return true;
       };
       auto lanes = [&](int r, int& p, int& q) {  // the warpgroups of an item
@@ -573,8 +606,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               lanes(n_rows, n0, n1);
               // ahead of the current item's last values, if all is there: the other
               // warpgroup may still be busy with the item before
-              early = l0 == l1 && n0 == n1 && n0 != l0 && tc::mbar_try_wait(&bars.q_full[n0], q_n[n0] & 1u) &&
-                      tc::mbar_try_wait(&bars.full[then.stage], then.phase);
+              early = l0 == l1 && n0 == n1 && n0 != l0 &&
+                      __all_sync(0xffffffffu, tc::mbar_try_wait(&bars.q_full[n0], q_n[n0] & 1u) &&
+                                                  tc::mbar_try_wait(&bars.full[then.stage], then.phase));
               if (early) begin(n0, n1, then, n_tiles);
             }
           }
@@ -585,12 +619,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc::fence_after_sync();
             values(t, val, i == 0);
-            if (last) tc::mma_commit(&bars.o_full[t]);
+            if (last) commit_if(lead, &bars.o_full[t]);
             else scores(t, then, i + 2 == tiles);
           }
           if (!ok) break;
-          tc::mma_commit(&bars.empty[val.stage]);
-          if (!last) tc::mma_commit(&bars.empty[then.stage]);
+          commit_if(lead, &bars.empty[val.stage]);
+          if (!last) commit_if(lead, &bars.empty[then.stage]);
           key = then;
         }
         if (!ok) break;
@@ -602,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (more && !early) begin(l0, l1, key, tiles);
       }
       if (!ok) {  // the products in flight end before TMEM is freed
-        tc::mma_commit(&bars.drain);
+        commit_if(lead, &bars.drain);
         tc::mbar_wait(&bars.drain, 0, kWaitNs);
       }
     }
@@ -672,16 +706,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (abort_flag && q_box > 0)
       for (int t = 0; t < 2; ++t)
         if (n[t] > 0) tc::mbar_wait(&bars.q_full[t], (n[t] - 1u) & 1u, kWaitNs);
-  } else if (warp < 8) {
+  } else if (warp < kSoftWarps) {
     // ------------------------------------------------------------- softmax --
-    const int t = warp >> 2, tid_g = tid & 127;
-    const uint32_t lane_base = (uint32_t)(warp & 3) << 21;  // 32 TMEM lanes a warp, lanes in the high half
-    const uint32_t s_addr = tmem + lane_base + t * kTile, o_addr = tmem + lane_base + 2 * kTile + t * kTile;
+    constexpr int kCols = kTile / 2, kDims = D / 2;  // scores and result columns of a thread
+    const int t = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, in_t = quarter * 32 + lane;
+    const uint32_t lane_base = (uint32_t)quarter << 21;  // 32 TMEM lanes a warp, lanes in the high half
+    const uint32_t s_addr = tmem + lane_base + t * kTile + half * kCols;
+    const uint32_t p_addr = tmem + lane_base + t * kTile + half * (kCols / 2);
+    const uint32_t o_addr = tmem + lane_base + 2 * kTile + t * kTile + half * kDims;
     const float sl = a.scale * kLog2e;
     const bool wide_out = ((uintptr_t)a.out & 15) == 0 && a.out_row % 8 == 0 && a.out_head % 8 == 0;
-    uint32_t seq = 0, n_item = 0, s_n = 0, o_n = 0;  // ring position, items seen, scores and results waited for
+    uint32_t seq = 0, n_item = 0, s_n = 0, o_n = 0, b_n = 0;  // ring position, items seen, waits done
     int turn = 0;
     bool ok = true;
+    // The other thread of the row: gives `v`, gets its value.
+    auto swap = [&](float v) {
+      bars.row[t][half][in_t] = v;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars.both[t][quarter]);
+      ok = warp_wait(&bars.both[t][quarter], b_n++);
+      return bars.row[t][half ^ 1][in_t];
+    };
     // This warpgroup's next item and its ring position.
     auto next = [&](Item& it, uint32_t& seq0) {
       while (true) {
@@ -692,21 +737,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&bars.item_empty[n_item % kItemSlots]);
         ++n_item;
-        const bool both = it.rows > kTile;
-        const int mine = both ? t : turn;
-        if (!both) turn ^= 1;
+        const bool pair_item = it.rows > kTile;
+        const int mine = pair_item ? t : turn;
+        if (!pair_item) turn ^= 1;
         seq0 = seq;
         seq += 2u * (uint32_t)(it.hi - it.lo);
-        if (mine == t) break;
+        if (mine == t) return true;
       }
-      return true;
     };
     Item it;
     uint32_t seq0 = 0;
     bool more = next(it, seq0);
     while (more) {
-      const bool both = it.rows > kTile;
-      const int m = (both ? t * kTile : 0) + tid_g;
+      const bool pair_item = it.rows > kTile;
+      const int m = (pair_item ? t * kTile : 0) + in_t;
       const bool valid = m < it.rows;
       const int qrow = it.m0 + m, j = qrow / per_head;
       const int limit = it.prefix ? it.keys : min(it.keys, it.first_own + j);  // keys of this row
@@ -715,38 +759,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = warp_wait(&bars.s_full[t], s_n++);
         if (!ok) break;
         tc::fence_after_sync();
-        // Scores are read twice: a row's maximum, then its weights, in loops of few
-        // instructions.  Held in registers in between, or in one pass against the old
-        // reference, they cost straight-line code that the instruction cache does not
-        // feed to two warps a scheduler: both were slower, on long items too.
-        const int lim = limit - i * kTile;
-        const bool cut = __any_sync(0xffffffffu, lim < kTile);
-        float m0 = -CUDART_INF_F, m1 = m0, m2 = m0, m3 = m0;
-#pragma unroll 1
-        for (int c = 0; c < kTile; c += 64) {
-          uint32_t s[64];
-          tmem_ld32(s_addr + c, s);
-          tmem_ld32(s_addr + c + 32, s + 32);
-          tc::tmem_ld_wait();
-          if (cut) {  // -inf past the row's keys, in place
+        uint32_t s[kCols];
+        tmem_ld32(s_addr, s);
+        tmem_ld32(s_addr + 32, s + 32);
+        tc::tmem_ld_wait();
+        const int lim = limit - i * kTile - half * kCols;
+        if (__any_sync(0xffffffffu, lim < kCols)) {
 #pragma unroll
-            for (int e = 0; e < 64; ++e)
-              if (c + e >= lim) s[e] = 0xff800000u;
-            tmem_st32(s_addr + c, s);
-            tmem_st32(s_addr + c + 32, s + 32);
-          }
-#pragma unroll
-          for (int e = 0; e < 64; e += 8) {
-            m0 = max3(m0, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-            m1 = max3(m1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
-            m2 = max3(m2, __uint_as_float(s[e + 4]), __uint_as_float(s[e + 5]));
-            m3 = max3(m3, __uint_as_float(s[e + 6]), __uint_as_float(s[e + 7]));
-          }
+          for (int c = 0; c < kCols; ++c)
+            if (c >= lim) s[c] = 0xff800000u;  // -inf
         }
-        if (cut) tmem_st_wait();
-        uint32_t s[2][32];
-        tmem_ld32(s_addr, s[0]);
-        const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sl;
+        float m0 = -CUDART_INF_F, m1 = m0, m2 = m0, m3 = m0;
+#pragma unroll
+        for (int e = 0; e < kCols; e += 8) {
+          m0 = max3(m0, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+          m1 = max3(m1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+          m2 = max3(m2, __uint_as_float(s[e + 4]), __uint_as_float(s[e + 5]));
+          m3 = max3(m3, __uint_as_float(s[e + 6]), __uint_as_float(s[e + 7]));
+        }
+        float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sl;
+        top = fmaxf(top, swap(top));
+        if (!ok) break;
         if (__any_sync(0xffffffffu, top > ref + kSlack)) {
           // each row by its own scores alone: its bits do not depend on its neighbours
           const float to = top > ref + kSlack ? top : ref;
@@ -755,56 +788,45 @@ __global__ void __launch_bounds__(kThreads, 1)
           l *= c;
           if (i > it.lo) {
 #pragma unroll 1
-            for (int d = 0; d < D; d += 32) {
-              uint32_t o[32];
-              tmem_ld32(o_addr + d, o);
+            for (int d = 0; d < kDims; d += 16) {
+              uint32_t o[16];
+              tc::tmem_ld16(o_addr + d, o);
               tc::tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * c);
-              tmem_st32(o_addr + d, o);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * c);
+              tmem_st16(o_addr + d, o);
             }
           }
         }
         const float sub = ref == -CUDART_INF_F ? 0.f : ref;
         const uint64_t sl2 = pair(sl, sl), sub2 = pair(-sub, -sub);
         uint64_t a0 = 0, a1 = 0;
-        // the weights of 32 scores take 16 columns: behind the reads
-        auto weights = [&](const uint32_t* x, int c) {
-          uint32_t p[16];
+        uint32_t p[kCols / 2];
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float2 z0 = halves(fma2(pair(x[e], x[e + 1]), sl2, sub2));
-            const float2 z1 = halves(fma2(pair(x[e + 2], x[e + 3]), sl2, sub2));
-            const float p0 = tc::ex2(z0.x), p1 = tc::ex2(z0.y), p2 = tc::ex2(z1.x), p3 = tc::ex2(z1.y);
-            a0 = add2(a0, pair(p0, p1));
-            a1 = add2(a1, pair(p2, p3));
-            p[e / 2] = pack_bf16(p0, p1);
-            p[e / 2 + 1] = pack_bf16(p2, p3);
-          }
-          tmem_st16(s_addr + c / 2, p);
-        };
-#pragma unroll 1
-        for (int c = 0; c < kTile; c += 64) {
-          tc::tmem_ld_wait();
-          tmem_ld32(s_addr + c + 32, s[1]);
-          weights(s[0], c);
-          tc::tmem_ld_wait();
-          if (c == 0) tmem_ld32(s_addr + 64, s[0]);
-          weights(s[1], c + 32);
+        for (int e = 0; e < kCols; e += 4) {
+          const float2 z0 = halves(fma2(pair(s[e], s[e + 1]), sl2, sub2));
+          const float2 z1 = halves(fma2(pair(s[e + 2], s[e + 3]), sl2, sub2));
+          const float p0 = tc::ex2(z0.x), p1 = tc::ex2(z0.y), p2 = tc::ex2(z1.x), p3 = tc::ex2(z1.y);
+          a0 = add2(a0, pair(p0, p1));
+          a1 = add2(a1, pair(p2, p3));
+          p[e / 2] = pack_bf16(p0, p1);
+          p[e / 2 + 1] = pack_bf16(p2, p3);
         }
+        // over the scores, which both threads of every row have read by now
+        tmem_st32(p_addr, p);
         const float2 sum = halves(add2(a0, a1));
         l += sum.x + sum.y;
         // Values past the item's keys may be anything, NaN among them: zeros instead.
-        // (The first warpgroup of two does it, whose product is issued first.)
+        // (The first warpgroup pair of two does it, whose product is issued first.)
         const int live = it.keys - i * kTile;
-        if (live < kTile && (!both || t == 0)) {
+        if (live < kTile && (!pair_item || t == 0)) {
           const uint32_t sv = seq0 + 2u * (uint32_t)(i - it.lo) + 1u;
           ok = warp_wait(&bars.full[sv % S::kStages], sv / S::kStages);
           if (!ok) break;
-          if (tid_g >= live) {
-            uint8_t* to = smem + S::kRing + (sv % S::kStages) * S::kTileBytes + tid_g * 128;
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c)
+          if (in_t >= live) {
+            uint8_t* to = smem + S::kRing + (sv % S::kStages) * S::kTileBytes + in_t * 128;
+#pragma unroll 1
+            for (int c = half; c < D / 8; c += 2)
               *reinterpret_cast<uint4*>(to + (c >> 3) * kHalfBytes + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
           }
           tc::fence_proxy_async();
@@ -821,23 +843,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = warp_wait(&bars.o_full[t], o_n++);
       if (!ok) break;
       tc::fence_after_sync();
+      l += swap(l);
+      if (!ok) break;
       const float inv = l == 0.f ? 0.f : 1.f / l;  // a row without keys: zeros
 #pragma unroll 1
-      for (int d = 0; d < D; d += 32) {
+      for (int d = 0; d < kDims; d += 32) {
         uint32_t o[32];
         tmem_ld32(o_addr + d, o);
         tc::tmem_ld_wait();
         if (!valid) continue;
         if (!direct) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) store32(part + slot * D + d + e, o + e);
+          for (int e = 0; e < 32; e += 8) store32(part + slot * D + half * kDims + d + e, o + e);
           continue;
         }
         uint32_t p[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           p[e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-        __nv_bfloat16* out = (__nv_bfloat16*)a.out + (size_t)row * a.out_row + (size_t)hq * a.out_head + d;
+        __nv_bfloat16* out =
+            (__nv_bfloat16*)a.out + (size_t)row * a.out_row + (size_t)hq * a.out_head + half * kDims + d;
         if (wide_out) {
 #pragma unroll
           for (int e = 0; e < 16; e += 4)
@@ -848,10 +873,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc::fence_before_sync();
-      if (valid) {
+      if (valid && half == 0) {
         if (!direct) stat[slot] = make_float2(ref, l);
         else if (a.lse) a.lse[(size_t)row * a.Hq + hq] = l == 0.f ? -CUDART_INF_F : (ref + log2f(l)) * kLn2;
       }
+      // the partner has read this row's sum before the next item writes there
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars.both[t][quarter]);
+      ok = warp_wait(&bars.both[t][quarter], b_n++);
+      if (!ok) break;
       more = next(it, seq0);
     }
   }
