@@ -42,6 +42,13 @@ def test_every_field_sits_where_c_puts_it(tmp_path):
             assert int(got[f"{c}.{f[0]}"]) == getattr(cls, f[0]).offset, (c, f[0])
 
 
+def test_packed_bytes_are_the_struct():
+    for call in (target._RESERVE, target._COMMIT, target._ROPE, target._ATTENTION, target._LOGITS):
+        values = [i + 1.5 if k is ctypes.c_float else i + 1 for i, (_, k) in enumerate(call.cls._fields_)]
+        got = call.cls.from_buffer_copy(call.pack(*values))
+        assert [getattr(got, f[0]) for f in call.cls._fields_] == values, call.name
+
+
 def _filled(cls, **sizes):
     """Every pointer at an address of its own (never read: the calls under test are refused)."""
     a = cls()

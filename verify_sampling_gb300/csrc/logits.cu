@@ -8,12 +8,14 @@
 //   z <- z + bias[v],   z <- -inf where the row's mask bit is 0.
 //
 // Layout: a block takes a slice of the vocabulary of one request for all its
-// rows.  It reads the request's tokens once, counts those of its slice in shared
-// memory and lists each token that a rule names once.  The rows then stream
-// through as 16-byte vectors that only the mask can change; after that the listed
-// entries are computed from the inputs and written over, one thread each.  (With
-// the rules applied inside the stream a warp met a named entry in two of three
-// vectors and the round case below took 1390 us.)
+// rows.  Half of its warps read the request's tokens, count those of the slice in
+// shared memory and list each token that a rule names once; the others stream the
+// rows through as 16-byte vectors that only the mask can change, a warp at a time
+// taking the next piece, and the first half joins them when its tables stand.  Then
+// the listed entries are computed from the inputs and written over, one thread
+// each.  (With the rules applied inside the stream a warp met a named entry in two
+// of three vectors and the round case below took 1390 us; with the tables built
+// before the stream, 622 us.)
 // The history costs 4 bytes a token and slice from L2, where a table of counts
 // over the vocabulary would cost 4 bytes an entry and request from HBM, and has to
 // be kept up between rounds.  Rows share the counts: a row's drafted tokens are
@@ -31,6 +33,7 @@ constexpr int kThreads = 256;
 constexpr int kMaxSlice = 4096;  // 41 KB of tables: five blocks an SM
 constexpr int kMinSlice = 1024;
 constexpr int kUnroll = 4;
+constexpr int kBuilders = kThreads / 2;  // threads that build the tables
 constexpr int kMaxDraft = 64;
 constexpr uint32_t kPrompt = 0x80000000u;
 
@@ -86,7 +89,7 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(spec_logits_args p, in
   uint16_t* named = reinterpret_cast<uint16_t*>(smem + 2 * slice);
   uint32_t* seen = smem + 2 * slice + slice / 2;  // bitmap of the named tokens
   __shared__ int32_t draft_s[kMaxDraft];
-  __shared__ int n_named;
+  __shared__ int n_named, n_taken;
   const int tid = threadIdx.x, r = blockIdx.y;
   const int s0 = blockIdx.x * slice, s1 = min(s0 + slice, p.V);
   const bool counts = p.repetition || p.frequency || p.presence;
@@ -108,57 +111,61 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(spec_logits_args p, in
     uint4* clear = reinterpret_cast<uint4*>(smem);
     for (int i = tid; i < (2 * slice) / 4; i += kThreads) clear[i] = make_uint4(0, 0, 0, 0);
     for (int i = tid; i < slice / 32; i += kThreads) seen[i] = 0u;
-    if (tid == 0) n_named = 0;
+    if (tid == 0) n_named = n_taken = 0;
     __syncthreads();
     auto name = [&](int d) {
       const uint32_t bit = 1u << (d & 31);
       if (!(atomicOr(&seen[d >> 5], bit) & bit)) named[atomicAdd(&n_named, 1)] = (uint16_t)d;
     };
     auto inside = [&](int t) { return t >= s0 && t < s1; };
-    if (counts) {
-      const int32_t* tok = p.tokens + (size_t)r * p.tokens_ld;
-      int len = p.length[r];
-      if (len < 0 || len > p.tokens_cols) {
-        bad |= SPEC_STATUS_BAD_LEN;
-        len = min(max(len, 0), p.tokens_cols);
-      }
-      const int prompt = p.prompt_len ? p.prompt_len[r] : 0;
-      for (int i = tid; i < len; i += kThreads * kUnroll) {
-        int t[kUnroll];
+    if (tid < kBuilders) {
+      if (counts) {
+        const int32_t* tok = p.tokens + (size_t)r * p.tokens_ld;
+        int len = p.length[r];
+        if (len < 0 || len > p.tokens_cols) {
+          bad |= SPEC_STATUS_BAD_LEN;
+          len = min(max(len, 0), p.tokens_cols);
+        }
+        const int prompt = p.prompt_len ? p.prompt_len[r] : 0;
+        constexpr int kDeep = 8;
+        for (int i = tid; i < len; i += kBuilders * kDeep) {
+          int t[kDeep];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) t[k] = i + k * kThreads < len ? tok[i + k * kThreads] : -1;
+          for (int k = 0; k < kDeep; ++k) t[k] = i + k * kBuilders < len ? tok[i + k * kBuilders] : 0;
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-          const int at = i + k * kThreads;
-          if (at < len && (unsigned)t[k] >= (unsigned)p.V) bad |= SPEC_STATUS_BAD_TOKEN;
-          if (inside(t[k])) {
-            const int d = t[k] - s0;
-            if (at < prompt) atomicOr(&count[d], kPrompt);
-            else atomicAdd(&count[d], 1u);
-            name(d);
+          for (int k = 0; k < kDeep; ++k) {
+            const int at = i + k * kBuilders;
+            if (at >= len) break;
+            if ((unsigned)t[k] >= (unsigned)p.V) bad |= SPEC_STATUS_BAD_TOKEN;
+            if (inside(t[k])) {
+              const int d = t[k] - s0;
+              if (at < prompt) atomicOr(&count[d], kPrompt);
+              else atomicAdd(&count[d], 1u);
+              name(d);
+            }
           }
         }
+        for (int i = tid; i < n_draft; i += kBuilders) {
+          const int t = p.x[(size_t)r * p.x_ld + i];
+          draft_s[i] = t;
+          if ((unsigned)t >= (unsigned)p.V) bad |= SPEC_STATUS_BAD_TOKEN;
+          if (inside(t)) name(t - s0);
+        }
       }
-      for (int i = tid; i < n_draft; i += kThreads) {
-        const int t = p.x[(size_t)r * p.x_ld + i];
-        draft_s[i] = t;
-        if ((unsigned)t >= (unsigned)p.V) bad |= SPEC_STATUS_BAD_TOKEN;
-        if (inside(t)) name(t - s0);
-      }
-    }
-    if (p.bias_off) {
-      int b0 = p.bias_off[r], b1 = p.bias_off[r + 1];
-      if (b0 < 0 || b1 < b0 || b1 > p.n_bias) {
-        bad |= SPEC_STATUS_BAD_LEN;
-        b0 = min(max(b0, 0), p.n_bias);
-        b1 = min(max(b1, b0), p.n_bias);
-      }
-      for (int i = b0 + tid; i < b1; i += kThreads) {
-        const int t = p.bias_tok[i];
-        if ((unsigned)t >= (unsigned)p.V) bad |= SPEC_STATUS_BAD_TOKEN;
-        if (inside(t)) {
-          atomicMax(&bias[t - s0], i + 1);  // a token's last entry counts
-          name(t - s0);
+      if (p.bias_off) {
+        int b0 = p.bias_off[r], b1 = p.bias_off[r + 1];
+        if (b0 < 0 || b1 < b0 || b1 > p.n_bias) {
+          bad |= SPEC_STATUS_BAD_LEN;
+          b0 = min(max(b0, 0), p.n_bias);
+          b1 = min(max(b1, b0), p.n_bias);
+        }
+        for (int i = b0 + tid; i < b1; i += kBuilders) {
+          const int t = p.bias_tok[i];
+          if ((unsigned)t >= (unsigned)p.V) bad |= SPEC_STATUS_BAD_TOKEN;
+          if (inside(t)) {
+            atomicMax(&bias[t - s0], i + 1);  // a token's last entry counts
+            name(t - s0);
+          }
         }
       }
     }
@@ -171,48 +178,58 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(spec_logits_args p, in
       return m < 0 || m >= p.n_masks ? nullptr
                                      : reinterpret_cast<const uint32_t*>(p.mask) + (size_t)m * p.mask_ld;
     };
-    for (int j = j0; j < j1; ++j) {
+    using V = Vec<T, VEC>;
+    using R = decltype(V().raw);
+    // Pieces of 32 x kUnroll vectors.  Vectors lie on 16 bytes of memory: vector i
+    // of a row starts at entry i * VEC - lead, so a slice meets one more of them
+    // than it is long.  One that reaches past the slice is taken entry by entry, so
+    // that no entry is written by two blocks.
+    constexpr uint32_t kAll = (1u << VEC) - 1u;
+    const int pieces = (slice / VEC + 32 * kUnroll) / (32 * kUnroll);
+    while (!same || p.mask) {
+      int u = 0;
+      if ((tid & 31) == 0) u = atomicAdd(&n_taken, 1);
+      u = __shfl_sync(0xffffffffu, u, 0);
+      const int j = j0 + u / pieces;
+      if (j >= j1) break;
       const size_t b = (size_t)(row0 + j);
       const T* in = (const T*)p.logits + b * p.ld;
       T* out = (T*)p.out + b * p.out_ld;
-      const uint32_t* mask = mask_of(b);
-      if (!mask && same) continue;
-      // Vectors lie on 16 bytes of memory: vector i starts at entry i * VEC - lead.
-      // One that reaches past the slice is taken entry by entry, so that no entry
-      // is written by two blocks.
       const int lead = VEC == 1 ? 0 : (int)(((uintptr_t)in / sizeof(T)) & (VEC - 1));
-      const int i_begin = (s0 + lead) / VEC, i_end = (s1 + lead + VEC - 1) / VEC;
-      using V = Vec<T, VEC>;
-      using R = decltype(V().raw);
-      for (int i = i_begin + tid; i < i_end; i += kThreads * kUnroll) {
-        V x[kUnroll];
-        uint32_t al[kUnroll];
+      const int i0 = (s0 + lead) / VEC + (u % pieces) * 32 * kUnroll + (tid & 31);
+      const int i_end = (s1 + lead + VEC - 1) / VEC;
+      V x[kUnroll];
+      uint32_t al[kUnroll];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-          const int v = (i + k * kThreads) * VEC - lead;
-          al[k] = (1u << VEC) - 1u;
-          if (i + k * kThreads < i_end && v >= s0 && v + VEC <= s1) {
-            x[k].raw = *reinterpret_cast<const R*>(in + v);
-            if (mask) al[k] = bits_at(mask, v, VEC);
-          }
-        }
+      for (int k = 0; k < kUnroll; ++k) {
+        const int v = (i0 + k * 32) * VEC - lead;
+        if (v >= s0 && v + VEC <= s1) x[k].raw = *reinterpret_cast<const R*>(in + v);
+      }
+      const uint32_t* mask = mask_of(b);
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-          if (i + k * kThreads >= i_end) break;
-          const int v = (i + k * kThreads) * VEC - lead;
-          if (v >= s0 && v + VEC <= s1) {
+      for (int k = 0; k < kUnroll; ++k) {
+        const int v = (i0 + k * 32) * VEC - lead;
+        al[k] = kAll;
+        if (mask && v >= s0 && v + VEC <= s1) al[k] = bits_at(mask, v, VEC);
+      }
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        if (i0 + k * 32 >= i_end) break;
+        const int v = (i0 + k * 32) * VEC - lead;
+        if (v >= s0 && v + VEC <= s1) {
+          if (al[k] != kAll) {
 #pragma unroll
             for (int e = 0; e < VEC; ++e)
               if (!(al[k] >> e & 1u)) hide(x[k].e[e]);
-            if (!same || al[k] != (1u << VEC) - 1u) *reinterpret_cast<R*>(out + v) = x[k].raw;
-          } else {
-            for (int e = 0; e < VEC; ++e) {
-              const int w = v + e;
-              if (w < s0 || w >= s1) continue;
-              T z = in[w];
-              if (mask && !bits_at(mask, w, 1)) hide(z);
-              out[w] = z;
-            }
+          }
+          if (!same || al[k] != kAll) *reinterpret_cast<R*>(out + v) = x[k].raw;
+        } else {
+          for (int e = 0; e < VEC; ++e) {
+            const int w = v + e;
+            if (w < s0 || w >= s1) continue;
+            T z = in[w];
+            if (mask && !bits_at(mask, w, 1)) hide(z);
+            out[w] = z;
           }
         }
       }
@@ -222,21 +239,25 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(spec_logits_args p, in
     const float rep = p.repetition ? p.repetition[r] : 1.f, freq = p.frequency ? p.frequency[r] : 0.f,
                 pres = p.presence ? p.presence[r] : 0.f;
     const int listed = n_named;
-    for (int j = j0; j < j1; ++j) {
+    // a row's listed entries side by side; several rows where the list is short
+    const int wide = listed == 0 ? 0 : min(listed, kThreads), tall = wide == 0 ? 0 : kThreads / wide;
+    const int jt = wide == 0 ? 0 : tid / wide;
+    for (int j = j0 + jt; jt < tall && j < j1; j += tall) {
       const size_t b = (size_t)(row0 + j);
       const T* in = (const T*)p.logits + b * p.ld;
       T* out = (T*)p.out + b * p.out_ld;
       const uint32_t* mask = mask_of(b);
       const int upto = min(j, n_draft);
-      for (int i = tid; i < listed; i += kThreads) {
+      for (int i = tid - jt * wide; i < listed; i += wide) {
         const int d = named[i], v = s0 + d;
+        const float z0 = to_f(in[v]);
         if (mask && !bits_at(mask, v, 1)) continue;
         const uint32_t w = count[d];
         const int bi = bias[d];
         uint32_t c = w & ~kPrompt;
         for (int k = 0; k < upto; ++k) c += draft_s[k] == v;
         if (c == 0 && w == 0 && bi == 0) continue;  // drafted for a later row only
-        float z = to_f(in[v]);
+        float z = z0;
         if (c > 0 || w != 0) z = z > 0.f ? z / rep : z * rep;
         if (c > 0) z = z - freq * (float)c - pres;
         if (bi > 0) z += p.bias_val[bi - 1];

@@ -7,14 +7,14 @@ itself belong to the stream it runs on.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
+import struct
 from typing import Optional
 
 import torch
 
-from . import _check, _dev, _dtype_code, _P, lib
+from . import SPEC_BF16, SPEC_F32, _check, _dev, _dtype_code, _P, lib
 
 _I, _L, _F = ctypes.c_int, ctypes.c_int64, ctypes.c_float
 
@@ -60,40 +60,85 @@ class LogitsArgs(ctypes.Structure):
                 ("mask", _P), ("mask_ld", _L), ("mask_row", _P), ("n_masks", _I), ("status", _P)]
 
 
+class _Call:
+    """An entry point whose argument struct is packed straight into bytes: these calls run once a
+    layer, and filling a ctypes structure field by field took longer than the small kernels do."""
+
+    def __init__(self, name: str, cls):
+        self.name, self.cls, self.f = name, cls, None
+        codes = {_I: "i", _F: "f", _L: "q", _P: "Q", ctypes.c_size_t: "Q"}
+        fmt, at = "=", 0
+        for field, kind in cls._fields_:
+            gap = getattr(cls, field).offset - at
+            fmt += (f"{gap}x" if gap else "") + codes[kind]
+            at += gap + ctypes.sizeof(kind)
+        self.pack = struct.Struct(fmt + f"{ctypes.sizeof(cls) - at}x").pack
+
+    def bind(self, L: ctypes.CDLL) -> None:
+        f = getattr(L, self.name)
+        f.argtypes, f.restype = [ctypes.POINTER(self.cls), _P], ctypes.c_int
+        self.f = L[self.name]  # another handle of the same function
+        self.f.argtypes, self.f.restype = [ctypes.c_char_p, _P], ctypes.c_int
+
+    def __call__(self, stream: int, *values) -> None:
+        if self.f is None:
+            lib()
+        rc = self.f(self.pack(*values), stream)
+        if rc:
+            _check(rc, self.name)
+
+
+_RESERVE = _Call("spec_cache_reserve", CacheReserveArgs)
+_COMMIT = _Call("spec_cache_commit", CacheCommitArgs)
+_ROPE = _Call("spec_rope_cache", RopeCacheArgs)
+_ATTENTION = _Call("spec_prefix_attention", PrefixAttentionArgs)
+_LOGITS = _Call("spec_adjust_logits", LogitsArgs)
+
+
 def _bind(L: ctypes.CDLL) -> None:
     """Prototypes of this module's entry points (called once by ``lib``)."""
-    for name, cls in (("spec_cache_reserve", CacheReserveArgs),
-                      ("spec_cache_commit", CacheCommitArgs),
-                      ("spec_rope_cache", RopeCacheArgs),
-                      ("spec_prefix_attention", PrefixAttentionArgs),
-                      ("spec_adjust_logits", LogitsArgs)):
-        f = getattr(L, name)
-        f.argtypes, f.restype = [ctypes.POINTER(cls), _P], ctypes.c_int
+    for call in (_RESERVE, _COMMIT, _ROPE, _ATTENTION, _LOGITS):
+        call.bind(L)
     L.spec_attention_workspace_bytes.argtypes = [_I] * 4
     L.spec_attention_workspace_bytes.restype = ctypes.c_size_t
 
 
-def _t(t: torch.Tensor, name: str, dtype: torch.dtype, numel: int = -1) -> int:
+_i32, _i64, _f32, _f64 = torch.int32, torch.int64, torch.float32, torch.float64
+_codes = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16}
+
+
+def _t(t: torch.Tensor, name: str, dtype: torch.dtype, numel: int = 0) -> int:
     """Address of a contiguous device tensor of this dtype (and at least numel entries)."""
-    if _dev(t, name).dtype != dtype:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+        _dev(t, name)
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
     if t.numel() < numel:
         raise ValueError(f"{name} must have {numel} entries")
     return t.data_ptr()
 
 
-def _opt(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, numel: int = -1) -> Optional[int]:
-    return None if t is None else _t(t, name, dtype, numel)
+def _opt(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, numel: int = 0) -> int:
+    return 0 if t is None else _t(t, name, dtype, numel)
 
 
-def _on(stream) -> int:
-    """Handle of the stream to launch on."""
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def _code(t: torch.Tensor) -> int:
+    return _codes[t.dtype] if t.dtype in _codes else _dtype_code(t)
 
 
-def _made_on(stream):
-    """Context in which the call's own tensors are allocated: memory of the stream it runs on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _on(stream, t: torch.Tensor) -> int:
+    """Handle of the stream to launch on: the given one, or the current one of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _made(stream, make):
+    """The call's own tensors: memory of the stream it runs on."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        return make()
 
 
 # ------------------------------------------------------------- cache tables --
@@ -118,22 +163,18 @@ def cache_reserve(cache: dict, row_off: torch.Tensor, rows: int, *,
     table, ring = cache["block_table"], cache["ring"]
     R, width = table.shape
     if out is None:
-        dev = table.device
-        with _made_on(stream):
-            position, request, slot = torch.empty(3, rows, dtype=torch.int32, device=dev).unbind(0)
-            out = {"new_len": torch.empty(R, dtype=torch.int32, device=dev), "position": position,
-                   "request": request, "slot": slot,
-                   "ring_pos": torch.empty(2, dtype=torch.int64, device=dev)}
-    i32, i64 = torch.int32, torch.int64
-    a = CacheReserveArgs(
-        R, rows, cache["page_size"], ring.numel(), width, _t(cache["kv_len"], "kv_len", i32, R),
-        _t(row_off, "row_off", i32, R + 1), _opt(pos_base, "pos_base", i32, R),
-        _t(table, "block_table", i32), _t(ring, "ring", i32),
-        _t(cache["ring_pos"], "ring_pos", i64, 2), _t(out["ring_pos"], "out ring_pos", i64, 2),
-        _t(out["new_len"], "new_len", i32, R), _t(out["position"], "position", i32, rows),
-        _t(out["request"], "request", i32, rows), _t(out["slot"], "slot", i32, rows),
-        _opt(status, "status", i32, 1))
-    _check(lib().spec_cache_reserve(ctypes.byref(a), _on(stream)), "spec_cache_reserve")
+        def make():
+            new_len, position, request, slot = table.new_empty(R + 3 * rows).split((R, rows, rows, rows))
+            return {"new_len": new_len, "position": position, "request": request, "slot": slot,
+                    "ring_pos": cache["ring_pos"].new_empty(2)}
+        out = _made(stream, make)
+    _RESERVE(_on(stream, table), R, rows, cache["page_size"], ring.numel(), width,
+             _t(cache["kv_len"], "kv_len", _i32, R), _t(row_off, "row_off", _i32, R + 1),
+             _opt(pos_base, "pos_base", _i32, R), _t(table, "block_table", _i32), _t(ring, "ring", _i32),
+             _t(cache["ring_pos"], "ring_pos", _i64, 2), _t(out["ring_pos"], "out ring_pos", _i64, 2),
+             _t(out["new_len"], "new_len", _i32, R), _t(out["position"], "position", _i32, rows),
+             _t(out["request"], "request", _i32, rows), _t(out["slot"], "slot", _i32, rows),
+             _opt(status, "status", _i32, 1))
     return out
 
 
@@ -147,17 +188,13 @@ def cache_commit(cache: dict, reserved: dict, keep: torch.Tensor, *, out: Option
     table, ring = cache["block_table"], cache["ring"]
     R, width = table.shape
     if out is None:
-        with _made_on(stream):
-            out = {"kv_len": torch.empty(R, dtype=torch.int32, device=table.device),
-                   "ring_pos": torch.empty(2, dtype=torch.int64, device=table.device)}
-    i32, i64 = torch.int32, torch.int64
-    a = CacheCommitArgs(
-        R, cache["page_size"], ring.numel(), width, _t(cache["kv_len"], "kv_len", i32, R),
-        _t(reserved["new_len"], "new_len", i32, R), _t(keep, "keep", i32, R),
-        _t(table, "block_table", i32), _t(ring, "ring", i32),
-        _t(reserved["ring_pos"], "ring_pos", i64, 2), _t(out["ring_pos"], "out ring_pos", i64, 2),
-        _t(out["kv_len"], "out kv_len", i32, R), _opt(status, "status", i32, 1))
-    _check(lib().spec_cache_commit(ctypes.byref(a), _on(stream)), "spec_cache_commit")
+        out = _made(stream, lambda: {"kv_len": cache["kv_len"].new_empty(R),
+                                     "ring_pos": cache["ring_pos"].new_empty(2)})
+    _COMMIT(_on(stream, table), R, cache["page_size"], ring.numel(), width,
+            _t(cache["kv_len"], "kv_len", _i32, R), _t(reserved["new_len"], "new_len", _i32, R),
+            _t(keep, "keep", _i32, R), _t(table, "block_table", _i32), _t(ring, "ring", _i32),
+            _t(reserved["ring_pos"], "ring_pos", _i64, 2), _t(out["ring_pos"], "out ring_pos", _i64, 2),
+            _t(out["kv_len"], "out kv_len", _i32, R), _opt(status, "status", _i32, 1))
     return out
 
 
@@ -207,7 +244,7 @@ def _strided(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) -> tu
     """Address and the row and head strides of [rows, heads, D] whose last dimension is dense."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}")
@@ -226,29 +263,25 @@ def rope_cache(q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Ten
     to their slots of the caches [pages, page_size, Hk, D]; returns the turned queries (``q_out``,
     which may be ``q`` itself).  2 * freq.numel() elements of each head turn.  q, k and v may be
     parts of one wider tensor; with k None only the queries turn."""
-    rows, Hq, D = q.shape
+    rows, Hq, D = shape = q.shape
     dt = q.dtype
+    qp, qr, qh = _strided(q, "q", dt, shape)
     if q_out is None:
-        with _made_on(stream):
-            q_out = torch.empty((rows, Hq, D), dtype=dt, device=q.device)
-    qp, qr, qh = _strided(q, "q", dt, (rows, Hq, D))
-    op, orow, oh = _strided(q_out, "q_out", dt, (rows, Hq, D))
+        q_out = _made(stream, lambda: torch.empty(shape, dtype=dt, device=q.device))
+    op, orow, oh = _strided(q_out, "q_out", dt, shape)
     if k is None:
-        Hk, n_slots, kv, sp, kc, vc = 0, 0, (None, None, 0, 0, 0, 0), None, None, None
+        Hk = n_slots = sp = kc = vc = kp = vp = kr = kh = vr = vh = 0
     else:
         Hk = k.shape[1]
         kp, kr, kh = _strided(k, "k", dt, (rows, Hk, D))
         vp, vr, vh = _strided(v, "v", dt, (rows, Hk, D))
-        kv = (kp, vp, kr, kh, vr, vh)
         if k_cache.dim() != 4 or k_cache.shape[2:] != (Hk, D) or v_cache.shape != k_cache.shape:
             raise ValueError("k_cache and v_cache must both be [pages, page_size, Hk, D]")
         kc, vc = _t(k_cache, "k_cache", dt), _t(v_cache, "v_cache", dt)
-        n_slots, sp = k_cache.shape[0] * k_cache.shape[1], _t(slot, "slot", torch.int32, rows)
-    a = RopeCacheArgs(rows, Hq, Hk, D, 2 * freq.numel(), _dtype_code(q), int(interleaved), scale, qp,
-                      kv[0], kv[1], qr, qh, *kv[2:], op, orow, oh, kc, vc, n_slots,
-                      _t(freq, "freq", torch.float64), _t(position, "position", torch.int32, rows), sp,
-                      _opt(status, "status", torch.int32, 1))
-    _check(lib().spec_rope_cache(ctypes.byref(a), _on(stream)), "spec_rope_cache")
+        n_slots, sp = k_cache.shape[0] * k_cache.shape[1], _t(slot, "slot", _i32, rows)
+    _ROPE(_on(stream, q), rows, Hq, Hk, D, 2 * freq.numel(), _code(q), int(interleaved), scale, qp, kp, vp,
+          qr, qh, kr, kh, vr, vh, op, orow, oh, kc, vc, n_slots, _t(freq, "freq", _f64),
+          _t(position, "position", _i32, rows), sp, _opt(status, "status", _i32, 1))
     return q_out
 
 
@@ -271,37 +304,35 @@ def prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     (causal over its rows) and, for requests ``group_off[g]`` .. ``group_off[g + 1]``, the
     ``prefix_len[g]`` keys in ``prefix_table[g]``.  ``scale`` defaults to D^-1/2.  Returns out
     [rows, Hq, D], or (out, lse [rows, Hq]) with ``want_lse``."""
-    i32 = torch.int32
-    rows, Hq, D = q.shape
+    rows, Hq, D = shape = q.shape
     dt = q.dtype
     if k_cache.dim() != 4 or k_cache.shape[3] != D or v_cache.shape != k_cache.shape:
         raise ValueError("k_cache and v_cache must both be [pages, page_size, Hk, D]")
     n_pages, P, Hk, _ = k_cache.shape
     R, width = block_table.shape
-    G = 0 if prefix_len is None else prefix_len.numel()
-    if G and (group_off is None or prefix_table is None or prefix_table.dim() != 2 or
-              prefix_table.shape[0] != G):
-        raise ValueError("prefixes need group_off [G + 1], prefix_len [G] and prefix_table [G, pages]")
-    need = attention_workspace_bytes(rows, R, Hq, D)
-    with _made_on(stream):
-        if out is None:
-            out = torch.empty((rows, Hq, D), dtype=dt, device=q.device)
-        if want_lse and lse is None:
-            lse = torch.empty((rows, Hq), dtype=torch.float32, device=q.device)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    a = PrefixAttentionArgs(
-        R, rows, Hq, Hk, D, _dtype_code(q), P, n_pages, width, G, prefix_table.shape[1] if G else 0,
-        D ** -0.5 if scale is None else scale, *_strided(q, "q", dt, (rows, Hq, D)),
-        _t(k_cache, "k_cache", dt), _t(v_cache, "v_cache", dt), _t(row_off, "row_off", i32, R + 1),
-        _t(kv_len, "kv_len", i32, R), _t(block_table, "block_table", i32),
-        _t(group_off, "group_off", i32, G + 1) if G else None,
-        _t(prefix_len, "prefix_len", i32) if G else None,
-        _t(prefix_table, "prefix_table", i32) if G else None,
-        *_strided(out, "out", dt, (rows, Hq, D)), _opt(lse, "lse", torch.float32, rows * Hq),
-        _dev(workspace, "workspace").data_ptr(), workspace.numel() * workspace.element_size(),
-        _opt(status, "status", i32, 1))
-    _check(lib().spec_prefix_attention(ctypes.byref(a), _on(stream)), "spec_prefix_attention")
+    G = pages = go = pl = pt = 0
+    if prefix_len is not None and prefix_len.numel() > 0:
+        G = prefix_len.numel()
+        if group_off is None or prefix_table is None or prefix_table.dim() != 2 or prefix_table.shape[0] != G:
+            raise ValueError("prefixes need group_off [G + 1], prefix_len [G] and prefix_table [G, pages]")
+        pages = prefix_table.shape[1]
+        go, pl = _t(group_off, "group_off", _i32, G + 1), _t(prefix_len, "prefix_len", _i32)
+        pt = _t(prefix_table, "prefix_table", _i32)
+    strides = _strided(q, "q", dt, shape)
+    dev = q.device
+
+    def make():
+        return (torch.empty(shape, dtype=dt, device=dev) if out is None else out,
+                torch.empty((rows, Hq), dtype=_f32, device=dev) if want_lse and lse is None else lse,
+                torch.empty(attention_workspace_bytes(rows, R, Hq, D), dtype=torch.uint8, device=dev)
+                if workspace is None else workspace)
+    out, lse, workspace = _made(stream, make)
+    _ATTENTION(_on(stream, q), R, rows, Hq, Hk, D, _code(q), P, n_pages, width, G, pages,
+               D ** -0.5 if scale is None else scale, *strides, _t(k_cache, "k_cache", dt),
+               _t(v_cache, "v_cache", dt), _t(row_off, "row_off", _i32, R + 1), _t(kv_len, "kv_len", _i32, R),
+               _t(block_table, "block_table", _i32), go, pl, pt, *_strided(out, "out", dt, shape),
+               _opt(lse, "lse", _f32, rows * Hq), _dev(workspace, "workspace").data_ptr(),
+               workspace.numel() * workspace.element_size(), _opt(status, "status", _i32, 1))
     return (out, lse) if want_lse else out
 
 
@@ -310,7 +341,7 @@ def _matrix(t: torch.Tensor, name: str, dtype: torch.dtype) -> tuple:
     """Address and row stride of a device matrix with dense rows."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be a matrix with dense rows")
@@ -333,51 +364,43 @@ def adjust_logits(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None,
     drafted tokens of ``x`` [R, gamma] too.  ``bias`` = (offsets [R + 1], tokens, values),
     ``mask`` [n, ceil(V / 32)] int32 bits with ``mask_row`` [rows] (negative: no mask).
     ``out`` may be ``logits``.  Rows outside every request's are left as they are in ``out``."""
-    i32, f32 = torch.int32, torch.float32
     dt = logits.dtype
     lp, ld = _matrix(logits, "logits", dt)
-    rows, V = logits.shape
+    rows, V = shape = logits.shape
     if out is None:
-        with _made_on(stream):
-            out = torch.empty((rows, V), dtype=dt, device=logits.device)
+        out = _made(stream, lambda: torch.empty(shape, dtype=dt, device=logits.device))
         op, old = out.data_ptr(), V
     else:
         op, old = _matrix(out, "out", dt)
-        if out.shape != logits.shape:
+        if out.shape != shape:
             raise ValueError("out must have the shape of logits")
     if row_off is not None:
         R = row_off.numel() - 1
     else:
         R = length.numel() if length is not None else rows // max(rows_per_request, 1)
-    tp, tl, tc = None, 0, 0
+    tp = tl = tc = xp = xl = xc = bo = bt = bv = nb = mp = ml = nm = 0
     if tokens is not None:
-        tp, tl = _matrix(tokens, "tokens", i32)
+        tp, tl = _matrix(tokens, "tokens", _i32)
         tc = tokens.shape[1]
         if tokens.shape[0] < R:
             raise ValueError("tokens must have a row for each request")
-    xp, xl, xc = None, 0, 0
     if x is not None:
-        xp, xl = _matrix(x, "x", i32)
+        xp, xl = _matrix(x, "x", _i32)
         xc = x.shape[1]
         if x.shape[0] < R:
             raise ValueError("x must have a row for each request")
-    bo = bt = bv = None
-    nb = 0
     if bias is not None and bias[1].numel() > 0:
         nb = bias[1].numel()
-        bo, bt, bv = (_t(bias[0], "bias offsets", i32, R + 1), _t(bias[1], "bias tokens", i32),
-                      _t(bias[2], "bias values", f32, nb))
-    mp, ml, nm = None, 0, 0
+        bo, bt, bv = (_t(bias[0], "bias offsets", _i32, R + 1), _t(bias[1], "bias tokens", _i32),
+                      _t(bias[2], "bias values", _f32, nb))
     if mask is not None:
-        mp, ml = _matrix(mask, "mask", i32)
+        mp, ml = _matrix(mask, "mask", _i32)
         nm = mask.shape[0]
         if mask.shape[1] * 32 < V:
             raise ValueError("mask rows must have ceil(V / 32) words")
-    a = LogitsArgs(
-        R, V, rows, rows_per_request, _dtype_code(logits), lp, ld, op, old,
-        _opt(row_off, "row_off", i32, 1), tp, tl, _opt(prompt_len, "prompt_len", i32, R),
-        _opt(length, "length", i32, R), xp, xl, tc, xc, nb, _opt(repetition, "repetition", f32, R),
-        _opt(frequency, "frequency", f32, R), _opt(presence, "presence", f32, R), bo, bt, bv, mp, ml,
-        _opt(mask_row, "mask_row", i32, rows), nm, _opt(status, "status", i32, 1))
-    _check(lib().spec_adjust_logits(ctypes.byref(a), _on(stream)), "spec_adjust_logits")
+    _LOGITS(_on(stream, logits), R, V, rows, rows_per_request, _code(logits), lp, ld, op, old,
+            _opt(row_off, "row_off", _i32, 1), tp, tl, _opt(prompt_len, "prompt_len", _i32, R),
+            _opt(length, "length", _i32, R), xp, xl, tc, xc, nb, _opt(repetition, "repetition", _f32, R),
+            _opt(frequency, "frequency", _f32, R), _opt(presence, "presence", _f32, R), bo, bt, bv, mp, ml,
+            _opt(mask_row, "mask_row", _i32, rows), nm, _opt(status, "status", _i32, 1))
     return out
