@@ -68,6 +68,7 @@ __device__ __forceinline__ int page_of(const spec_prefix_attention_args& a, cons
 // Last i in [0, n) with off[i] <= v (0 if there is none): the request of a row, the group of a request.
 __device__ __forceinline__ int last_at_or_below(const int32_t* off, int n, int v) {
   int lo = 0, hi = n;
+#pragma unroll 1
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (off[mid] <= v) lo = mid;
