@@ -35,6 +35,8 @@
 // for its copies and products in flight and frees its TMEM.
 #include <cuda.h>
 
+#include <cstddef>
+
 #include "attention.cuh"
 #include "fused_tc.cuh"
 #include "tc.cuh"
@@ -120,26 +122,29 @@ __device__ __forceinline__ int item_keys(const Segment& s, int i, int per_head) 
   return max(0, min(s.keys, s.first_own + j));
 }
 __device__ __forceinline__ int item_count(const Segment& s, int per_head) {
-  return (int)(((int64_t)s.n * per_head + kItemRows - 1) / kItemRows);
+  return (int)(((unsigned)s.n * (unsigned)per_head + kItemRows - 1) / kItemRows);  // rows * Hq < 2^31
 }
 __device__ __forceinline__ int tile_cost(int rows) { return rows > kTile ? kCostPair : kCostSingle; }
 __device__ __forceinline__ int start_cost(int rows) { return rows > kTile ? kCostStartPair : kCostStartSingle; }
 // Cost of an item of `rows` query rows (or more: 256 are its own).
-__device__ __forceinline__ int64_t item_cost(int keys, int rows) {
+__device__ __forceinline__ int item_cost(int keys, int rows) {
   const int tiles = (keys + kTile - 1) / kTile;
-  return tiles ? start_cost(rows) + (int64_t)tiles * tile_cost(rows) : 0;
+  return tiles ? start_cost(rows) + tiles * tile_cost(rows) : 0;
 }
 __device__ __forceinline__ int64_t head_cost(const Segment& s, int per_head) {
   const int n = item_count(s, per_head);
-  int64_t c = 0;
-  if (s.prefix) {
-    if (n > 0)
-      c = (n - 1) * item_cost(s.keys, kItemRows) +
-          item_cost(s.keys, s.n * per_head - (n - 1) * kItemRows);
-    return c;
-  }
-  for (int i = 0; i < n; ++i) c += item_cost(item_keys(s, i, per_head), s.n * per_head - i * kItemRows);
+  if (n == 0) return 0;
+  int64_t c = item_cost(item_keys(s, n - 1, per_head), s.n * per_head - (n - 1) * kItemRows);
+  if (s.prefix) return c + (int64_t)(n - 1) * item_cost(s.keys, kItemRows);
+#pragma unroll 1
+  for (int i = 0; i < n - 1; ++i) c += item_cost(item_keys(s, i, per_head), kItemRows);
   return c;
+}
+// x / y rounded up or a little more, by one 32-bit division: the code of a 64-bit one
+// is a good part of what a block with little work has to fetch before it starts.
+__device__ __forceinline__ int64_t share_of(int64_t x, unsigned y) {
+  const int drop = max(0, 32 - __clzll(x));
+  return (int64_t)((unsigned)(x >> drop) / y + 1) << drop;
 }
 
 // The block's items in order.
@@ -157,9 +162,9 @@ struct Walker {
     if (x0 >= x1) return;
     load();
     const int64_t c = head_cost(seg, per_head);
-    if (c > 0) {
-      h = (int)((x0 - pos) / c);
-      pos += h * c;
+    while (pos + c <= x0) {  // (the layout starts in this segment: c > 0, and h < Hk)
+      pos += c;
+      ++h;
     }
   }
   __device__ void load() {
@@ -182,13 +187,14 @@ struct Walker {
       if (pos >= x1) return false;
       const int keys = item_keys(seg, i, per_head);
       const int left = seg.n * per_head - i * kItemRows;
-      const int64_t cost = item_cost(keys, left), at = pos + start_cost(left);
+      const int cost = item_cost(keys, left);
+      const int64_t at = pos + start_cost(left);
       pos += cost;
       const int mine = i++;
       if (cost == 0 || pos <= x0) continue;
       const int w = tile_cost(left), tiles = (keys + kTile - 1) / kTile;
-      it.lo = x0 <= at ? 0 : (int)((x0 - at + w - 1) / w);
-      it.hi = x1 <= at ? 0 : (int)min((int64_t)tiles, (x1 - at + w - 1) / w);
+      it.lo = x0 <= at ? 0 : ((int)(x0 - at) + w - 1) / w;  // x0 - at < cost
+      it.hi = x1 <= at ? 0 : x1 >= pos ? tiles : ((int)(x1 - at) + w - 1) / w;
       if (it.lo >= it.hi) continue;
       const int m = seg.n * per_head;
       it.row0 = seg.row0;
@@ -395,8 +401,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n_seg = a.G + a.R, run = (n_seg + kThreads - 1) / kThreads;
     const int k0 = min(tid * run, n_seg), k1 = min(k0 + run, n_seg);
     uint32_t bad = 0;
+    auto cost_of = [&](int k) { return a.Hk * head_cost(segment(a, k, &bad), per_head); };
     int64_t mine = 0;
-    for (int k = k0; k < k1; ++k) mine += a.Hk * head_cost(segment(a, k, &bad), per_head);
+#pragma unroll 1
+    for (int k = k0; k < k1; ++k) mine += cost_of(k);
     int64_t inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -404,49 +412,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane >= o) inc += t;
     }
     if (lane == 31) warp_sum[warp] = inc;
-    if (tid == 0) {
-      abort_flag = 0;
-      lay = Layout{0, 0, 0, 0, 0};
-      for (int i = 0; i < S::kStages; ++i) {
-        tc::mbar_init(&bars.full[i], 1);
-        tc::mbar_init(&bars.empty[i], 1);
-      }
-      for (int i = 0; i < 2; ++i) {
-        tc::mbar_init(&bars.q_full[i], 1);
-        tc::mbar_init(&bars.q_empty[i], 1);
-        tc::mbar_init(&bars.s_full[i], 1);
-        tc::mbar_init(&bars.p_full[i], 8);
-        for (int w = 0; w < 4; ++w) tc::mbar_init(&bars.both[i][w], 2);
-        tc::mbar_init(&bars.o_full[i], 1);
-      }
-      tc::mbar_init(&bars.drain, 1);
-      for (int i = 0; i < kItemSlots; ++i) {
-        tc::mbar_init(&bars.item_full[i], 1);
-        tc::mbar_init(&bars.item_empty[i], kItemReaders);
-      }
+    if (warp == kMma) tc::tmem_alloc(&bars.tmem, 512);
+    if (warp == kLoader) {
+      // arrivals of each barrier, in the order they lie in
+      constexpr int kP = 2 * kItemSlots + 20 + 6, kBoth = kP + 5, kEnd = kBoth + 8;
+      static_assert(offsetof(Shared, p_full) == 8 * kP && offsetof(Shared, both) == 8 * kBoth, "order");
+      uint64_t* bar = bars.item_full;
+      for (int i = lane; i < kEnd; i += 32)
+        tc::mbar_init(bar + i, i >= kItemSlots && i < 2 * kItemSlots ? kItemReaders
+                               : i == kP || i == kP + 1              ? 8
+                               : i >= kBoth                          ? 2
+                                                                     : 1);
       tc::fence_barrier_init();
     }
-    if (warp == kMma) tc::tmem_alloc(&bars.tmem, 512);
     if (warp == kProducer && lane == 0) {
+      abort_flag = 0;
+      lay = Layout{0, 0, 0, 0, 0};
       tc::tma_prefetch_desc(&k_map);
       tc::tma_prefetch_desc(&v_map);
       if (q_box > 0) tc::tma_prefetch_desc(&q_map);
     }
     __syncthreads();
-    int64_t before = 0, total = 0;
+    int64_t sum = lane < kThreads / 32 ? warp_sum[lane] : 0;  // every warp scans the warps' sums
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      before += w < warp ? warp_sum[w] : 0;
-      total += warp_sum[w];
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t t = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += t;
     }
-    int64_t at = before + inc - mine;  // position of the thread's first segment
+    const int64_t total = __shfl_sync(0xffffffffu, sum, 31);
+    const int64_t upto = __shfl_sync(0xffffffffu, sum, warp);
+    int64_t at = upto - __shfl_sync(0xffffffffu, inc, 31) + inc - mine;  // the thread's first segment
     // at least one tile a block, so that every block of an item's range has one
-    const int64_t per = max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)max(kCostPair, kCostSingle));
+    const int64_t per = max(share_of(total, gridDim.x), (int64_t)max(kCostPair, kCostSingle));
     const int64_t x0 = per * blockIdx.x, x1 = min(x0 + per, total);
     const bool here = x0 < x1 && at <= x0 && x0 < at + mine;
     if (here || blockIdx.x == 0) {
+#pragma unroll 1
       for (int k = k0; k < k1; ++k) {
-        const int64_t c = a.Hk * head_cost(segment(a, k, &bad), per_head);
+        const int64_t c = run == 1 ? mine : cost_of(k);
         if (blockIdx.x == 0) plan[1 + k] = at;
         if (here && at <= x0 && x0 < at + c) lay = Layout{per, x0, x1, k, at};
         at += c;
