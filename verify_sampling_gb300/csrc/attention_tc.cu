@@ -897,6 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ----------------------------------------------------------------- join ----
 constexpr int kJoinThreads = 256;
+constexpr int kJoinBlocks = 152 * 16;
 constexpr int kJoinRows = 32;  // query rows (packed rows x heads of a key head) of a block at a time
 
 // Cost of a head's items before item `upto`, and of all of them; a warp adds them up.
@@ -917,14 +918,14 @@ __device__ __forceinline__ void costs_of(const Segment& s, int per_head, int upt
   *all = y;
 }
 
-// Joins the pieces of every row that has more than one.  A block takes rows of one
-// request and key head, which share nearly all of what says where their pieces
-// are: that chain of dependent loads is paid once for up to 32 rows.  A warp a row.
+// Joins the pieces of every row that has more than one.  A block takes a request's
+// rows, tiles of 32 of one key head after the other: what says where their pieces are
+// is a chain of dependent loads, paid once a block.  A warp a row.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads)
     join_tc_kernel(const spec_prefix_attention_args a, const float* part, const float2* stat, const int64_t* plan) {
   constexpr int kPer = D / 32, kBatch = 4;
-  const int r = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, per_head = a.Hq / a.Hk;
+  const int r = blockIdx.x, lane = threadIdx.x & 31, per_head = a.Hq / a.Hk;
   uint32_t bad = 0;
   const Segment own = segment(a, a.G + r, &bad);
   int g = group_of(a, r, &bad);
@@ -937,78 +938,91 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int64_t per = plan[0];
   const int64_t own_at = plan[1 + a.G + r], pre_at = g >= 0 ? plan[1 + g] : 0;
 
-  int item[2] = {-1, -1};  // own and prefix item whose pieces are known
+  const int tiles = (m_own + kJoinRows - 1) / kJoinRows, all_tiles = tiles * a.Hk;
+  int item[2] = {-1, -1}, head = -1;  // own and prefix item, and key head, whose pieces are known
+  int64_t before[2] = {0, 0}, all[2] = {0, 0};
   int first[2] = {0, 0}, count[2] = {0, 0};
-  auto pieces = [&](int w, const Segment& s, int64_t at, int i) {  // blocks that have pieces of item i
-    if (i == item[w]) return;
-    item[w] = i;
+  auto pieces = [&](int w, const Segment& s, int64_t at, int h, int i) {  // blocks that have pieces of item i
+    if (i == item[w] && h == head) return;
     const int tiles = (item_keys(s, i, per_head) + kTile - 1) / kTile;
     count[w] = 0;
+    if (i != item[w]) costs_of(s, per_head, i, &before[w], &all[w]);
+    item[w] = i;
     if (tiles == 0) return;
-    int64_t before, all;
-    costs_of(s, per_head, i, &before, &all);
     const int rows = s.n * per_head - i * kItemRows;
-    at += h * all + before + start_cost(rows);
+    at += h * all[w] + before[w] + start_cost(rows);
     first[w] = (int)(at / per);
     count[w] = (int)((at + (int64_t)(tiles - 1) * tile_cost(rows)) / per) - first[w] + 1;
   };
-  const size_t own_slot = (size_t)a.rows * a.Hq + (size_t)own.row0 * a.Hq + (size_t)h * m_own;
-  const size_t pre_slot = (size_t)pre.row0 * a.Hq + (size_t)h * pre.n * per_head + m_off;
 
-  for (int m0 = blockIdx.z * kJoinRows; m0 < m_own; m0 += gridDim.z * kJoinRows) {
+  const bool wide_out = ((uintptr_t)a.out & 7) == 0 && a.out_row % 4 == 0 && a.out_head % 4 == 0;
+
+#pragma unroll 1
+  for (int x = blockIdx.y; x < all_tiles; x += gridDim.y) {
+    const int h = x / tiles, m0 = (x - h * tiles) * kJoinRows;
+    const size_t own_slot = (size_t)a.rows * a.Hq + (size_t)own.row0 * a.Hq + (size_t)h * m_own;
+    const size_t pre_slot = (size_t)pre.row0 * a.Hq + (size_t)h * pre.n * per_head + m_off;
     for (int m = m0 + (threadIdx.x >> 5); m < min(m0 + kJoinRows, m_own); m += kJoinThreads / 32) {
-      pieces(0, own, own_at, m / kItemRows);
-      if (g >= 0) pieces(1, pre, pre_at, (m_off + m) / kItemRows);
-      const int n = count[0] + count[1];
+      pieces(0, own, own_at, h, m / kItemRows);
+      if (g >= 0) pieces(1, pre, pre_at, h, (m_off + m) / kItemRows);
+      head = h;
+      const int c0 = count[0], n = c0 + count[1];
       if (count[1] == 0 && n == 1) continue;  // written by its block
-      auto place = [&](int p) {
-        return p < count[0] ? own_slot + m + (size_t)kItemRows * (first[0] + p)
-                            : pre_slot + m + (size_t)kItemRows * (first[1] + p - count[0]);
-      };
+      // piece p lies at one of two places plus p steps of 256 rows
+      const size_t own_at_row = own_slot + m + (size_t)kItemRows * first[0];
+      const size_t pre_at_row = pre_slot + m + (size_t)kItemRows * first[1] - (size_t)kItemRows * c0;
+      const float* own_part = part + own_at_row * D + lane * kPer;
+      const float* pre_part = part + (ptrdiff_t)pre_at_row * D + lane * kPer;
       float top = -CUDART_INF_F, sum = 0.f, o[kPer];
 #pragma unroll
       for (int d = 0; d < kPer; ++d) o[d] = 0.f;
+#pragma unroll 1
       for (int p0 = 0; p0 < n; p0 += kBatch) {
         float2 st[kBatch];
         float v[kBatch][kPer];
 #pragma unroll
-        for (int p = 0; p < kBatch; ++p) {
-          st[p] = make_float2(-CUDART_INF_F, 0.f);
-          if (p0 + p < n) {
-            const size_t at = place(p0 + p);
-            st[p] = stat[at];
-            const float* src = part + at * D + lane * kPer;
+        for (int i = 0; i < kBatch; ++i) {
+          const int p = p0 + i;
+          st[i] = make_float2(-CUDART_INF_F, 0.f);
+          if (p < n) {
+            st[i] = stat[(p < c0 ? own_at_row : pre_at_row) + (size_t)(p * kItemRows)];
+            const float* src = (p < c0 ? own_part : pre_part) + (size_t)p * (kItemRows * D);
             if constexpr (kPer == 4) {
-              const float4 x = *reinterpret_cast<const float4*>(src);
-              v[p][0] = x.x, v[p][1] = x.y, v[p][2] = x.z, v[p][3] = x.w;
+              const float4 y = *reinterpret_cast<const float4*>(src);
+              v[i][0] = y.x, v[i][1] = y.y, v[i][2] = y.z, v[i][3] = y.w;
             } else {
-              const float2 x = *reinterpret_cast<const float2*>(src);
-              v[p][0] = x.x, v[p][1] = x.y;
+              const float2 y = *reinterpret_cast<const float2*>(src);
+              v[i][0] = y.x, v[i][1] = y.y;
             }
           }
         }
-        float m_new = top;
-#pragma unroll
-        for (int p = 0; p < kBatch; ++p) m_new = fmaxf(m_new, st[p].x);
+        const float m_new = fmaxf(max3(st[0].x, st[1].x, st[2].x), fmaxf(st[3].x, top));
         const float c = top == -CUDART_INF_F ? 0.f : tc::ex2(top - m_new);
         sum *= c;
 #pragma unroll
         for (int d = 0; d < kPer; ++d) o[d] *= c;
 #pragma unroll
-        for (int p = 0; p < kBatch; ++p) {
-          if (p0 + p >= n) break;
-          const float w = st[p].x == -CUDART_INF_F ? 0.f : tc::ex2(st[p].x - m_new);
-          sum = fmaf(st[p].y, w, sum);
+        for (int i = 0; i < kBatch; ++i) {
+          if (p0 + i >= n) break;
+          const float w = st[i].x == -CUDART_INF_F ? 0.f : tc::ex2(st[i].x - m_new);
+          sum = fmaf(st[i].y, w, sum);
 #pragma unroll
-          for (int d = 0; d < kPer; ++d) o[d] = fmaf(v[p][d], w, o[d]);
+          for (int d = 0; d < kPer; ++d) o[d] = fmaf(v[i][d], w, o[d]);
         }
         top = m_new;
       }
-      const int b = own.row0 + m / per_head, hq = h * per_head + m % per_head;
+      const int j = m / per_head, b = own.row0 + j, hq = h * per_head + (m - j * per_head);
       const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row without keys: zeros
       __nv_bfloat16* out = (__nv_bfloat16*)a.out + (size_t)b * a.out_row + (size_t)hq * a.out_head + lane * kPer;
+      uint32_t r2[kPer / 2];
 #pragma unroll
-      for (int d = 0; d < kPer; d += 2) *reinterpret_cast<uint32_t*>(out + d) = pack_bf16(o[d] * inv, o[d + 1] * inv);
+      for (int d = 0; d < kPer; d += 2) r2[d / 2] = pack_bf16(o[d] * inv, o[d + 1] * inv);
+      if (kPer == 4 && wide_out) {
+        *reinterpret_cast<uint2*>(out) = make_uint2(r2[0], r2[kPer / 2 - 1]);
+      } else {
+#pragma unroll
+        for (int d = 0; d < kPer / 2; ++d) *reinterpret_cast<uint32_t*>(out + 2 * d) = r2[d];
+      }
       if (a.lse && lane == 0)
         a.lse[(size_t)b * a.Hq + hq] = sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * kLn2;
     }
@@ -1042,9 +1056,10 @@ cudaError_t launch(const spec_prefix_attention_args& a, int sms, float* part, fl
   attention_tc_kernel<D><<<sms, kThreads, Smem<D>::kBytes, stream>>>(km, vm, qm, q_box, a, part, stat, plan);
   if ((err = cudaGetLastError()) != cudaSuccess) return err;
   cudaLaunchConfig_t cfg{};
-  // blocks for the mean request's rows; a longer one's loop
-  const int64_t blocks = ((int64_t)a.rows * (a.Hq / a.Hk) + (int64_t)kJoinRows * a.R - 1) / ((int64_t)kJoinRows * a.R);
-  cfg.gridDim = dim3(a.R, a.Hk, (unsigned)(blocks < 1024 ? blocks : 1024));
+  // a block a tile of the mean request, until there are kJoinBlocks of them
+  const int64_t tiles = (((int64_t)a.rows * (a.Hq / a.Hk) + (int64_t)kJoinRows * a.R - 1) / ((int64_t)kJoinRows * a.R)) * a.Hk;
+  const int64_t most = (kJoinBlocks + a.R - 1) / a.R;
+  cfg.gridDim = dim3(a.R, (unsigned)(tiles < most ? tiles : most));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
