@@ -23,10 +23,10 @@
 // producer warp (TMA of key and value tiles, 64 x page boxes, into one ring), loader
 // warp (query rows: TMA where the heads of a key head divide a box, else 16-byte
 // copies into the swizzled places), MMA warp (S = Q K^T into TMEM, O += P V with P
-// read from TMEM), and two softmax groups of 128 rows.  A row has two threads, each
-// half of its columns, that meet once a tile for the maximum: with one thread a row
-// the time from scores to weights (1870 clocks) was most of the 3860 of a tile, and
-// the tensor pipe waited for it.  An item of more than 128 rows uses both groups on
+// read from TMEM), and two softmax groups of 128 rows.  A row has two threads of a
+// warp, each half of its columns, that meet in a shuffle for the maximum: with one
+// thread a row the time from scores to weights (1870 clocks) was most of the 3860 of a
+// tile, and the tensor pipe waited for it.  An item of more than 128 rows uses both groups on
 // the same key tile, one's softmax under the other's products; smaller items
 // alternate between them, and the next item's first product is issued before the
 // current one's last weights are ready.
@@ -48,9 +48,9 @@ namespace {
 using namespace attn;
 
 constexpr int kTile = 128;  // keys of a tile, rows of a warpgroup
-// Softmax warps: warpgroup pair t (rows 128 t ..) is warps 8 t .. 8 t + 7; warps w and
-// w + 4 of it take the same 32 rows (TMEM lanes go by the warp's number mod 4), the
-// first the even half of the columns, the second the odd half.
+// Softmax warps: group t (rows 128 t ..) is warps 8 t .. 8 t + 7; warps w and w + 4 of it
+// share 32 rows (TMEM lanes go by the warp's number mod 4), 16 each, and a row has
+// threads i and i + 16 of its warp, each half of its columns.
 constexpr int kSoftWarps = 16, kProducer = 16, kMma = 17, kPlanner = 18, kLoader = 19;
 constexpr int kThreads = 640;
 constexpr int kItemSlots = 4, kItemReaders = 3 + kSoftWarps;  // producer, MMA, loader, softmax warps
@@ -259,35 +259,63 @@ __device__ __forceinline__ uint32_t elected() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+// Columns [0, 16) of 16 TMEM lanes to threads 0-15, the 16 from `SPLIT` on of the same
+// lanes to threads 16-31: a row's two halves in one warp.
+template <int SPLIT>
+__device__ __forceinline__ void tmem_ld16h(uint32_t taddr, uint32_t* r) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
+      "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], %17;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr), "n"(SPLIT)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+template <int SPLIT>
+__device__ __forceinline__ void tmem_ld32h(uint32_t taddr, uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      "tcgen05.ld.sync.aligned.16x32bx2.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32], %33;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr), "n"(SPLIT)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+template <int SPLIT>
+__device__ __forceinline__ void tmem_ld64h(uint32_t taddr, uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      "tcgen05.ld.sync.aligned.16x32bx2.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,"
+      "%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64], %65;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr), "n"(SPLIT)
       : "memory");
+}
+template <int SPLIT>
+__device__ __forceinline__ void tmem_st16h(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.16x32bx2.x16.b32 [%0], %1, {%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17};" ::"r"(taddr), "n"(SPLIT),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+               : "memory");
+}
+template <int SPLIT>
+__device__ __forceinline__ void tmem_st32h(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.16x32bx2.x32.b32 [%0], %1, {%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33};" ::"r"(taddr), "n"(SPLIT),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -357,13 +385,11 @@ struct Shared {
   uint64_t item_full[kItemSlots], item_empty[kItemSlots];
   uint64_t full[10], empty[10];
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain;
-  uint64_t both[2][4];  // the two warps of 32 rows
   Item items[kItemSlots];
   Layout lay;
   int64_t warp_sum[kThreads / 32];
   uint32_t tmem;
   volatile int abort_flag;
-  float row[2][2][kTile];  // what the two threads of a row tell each other
 };
 
 template <int D>
@@ -415,13 +441,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kMma) tc::tmem_alloc(&bars.tmem, 512);
     if (warp == kLoader) {
       // arrivals of each barrier, in the order they lie in
-      constexpr int kP = 2 * kItemSlots + 20 + 6, kBoth = kP + 5, kEnd = kBoth + 8;
-      static_assert(offsetof(Shared, p_full) == 8 * kP && offsetof(Shared, both) == 8 * kBoth, "order");
+      constexpr int kP = 2 * kItemSlots + 20 + 6, kEnd = kP + 5;
+      static_assert(offsetof(Shared, p_full) == 8 * kP && offsetof(Shared, drain) == 8 * (kEnd - 1), "order");
       uint64_t* bar = bars.item_full;
       for (int i = lane; i < kEnd; i += 32)
         tc::mbar_init(bar + i, i >= kItemSlots && i < 2 * kItemSlots ? kItemReaders
                                : i == kP || i == kP + 1              ? 8
-                               : i >= kBoth                          ? 2
                                                                      : 1);
       tc::fence_barrier_init();
     }
@@ -712,24 +737,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < kSoftWarps) {
     // ------------------------------------------------------------- softmax --
     constexpr int kCols = kTile / 2, kDims = D / 2;  // scores and result columns of a thread
-    const int t = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, in_t = quarter * 32 + lane;
-    const uint32_t lane_base = (uint32_t)quarter << 21;  // 32 TMEM lanes a warp, lanes in the high half
-    const uint32_t s_addr = tmem + lane_base + t * kTile + half * kCols;
-    const uint32_t p_addr = tmem + lane_base + t * kTile + half * (kCols / 2);
-    const uint32_t o_addr = tmem + lane_base + 2 * kTile + t * kTile + half * kDims;
+    const int t = warp >> 3, half = lane >> 4;
+    const int row16 = (warp & 3) * 32 + (warp >> 2 & 1) * 16, in_t = row16 + (lane & 15);
+    const uint32_t lane_base = (uint32_t)row16 << 16;  // TMEM lanes in the high half
+    const uint32_t s_addr = tmem + lane_base + t * kTile, o_addr = s_addr + 2 * kTile;
     const float sl = a.scale * kLog2e;
     const bool wide_out = ((uintptr_t)a.out & 15) == 0 && a.out_row % 8 == 0 && a.out_head % 8 == 0;
-    uint32_t seq = 0, n_item = 0, s_n = 0, o_n = 0, b_n = 0;  // ring position, items seen, waits done
+    uint32_t seq = 0, n_item = 0, s_n = 0, o_n = 0;  // ring position, items seen, waits done
     int turn = 0;
     bool ok = true;
-    // The other thread of the row: gives `v`, gets its value.
-    auto swap = [&](float v) {
-      bars.row[t][half][in_t] = v;
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bars.both[t][quarter]);
-      ok = warp_wait(&bars.both[t][quarter], b_n++);
-      return bars.row[t][half ^ 1][in_t];
-    };
+    auto other = [](float v) { return __shfl_xor_sync(0xffffffffu, v, 16); };  // the row's other thread's
     // This warpgroup's next item and its ring position.
     auto next = [&](Item& it, uint32_t& seq0) {
       while (true) {
@@ -763,8 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc::fence_after_sync();
         uint32_t s[kCols];
-        tmem_ld32(s_addr, s);
-        tmem_ld32(s_addr + 32, s + 32);
+        tmem_ld64h<kCols>(s_addr, s);
         tc::tmem_ld_wait();
         const int lim = limit - i * kTile - half * kCols;
         if (__any_sync(0xffffffffu, lim < kCols)) {
@@ -781,8 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           m3 = max3(m3, __uint_as_float(s[e + 6]), __uint_as_float(s[e + 7]));
         }
         float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sl;
-        top = fmaxf(top, swap(top));
-        if (!ok) break;
+        top = fmaxf(top, other(top));
         if (__any_sync(0xffffffffu, top > ref + kSlack)) {
           // each row by its own scores alone: its bits do not depend on its neighbours
           const float to = top > ref + kSlack ? top : ref;
@@ -793,11 +808,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int d = 0; d < kDims; d += 16) {
               uint32_t o[16];
-              tc::tmem_ld16(o_addr + d, o);
+              tmem_ld16h<kDims>(o_addr + d, o);
               tc::tmem_ld_wait();
 #pragma unroll
               for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * c);
-              tmem_st16(o_addr + d, o);
+              tmem_st16h<kDims>(o_addr + d, o);
             }
           }
         }
@@ -815,8 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           p[e / 2] = pack_bf16(p0, p1);
           p[e / 2 + 1] = pack_bf16(p2, p3);
         }
-        // over the scores, which both threads of every row have read by now
-        tmem_st32(p_addr, p);
+        tmem_st32h<kCols / 2>(s_addr, p);  // over the scores, which the warp has read
         const float2 sum = halves(add2(a0, a1));
         l += sum.x + sum.y;
         // Values past the item's keys may be anything, NaN among them: zeros instead.
@@ -846,13 +860,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = warp_wait(&bars.o_full[t], o_n++);
       if (!ok) break;
       tc::fence_after_sync();
-      l += swap(l);
-      if (!ok) break;
+      l += other(l);
       const float inv = l == 0.f ? 0.f : 1.f / l;  // a row without keys: zeros
 #pragma unroll 1
       for (int d = 0; d < kDims; d += 32) {
         uint32_t o[32];
-        tmem_ld32(o_addr + d, o);
+        tmem_ld32h<kDims>(o_addr + d, o);
         tc::tmem_ld_wait();
         if (!valid) continue;
         if (!direct) {
@@ -880,11 +893,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!direct) stat[slot] = make_float2(ref, l);
         else if (a.lse) a.lse[(size_t)row * a.Hq + hq] = l == 0.f ? -CUDART_INF_F : (ref + log2f(l)) * kLn2;
       }
-      // the partner has read this row's sum before the next item writes there
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bars.both[t][quarter]);
-      ok = warp_wait(&bars.both[t][quarter], b_n++);
-      if (!ok) break;
       more = next(it, seq0);
     }
   }
