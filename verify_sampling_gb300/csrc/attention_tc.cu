@@ -307,16 +307,6 @@ __device__ __forceinline__ void tmem_st16h(uint32_t taddr, const uint32_t* r) {
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
                : "memory");
 }
-template <int SPLIT>
-__device__ __forceinline__ void tmem_st32h(uint32_t taddr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.16x32bx2.x32.b32 [%0], %1, {%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33};" ::"r"(taddr), "n"(SPLIT),
-               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-               : "memory");
-}
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -384,7 +374,7 @@ __device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t phase, volatile i
 struct Shared {
   uint64_t item_full[kItemSlots], item_empty[kItemSlots];
   uint64_t full[10], empty[10];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], drain;
   Item items[kItemSlots];
   Layout lay;
   int64_t warp_sum[kThreads / 32];
@@ -441,12 +431,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kMma) tc::tmem_alloc(&bars.tmem, 512);
     if (warp == kLoader) {
       // arrivals of each barrier, in the order they lie in
-      constexpr int kP = 2 * kItemSlots + 20 + 6, kEnd = kP + 5;
-      static_assert(offsetof(Shared, p_full) == 8 * kP && offsetof(Shared, drain) == 8 * (kEnd - 1), "order");
+      constexpr int kP = 2 * kItemSlots + 20 + 6, kEnd = kP + 7;
+      static_assert(offsetof(Shared, p_half) == 8 * kP && offsetof(Shared, drain) == 8 * (kEnd - 1), "order");
       uint64_t* bar = bars.item_full;
       for (int i = lane; i < kEnd; i += 32)
         tc::mbar_init(bar + i, i >= kItemSlots && i < 2 * kItemSlots ? kItemReaders
-                               : i == kP || i == kP + 1              ? 8
+                               : i >= kP && i < kP + 4               ? 8
                                                                      : 1);
       tc::fence_barrier_init();
     }
@@ -577,12 +567,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         commit_if(lead, &bars.s_full[t]);
         if (last) commit_if(lead, &bars.q_empty[t]);
       };
-      auto values = [&](int t, const Place& v, bool first) {  // O_t (+)= P_t V
+      // O_t (+)= P_t V, the keys of one half of each thread's weights at a time: keys 0-31
+      // and 64-95 of the tile, then the others
+      auto values = [&](int t, const Place& v, bool first, int part) {
         const uint32_t vb = v_lo + v.stage * (S::kTileBytes >> 4);
 #pragma unroll
-        for (int c = 0; c < kTile / 16; ++c)
+        for (int x = 0; x < kTile / 32; ++x) {
+          const int c = (x >> 1) * 4 + part * 2 + (x & 1);
           mma_ts(lead, tmem + 2 * kTile + t * kTile, tmem + t * kTile + c * 8, vb + c * (2048 >> 4), kDescO,
-                 c > 0 || !first);
+                 x > 0 || part > 0 || !first);
+        }
       };
       auto begin = [&](int l0, int l1, const Place& k, int tiles) {  // an item's first scores
         wait(&bars.full[k.stage], k.phase);
@@ -643,10 +637,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait(&bars.full[val.stage], val.phase);
           if (!last) wait(&bars.full[then.stage], then.phase);
           for (int t = l0; t <= l1 && ok; ++t) {
+            wait(&bars.p_half[t], p_n[t]);
+            if (!ok) break;
+            tc::fence_after_sync();
+            values(t, val, i == 0, 0);
             wait(&bars.p_full[t], p_n[t]++);
             if (!ok) break;
             tc::fence_after_sync();
-            values(t, val, i == 0);
+            values(t, val, i == 0, 1);
             if (last) commit_if(lead, &bars.o_full[t]);
             else scores(t, then, i + 2 == tiles);
           }
@@ -818,21 +816,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float sub = ref == -CUDART_INF_F ? 0.f : ref;
         const uint64_t sl2 = pair(sl, sl), sub2 = pair(-sub, -sub);
-        uint64_t a0 = 0, a1 = 0;
-        uint32_t p[kCols / 2];
-#pragma unroll
-        for (int e = 0; e < kCols; e += 4) {
-          const float2 z0 = halves(fma2(pair(s[e], s[e + 1]), sl2, sub2));
-          const float2 z1 = halves(fma2(pair(s[e + 2], s[e + 3]), sl2, sub2));
-          const float p0 = tc::ex2(z0.x), p1 = tc::ex2(z0.y), p2 = tc::ex2(z1.x), p3 = tc::ex2(z1.y);
-          a0 = add2(a0, pair(p0, p1));
-          a1 = add2(a1, pair(p2, p3));
-          p[e / 2] = pack_bf16(p0, p1);
-          p[e / 2 + 1] = pack_bf16(p2, p3);
-        }
-        tmem_st32h<kCols / 2>(s_addr, p);  // over the scores, which the warp has read
-        const float2 sum = halves(add2(a0, a1));
-        l += sum.x + sum.y;
         // Values past the item's keys may be anything, NaN among them: zeros instead.
         // (The first warpgroup pair of two does it, whose product is issued first.)
         const int live = it.keys - i * kTile;
@@ -848,6 +831,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc::fence_proxy_async();
         }
+        // The first half of the weights goes to the products while the second is
+        // computed: over the scores, which the warp has read.
+        uint64_t a0 = 0, a1 = 0;
+        uint32_t p[kCols / 2];
+        auto weights = [&](int from, int to) {
+#pragma unroll
+          for (int e = from; e < to; e += 4) {
+            const float2 z0 = halves(fma2(pair(s[e], s[e + 1]), sl2, sub2));
+            const float2 z1 = halves(fma2(pair(s[e + 2], s[e + 3]), sl2, sub2));
+            const float p0 = tc::ex2(z0.x), p1 = tc::ex2(z0.y), p2 = tc::ex2(z1.x), p3 = tc::ex2(z1.y);
+            a0 = add2(a0, pair(p0, p1));
+            a1 = add2(a1, pair(p2, p3));
+            p[e / 2] = pack_bf16(p0, p1);
+            p[e / 2 + 1] = pack_bf16(p2, p3);
+          }
+        };
+        weights(0, kCols / 2);
+        tmem_st16h<kCols / 2>(s_addr, p);
+        weights(kCols / 2, kCols * 3 / 4);
+        tmem_st_wait();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars.p_half[t]);
+        weights(kCols * 3 / 4, kCols);
+        tmem_st16h<kCols / 2>(s_addr + kCols / 4, p + kCols / 4);
+        const float2 sum = halves(add2(a0, a1));
+        l += sum.x + sum.y;
         tmem_st_wait();
         tc::fence_before_sync();
         __syncwarp();
