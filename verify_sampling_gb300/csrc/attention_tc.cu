@@ -147,7 +147,13 @@ __device__ __forceinline__ int64_t share_of(int64_t x, unsigned y) {
   return (int64_t)((unsigned)(x >> drop) / y + 1) << drop;
 }
 
-// The block's items in order.
+// Tiles whose costs begin before `x` units of an item's tiles.
+__device__ __forceinline__ int tiles_before(int x, int rows) {
+  return rows > kTile ? (unsigned)(x + kCostPair - 1) / kCostPair : (unsigned)(x + kCostSingle - 1) / kCostSingle;
+}
+
+// The block's items in order.  (One copy of each step: a block's first item waits for
+// this code to be fetched.)
 struct Walker {
   const spec_prefix_attention_args& a;
   int64_t pos, x0, x1;
@@ -157,49 +163,40 @@ struct Walker {
   uint32_t bad;
 
   __device__ Walker(const spec_prefix_attention_args& args, const Layout& lay)
-      : a(args), pos(lay.s0), x0(lay.x0), x1(lay.x1), k(lay.k0), h(0), i(0),
-        per_head(args.Hq / args.Hk), count(0), alone(false), bad(0) {
-    if (x0 >= x1) return;
-    load();
-    const int64_t c = head_cost(seg, per_head);
-    while (pos + c <= x0) {  // (the layout starts in this segment: c > 0, and h < Hk)
-      pos += c;
-      ++h;
-    }
-  }
-  __device__ void load() {
-    seg = segment(a, k, &bad);
-    count = item_count(seg, per_head);
-    alone = k >= a.G && shared_keys(a, k - a.G, &bad) == 0;
-  }
-  __device__ bool next(Item& it) {
-    if (x0 >= x1) return false;
-    while (true) {
-      while (i >= count || h >= a.Hk) {  // next head, or next segment
+      : a(args), pos(lay.s0), x0(lay.x0), x1(lay.x1), k(lay.k0 - 1), h(0), i(0),
+        per_head(args.Hq / args.Hk), count(0), alone(false), bad(0) {}
+  __device__ __forceinline__ bool next(Item& it) {
+#pragma unroll 1
+    while (pos < x1) {
+      if (i >= count) {  // next head, or next segment
         i = 0;
         if (count == 0 || ++h >= a.Hk) {
           h = 0;
           if (++k >= a.G + a.R) return false;
-          if (pos >= x1) return false;
-          load();
+          seg = segment(a, k, &bad);
+          count = item_count(seg, per_head);
+          alone = k >= a.G && (a.G == 0 || shared_keys(a, k - a.G, &bad) == 0);
+          if (count > 0 && pos < x0) {  // the layout starts in this segment: whole heads before it
+            const int64_t c = head_cost(seg, per_head);
+#pragma unroll 1
+            for (; pos + c <= x0 && h + 1 < a.Hk; ++h) pos += c;
+          }
         }
+        continue;
       }
-      if (pos >= x1) return false;
-      const int keys = item_keys(seg, i, per_head);
-      const int left = seg.n * per_head - i * kItemRows;
-      const int cost = item_cost(keys, left);
+      const int keys = item_keys(seg, i, per_head), m = seg.n * per_head;
+      it.m0 = i * kItemRows;
+      ++i;
+      const int left = m - it.m0;
+      const int cost = item_cost(keys, left), tiles = (keys + kTile - 1) / kTile;
       const int64_t at = pos + start_cost(left);
       pos += cost;
-      const int mine = i++;
       if (cost == 0 || pos <= x0) continue;
-      const int w = tile_cost(left), tiles = (keys + kTile - 1) / kTile;
-      it.lo = x0 <= at ? 0 : ((int)(x0 - at) + w - 1) / w;  // x0 - at < cost
-      it.hi = x1 <= at ? 0 : x1 >= pos ? tiles : ((int)(x1 - at) + w - 1) / w;
+      it.lo = x0 <= at ? 0 : tiles_before((int)(x0 - at), left);  // x0 - at < cost
+      it.hi = x1 <= at ? 0 : x1 >= pos ? tiles : tiles_before((int)(x1 - at), left);
       if (it.lo >= it.hi) continue;
-      const int m = seg.n * per_head;
       it.row0 = seg.row0;
-      it.m0 = mine * kItemRows;
-      it.rows = min(kItemRows, m - it.m0);
+      it.rows = min(kItemRows, left);
       it.h = h;
       it.keys = keys;
       it.first_own = seg.first_own;
@@ -210,6 +207,7 @@ struct Walker {
                 it.m0 + (size_t)kItemRows * blockIdx.x;
       return true;
     }
+    return false;
   }
 };
 
