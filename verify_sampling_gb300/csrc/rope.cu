@@ -25,6 +25,7 @@
 #include "rope.cuh"
 
 #include <algorithm>
+#include <climits>
 
 namespace spec {
 
@@ -277,7 +278,18 @@ cudaError_t launch_wide(const spec_rope_cache_args& a, cudaStream_t stream) {
   const int chunks = (heads + kUnroll * at_once - 1) / (kUnroll * at_once);
   const int group = units * at_once;
   const int groups = std::max(1, std::min({kRopeTokens, kMaxThreads / group, std::max(1, a.rows / 304)}));
-  const int reps = std::max(1, std::min({kReps, kRopeTokens / groups, a.rows / (groups * 608)}));
+  // As many tokens a thread as fill whole rounds of blocks best; a block's start costs
+  // about two tokens (2560 rows of 80 heads: 25.9 us with three, 29.5 with four in 2.1
+  // rounds, 31.2 with one).
+  const int slots = 152 * std::max(1, 2 * kMaxThreads / (group * groups));
+  int reps = 1, best = INT_MAX;
+  for (int r = std::min(kReps, kRopeTokens / groups); r >= 1; --r) {
+    const int blocks = (a.rows + groups * r - 1) / (groups * r), cost = (blocks + slots - 1) / slots * (r + 2);
+    if (cost < best) {
+      best = cost;
+      reps = r;
+    }
+  }
   const size_t smem = (size_t)groups * reps * 2 * ((half + VEC - 1) / VEC) * VEC * sizeof(float);
   const dim3 grid((a.rows + groups * reps - 1) / (groups * reps));
   if (inter) rope_kernel<T, true><<<grid, group * groups, smem, stream>>>(a, groups, reps, units, at_once, chunks);

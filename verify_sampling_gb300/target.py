@@ -164,9 +164,12 @@ def cache_reserve(cache: dict, row_off: torch.Tensor, rows: int, *,
     R, width = table.shape
     if out is None:
         def make():
-            new_len, position, request, slot = table.new_empty(R + 3 * rows).split((R, rows, rows, rows))
-            return {"new_len": new_len, "position": position, "request": request, "slot": slot,
-                    "ring_pos": cache["ring_pos"].new_empty(2)}
+            dev = table.device  # (tensors of their own: views of one cost twice as much to make)
+            return {"new_len": torch.empty(R, dtype=_i32, device=dev),
+                    "position": torch.empty(rows, dtype=_i32, device=dev),
+                    "request": torch.empty(rows, dtype=_i32, device=dev),
+                    "slot": torch.empty(rows, dtype=_i32, device=dev),
+                    "ring_pos": torch.empty(2, dtype=_i64, device=dev)}
         out = _made(stream, make)
     _RESERVE(_on(stream, table), R, rows, cache["page_size"], ring.numel(), width,
              _t(cache["kv_len"], "kv_len", _i32, R), _t(row_off, "row_off", _i32, R + 1),
@@ -188,8 +191,9 @@ def cache_commit(cache: dict, reserved: dict, keep: torch.Tensor, *, out: Option
     table, ring = cache["block_table"], cache["ring"]
     R, width = table.shape
     if out is None:
-        out = _made(stream, lambda: {"kv_len": cache["kv_len"].new_empty(R),
-                                     "ring_pos": cache["ring_pos"].new_empty(2)})
+        dev = table.device
+        out = _made(stream, lambda: {"kv_len": torch.empty(R, dtype=_i32, device=dev),
+                                     "ring_pos": torch.empty(2, dtype=_i64, device=dev)})
     _COMMIT(_on(stream, table), R, cache["page_size"], ring.numel(), width,
             _t(cache["kv_len"], "kv_len", _i32, R), _t(reserved["new_len"], "new_len", _i32, R),
             _t(keep, "keep", _i32, R), _t(table, "block_table", _i32), _t(ring, "ring", _i32),
