@@ -47,7 +47,7 @@ namespace {
 
 using namespace attn;
 
-constexpr int kTile = 128;  // keys of a tile, rows of a warpgroup
+constexpr int kTile = 128;  // keys of a tile, rows of a softmax group
 // Softmax warps: group t (rows 128 t ..) is warps 8 t .. 8 t + 7; warps w and w + 4 of it
 // share 32 rows (TMEM lanes go by the warp's number mod 4), 16 each, and a row has
 // threads i and i + 16 of its warp, each half of its columns.
@@ -56,7 +56,7 @@ constexpr int kThreads = 640;
 constexpr int kItemSlots = 4, kItemReaders = 3 + kSoftWarps;  // producer, MMA, loader, softmax warps
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kSlack = 8.f;  // log2 units the maximum may grow by before O is rescaled
-// Costs, in units of 0.1 us, measured: a tile of an item of two warpgroups (bound
+// Costs, in units of 0.1 us, measured: a tile of an item of both softmax groups (bound
 // by the products), a tile of a smaller one (bound by its 64 KB), and an item's
 // start and end.
 constexpr int kCostPair = 17, kCostSingle = 15, kCostStartPair = 57, kCostStartSingle = 21;
@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int rows = 0, tiles = 0, n_rows = 0, n_tiles = 0;  // of the current and the next item
       uint32_t n_item = 0;
       uint32_t q_n[2] = {0, 0}, p_n[2] = {0, 0};
-      int turn = 0;  // warpgroup of the next small item
+      int turn = 0;  // softmax group of the next small item
       bool ok = true;
       constexpr uint32_t kDescS = tc::bf16_idesc(128, kTile);
       constexpr uint32_t kDescO = tc::bf16_idesc(128, D) | (1u << 16);  // values: keys down, head across
@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) tc::mbar_arrive(&bars.item_empty[slot]);
         return true;
       };
-      auto lanes = [&](int r, int& p, int& q) {  // the warpgroups of an item
+      auto lanes = [&](int r, int& p, int& q) {  // the softmax groups of an item
         if (r > kTile) {
           p = 0;
           q = 1;
@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (more_next) {
               lanes(n_rows, n0, n1);
               // ahead of the current item's last values, if all is there: the other
-              // warpgroup may still be busy with the item before
+              // group may still be busy with the item before
               early = l0 == l1 && n0 == n1 && n0 != l0 &&
                       __all_sync(0xffffffffu, tc::mbar_try_wait(&bars.q_full[n0], q_n[n0] & 1u) &&
                                                   tc::mbar_try_wait(&bars.full[then.stage], then.phase));
@@ -743,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int turn = 0;
     bool ok = true;
     auto other = [](float v) { return __shfl_xor_sync(0xffffffffu, v, 16); };  // the row's other thread's
-    // This warpgroup's next item and its ring position.
+    // This softmax group's next item and its ring position.
     auto next = [&](Item& it, uint32_t& seq0) {
       while (true) {
         const Item& posted = items[n_item % kItemSlots];
@@ -815,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sub = ref == -CUDART_INF_F ? 0.f : ref;
         const uint64_t sl2 = pair(sl, sl), sub2 = pair(-sub, -sub);
         // Values past the item's keys may be anything, NaN among them: zeros instead.
-        // (The first warpgroup pair of two does it, whose product is issued first.)
+        // (The first softmax group of two does it, whose product is issued first.)
         const int live = it.keys - i * kTile;
         if (live < kTile && (!pair_item || t == 0)) {
           const uint32_t sv = seq0 + 2u * (uint32_t)(i - it.lo) + 1u;

@@ -18,10 +18,11 @@
 // more tokens, the next step's loads ahead of this step's products: its cosines and
 // sines are read from shared memory once a token (one float4 column a unit, free of bank
 // conflicts) and stay in registers, and a step is two loads, the products and two
-// stores.  All of a thread's loads go out before the cosines are computed.
-// Bound by memory: every element is read and written once.  (With units dealt out
-// to threads one by one, each with its own addresses and cosines, the round case
-// took 40 us.)
+// stores.  A thread's first loads go out before the cosines are computed.
+// Bound by memory: every element is read and written once (2560 rows of 64 + 2 * 8
+// heads of 128, bf16: 26.1 us, 4.0 TB/s; 40001 rows of 32 + 2 * 4 heads: 165 us, 5.0
+// TB/s).  With units dealt out to threads one by one, each with its own addresses and
+// cosines, the first took 40 us.
 #include "rope.cuh"
 
 #include <algorithm>
@@ -32,7 +33,7 @@ namespace spec {
 namespace {
 
 constexpr int kThreads = 256;     // of the element-wise kernel
-constexpr int kMaxThreads = 320;  // of the other: two blocks an SM at 102 registers
+constexpr int kMaxThreads = 320;  // of the other: two blocks an SM at 96 registers (three spill: 98 us for 26)
 constexpr int kUnroll = 2;
 constexpr int kRopeTokens = 8;  // of a block
 constexpr int kReps = 4;        // of a thread, one after the other
