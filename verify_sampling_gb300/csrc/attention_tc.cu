@@ -912,36 +912,40 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ----------------------------------------------------------------- join ----
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 128;
 constexpr int kJoinBlocks = 152 * 16;
-constexpr int kJoinRows = 32;  // query rows (packed rows x heads of a key head) of a block at a time
+constexpr int kJoinRows = 64;  // query rows (packed rows x heads of a key head) of a block at a time
 
-// Cost of a head's items before item `upto`, and of all of them; a warp adds them up.
+constexpr int kJoinLanes = 16;  // threads of a row
+
+// Cost of a head's items before item `upto`, and of all of them; a row's threads add them up.
 __device__ __forceinline__ void costs_of(const Segment& s, int per_head, int upto, int64_t* before, int64_t* all) {
-  const int n = item_count(s, per_head), lane = threadIdx.x & 31;
+  const int n = item_count(s, per_head), lane = threadIdx.x % kJoinLanes;
+  const uint32_t lanes = (uint32_t)((1ull << kJoinLanes) - 1) << (threadIdx.x & 31 & ~(kJoinLanes - 1));
   int64_t x = 0, y = 0;
-  for (int i = lane; i < n; i += 32) {
+  for (int i = lane; i < n; i += kJoinLanes) {
     const int64_t c = item_cost(item_keys(s, i, per_head), s.n * per_head - i * kItemRows);
     y += c;
     if (i < upto) x += c;
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    x += __shfl_xor_sync(0xffffffffu, x, o);
-    y += __shfl_xor_sync(0xffffffffu, y, o);
+  for (int o = kJoinLanes / 2; o > 0; o >>= 1) {
+    x += __shfl_xor_sync(lanes, x, o);
+    y += __shfl_xor_sync(lanes, y, o);
   }
   *before = x;
   *all = y;
 }
 
 // Joins the pieces of every row that has more than one.  A block takes a request's
-// rows, tiles of 32 of one key head after the other: what says where their pieces are
-// is a chain of dependent loads, paid once a block.  A warp a row.
+// rows, tiles of 64 of one key head after the other: what says where their pieces are
+// is a chain of dependent loads, paid once a block.  Half a warp a row: twice the rows in
+// flight (the round of 256 requests behind a prefix 779 us in all, 790 with a warp a row).
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinThreads, 4)
     join_tc_kernel(const spec_prefix_attention_args a, const float* part, const float2* stat, const int64_t* plan) {
-  constexpr int kPer = D / 32, kBatch = 4;
-  const int r = blockIdx.x, lane = threadIdx.x & 31, per_head = a.Hq / a.Hk;
+  constexpr int kPer = D / kJoinLanes, kBatch = 4;
+  const int r = blockIdx.x, lane = threadIdx.x % kJoinLanes, per_head = a.Hq / a.Hk;
   uint32_t bad = 0;
   const Segment own = segment(a, a.G + r, &bad);
   int g = group_of(a, r, &bad);
@@ -978,7 +982,7 @@ __global__ void __launch_bounds__(kJoinThreads)
     const int h = x / tiles, m0 = (x - h * tiles) * kJoinRows;
     const size_t own_slot = (size_t)a.rows * a.Hq + (size_t)own.row0 * a.Hq + (size_t)h * m_own;
     const size_t pre_slot = (size_t)pre.row0 * a.Hq + (size_t)h * pre.n * per_head + m_off;
-    for (int m = m0 + (threadIdx.x >> 5); m < min(m0 + kJoinRows, m_own); m += kJoinThreads / 32) {
+    for (int m = m0 + threadIdx.x / kJoinLanes; m < min(m0 + kJoinRows, m_own); m += kJoinThreads / kJoinLanes) {
       pieces(0, own, own_at, h, m / kItemRows);
       if (g >= 0) pieces(1, pre, pre_at, h, (m_off + m) / kItemRows);
       head = h;
@@ -1003,12 +1007,10 @@ __global__ void __launch_bounds__(kJoinThreads)
           if (p < n) {
             st[i] = stat[(p < c0 ? own_at_row : pre_at_row) + (size_t)(p * kItemRows)];
             const float* src = (p < c0 ? own_part : pre_part) + (size_t)p * (kItemRows * D);
-            if constexpr (kPer == 4) {
-              const float4 y = *reinterpret_cast<const float4*>(src);
-              v[i][0] = y.x, v[i][1] = y.y, v[i][2] = y.z, v[i][3] = y.w;
-            } else {
-              const float2 y = *reinterpret_cast<const float2*>(src);
-              v[i][0] = y.x, v[i][1] = y.y;
+#pragma unroll
+            for (int d = 0; d < kPer; d += 4) {
+              const float4 y = *reinterpret_cast<const float4*>(src + d);
+              v[i][d] = y.x, v[i][d + 1] = y.y, v[i][d + 2] = y.z, v[i][d + 3] = y.w;
             }
           }
         }
@@ -1033,8 +1035,9 @@ __global__ void __launch_bounds__(kJoinThreads)
       uint32_t r2[kPer / 2];
 #pragma unroll
       for (int d = 0; d < kPer; d += 2) r2[d / 2] = pack_bf16(o[d] * inv, o[d + 1] * inv);
-      if (kPer == 4 && wide_out) {
-        *reinterpret_cast<uint2*>(out) = make_uint2(r2[0], r2[kPer / 2 - 1]);
+      if (wide_out) {
+#pragma unroll
+        for (int d = 0; d < kPer / 2; d += 2) *reinterpret_cast<uint2*>(out + 2 * d) = make_uint2(r2[d], r2[d + 1]);
       } else {
 #pragma unroll
         for (int d = 0; d < kPer / 2; ++d) *reinterpret_cast<uint32_t*>(out + 2 * d) = r2[d];
