@@ -121,3 +121,55 @@ def test_refusals():
             vs.rope_cache(*args)
     with pytest.raises(vs.SpecError):
         vs.rope_cache(q, k, v, torch.cat([freq, freq]), position, slot, kc, vc)  # 128 elements of 64
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rows,Hq,Hk,D,rot", [
+    (609, 64, 8, 128, 128), (2601, 16, 2, 128, 64), (4301, 8, 1, 160, 96), (6001, 7, 1, 128, 128), (2500, 5, 1, 512, 512),
+    (60001, 2, 1, 48, 16), (99991, 1, 0, 64, 64), (32003, 0, 3, 64, 64), (20001, 3, 1, 64, 0), (1300, 20, 8, 256, 32),
+    (700, 100, 4, 256, 128)])
+def test_many_rows_with_heads_side_by_side(rows, Hq, Hk, D, rot, interleaved, dt):
+    """The formula, the same bits as calls of a few rows each, and rows that go nowhere."""
+    qkv, position, slot, (kc, vc) = _inputs(rows, Hq, Hk, D, dt, far=1 << 20)
+    q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hk], qkv[:, Hq + Hk:]
+    freq, _ = vs.rope_frequencies(rot) if rot else (torch.zeros(0, dtype=torch.float64, device="cuda"), 1)
+    n_slots = kc.shape[0] * kc.shape[1]
+    position[5], position[rows - 2], slot[7], slot[9], position[11] = -1, -1, -1, n_slots, 1 << 24
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    few, many, part = [torch.full((rows, Hq, D), 5.0, dtype=dt, device="cuda") for _ in range(3)]
+    kw = dict(interleaved=interleaved, scale=1.25, status=status)
+    kf, vf = kc.clone(), vc.clone()
+
+    def call(rows, out, kc, vc):
+        if Hk == 0:
+            return vs.rope_cache(q[rows], None, None, freq, position[rows], None, None, None, q_out=out[rows], **kw)
+        return vs.rope_cache(q[rows], k[rows], v[rows], freq, position[rows], slot[rows], kc, vc, q_out=out[rows], **kw)
+
+    call(slice(0, rows), many, kc, vc)
+    assert status.item() == vs.STATUS_BAD_POSITION | (vs.STATUS_BAD_PAGE if Hk else 0)
+    step = min(500, 10000000 // ((Hq + 2 * Hk) * D * 4))  # too few for the kernel of long batches
+    for a in range(0, rows, step):
+        call(slice(a, a + step), few, kf, vf)
+    assert torch.equal(many, few) and torch.equal(kc, kf) and torch.equal(vc, vf)
+    assert Hq == 0 or (torch.all(many[5] == 5) and torch.all(many[rows - 2] == 5))
+    live = torch.ones(rows, dtype=torch.bool)
+    live[[5, rows - 2, 11]] = False
+    if Hq:
+        want, size = _turned(q[live], position[live], freq, 1.25, interleaved)
+        _check(many[live], want, size)
+    if Hk:
+        live[[7, 9]] = False
+        at = slot[live].long()
+        want, size = _turned(k[live], position[live], freq, 1.25, interleaved)
+        _check(kc.flatten(0, 1)[at], want, size)
+        assert torch.equal(vc.flatten(0, 1)[at], v[live])
+        rest = torch.ones(n_slots, dtype=torch.bool, device="cuda")
+        rest[at] = False
+        rest[slot[11].long()] = False
+        assert torch.all(kc.flatten(0, 1)[rest] == 7) and torch.all(vc.flatten(0, 1)[rest] == 7)
+    if Hq:  # the queries in place
+        part.copy_(q)
+        vs.rope_cache(part, None, None, freq, position, None, None, None, q_out=part, interleaved=interleaved, scale=1.25)
+        live[:] = position.cpu() >= 0
+        assert torch.equal(part[live], many[live]) and torch.equal(part[~live], q[~live])

@@ -11,19 +11,22 @@
 // there.  It costs two fmas an angle, where 64-bit products would hold up the
 // heads of small models (the fp64 pipe is 1/64 of the fp32 one).
 //
-// Layout: a unit is two 16-byte vectors of a head: the two halves of its pairs in
-// the half layout, two vectors next to each other otherwise; either way unit u
-// takes the frequencies [u VEC, (u + 1) VEC).  A thread keeps one unit of one token
-// and steps over the heads, queries, keys and values in turn, and then over a few
-// more tokens, the next step's loads ahead of this step's products: its cosines and
-// sines are read from shared memory once a token (one float4 column a unit, free of bank
-// conflicts) and stay in registers, and a step is two loads, the products and two
-// stores.  A thread's first loads go out before the cosines are computed.
-// Bound by memory: every element is read and written once (2560 rows of 64 + 2 * 8
-// heads of 128, bf16: 26.1 us, 4.0 TB/s; 40001 rows of 32 + 2 * 4 heads: 165 us, 5.0
-// TB/s).  With units dealt out to threads one by one, each with its own addresses and
-// cosines, the first took 40 us.
+// Layout, small batches and strided heads (rope_kernel): a unit is two 16-byte vectors
+// of a head: the two halves of its pairs in the half layout, two vectors next to each
+// other otherwise; either way unit u takes the frequencies [u VEC, (u + 1) VEC).  A thread
+// keeps one unit of one token and steps over the heads, queries, keys and values in turn,
+// and then over a few more tokens, the next step's loads ahead of this step's products:
+// its cosines and sines are read from shared memory once a token (one float4 column a
+// unit, free of bank conflicts) and stay in registers, and a step is two loads, the
+// products and two stores.  A thread's first loads go out before the cosines are computed.
+//
+// Long batches (rope_bulk_kernel): bulk copies through a ring in shared memory, described
+// there.  What bounds both is memory, every element read and written once; a thread's
+// registers hold too few bytes in flight for it: 2560 rows of 64 + 2 * 8 heads of 128 in
+// bf16 took 26.0 us (4.0 TB/s) by the first kernel, 19.7 (5.3 TB/s) by the second, 40001
+// rows of 32 + 2 * 4 heads 164 us and 122 (6.7 TB/s).
 #include "rope.cuh"
+#include "tc.cuh"
 
 #include <algorithm>
 #include <climits>
@@ -33,7 +36,7 @@ namespace spec {
 namespace {
 
 constexpr int kThreads = 256;     // of the element-wise kernel
-constexpr int kMaxThreads = 320;  // of the other: two blocks an SM at 96 registers (three spill: 98 us for 26)
+constexpr int kMaxThreads = 320;  // of rope_kernel: two blocks an SM at 96 registers (three spill: 98 us for 26)
 constexpr int kUnroll = 2;
 constexpr int kRopeTokens = 8;  // of a block
 constexpr int kReps = 4;        // of a thread, one after the other
@@ -59,15 +62,22 @@ __device__ __forceinline__ void turn(T& x, T& y, float2 cs) {
   from_f(fmaf(b, cs.x, __fmul_rn(a, cs.y)), &y);
 }
 
-// cos and sin, times the scale, of position x times the frequency (radians).
-__device__ __forceinline__ float2 cos_sin(float x, double freq, float scale) {
+// A frequency (radians) in turns, hi + lo.
+__device__ __forceinline__ float2 in_turns(double freq) {
   const double turns = freq * 0.15915494309189533577;  // 1 / (2 pi)
-  const float hi = (float)turns, lo = (float)(turns - (double)hi);
-  const float m = x * hi, e = fmaf(x, hi, -m);
-  const float frac = (m - rintf(m)) + fmaf(x, lo, e);
+  const float hi = (float)turns;
+  return make_float2(hi, (float)(turns - (double)hi));
+}
+// cos and sin, times the scale, of position x times the frequency.
+__device__ __forceinline__ float2 cos_sin(float x, float2 turns, float scale) {
+  const float m = x * turns.x, e = fmaf(x, turns.x, -m);
+  const float frac = (m - rintf(m)) + fmaf(x, turns.y, e);
   float s, c;
   sincospif(2.f * frac, &s, &c);
   return make_float2(c * scale, s * scale);
+}
+__device__ __forceinline__ float2 cos_sin(float x, double freq, float scale) {
+  return cos_sin(x, in_turns(freq), scale);
 }
 
 // Where head h of a row (queries, keys, values in turn) is read and written (null:
@@ -263,11 +273,234 @@ __global__ void __launch_bounds__(kThreads) rope_scalar_kernel(spec_rope_cache_a
   }
 }
 
+// ------------------------------------------------------------ long batches --
+// Rows whose heads lie side by side, by bulk copies through a ring of stages in
+// shared memory: a stage is a few tokens, turned in place.  One warp issues the loads
+// and, when a stage is turned, its stores (values are not touched in between); one
+// computes the cosines of the stages ahead; the others turn queries and keys.  Every wait
+// is bounded: on a timeout the block sets SPEC_STATUS_TIMEOUT, waits for its copies in
+// flight and returns.
+constexpr int kWorkers = 256, kBulkThreads = kWorkers + 64;
+constexpr int kMaxStages = 4, kMaxTokens = 16;
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+struct Ring {
+  uint64_t full[kMaxStages], done[kMaxStages], freed[kMaxStages];
+  int2 at[kMaxStages][kMaxTokens];  // position (-1: left out) and slot (-1: none) of a stage's tokens
+};
+
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t phase) {
+  return tc::mbar_try_wait(bar, phase & 1u) || tc::mbar_wait(bar, phase & 1u, kWaitNs);
+}
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"((uint64_t)dst),
+               "r"(tc::smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+
+// Stage i of the block holds tokens (blockIdx.x + i * gridDim.x) * tokens and on.
+template <typename T, bool INTER>
+__global__ void __launch_bounds__(kBulkThreads, 3) rope_bulk_kernel(spec_rope_cache_args p, int tokens, int stages) {
+  constexpr int VEC = 16 / (int)sizeof(T);
+  constexpr int kPairs = INTER ? VEC / 2 : VEC;  // of a unit: a vector, or a vector of each half
+  constexpr int kCol = kPairs / 2;               // float4s of its cosines and sines
+  extern __shared__ __align__(128) uint8_t bulk_s[];
+  const int half = p.rot >> 1, units = half / kPairs, turned = p.Hq + p.Hk;
+  const uint32_t head_bytes = p.D * (uint32_t)sizeof(T), row_bytes = (turned + p.Hk) * head_bytes;
+  const uint32_t stage_bytes = tokens * row_bytes;
+  Ring& ring = *reinterpret_cast<Ring*>(bulk_s + stages * stage_bytes);
+  float2* freq_s = reinterpret_cast<float2*>(&ring + 1);
+  float4* cs_s = reinterpret_cast<float4*>(freq_s + ((half + 1) & ~1));  // [stage][token][kCol][units]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int groups = (p.rows + tokens - 1) / tokens;
+  const int n = (groups - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  auto first_row = [&](int i) { return ((int)blockIdx.x + i * (int)gridDim.x) * tokens; };
+  constexpr int kLoader = kWorkers / 32, kCosines = kLoader + 1;
+
+  // the copies of a token: queries, keys, values
+  auto load = [&](int i) {
+    const int row0 = first_row(i), count = min(tokens, p.rows - row0), st = i % stages;
+    if (lane == 0) tc::mbar_expect_tx(&ring.full[st], count * row_bytes);
+    __syncwarp();
+    for (int c = lane; c < 3 * count; c += 32) {
+      const int t = c / 3, part = c - 3 * t;
+      const size_t row = (size_t)(row0 + t);
+      const T* from = part == 0 ? (const T*)p.q + row * p.q_row
+                      : part == 1 ? (const T*)p.k + row * p.k_row : (const T*)p.v + row * p.v_row;
+      const uint32_t bytes = (part == 0 ? p.Hq : p.Hk) * head_bytes;
+      const uint32_t to = part == 0 ? 0 : part == 1 ? p.Hq * head_bytes : turned * head_bytes;
+      if (bytes) tc::bulk_load(bulk_s + st * stage_bytes + t * row_bytes + to, from, bytes, &ring.full[st]);
+    }
+  };
+
+  if (warp == kLoader) {
+    if (lane < stages) {
+      tc::mbar_init(&ring.full[lane], 2);
+      tc::mbar_init(&ring.done[lane], kWorkers / 32);
+      tc::mbar_init(&ring.freed[lane], 1);
+    }
+    tc::fence_barrier_init();
+    __syncwarp();
+    for (int i = 0; i < min(stages, n); ++i) load(i);  // nobody waits for one before the barrier below
+  } else {
+    for (int f = tid; f < half; f += kWorkers) freq_s[f] = in_turns(p.freq[f]);
+  }
+  __syncthreads();
+
+  if (warp == kLoader) {
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const int st = i % stages;
+      ok = __all_sync(0xffffffffu, wait_for(&ring.done[st], i / stages));
+      if (!ok) break;
+      const int row0 = first_row(i), count = min(tokens, p.rows - row0);
+      for (int c = lane; c < 3 * count; c += 32) {
+        const int t = c / 3, part = c - 3 * t;
+        const int2 at = ring.at[st][t];
+        const uint8_t* from = bulk_s + st * stage_bytes + t * row_bytes;
+        const size_t slot = (size_t)at.y * p.Hk * p.D;
+        if (part == 0 && p.Hq && at.x >= 0)
+          bulk_store((T*)p.q_out + (size_t)(row0 + t) * p.q_out_row, from, p.Hq * head_bytes);
+        if (part == 1 && p.Hk && at.x >= 0 && at.y >= 0)
+          bulk_store((T*)p.k_cache + slot, from + p.Hq * head_bytes, p.Hk * head_bytes);
+        if (part == 2 && p.Hk && at.x >= 0 && at.y >= 0)
+          bulk_store((T*)p.v_cache + slot, from + turned * head_bytes, p.Hk * head_bytes);
+      }
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      if (i > 0 && i - 1 + stages < n) {  // the stage before this one has been read: its next tokens
+        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&ring.freed[(i - 1) % stages]);
+        load(i - 1 + stages);
+      }
+    }
+    if (!ok) {  // the loads in flight land before the block's memory goes
+      if (lane == 0) set_status(p.status, SPEC_STATUS_TIMEOUT);
+      for (int st = 0; st < stages; ++st) {
+        // the last load of a stage: the phase its barrier is in, or the one before
+        wait_for(&ring.full[st], 0);
+        wait_for(&ring.full[st], 1);
+      }
+    }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  } else if (warp == kCosines) {
+    auto read = [&](int i) {  // position and slot of token `lane` of stage i
+      const int row = first_row(i) + lane;
+      if (i >= n || lane >= tokens || row >= p.rows) return make_int2(0, -1);
+      return make_int2(p.position[row], p.slot ? p.slot[row] : -1);
+    };
+    int2 next = read(0);
+    uint32_t bad = 0;
+    for (int i = 0; i < n; ++i) {
+      const int st = i % stages;
+      int2 at = next;
+      next = read(i + 1);
+      if (at.x >= (1 << 24)) bad |= SPEC_STATUS_BAD_POSITION;
+      if (at.y >= p.n_slots) bad |= SPEC_STATUS_BAD_PAGE, at.y = -1;
+      const float x = (float)min(max(at.x, 0), (1 << 24) - 1);
+      if (i >= stages && !__all_sync(0xffffffffu, wait_for(&ring.freed[st], i / stages - 1))) break;
+      if (lane < tokens) ring.at[st][lane] = at;
+      for (int t = 0; t < tokens; ++t) {
+        const float pos = __shfl_sync(0xffffffffu, x, t);
+        float2* cs = reinterpret_cast<float2*>(cs_s + (size_t)(st * tokens + t) * kCol * units);
+        for (int f = lane; f < half; f += 32) {
+          const int u = f / kPairs, e = f % kPairs;
+          cs[((e >> 1) * units + u) * 2 + (e & 1)] = cos_sin(pos, freq_s[f], p.scale);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&ring.full[st]);
+    }
+    if (bad) set_status(p.status, bad);
+  } else {
+    const int share = kWorkers / tokens, t = tid / share, in_t = tid - t * share;  // a token's threads
+    const int at_once = units > 0 ? share / units : 0, h0 = units > 0 ? in_t / units : 0, u = in_t - h0 * units;
+    for (int i = 0; i < n; ++i) {
+      const int st = i % stages;
+      if (!__all_sync(0xffffffffu, wait_for(&ring.full[st], i / stages))) break;
+      if (t < tokens && h0 < at_once && first_row(i) + t < p.rows) {
+        const float4* col = cs_s + (size_t)(st * tokens + t) * kCol * units + u;
+        float4 cs[kCol];
+#pragma unroll
+        for (int j = 0; j < kCol; ++j) cs[j] = col[j * units];
+        uint8_t* at = bulk_s + st * stage_bytes + t * row_bytes + u * 16;
+#pragma unroll 3
+        for (int h = h0; h < turned; h += at_once) {
+          uint4* a = reinterpret_cast<uint4*>(at + h * head_bytes);
+          Vec<T, VEC> x, y;
+          x.raw = a[0];
+          if (INTER) {
+#pragma unroll
+            for (int j = 0; j < kCol; ++j) {
+              turn(x.e[4 * j], x.e[4 * j + 1], make_float2(cs[j].x, cs[j].y));
+              turn(x.e[4 * j + 2], x.e[4 * j + 3], make_float2(cs[j].z, cs[j].w));
+            }
+          } else {
+            y.raw = a[units];
+#pragma unroll
+            for (int j = 0; j < kCol; ++j) {
+              turn(x.e[2 * j], y.e[2 * j], make_float2(cs[j].x, cs[j].y));
+              turn(x.e[2 * j + 1], y.e[2 * j + 1], make_float2(cs[j].z, cs[j].w));
+            }
+            a[units] = y.raw;
+          }
+          a[0] = x.raw;
+        }
+      }
+      tc::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&ring.done[st]);
+    }
+  }
+}
+
+// Shared memory of a block with `stages` stages.
+template <typename T>
+size_t bulk_bytes(const spec_rope_cache_args& a, int tokens, int stages) {
+  const size_t half = a.rot / 2, row = (size_t)(a.Hq + 2 * a.Hk) * a.D * sizeof(T);
+  return stages * tokens * row + sizeof(Ring) + (half + 1) / 2 * 16 + stages * tokens * half * sizeof(float2);
+}
+// Three blocks an SM where four stages fit (40001 rows of 10 KB: 122 us, 125 with two
+// blocks and stages of 20 KB, 152 with one block), else two (9000 rows of 20 KB: 57.5 us,
+// 64 with three blocks of three stages).
+constexpr size_t kBulkMemory = 222 * 1024, kStageBytes = 17 * 1024;
+// From 12 MB on: below, the first round of stages is most of the work (3.7 MB: 6.9 us
+// against 5.5 of the kernel above; 12.5 MB: 6.2 both; 25 MB: 11.7 against 13.0; 52 MB: 19.7
+// against 26.0).  Two stages a block at least.
+constexpr size_t kBulkBytes = 12000000;
+constexpr int kBulkRows = 608;
+bool bulk_ok(const spec_rope_cache_args& a, size_t row_bytes) {
+  auto dense = [&](int n, int64_t head) { return n < 2 || head == a.D; };  // heads side by side
+  return a.rows >= kBulkRows && a.rows * row_bytes >= kBulkBytes && dense(a.Hq, a.q_head) &&
+         dense(a.Hq, a.q_out_head) && dense(a.Hk, a.k_head) && dense(a.Hk, a.v_head);
+}
+
+template <typename T>
+cudaError_t launch_bulk(const spec_rope_cache_args& a, int tokens, int stages, int blocks, cudaStream_t stream) {
+  const int groups = (a.rows + tokens - 1) / tokens, grid = std::min(groups, blocks * 152);
+  const size_t smem = bulk_bytes<T>(a, tokens, stages);
+  auto kernel = a.layout == SPEC_ROPE_INTERLEAVED ? rope_bulk_kernel<T, true> : rope_bulk_kernel<T, false>;
+  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBulkMemory / 2);
+  if (err != cudaSuccess) return err;
+  kernel<<<grid, kBulkThreads, smem, stream>>>(a, tokens, stages);
+  return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t launch_wide(const spec_rope_cache_args& a, cudaStream_t stream) {
   constexpr int VEC = 16 / (int)sizeof(T);
   const bool inter = a.layout == SPEC_ROPE_INTERLEAVED;
   const int half = a.rot / 2, heads = a.Hq + 2 * a.Hk;
+  if (bulk_ok(a, (size_t)heads * a.D * sizeof(T))) {
+    const size_t row = (size_t)heads * a.D * sizeof(T);
+    const int units = half / (inter ? VEC / 2 : VEC);  // no more of a token than its threads: 128 at most of 256
+    const int tokens = std::min({kMaxTokens, kWorkers / std::max(1, units), a.rows / kBulkRows,
+                                 std::max(1, (int)(kStageBytes / row))});
+    for (int blocks = 3; blocks >= 2; --blocks)
+      for (int stages = kMaxStages; stages >= (blocks == 3 ? kMaxStages : 3); --stages)
+        if (bulk_bytes<T>(a, tokens, stages) <= kBulkMemory / blocks)
+          return launch_bulk<T>(a, tokens, stages, blocks, stream);
+  }
   const int copied = (a.D + 2 * VEC - 1) / (2 * VEC);
   const int turned = inter ? copied : half / VEC + (a.D - a.rot + 2 * VEC - 1) / (2 * VEC);
   const int units = std::max(copied, turned);
