@@ -224,3 +224,23 @@ def test_refusals():
         vs.adjust_logits(z, presence=_f32([1] * 4))  # a penalty without tokens
     with pytest.raises(vs.SpecError):
         vs.adjust_logits(z, length=_i32([1] * 4), rows_per_request=2)  # eight rows of four
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("R,V,kw", [
+    (500, 1000, dict(new=5, hist=90)), (120, 9025, dict(new=9, offs=3)), (160, 6015, dict(new=4, n_masks=0)), (460, 7, dict(new=3)),
+    (456, 3009, dict(new=2, n_bias=40)), (40, 50257, dict(new=12, hist=300, n_bias=90)), (20, 40000, dict(new=64, hist=2000)),
+    (500, 3005, dict(pen=False, n_bias=0, n_masks=0)), (470, 3013, dict(new=3, ld=3019)), (230, 6008, dict(new=7, ld=6032, offs=1))])
+def test_many_rows(R, V, kw, dt):
+    """The formula, and the same bits as in place, where the results are written over the logits."""
+    c = Case(R, V, dt, **kw)
+    got = c.call()
+    c.check(got)
+    a, b = int(c.off[0]), int(c.off[-1])
+    src, c.logits = c.logits, c.logits.clone()
+    assert torch.equal(c.call(out=c.logits)[a:b], got[a:b])
+    # strided results on the same offsets from 16 bytes
+    c.logits = src
+    wide = torch.full((c.rows, src.stride(0) + 16), 3.0, dtype=dt, device="cuda")
+    assert torch.equal(c.call(out=wide[:, :V])[a:b], got[a:b])
+    assert torch.all(wide[:, V:] == 3) and torch.all(wide[:a] == 3) and torch.all(wide[b:] == 3)

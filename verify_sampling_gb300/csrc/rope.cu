@@ -292,11 +292,6 @@ struct Ring {
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t phase) {
   return tc::mbar_try_wait(bar, phase & 1u) || tc::mbar_wait(bar, phase & 1u, kWaitNs);
 }
-__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"((uint64_t)dst),
-               "r"(tc::smem_u32(src)), "r"(bytes)
-               : "memory");
-}
 
 // Stage i of the block holds tokens (blockIdx.x + i * gridDim.x) * tokens and on; `tokens`
 // divides the workers.
@@ -361,15 +356,15 @@ __global__ void __launch_bounds__(kBulkThreads, 3) rope_bulk_kernel(spec_rope_ca
         const uint8_t* from = bulk_s + st * stage_bytes + t * row_bytes;
         const size_t slot = (size_t)at.y * p.Hk * p.D;
         if (part == 0 && p.Hq && at.x >= 0)
-          bulk_store((T*)p.q_out + (size_t)(row0 + t) * p.q_out_row, from, p.Hq * head_bytes);
+          tc::bulk_store((T*)p.q_out + (size_t)(row0 + t) * p.q_out_row, from, p.Hq * head_bytes);
         if (part == 1 && p.Hk && at.x >= 0 && at.y >= 0)
-          bulk_store((T*)p.k_cache + slot, from + p.Hq * head_bytes, p.Hk * head_bytes);
+          tc::bulk_store((T*)p.k_cache + slot, from + p.Hq * head_bytes, p.Hk * head_bytes);
         if (part == 2 && p.Hk && at.x >= 0 && at.y >= 0)
-          bulk_store((T*)p.v_cache + slot, from + turned * head_bytes, p.Hk * head_bytes);
+          tc::bulk_store((T*)p.v_cache + slot, from + turned * head_bytes, p.Hk * head_bytes);
       }
-      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      tc::bulk_commit();
       if (i > 0 && i - 1 + stages < n) {  // the stage before this one has been read: its next tokens
-        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        tc::bulk_wait_read<1>();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&ring.freed[(i - 1) % stages]);
         load(i - 1 + stages);
@@ -383,7 +378,7 @@ __global__ void __launch_bounds__(kBulkThreads, 3) rope_bulk_kernel(spec_rope_ca
         wait_for(&ring.full[st], 1);
       }
     }
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    tc::bulk_wait();
   } else if (warp == kCosines) {
     auto read = [&](int i) {  // position and slot of token `lane` of stage i
       const int row = first_row(i) + lane;
