@@ -7,6 +7,7 @@ itself belong to the stream it runs on.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import struct
@@ -104,18 +105,19 @@ def _bind(L: ctypes.CDLL) -> None:
 
 
 _i32, _i64, _f32, _f64 = torch.int32, torch.int64, torch.float32, torch.float64
+_Tensor = torch.Tensor
 _codes = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16}
 
 
 def _t(t: torch.Tensor, name: str, dtype: torch.dtype, numel: int = 0) -> int:
     """Address of a contiguous device tensor of this dtype (and at least numel entries)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
-        _dev(t, name)
+    if isinstance(t, _Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous():
+        if not numel or t.numel() >= numel:
+            return t.data_ptr()
+    _dev(t, name)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if t.numel() < numel:
-        raise ValueError(f"{name} must have {numel} entries")
-    return t.data_ptr()
+    raise ValueError(f"{name} must have {numel} entries")
 
 
 def _opt(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, numel: int = 0) -> int:
@@ -133,12 +135,12 @@ def _on(stream, t: torch.Tensor) -> int:
     return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
-def _made(stream, make):
-    """The call's own tensors: memory of the stream it runs on."""
-    if stream is None:
-        return make()
-    with torch.cuda.stream(stream):
-        return make()
+_HERE = contextlib.nullcontext()
+
+
+def _made(stream):
+    """The call's own tensors are memory of the stream it runs on."""
+    return _HERE if stream is None else torch.cuda.stream(stream)
 
 
 # ------------------------------------------------------------- cache tables --
@@ -162,22 +164,24 @@ def cache_reserve(cache: dict, row_off: torch.Tensor, rows: int, *,
     "position", "request", "slot" [rows] int32, "ring_pos" [2] int64}, which ``cache_commit`` takes."""
     table, ring = cache["block_table"], cache["ring"]
     R, width = table.shape
-    if out is None:
-        def make():
-            dev = table.device  # (tensors of their own: views of one cost twice as much to make)
-            return {"new_len": torch.empty(R, dtype=_i32, device=dev),
-                    "position": torch.empty(rows, dtype=_i32, device=dev),
-                    "request": torch.empty(rows, dtype=_i32, device=dev),
-                    "slot": torch.empty(rows, dtype=_i32, device=dev),
-                    "ring_pos": torch.empty(2, dtype=_i64, device=dev)}
-        out = _made(stream, make)
+    if out is None:  # (tensors of their own: views of one cost twice as much to make)
+        dev = table.device
+        with _made(stream):
+            new = torch.empty(R, dtype=_i32, device=dev)
+            position = torch.empty(rows, dtype=_i32, device=dev)
+            request = torch.empty(rows, dtype=_i32, device=dev)
+            slot = torch.empty(rows, dtype=_i32, device=dev)
+            pos = torch.empty(2, dtype=_i64, device=dev)
+        out = {"new_len": new, "position": position, "request": request, "slot": slot, "ring_pos": pos}
+        made = pos.data_ptr(), new.data_ptr(), position.data_ptr(), request.data_ptr(), slot.data_ptr()
+    else:
+        made = (_t(out["ring_pos"], "out ring_pos", _i64, 2), _t(out["new_len"], "new_len", _i32, R),
+                _t(out["position"], "position", _i32, rows), _t(out["request"], "request", _i32, rows),
+                _t(out["slot"], "slot", _i32, rows))
     _RESERVE(_on(stream, table), R, rows, cache["page_size"], ring.numel(), width,
              _t(cache["kv_len"], "kv_len", _i32, R), _t(row_off, "row_off", _i32, R + 1),
              _opt(pos_base, "pos_base", _i32, R), _t(table, "block_table", _i32), _t(ring, "ring", _i32),
-             _t(cache["ring_pos"], "ring_pos", _i64, 2), _t(out["ring_pos"], "out ring_pos", _i64, 2),
-             _t(out["new_len"], "new_len", _i32, R), _t(out["position"], "position", _i32, rows),
-             _t(out["request"], "request", _i32, rows), _t(out["slot"], "slot", _i32, rows),
-             _opt(status, "status", _i32, 1))
+             _t(cache["ring_pos"], "ring_pos", _i64, 2), *made, _opt(status, "status", _i32, 1))
     return out
 
 
@@ -191,14 +195,17 @@ def cache_commit(cache: dict, reserved: dict, keep: torch.Tensor, *, out: Option
     table, ring = cache["block_table"], cache["ring"]
     R, width = table.shape
     if out is None:
-        dev = table.device
-        out = _made(stream, lambda: {"kv_len": torch.empty(R, dtype=_i32, device=dev),
-                                     "ring_pos": torch.empty(2, dtype=_i64, device=dev)})
+        with _made(stream):
+            kv = torch.empty(R, dtype=_i32, device=table.device)
+            pos = torch.empty(2, dtype=_i64, device=table.device)
+        out = {"kv_len": kv, "ring_pos": pos}
+        made = pos.data_ptr(), kv.data_ptr()
+    else:
+        made = _t(out["ring_pos"], "out ring_pos", _i64, 2), _t(out["kv_len"], "out kv_len", _i32, R)
     _COMMIT(_on(stream, table), R, cache["page_size"], ring.numel(), width,
             _t(cache["kv_len"], "kv_len", _i32, R), _t(reserved["new_len"], "new_len", _i32, R),
             _t(keep, "keep", _i32, R), _t(table, "block_table", _i32), _t(ring, "ring", _i32),
-            _t(reserved["ring_pos"], "ring_pos", _i64, 2), _t(out["ring_pos"], "out ring_pos", _i64, 2),
-            _t(out["kv_len"], "out kv_len", _i32, R), _opt(status, "status", _i32, 1))
+            _t(reserved["ring_pos"], "ring_pos", _i64, 2), *made, _opt(status, "status", _i32, 1))
     return out
 
 
@@ -246,7 +253,7 @@ def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: str = "none", 
 
 def _strided(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) -> tuple:
     """Address and the row and head strides of [rows, heads, D] whose last dimension is dense."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
@@ -271,8 +278,11 @@ def rope_cache(q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Ten
     dt = q.dtype
     qp, qr, qh = _strided(q, "q", dt, shape)
     if q_out is None:
-        q_out = _made(stream, lambda: torch.empty(shape, dtype=dt, device=q.device))
-    op, orow, oh = _strided(q_out, "q_out", dt, shape)
+        with _made(stream):
+            q_out = torch.empty(shape, dtype=dt, device=q.device)
+        op, orow, oh = q_out.data_ptr(), Hq * D, D
+    else:
+        op, orow, oh = _strided(q_out, "q_out", dt, shape)
     if k is None:
         Hk = n_slots = sp = kc = vc = kp = vp = kr = kh = vr = vh = 0
     else:
@@ -325,16 +335,19 @@ def prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     strides = _strided(q, "q", dt, shape)
     dev = q.device
 
-    def make():
-        return (torch.empty(shape, dtype=dt, device=dev) if out is None else out,
-                torch.empty((rows, Hq), dtype=_f32, device=dev) if want_lse and lse is None else lse,
-                torch.empty(attention_workspace_bytes(rows, R, Hq, D), dtype=torch.uint8, device=dev)
-                if workspace is None else workspace)
-    out, lse, workspace = _made(stream, make)
+    with _made(stream):
+        made = out is None
+        if made:
+            out = torch.empty(shape, dtype=dt, device=dev)
+        if want_lse and lse is None:
+            lse = torch.empty((rows, Hq), dtype=_f32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(attention_workspace_bytes(rows, R, Hq, D), dtype=torch.uint8, device=dev)
     _ATTENTION(_on(stream, q), R, rows, Hq, Hk, D, _code(q), P, n_pages, width, G, pages,
                D ** -0.5 if scale is None else scale, *strides, _t(k_cache, "k_cache", dt),
                _t(v_cache, "v_cache", dt), _t(row_off, "row_off", _i32, R + 1), _t(kv_len, "kv_len", _i32, R),
-               _t(block_table, "block_table", _i32), go, pl, pt, *_strided(out, "out", dt, shape),
+               _t(block_table, "block_table", _i32), go, pl, pt,
+               *((out.data_ptr(), Hq * D, D) if made else _strided(out, "out", dt, shape)),
                _opt(lse, "lse", _f32, rows * Hq), _dev(workspace, "workspace").data_ptr(),
                workspace.numel() * workspace.element_size(), _opt(status, "status", _i32, 1))
     return (out, lse) if want_lse else out
@@ -372,7 +385,8 @@ def adjust_logits(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None,
     lp, ld = _matrix(logits, "logits", dt)
     rows, V = shape = logits.shape
     if out is None:
-        out = _made(stream, lambda: torch.empty(shape, dtype=dt, device=logits.device))
+        with _made(stream):
+            out = torch.empty(shape, dtype=dt, device=logits.device)
         op, old = out.data_ptr(), V
     else:
         op, old = _matrix(out, "out", dt)
