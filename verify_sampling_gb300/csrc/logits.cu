@@ -31,7 +31,9 @@ namespace {
 
 constexpr int kThreads = 256;
 // A slice of any alignment meets slice / VEC + 1 vectors: just under whole pieces of 128.
-constexpr int kMaxSlice = 3040;  // 31 KB of tables: seven blocks an SM (4096: 545 us at the round case, against 460)
+// 31 KB of tables; registers (48) allow five blocks an SM.  At the round case 461 us,
+// slices of 4096 545, six blocks (42 registers) 500, seven 662.
+constexpr int kMaxSlice = 3040;
 constexpr int kMinSlice = 992;
 constexpr int kUnroll = 4;
 constexpr int kBuilders = kThreads / 2;  // threads that build the tables
