@@ -328,7 +328,8 @@ cudaError_t launch(const spec_prefix_attention_args& a, float* part, float2* sta
   const long long units = (long long)a.rows * a.Hq;
   // Blocks for the mean request's rows (a longer one's loop), and shares of at least
   // 64 keys, until there are about eight blocks an SM for 152 SMs, within the
-  // workspace's partial rows.
+  // workspace's partial rows.  (fp32, heads of 80: 40 requests 84 us, 95 with four blocks
+  // an SM, 89 with sixteen; 9 requests 26.7 us, 34.2 with shares of 128 keys.)
   const long long keys = ((long long)a.max_pages + (a.G > 0 ? a.max_prefix_pages : 0)) * a.page_size;
   const long long per_head = a.Hq / a.Hk;
   const long long tiles = std::min<long long>(512, (a.rows * per_head + (long long)kRows * a.R - 1) / ((long long)kRows * a.R));

@@ -231,16 +231,22 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(spec_cache_commit_args
 // Up to 256 requests are one round of 256 threads' scan; more take fewer rounds of
 // 1024, whose start and barriers cost more (R = 1: 4.9 us a reserve and commit
 // against 6.9; R = 512: 11.7 against 8.9).
+// Small blocks where the scan is one round of a few warps (reserve and commit of 32
+// requests: 6.2 us, 7.5 with 1024 threads; of 128: 11.0 and 9.0), and, for the reserve,
+// where there are more blocks than two an SM (250 prompts in 489 blocks: both 11.7, 15.1
+// with 1024 threads).
+constexpr int kFew = 32;
+
 cudaError_t launch_cache_reserve(const spec_cache_reserve_args& a, cudaStream_t stream) {
   const int blocks = std::max(1, (int)(((long long)a.rows + kChunk - 1) / kChunk));
-  if (a.R <= 256) reserve_kernel<256><<<blocks, 256, 0, stream>>>(a);
+  if (a.R <= kFew || (a.R <= 256 && blocks > 2 * 152)) reserve_kernel<256><<<blocks, 256, 0, stream>>>(a);
   else reserve_kernel<1024><<<blocks, 1024, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
 cudaError_t launch_cache_commit(const spec_cache_commit_args& a, cudaStream_t stream) {
   const int blocks = std::max(1, (a.R + kOwn - 1) / kOwn);
-  if (a.R <= 256) commit_kernel<256><<<blocks, 256, 0, stream>>>(a);
+  if (a.R <= kFew) commit_kernel<256><<<blocks, 256, 0, stream>>>(a);
   else commit_kernel<1024><<<blocks, 1024, 0, stream>>>(a);
   return cudaGetLastError();
 }

@@ -502,11 +502,9 @@ cudaError_t launch_wide(const spec_rope_cache_args& a, cudaStream_t stream) {
   const int copied = (a.D + 2 * VEC - 1) / (2 * VEC);
   const int turned = inter ? copied : half / VEC + (a.D - a.rot + 2 * VEC - 1) / (2 * VEC);
   const int units = std::max(copied, turned);
-  // Heads at once: a token's heads over a group of threads, kUnroll a thread
-  // where there are rows enough; with few rows one, so that a token is one step.
-  const int share = a.rows >= 304 ? kUnroll : 1;
+  // Heads at once: a token's heads over a group of threads, kUnroll a thread.
   const int most = std::max(1, kMaxThreads / units);
-  const int at_once = std::min(most, (heads + share - 1) / share);
+  const int at_once = std::min(most, (heads + kUnroll - 1) / kUnroll);
   const int chunks = (heads + kUnroll * at_once - 1) / (kUnroll * at_once);
   const int group = units * at_once;
   const int groups = std::max(1, std::min({kRopeTokens, kMaxThreads / group, std::max(1, a.rows / 304)}));
