@@ -154,3 +154,18 @@ def test_refusals():
         vs.cache_reserve(c, torch.zeros(5, dtype=torch.int32), 4)
     with pytest.raises(vs.SpecError):
         vs.cache_reserve(c, _i32([0] * 5), 4, out={**vs.cache_reserve(c, _i32([0] * 5), 4), "ring_pos": c["ring_pos"]})
+
+
+@pytest.mark.parametrize("R,n", [(40, 30), (100, 3), (200, 1700)])
+def test_a_wide_capacity_gives_the_same_rows_and_pads_the_rest(R, n):
+    off, width = np.arange(R + 1) * n, 2 * (n // 16 + 2)
+    few, many = [vs.cache_tables(R, R * width, 16, width) for _ in range(2)]
+    for _ in range(2):
+        a, b = vs.cache_reserve(few, _i32(off), R * n), vs.cache_reserve(many, _i32(off), R * n + 330000)
+        for key in ("position", "request", "slot"):
+            assert torch.equal(b[key][:R * n], a[key]) and torch.all(b[key][R * n:] == -1)
+        assert torch.equal(a["new_len"], b["new_len"]) and torch.equal(few["block_table"], many["block_table"])
+        assert a["slot"].min() >= 0 and a["slot"].unique().numel() == R * n
+        for c, p in ((few, a), (many, b)):
+            c.update(vs.cache_commit(c, p, _i32(np.full(R, n - 1))))
+        assert torch.equal(few["kv_len"], many["kv_len"]) and torch.equal(few["ring"], many["ring"])
