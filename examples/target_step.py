@@ -26,8 +26,9 @@ BF16, I32 = torch.bfloat16, torch.int32
 
 
 class TargetStep:
-    """R requests behind one shared prefix; ``tokens`` [R, room] int32 are each request's own tokens so
-    far (``length`` of them, ``prompt_len`` of those the prompt).  All but a request's last token are in the cache."""
+    """R requests behind one shared prefix; ``tokens`` are each request's own tokens so far (``length`` of them,
+    ``prompt_len`` of those the prompt).  All but a request's last token are in the cache, which has pages for
+    ``room`` tokens a request: one whose next rows do not fit is refused by cache_reserve and stays as it is."""
 
     def __init__(self, R=6, gamma=4, V=1000, Hq=8, Hk=2, D=64, page_size=16, prefix=75, prompt=9, room=400, seed=0):
         dev, g = "cuda", torch.Generator("cuda").manual_seed(seed)
@@ -59,7 +60,8 @@ class TargetStep:
         self.group_off = torch.tensor([0, R], dtype=I32, device=dev)
         self.pos_base = torch.full((R,), prefix, dtype=I32, device=dev)
 
-        self.tokens = torch.zeros(R, room, dtype=I32, device=dev)
+        # a full cache's tokens and the last emitted one; the last column takes what a round does not emit
+        self.tokens = torch.zeros(R, own * page_size + 2, dtype=I32, device=dev)
         self.tokens[:, :prompt] = torch.randint(0, V, (R, prompt), generator=g, device=dev, dtype=I32)
         self.prompt_len = torch.full((R,), prompt, dtype=I32, device=dev)
         self.length = self.prompt_len.clone()
@@ -81,11 +83,13 @@ class TargetStep:
         self.cache.update(vs.cache_commit(self.cache, r, torch.full((R,), n, dtype=I32, device=dev), status=self.status))
 
     def _project(self, tokens, position, slot):
-        """Embeddings of the rows and their turned queries; keys and values go to the cache."""
+        """Embeddings of the rows and their turned queries (zeros where a row has no position); keys and values
+        go to the cache."""
         h = self.embed[tokens.long()]
         qkv = (h @ self.w_qkv).view(len(h), self.Hq + 2 * self.Hk, self.D)
         q = vs.rope_cache(qkv[:, :self.Hq], qkv[:, self.Hq:self.Hq + self.Hk], qkv[:, self.Hq + self.Hk:], self.freq, position,
-                          slot, self.k_cache, self.v_cache, scale=self.rope_scale, status=self.status)
+                          slot, self.k_cache, self.v_cache, scale=self.rope_scale, status=self.status,
+                          q_out=torch.zeros(len(h), self.Hq, self.D, dtype=BF16, device=h.device))
         return h, q
 
     def round(self, seed: int) -> dict:
@@ -107,13 +111,16 @@ class TargetStep:
                                   mask_row=self.mask_row, status=self.status, **self.penalty)
         v = vs.verify(vs.VERIFY_SAMPLE, logits, s["row_off"], s["ell"], d["x"], seed, q_tok=d["q_tok"], lse_q=d["lse_q"],
                       draft=self.draft_in, status=self.status)
-        self.cache.update(vs.cache_commit(self.cache, r, v["n_out"], status=self.status))
+        # a refused request (its new rows, one at least, are not in the cache) emits nothing
+        n_out = torch.where(r["new_len"] > self.cache["kv_len"], v["n_out"], 0)
+        self.cache.update(vs.cache_commit(self.cache, r, n_out, status=self.status))
         # emitted tokens join the history
         i = torch.arange(G1, device=req.device)[None, :]
-        to = torch.where(i < v["n_out"][:, None], self.length[:, None] + i, self.tokens.shape[1] - 1).long()
+        to = torch.where(i < n_out[:, None], self.length[:, None] + i, self.tokens.shape[1] - 1).long()
         self.tokens.scatter_(1, to, v["out_tok"].clamp(min=0))
-        self.length = self.length + v["n_out"]
-        self.x0 = v["out_tok"].gather(1, (v["n_out"][:, None] - 1).long())[:, 0].contiguous()
+        self.length = self.length + n_out
+        last = v["out_tok"].gather(1, (n_out[:, None] - 1).clamp(min=0).long())[:, 0]
+        self.x0 = torch.where(n_out > 0, last, self.x0)
         return {"fed": fed, "reserved": r, "sched": s, "draft": d, "raw": raw, "logits": logits, "verify": v}
 
 
