@@ -465,7 +465,9 @@ int spec_round_host(const spec_round_host_args *args, uint64_t seed, spec_stream
  * token before the draft and the accepted ones have their keys in the cache):
  *   kept_r = min(kv_r + keep[r], new_len[r]), or 0 where keep[r] < 0 (the request
  *   has ended); kv_out[r] = kept_r; the pages block_table[r][ceil(kept_r / P) ..
- *   ceil(new_len[r] / P)) go to the ring from its tail on, in request order.
+ *   ceil(new_len[r] / P)) go to the ring from its tail on, in request order.  A page
+ *   id outside [0, n_pages) is not given back (SPEC_STATUS_BAD_PAGE): the others
+ *   close up.
  *   Table entries past the kept ones keep their old values and mean nothing.
  *
  *   ring_pos  [2] int64 {head, tail}: pages ring[head mod n_pages ..) up to tail

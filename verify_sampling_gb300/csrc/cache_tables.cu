@@ -158,26 +158,34 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(spec_cache_reserve_ar
   if (bad) set_status(a.status, bad);
 }
 
+// A page id outside the cache gets no place in the ring: the ids after it close up.  So
+// a block looks at the ids of the requests before its own too, kPages a thread at a time
+// and in order; where none is strange (the one extra barrier tells) a page's place is its
+// number, otherwise the strange ones are scanned.
+constexpr int kPages = 4;
+
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) commit_kernel(spec_cache_commit_args a) {
   __shared__ unsigned long long warp_sum[kThreads / 32];
-  __shared__ int stay_s[kOwn];
-  __shared__ unsigned at_s[kOwn + 1];
+  __shared__ unsigned long long at_s[kThreads];  // of a scan's requests: number of the first page given back,
+  __shared__ int stay_s[kThreads];               // and its table entry
   const int tid = threadIdx.x, P = a.page_size;
   const int own0 = blockIdx.x * kOwn, own1 = min(own0 + kOwn, a.R);
-  const bool first = blockIdx.x == 0;
   const long long head = a.ring_pos[0], tail = a.ring_pos[1];
+  // the ring has room for n_pages ids: more than that can only come from bad lengths
+  const unsigned long long room = (unsigned long long)max(0ll, a.n_pages - max(tail - head, 0ll));
+  long long tm = tail % a.n_pages;
+  if (tm < 0) tm += a.n_pages;
   uint32_t bad = 0;
 
-  unsigned long long carry = 0;
-  const int upto = first ? a.R : own1;  // block 0 also needs the total
-  for (int r0 = 0; r0 < upto; r0 += kThreads) {
+  unsigned long long carry = 0;  // pages that have got a place
+  for (int r0 = 0; r0 < own1; r0 += kThreads) {
     const int r = r0 + tid;
-    int kept = 0, stay = 0, back = 0;
-    if (r < upto) {
+    int stay = 0, back = 0;
+    if (r < own1) {
       const int kv = a.kv_len[r], len = a.new_len[r], keep = a.keep[r];
-      const bool ok = kv >= 0 && len >= kv && ceil_div(len, P) <= a.max_pages;
-      if (ok) {
+      int kept;
+      if (kv >= 0 && len >= kv && ceil_div(len, P) <= a.max_pages) {
         kept = keep < 0 ? 0 : (keep < len - kv ? kv + keep : len);
         stay = ceil_div(kept, P);
         back = ceil_div(len, P) - stay;
@@ -185,43 +193,58 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(spec_cache_commit_args
         bad |= SPEC_STATUS_BAD_LEN;
         kept = max(kv, 0);
       }
+      if (r >= own0) a.kv_out[r] = kept;
     }
     unsigned long long all;
-    const unsigned at = (unsigned)(carry + block_scan<kThreads>((unsigned long long)back, warp_sum, &all));
-    carry += all;
-    if (r >= own0 && r < own1) {
-      stay_s[r - own0] = stay;
-      at_s[r - own0] = at;
-      if (r == own1 - 1) at_s[own1 - own0] = at + back;
-      a.kv_out[r] = kept;
-    }
-  }
-  __syncthreads();
-  // the ring has room for n_pages ids: more than that can only come from bad lengths
-  const long long room = max(0ll, a.n_pages - max(tail - head, 0ll));
-  if (first && tid == 0) {
-    const long long total = (long long)carry;
-    if (total > room) bad |= SPEC_STATUS_BAD_LEN;
-    a.ring_out[0] = head;
-    a.ring_out[1] = tail + min(total, room);
-  }
-  const int n_own = own1 - own0;
-  if (n_own > 0) {
-    long long tm = tail % a.n_pages;
-    if (tm < 0) tm += a.n_pages;
-    const unsigned end = at_s[n_own];
-    for (unsigned i = at_s[0] + tid; i < end; i += kThreads) {
-      if ((long long)i >= room) break;
-      int lo = 0, hi = n_own;  // the last request whose pages start at or before i
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (at_s[mid] <= i) lo = mid;
-        else hi = mid;
+    const unsigned long long at = block_scan<kThreads>((unsigned long long)back, warp_sum, &all);
+    if (all == 0) continue;
+    at_s[tid] = at;
+    stay_s[tid] = stay;
+    __syncthreads();
+    for (unsigned long long i0 = 0; i0 < all; i0 += kThreads * kPages) {
+      int page[kPages];
+      bool here[kPages], strange[kPages], found = false;  // here: a page of an own request
+#pragma unroll
+      for (int u = 0; u < kPages; ++u) {
+        const unsigned long long i = i0 + u * kThreads + tid;
+        here[u] = strange[u] = false;
+        page[u] = 0;
+        if (i >= all) continue;
+        int lo = 0, hi = kThreads;  // the last request whose pages start at or before i
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (at_s[mid] <= i) lo = mid;
+          else hi = mid;
+        }
+        here[u] = r0 + lo >= own0;
+        page[u] = a.block_table[(size_t)(r0 + lo) * a.max_pages + stay_s[lo] + (i - at_s[lo])];
       }
-      const int page = a.block_table[(size_t)(own0 + lo) * a.max_pages + stay_s[lo] + (i - at_s[lo])];
-      if (page < 0 || page >= a.n_pages) bad |= SPEC_STATUS_BAD_PAGE;
-      a.ring[(tm + i) % a.n_pages] = page;
+#pragma unroll
+      for (int u = 0; u < kPages; ++u) {
+        strange[u] = page[u] < 0 || page[u] >= a.n_pages;
+        found |= strange[u];
+      }
+      const bool any = __syncthreads_or(found);
+      if (any) bad |= SPEC_STATUS_BAD_PAGE;
+#pragma unroll
+      for (int u = 0; u < kPages; ++u) {
+        const unsigned long long i = i0 + u * kThreads + tid;
+        unsigned long long misses = 0, before = 0;
+        if (any) before = block_scan<kThreads>(strange[u] ? 1ull : 0ull, warp_sum, &misses);
+        const unsigned long long place = carry + i - before;
+        if (here[u] && !strange[u] && place < room) {
+          const long long q = tm + (long long)place;
+          a.ring[q < a.n_pages ? q : q - a.n_pages] = page[u];
+        }
+        carry -= misses;  // (counts from i = 0 of this scan)
+      }
     }
+    carry += all;
+  }
+  if (blockIdx.x == gridDim.x - 1 && tid == 0) {  // the block that has seen every request
+    if (carry > room) bad |= SPEC_STATUS_BAD_LEN;
+    a.ring_out[0] = head;
+    a.ring_out[1] = tail + (long long)min(carry, room);
   }
   if (bad) set_status(a.status, bad);
 }
