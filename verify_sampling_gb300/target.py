@@ -3,7 +3,8 @@ positions with the cache write, shared-prefix attention and logit adjustments.
 
 Like the rest of the binding these functions only marshal arguments; layouts,
 rules and status bits are in ``include/spec.h``.  Tensors that a call makes for
-itself belong to the stream it runs on.
+itself belong to the stream it runs on.  Tensors and streams have to be of the
+current device, where the kernels are launched.
 """
 from __future__ import annotations
 
@@ -109,11 +110,26 @@ _Tensor = torch.Tensor
 _codes = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16}
 
 
+def _device() -> int:
+    """The current device, which every launch goes to."""
+    return torch._C._cuda_getDevice()
+
+
+def _here(t: torch.Tensor, name: str) -> None:
+    """Raise unless t is a tensor of the current device."""
+    if not isinstance(t, _Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != _device():
+        raise ValueError(f"{name} must lie on the current device")
+
+
 def _t(t: torch.Tensor, name: str, dtype: torch.dtype, numel: int = 0) -> int:
-    """Address of a contiguous device tensor of this dtype (and at least numel entries)."""
-    if isinstance(t, _Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous():
+    """Address of a contiguous tensor of the current device, of this dtype (and at least numel entries)."""
+    # (a host tensor's device is -1)
+    if isinstance(t, _Tensor) and t.get_device() == _device() and t.dtype is dtype and t.is_contiguous():
         if not numel or t.numel() >= numel:
             return t.data_ptr()
+    _here(t, name)
     _dev(t, name)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
@@ -129,8 +145,11 @@ def _code(t: torch.Tensor) -> int:
 
 
 def _on(stream, t: torch.Tensor) -> int:
-    """Handle of the stream to launch on: the given one, or the current one of t's device."""
+    """Handle of the stream to launch on: the given one, or the current one of t's device, which the check
+    of t makes the current device."""
     if stream is not None:
+        if stream.device.index != _device():
+            raise ValueError("stream must be one of the current device")
         return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(t.get_device())
 
@@ -253,8 +272,8 @@ def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: str = "none", 
 
 def _strided(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) -> tuple:
     """Address and the row and head strides of [rows, heads, D] whose last dimension is dense."""
-    if not isinstance(t, _Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
+    if not isinstance(t, _Tensor) or t.get_device() != _device():
+        _here(t, name)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
     if t.shape != shape:
@@ -335,6 +354,8 @@ def prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     strides = _strided(q, "q", dt, shape)
     dev = q.device
 
+    if workspace is not None:
+        _here(workspace, "workspace")
     with _made(stream):
         made = out is None
         if made:
@@ -355,9 +376,8 @@ def prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
 
 # -------------------------------------------------------- logit adjustments --
 def _matrix(t: torch.Tensor, name: str, dtype: torch.dtype) -> tuple:
-    """Address and row stride of a device matrix with dense rows."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
+    """Address and row stride of a matrix with dense rows on the current device."""
+    _here(t, name)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
