@@ -523,7 +523,8 @@ int spec_cache_commit(const spec_cache_commit_args *args, spec_stream_t stream);
  * long-context scaling makes of the frequencies, scale its attention factor.
  *   q  [rows, Hq, D], k, v [rows, Hk, D] (dtype), element strides *_row and
  *      *_head, the last dimension dense: parts of one projection's output will do
- *   q_out  [rows, Hq, D] by q_out_row / q_out_head; may be q itself
+ *   q_out  [rows, Hq, D] by q_out_row / q_out_head; may be q itself, with q's
+ *      strides (SPEC_ERR_INVALID_ARG for others); otherwise it overlaps no input
  *   k_cache, v_cache  [n_slots, Hk, D] dense (n_slots = pages * page size)
  *   freq [rot / 2] f64 radians per position;  position, slot [rows] int32
  * position < 0: the row is left out (q_out not written).  position >= 2^24:

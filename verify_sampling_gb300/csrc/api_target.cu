@@ -131,6 +131,9 @@ int spec_rope_cache(const spec_rope_cache_args* args, spec_stream_t stream) {
   if (a.rows > 0) {
     if (!a.position || (a.rot > 0 && !a.freq)) return SPEC_ERR_INVALID_ARG;
     if (a.Hq > 0 && (!a.q || !a.q_out)) return SPEC_ERR_INVALID_ARG;
+    // in place: every element where it was, or one row's results would be another's input
+    if (a.Hq > 0 && a.q == a.q_out && ((a.rows > 1 && a.q_row != a.q_out_row) || (a.Hq > 1 && a.q_head != a.q_out_head)))
+      return SPEC_ERR_INVALID_ARG;
     if (a.Hk > 0 && (!a.k || !a.v || !a.k_cache || !a.v_cache || !a.slot || a.n_slots < 1))
       return SPEC_ERR_INVALID_ARG;
   }
