@@ -66,7 +66,8 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(spec_cache_reserve_ar
   __shared__ unsigned long long warp_sum[kThreads / 32];
   __shared__ unsigned taken_s;
   const int tid = threadIdx.x, P = a.page_size;
-  const int b0 = blockIdx.x * kChunk, b1 = min(b0 + kChunk, a.rows);
+  // (no sum of these passes a.rows, which may be any int)
+  const int b0 = blockIdx.x * kChunk, n_rows = min(kChunk, a.rows - b0), b1 = b0 + n_rows;
   const bool first = blockIdx.x == 0;
   const long long head = a.ring_pos[0], tail = a.ring_pos[1];
   const long long avail = min(max(tail - head, 0ll), (long long)a.n_pages);
@@ -122,7 +123,8 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(spec_cache_reserve_ar
   }
 
   const int n_list = min((int)(unsigned)carry, kChunk);
-  for (int b = b0 + tid; b < b1; b += kThreads) {
+  for (int i = tid; i < n_rows; i += kThreads) {
+    const int b = b0 + i;
     int lo = 0, hi = n_list;  // the last entry that starts at or before row b
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
