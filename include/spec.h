@@ -574,7 +574,9 @@ int spec_rope_cache(const spec_rope_cache_args *args, spec_stream_t stream);
  *   q, out  [rows, Hq, D] by element strides; caches [n_pages, page_size, Hk, D]
  *   kv_len [R], block_table [R, max_pages]; group_off [G + 1], prefix_len [G],
  *   prefix_table [G, max_prefix_pages] (G = 0: no prefixes); lse [rows, Hq] nullable
- *   workspace  spec_attention_workspace_bytes(rows, R, Hq, D) bytes
+ *   workspace  spec_attention_workspace_bytes(rows, R, Hq, D) bytes: about 4 (D + 2)
+ *            (2 min(rows Hq, 2^20) + 2^16), 34 MB to 1.1 GB at D = 128 (calls of more
+ *            query rows run in windows of packed rows, one after the other)
  * bf16 with D 64 or 128, pages of 8, 16, 32, 64 or a multiple of 128 tokens and
  * 16-byte rows take the tensor-core kernels; everything else the generic ones.
  * A length past its page table is cut to it, a bad row or group range left out

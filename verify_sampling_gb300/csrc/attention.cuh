@@ -1,6 +1,8 @@
 // Shared-prefix attention: what its kernels share, and their launchers.
 #pragma once
 
+#include <algorithm>
+
 #include "common.cuh"
 
 namespace spec {
@@ -79,9 +81,13 @@ __device__ __forceinline__ int last_at_or_below(const int32_t* off, int n, int v
 
 }  // namespace attn
 
+// The tensor-core kernels take packed rows in windows of up to 2^20 query rows (rows x
+// heads), one after the other, so that their workspace is bounded: 1.1 GB at heads of 128,
+// where 2^25 query rows in one would leave 34 GB of pieces.  A window is thousands of items.
+inline int attn_window_rows(int Hq) { return std::max(1, (1 << 20) / Hq); }
 // Partial rows (D fp32 values, a maximum and a sum each) that a workspace has room for.
 inline size_t attn_partial_rows(int rows, int Hq) {
-  return 2 * (size_t)rows * Hq + (size_t)attn::kMaxCtas * attn::kItemRows;
+  return 2 * (size_t)std::min(rows, attn_window_rows(Hq)) * Hq + (size_t)attn::kMaxCtas * attn::kItemRows;
 }
 // Bytes of the work positions that the tensor-core kernel leaves for its join.
 inline size_t attn_plan_bytes(int R) { return (size_t)(2 * (size_t)R + 2) * 8; }

@@ -62,8 +62,16 @@ constexpr float kSlack = 8.f;  // log2 units the maximum may grow by before O is
 constexpr int kCostPair = 17, kCostSingle = 15, kCostStartPair = 57, kCostStartSingle = 21;
 
 // ------------------------------------------------------------ work layout --
+struct Window {  // the packed rows of a launch: [lo, hi)
+  int lo, hi;
+};
+__device__ __forceinline__ Rows inside(const Rows& rows, const Window& w) {
+  const int lo = max(rows.row0, w.lo), hi = min(rows.row0 + rows.n, w.hi);
+  return Rows{lo, max(hi - lo, 0)};
+}
+
 struct Segment {  // a group's prefix or a request's own keys
-  int row0, n;    // packed rows
+  int row0, n;    // packed rows in the window
   int keys;
   int first_own;  // own index of row 0's last key + 1 (prefix: keys)
   const int32_t* table;
@@ -88,19 +96,20 @@ struct Layout {
   int64_t s0;
 };
 
-__device__ __forceinline__ Segment segment(const spec_prefix_attention_args& a, int k, uint32_t* bad) {
+__device__ __forceinline__ Segment segment(const spec_prefix_attention_args& a, const Window& w, int k, uint32_t* bad) {
   Segment s;
   if (k < a.G) {
     const int2 in = group_requests(a, k, bad);
-    const Rows rows = rows_between(a, in.x, in.y, bad);
+    const Rows rows = inside(rows_between(a, in.x, in.y, bad), w);
     s = Segment{rows.row0, rows.n, prefix_keys(a, k, bad), 0,
                 a.prefix_table + (size_t)k * a.max_prefix_pages, true};
     s.first_own = s.keys;
   } else {
     const int r = k - a.G;
-    const Rows rows = rows_between(a, r, r + 1, bad);
+    const Rows all = rows_between(a, r, r + 1, bad), rows = inside(all, w);
     const int kv = own_keys(a, r, bad);
-    s = Segment{rows.row0, rows.n, kv, kv - rows.n + 1, a.block_table + (size_t)r * a.max_pages, false};
+    s = Segment{rows.row0, rows.n, kv, kv - all.n + 1 + (rows.row0 - all.row0),
+                a.block_table + (size_t)r * a.max_pages, false};
   }
   return s;
 }
@@ -156,14 +165,15 @@ __device__ __forceinline__ int tiles_before(int x, int rows) {
 // this code to be fetched.)
 struct Walker {
   const spec_prefix_attention_args& a;
+  const Window& w;
   int64_t pos, x0, x1;
   int k, h, i, per_head, count;
   Segment seg;
   bool alone;  // a request without a prefix
   uint32_t bad;
 
-  __device__ Walker(const spec_prefix_attention_args& args, const Layout& lay)
-      : a(args), pos(lay.s0), x0(lay.x0), x1(lay.x1), k(lay.k0 - 1), h(0), i(0),
+  __device__ Walker(const spec_prefix_attention_args& args, const Window& window, const Layout& lay)
+      : a(args), w(window), pos(lay.s0), x0(lay.x0), x1(lay.x1), k(lay.k0 - 1), h(0), i(0),
         per_head(args.Hq / args.Hk), count(0), alone(false), bad(0) {}
   __device__ __forceinline__ bool next(Item& it) {
 #pragma unroll 1
@@ -173,7 +183,7 @@ struct Walker {
         if (count == 0 || ++h >= a.Hk) {
           h = 0;
           if (++k >= a.G + a.R) return false;
-          seg = segment(a, k, &bad);
+          seg = segment(a, w, k, &bad);
           count = item_count(seg, per_head);
           alone = k >= a.G && (a.G == 0 || shared_keys(a, k - a.G, &bad) == 0);
           if (count > 0 && pos < x0) {  // the layout starts in this segment: whole heads before it
@@ -203,7 +213,7 @@ struct Walker {
       it.prefix = seg.prefix;
       it.direct = alone && it.lo == 0 && it.hi == tiles;
       it.table = seg.table;
-      it.slot = (seg.prefix ? 0 : (size_t)a.rows * a.Hq) + (size_t)seg.row0 * a.Hq + (size_t)h * m +
+      it.slot = (seg.prefix ? 0 : (size_t)(w.hi - w.lo) * a.Hq) + (size_t)(seg.row0 - w.lo) * a.Hq + (size_t)h * m +
                 it.m0 + (size_t)kItemRows * blockIdx.x;
       return true;
     }
@@ -394,7 +404,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                         const __grid_constant__ CUtensorMap q_map, const int q_box,
-                        const spec_prefix_attention_args a, float* part, float2* stat, int64_t* plan) {
+                        const spec_prefix_attention_args a, const Window w, float* part, float2* stat, int64_t* plan) {
   using S = Smem<D>;
   constexpr int kHalves = D / 64;
   constexpr int kHalfBytes = kTile * 128;  // 64 elements of 128 keys
@@ -415,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n_seg = a.G + a.R, run = (n_seg + kThreads - 1) / kThreads;
     const int k0 = min(tid * run, n_seg), k1 = min(k0 + run, n_seg);
     uint32_t bad = 0;
-    auto cost_of = [&](int k) { return a.Hk * head_cost(segment(a, k, &bad), per_head); };
+    auto cost_of = [&](int k) { return a.Hk * head_cost(segment(a, w, k, &bad), per_head); };
     int64_t mine = 0;
 #pragma unroll 1
     for (int k = k0; k < k1; ++k) mine += cost_of(k);
@@ -667,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kPlanner) {
     // ------------------------------------------------------------- planner --
-    Walker walk(a, lay);
+    Walker walk(a, w, lay);
     Item it;
     for (uint32_t n_item = 0;; ++n_item) {
       if (!walk.next(it)) it.rows = 0;  // the end
@@ -942,15 +952,15 @@ __device__ __forceinline__ void costs_of(const Segment& s, int per_head, int upt
 // is a chain of dependent loads, paid once a block.  Half a warp a row: twice the rows in
 // flight (the round of 256 requests behind a prefix 779 us in all, 790 with a warp a row).
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads, 4)
-    join_tc_kernel(const spec_prefix_attention_args a, const float* part, const float2* stat, const int64_t* plan) {
+__device__ __forceinline__ void join_request(const spec_prefix_attention_args& a, const Window& w, int r,
+                                             const float* part, const float2* stat, const int64_t* plan) {
   constexpr int kPer = D / kJoinLanes, kBatch = 4;
-  const int r = blockIdx.x, lane = threadIdx.x % kJoinLanes, per_head = a.Hq / a.Hk;
+  const int lane = threadIdx.x % kJoinLanes, per_head = a.Hq / a.Hk;
   uint32_t bad = 0;
-  const Segment own = segment(a, a.G + r, &bad);
+  const Segment own = segment(a, w, a.G + r, &bad);
   int g = group_of(a, r, &bad);
   Segment pre{0, 0, 0, 0, nullptr, true};
-  if (g >= 0) pre = segment(a, g, &bad);
+  if (g >= 0) pre = segment(a, w, g, &bad);
   if (own.row0 < pre.row0 || own.row0 + own.n > pre.row0 + pre.n) g = -1;  // rows out of order
   const int m_own = own.n * per_head;
   const int m_off = (own.row0 - pre.row0) * per_head;  // the request's first row among the group's
@@ -962,17 +972,17 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
   int item[2] = {-1, -1}, head = -1;  // own and prefix item, and key head, whose pieces are known
   int64_t before[2] = {0, 0}, all[2] = {0, 0};
   int first[2] = {0, 0}, count[2] = {0, 0};
-  auto pieces = [&](int w, const Segment& s, int64_t at, int h, int i) {  // blocks that have pieces of item i
-    if (i == item[w] && h == head) return;
+  auto pieces = [&](int k, const Segment& s, int64_t at, int h, int i) {  // blocks that have pieces of item i
+    if (i == item[k] && h == head) return;
     const int tiles = (item_keys(s, i, per_head) + kTile - 1) / kTile;
-    count[w] = 0;
-    if (i != item[w]) costs_of(s, per_head, i, &before[w], &all[w]);
-    item[w] = i;
+    count[k] = 0;
+    if (i != item[k]) costs_of(s, per_head, i, &before[k], &all[k]);
+    item[k] = i;
     if (tiles == 0) return;
     const int rows = s.n * per_head - i * kItemRows;
-    at += h * all[w] + before[w] + start_cost(rows);
-    first[w] = (int)(at / per);
-    count[w] = (int)((at + (int64_t)(tiles - 1) * tile_cost(rows)) / per) - first[w] + 1;
+    at += h * all[k] + before[k] + start_cost(rows);
+    first[k] = (int)(at / per);
+    count[k] = (int)((at + (int64_t)(tiles - 1) * tile_cost(rows)) / per) - first[k] + 1;
   };
 
   const bool wide_out = ((uintptr_t)a.out & 7) == 0 && a.out_row % 4 == 0 && a.out_head % 4 == 0;
@@ -980,8 +990,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
 #pragma unroll 1
   for (int x = blockIdx.y; x < all_tiles; x += gridDim.y) {
     const int h = x / tiles, m0 = (x - h * tiles) * kJoinRows;
-    const size_t own_slot = (size_t)a.rows * a.Hq + (size_t)own.row0 * a.Hq + (size_t)h * m_own;
-    const size_t pre_slot = (size_t)pre.row0 * a.Hq + (size_t)h * pre.n * per_head + m_off;
+    const size_t own_slot = ((size_t)(w.hi - w.lo) + (own.row0 - w.lo)) * a.Hq + (size_t)h * m_own;
+    const size_t pre_slot = (size_t)(pre.row0 - w.lo) * a.Hq + (size_t)h * pre.n * per_head + m_off;
     for (int m = m0 + threadIdx.x / kJoinLanes; m < min(m0 + kJoinRows, m_own); m += kJoinThreads / kJoinLanes) {
       pieces(0, own, own_at, h, m / kItemRows);
       if (g >= 0) pieces(1, pre, pre_at, h, (m_off + m) / kItemRows);
@@ -1048,6 +1058,35 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
   }
 }
 
+// Where the window is a part of the rows (kPart), the blocks share out its requests, from
+// the first to the last that has rows in it; otherwise there is a block for each.
+template <int D, bool kPart>
+__global__ void __launch_bounds__(kJoinThreads, 4)
+    join_tc_kernel(const spec_prefix_attention_args a, const Window w, const float* part, const float2* stat,
+                   const int64_t* plan) {
+  int r = blockIdx.x;
+  if (!kPart) {
+    join_request<D>(a, w, r, part, stat, plan);
+    return;
+  }
+  __shared__ int first_s, last_s;
+  if (threadIdx.x == 0) first_s = a.R, last_s = -1;
+  __syncthreads();
+  int first = a.R, last = -1;
+#pragma unroll 8
+  for (int i = threadIdx.x; i < a.R; i += kJoinThreads) {
+    const int row0 = a.row_off[i], row1 = a.row_off[i + 1];
+    if (row0 < row1 && row0 < w.hi && row1 > w.lo) first = min(first, i), last = max(last, i);
+  }
+  if (last >= 0) {
+    atomicMin(&first_s, first);
+    atomicMax(&last_s, last);
+  }
+  __syncthreads();
+  for (r += first_s; r <= last_s; r += gridDim.x) join_request<D>(a, w, r, part, stat, plan);
+  tc::grid_dep_wait();  // a block without requests, too, ends after the pieces' kernel
+}
+
 template <int D>
 cudaError_t launch(const spec_prefix_attention_args& a, int sms, float* part, float2* stat, int64_t* plan,
                    cudaStream_t stream) {
@@ -1072,13 +1111,15 @@ cudaError_t launch(const spec_prefix_attention_args& a, int sms, float* part, fl
   cudaError_t err = cudaFuncSetAttribute(attention_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Smem<D>::kBytes);
   if (err != cudaSuccess) return err;
-  attention_tc_kernel<D><<<sms, kThreads, Smem<D>::kBytes, stream>>>(km, vm, qm, q_box, a, part, stat, plan);
-  if ((err = cudaGetLastError()) != cudaSuccess) return err;
+  // windows of equal size
+  const int most_rows = attn_window_rows(a.Hq), windows = (int)(((int64_t)a.rows + most_rows - 1) / most_rows);
+  const int step = (int)(((int64_t)a.rows + windows - 1) / windows);
+  // a block of the join a tile of the mean request, until there are kJoinBlocks of them
+  const int64_t tiles = (((int64_t)a.rows * per_head + (int64_t)kJoinRows * a.R - 1) / ((int64_t)kJoinRows * a.R)) * a.Hk;
+  const int at_once = std::min(a.R, (a.R + windows - 1) / windows + (windows > 1));  // requests of a window
+  const int64_t most = (kJoinBlocks + at_once - 1) / at_once;
   cudaLaunchConfig_t cfg{};
-  // a block a tile of the mean request, until there are kJoinBlocks of them
-  const int64_t tiles = (((int64_t)a.rows * (a.Hq / a.Hk) + (int64_t)kJoinRows * a.R - 1) / ((int64_t)kJoinRows * a.R)) * a.Hk;
-  const int64_t most = (kJoinBlocks + a.R - 1) / a.R;
-  cfg.gridDim = dim3(a.R, (unsigned)(tiles < most ? tiles : most));
+  cfg.gridDim = dim3(at_once, (unsigned)(tiles < most ? tiles : most));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1086,8 +1127,15 @@ cudaError_t launch(const spec_prefix_attention_args& a, int sms, float* part, fl
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_tc_kernel<D>, a, (const float*)part, (const float2*)stat,
-                            (const int64_t*)plan);
+  for (int64_t lo = 0; lo < a.rows; lo += step) {
+    const Window w{(int)lo, (int)std::min<int64_t>(lo + step, a.rows)};
+    attention_tc_kernel<D><<<sms, kThreads, Smem<D>::kBytes, stream>>>(km, vm, qm, q_box, a, w, part, stat, plan);
+    if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    err = cudaLaunchKernelEx(&cfg, windows > 1 ? join_tc_kernel<D, true> : join_tc_kernel<D, false>, a, w,
+                             (const float*)part, (const float2*)stat, (const int64_t*)plan);
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
