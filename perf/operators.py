@@ -241,11 +241,15 @@ def run(s):
 
 
 def _tables_own(vs, s):
+    # The commit writes to a second ring that the program keeps: returned pages may take the places of those that the
+    # reserve took, and a round that is run again from its start has to find these.
     c = s["cache"]
+    if "after" not in s:
+        s["after"] = {**c, "ring": c["ring"].clone()}
     p = vs.cache_reserve(c, s["row_off"], s["rows"], pos_base=s["base"])
-    d = vs.cache_commit(c, p, s["keep"])
+    d = vs.cache_commit(s["after"], p, s["keep"])
     return {"new_len": p["new_len"], "position": p["position"], "request": p["request"], "slot": p["slot"], "block_table": c["block_table"],
-            "ring": c["ring"], "ring_pos": d["ring_pos"], "kv_len": d["kv_len"]}
+            "ring": s["after"]["ring"], "ring_pos": d["ring_pos"], "kv_len": d["kv_len"]}
 
 
 def _rope_own(vs, s):
