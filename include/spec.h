@@ -458,7 +458,9 @@ int spec_round_host(const spec_round_host_args *args, uint64_t seed, spec_stream
  * tail - head, and it needs any) or in its page table (want_r > max_pages), gets
  * none: SPEC_STATUS_NO_PAGES, its rows get -1 and new_len[r] = max(kv_r, 0).  The same
  * holds, with SPEC_STATUS_BAD_LEN, for a request with kv_r < 0 or with rows
- * outside [0, rows] or in descending order.  A page id outside [0, n_pages)
+ * outside [0, rows] or in descending order.  Requests refused for their table, length
+ * or rows count nothing in off_r; one refused for the ring counts what it asked for, so
+ * that every later request that needs a page is refused too, whatever the ring still has.  A page id outside [0, n_pages)
  * gives slot -1 and SPEC_STATUS_BAD_PAGE.
  *
  * spec_cache_commit, after the verification (keep = spec_verify's n_out: the
@@ -478,7 +480,8 @@ int spec_round_host(const spec_round_host_args *args, uint64_t seed, spec_stream
  * arrays (SPEC_ERR_INVALID_ARG for equal pointers): blocks of the same launch
  * still read the inputs.  Repeating a call with the same inputs repeats its
  * outputs.  Sizes: 0 <= R <= 65535, page_size >= 1, 1 <= max_pages,
- * n_pages * page_size < 2^31, 0 <= rows < 2^31; positions stay below 2^31.
+ * n_pages * page_size < 2^31, 0 <= rows < 2^31; positions stay below 2^31
+ * (spec_rope_cache takes them below 2^24).
  */
 typedef struct spec_cache_reserve_args {
   int R, rows, page_size, n_pages, max_pages;

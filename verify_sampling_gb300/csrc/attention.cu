@@ -12,8 +12,8 @@
 // row's keys (few rows, long contexts) are joined by a second kernel.
 // Bound by FMA issue where a request has 8 rows x heads or more, else by the fetches.
 // (A warp a row and query head, 8 lanes to a key, fetched every key once for each of
-// them and spent most of its instructions on reductions: 390 us for 40 requests of 16
-// heads behind a prefix of 1500 tokens, 155 us now.)
+// them and spent most of its instructions on reductions: 390 us for 40 requests of up to 6
+// rows, 16 heads of 80 on 2 key heads, fp32, behind a prefix of 1500 tokens, 151 us now.)
 #include "attention.cuh"
 
 #include <algorithm>
@@ -328,8 +328,9 @@ cudaError_t launch(const spec_prefix_attention_args& a, float* part, float2* sta
   const long long units = (long long)a.rows * a.Hq;
   // Blocks for the mean request's rows (a longer one's loop), and shares of at least
   // 64 keys, until there are about eight blocks an SM for 152 SMs, within the
-  // workspace's partial rows.  (fp32, heads of 80: 40 requests 84 us, 95 with four blocks
-  // an SM, 89 with sixteen; 9 requests 26.7 us, 34.2 with shares of 128 keys.)
+  // workspace's partial rows.  (The 40 requests above 151 us, 159 with four blocks an SM, 147
+  // with sixteen; without their prefix 57.7, 60.0 and 57.9; 9 requests of 12 heads of 80 behind
+  // prefixes of 500 tokens 25.4 us, 32.8 with shares of 128 keys.)
   const long long keys = ((long long)a.max_pages + (a.G > 0 ? a.max_prefix_pages : 0)) * a.page_size;
   const long long per_head = a.Hq / a.Hk;
   const long long tiles = std::min<long long>(512, (a.rows * per_head + (long long)kRows * a.R - 1) / ((long long)kRows * a.R));

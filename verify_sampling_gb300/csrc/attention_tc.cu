@@ -57,8 +57,8 @@ constexpr int kItemSlots = 4, kItemReaders = 3 + kSoftWarps;  // producer, MMA, 
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kSlack = 8.f;  // log2 units the maximum may grow by before O is rescaled
 // Costs, in units of 0.1 us, measured: a tile of an item of both softmax groups (bound
-// by the products), a tile of a smaller one (bound by its 64 KB), and an item's
-// start and end.
+// by the products), a tile of a smaller one (bound by its 64 KB where all blocks stream,
+// otherwise by its chain of product, softmax and product), and an item's start and end.
 constexpr int kCostPair = 17, kCostSingle = 15, kCostStartPair = 57, kCostStartSingle = 21;
 
 // ------------------------------------------------------------ work layout --
@@ -950,7 +950,8 @@ __device__ __forceinline__ void costs_of(const Segment& s, int per_head, int upt
 // Joins the pieces of every row that has more than one.  A block takes a request's
 // rows, tiles of 64 of one key head after the other: what says where their pieces are
 // is a chain of dependent loads, paid once a block.  Half a warp a row: twice the rows in
-// flight (the round of 256 requests behind a prefix 779 us in all, 790 with a warp a row).
+// flight (the round of 256 requests behind a prefix 779 us in all, 790 with a warp a row, both in
+// short runs: after half a second the power limit's clock makes it 828).
 template <int D>
 __device__ __forceinline__ void join_request(const spec_prefix_attention_args& a, const Window& w, int r,
                                              const float* part, const float2* stat, const int64_t* plan) {

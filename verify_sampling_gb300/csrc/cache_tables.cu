@@ -8,7 +8,7 @@
 // Layout: no block waits for another.  Every block scans the lengths of all
 // requests itself (8 bytes a request, from L2 after the first block) and keeps
 // the part it needs: reserve the requests whose rows meet its kChunk packed rows,
-// commit the kOwn requests whose pages it returns.  One launch each, where a
+// commit the kOwn requests whose pages it returns (and a look at the ids of those before).  One launch each, where a
 // scan kernel followed by a map kernel would be two.  Rows are dealt out, not
 // requests, so one prompt of thousands of tokens spreads over the GPU like
 // thousands of requests of one token.
@@ -253,13 +253,10 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(spec_cache_commit_args
 
 }  // namespace
 
-// Up to 256 requests are one round of 256 threads' scan; more take fewer rounds of
-// 1024, whose start and barriers cost more (R = 1: 4.9 us a reserve and commit
-// against 6.9; R = 512: 11.7 against 8.9).
-// Small blocks where the scan is one round of a few warps (reserve and commit of 32
-// requests: 6.2 us, 7.5 with 1024 threads; of 128: 11.0 and 9.0), and, for the reserve,
-// where there are more blocks than two an SM (250 prompts in 489 blocks: both 11.7, 15.1
-// with 1024 threads).
+// Blocks of 256 threads where the scan is one round of a few warps (reserve and commit of 1
+// request: 4.7 us, 5.7 with 1024 threads; of 32: 7.3 and 8.0; of 128: 9.6 and 8.8; of 512:
+// 15.6 and 9.9), and, for the reserve, where there are more blocks than two an SM (250
+// prompts in 486 blocks: 6.2 us, 9.2 with 1024 threads; their commit 8.2 and 6.2).
 constexpr int kFew = 32;
 
 cudaError_t launch_cache_reserve(const spec_cache_reserve_args& a, cudaStream_t stream) {

@@ -461,8 +461,9 @@ size_t bulk_bytes(const spec_rope_cache_args& a, int tokens, int stages) {
 // 64 with three blocks of three stages).
 constexpr size_t kBulkMemory = 222 * 1024, kStageBytes = 17 * 1024;
 // From 12 MB on: below, the first round of stages is most of the work (3.7 MB: 6.9 us
-// against 5.5 of the kernel above; 12.5 MB: 6.2 both; 25 MB: 11.7 against 13.0; 52 MB: 19.7
-// against 26.0).  Two stages a block at least.
+// against 5.5 of the kernel above, 12.5 MB that lie in L2 6.2 both).  Inputs that do not lie
+// in L2: 12.3 MB in 750 rows, most blocks with one or two stages, 6.9 us against 8.3; 12.5 MB
+// in 610 rows 7.2 against 8.4; 26.6 MB 11.5 against 16.0.  kBulkRows is four tokens an SM.
 constexpr size_t kBulkBytes = 12000000;
 constexpr int kBulkRows = 608;
 bool bulk_ok(const spec_rope_cache_args& a, size_t row_bytes) {
