@@ -162,16 +162,21 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(spec_cache_reserve_ar
 
 // A page id outside the cache gets no place in the ring: the ids after it close up.  So
 // a block looks at the ids of the requests before its own too, kPages a thread at a time
-// and in order; where none is strange (the one extra barrier tells) a page's place is its
-// number, otherwise the strange ones are scanned.
+// and in order; where none is strange (one barrier tells) a page's place is its number,
+// otherwise the strange ones are scanned.  The request of a page is the last one that
+// starts at or before it: starts are marked in shared memory and a maximum runs over the
+// marks (a binary search a page spent 4 us of 11 on bank conflicts with 2000 requests).
 constexpr int kPages = 4;
 
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) commit_kernel(spec_cache_commit_args a) {
+  constexpr int kRound = kThreads * kPages;
   __shared__ unsigned long long warp_sum[kThreads / 32];
   __shared__ unsigned long long at_s[kThreads];  // of a scan's requests: number of the first page given back,
   __shared__ int stay_s[kThreads];               // and its table entry
-  const int tid = threadIdx.x, P = a.page_size;
+  __shared__ __align__(8) uint16_t mark_s[kRound];  // 1 + the request that starts at a page, 0: none
+  __shared__ int warp_top[kThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, P = a.page_size;
   const int own0 = blockIdx.x * kOwn, own1 = min(own0 + kOwn, a.R);
   const long long head = a.ring_pos[0], tail = a.ring_pos[1];
   // the ring has room for n_pages ids: more than that can only come from bad lengths
@@ -181,11 +186,15 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(spec_cache_commit_args
   uint32_t bad = 0;
 
   unsigned long long carry = 0;  // pages that have got a place
+  int kv = 0, len = 0, keep = 0;
+  auto lengths = [&](int r) {
+    if (r < own1) kv = a.kv_len[r], len = a.new_len[r], keep = a.keep[r];
+  };
+  lengths(tid);
   for (int r0 = 0; r0 < own1; r0 += kThreads) {
     const int r = r0 + tid;
     int stay = 0, back = 0;
     if (r < own1) {
-      const int kv = a.kv_len[r], len = a.new_len[r], keep = a.keep[r];
       int kept;
       if (kv >= 0 && len >= kv && ceil_div(len, P) <= a.max_pages) {
         kept = keep < 0 ? 0 : (keep < len - kv ? kv + keep : len);
@@ -197,27 +206,39 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(spec_cache_commit_args
       }
       if (r >= own0) a.kv_out[r] = kept;
     }
+    lengths(r + kThreads);  // the next scan's, on their way during this one's pages
     unsigned long long all;
     const unsigned long long at = block_scan<kThreads>((unsigned long long)back, warp_sum, &all);
-    if (all == 0) continue;
     at_s[tid] = at;
     stay_s[tid] = stay;
-    __syncthreads();
-    for (unsigned long long i0 = 0; i0 < all; i0 += kThreads * kPages) {
+    for (unsigned long long i0 = 0; i0 < all; i0 += kRound) {
+      reinterpret_cast<uint2*>(mark_s)[tid] = make_uint2(0u, 0u);
+      __syncthreads();
+      if (back > 0 && at < i0 + kRound && at + back > i0) mark_s[at > i0 ? at - i0 : 0] = (uint16_t)(tid + 1);
+      __syncthreads();
+      const uint2 m = reinterpret_cast<const uint2*>(mark_s)[tid];
+      int owner[kPages] = {(int)(m.x & 0xffffu), (int)(m.x >> 16), (int)(m.y & 0xffffu), (int)(m.y >> 16)};
+#pragma unroll
+      for (int u = 1; u < kPages; ++u) owner[u] = max(owner[u], owner[u - 1]);
+      int top = owner[kPages - 1];  // of the warp's threads up to this one
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, top, o);
+        if (lane >= o) top = max(top, t);
+      }
+      if (lane == 31) warp_top[warp] = top;
+      __syncthreads();
+      const int before_warp = __reduce_max_sync(0xffffffffu, lane < warp ? warp_top[lane] : 0);
+      const int up = __shfl_up_sync(0xffffffffu, top, 1), before = max(before_warp, lane > 0 ? up : 0);
       int page[kPages];
       bool here[kPages], strange[kPages], found = false;  // here: a page of an own request
 #pragma unroll
       for (int u = 0; u < kPages; ++u) {
-        const unsigned long long i = i0 + u * kThreads + tid;
-        here[u] = strange[u] = false;
+        const unsigned long long i = i0 + tid * kPages + u;
+        here[u] = false;
         page[u] = 0;
         if (i >= all) continue;
-        int lo = 0, hi = kThreads;  // the last request whose pages start at or before i
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (at_s[mid] <= i) lo = mid;
-          else hi = mid;
-        }
+        const int lo = max(owner[u], before) - 1;
         here[u] = r0 + lo >= own0;
         page[u] = a.block_table[(size_t)(r0 + lo) * a.max_pages + stay_s[lo] + (i - at_s[lo])];
       }
@@ -226,20 +247,24 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(spec_cache_commit_args
         strange[u] = page[u] < 0 || page[u] >= a.n_pages;
         found |= strange[u];
       }
-      const bool any = __syncthreads_or(found);
-      if (any) bad |= SPEC_STATUS_BAD_PAGE;
+      unsigned long long gone = 0, misses = 0;
+      if (__syncthreads_or(found)) {
+        bad |= SPEC_STATUS_BAD_PAGE;
+        unsigned long long mine = 0;
+#pragma unroll
+        for (int u = 0; u < kPages; ++u) mine += strange[u];
+        gone = block_scan<kThreads>(mine, warp_sum, &misses);
+      }
 #pragma unroll
       for (int u = 0; u < kPages; ++u) {
-        const unsigned long long i = i0 + u * kThreads + tid;
-        unsigned long long misses = 0, before = 0;
-        if (any) before = block_scan<kThreads>(strange[u] ? 1ull : 0ull, warp_sum, &misses);
-        const unsigned long long place = carry + i - before;
+        const unsigned long long place = carry + (i0 + tid * kPages + u) - gone;
         if (here[u] && !strange[u] && place < room) {
           const long long q = tm + (long long)place;
           a.ring[q < a.n_pages ? q : q - a.n_pages] = page[u];
         }
-        carry -= misses;  // (counts from i = 0 of this scan)
+        gone += strange[u];
       }
+      carry -= misses;  // (the pages' numbers count from this scan's first)
     }
     carry += all;
   }
@@ -253,10 +278,9 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(spec_cache_commit_args
 
 }  // namespace
 
-// Blocks of 256 threads where the scan is one round of a few warps (reserve and commit of 1
-// request: 4.7 us, 5.7 with 1024 threads; of 32: 7.3 and 8.0; of 128: 9.6 and 8.8; of 512:
-// 15.6 and 9.9), and, for the reserve, where there are more blocks than two an SM (250
-// prompts in 486 blocks: 6.2 us, 9.2 with 1024 threads; their commit 8.2 and 6.2).
+// Reserve: blocks of 256 threads where the scan is one round of a few warps (1 request 2.7 us,
+// 3.3 with 1024 threads; 32 requests 3.7 and 3.9; 64 4.5 and 4.1; 512 7.0 and 4.5), and where
+// there are more blocks than two an SM (250 prompts in 486 blocks: 6.2 us, 9.2 with 1024).
 constexpr int kFew = 32;
 
 cudaError_t launch_cache_reserve(const spec_cache_reserve_args& a, cudaStream_t stream) {
@@ -268,7 +292,10 @@ cudaError_t launch_cache_reserve(const spec_cache_reserve_args& a, cudaStream_t 
 
 cudaError_t launch_cache_commit(const spec_cache_commit_args& a, cudaStream_t stream) {
   const int blocks = std::max(1, (a.R + kOwn - 1) / kOwn);
-  if (a.R <= kFew) commit_kernel<256><<<blocks, 256, 0, stream>>>(a);
+  // 256 threads where one block has all requests (32 requests 3.1 us, 4.3 with 1024 threads; 128
+  // 3.4 and 4.6); more requests bring more pages (512 requests 5.8 and 4.7, 250 prompts 5.2 and
+  // 4.7; 256 requests that give back few 3.5 and 4.7).
+  if (a.R <= kOwn) commit_kernel<256><<<blocks, 256, 0, stream>>>(a);
   else commit_kernel<1024><<<blocks, 1024, 0, stream>>>(a);
   return cudaGetLastError();
 }
