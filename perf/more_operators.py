@@ -235,12 +235,12 @@ def _rows_own(vs, s):
                            q_weight=s["q_weight"], k_weight=s["k_weight"], eps=EPS, interleaved=s["interleaved"], scale=s["scale"])
     if s["op"] == "norm":
         return {"q": q, "k_cache": s["k_cache"], "v_cache": s["v_cache"]}
-    k, v = vs.cache_read_int4(s["k_cache"], s["v_cache"], s["slot"])
+    k, v = vs.cache_read_packed(s["k_cache"], s["v_cache"], s["slot"])
     return {"q": q, "k": k, "v": v}
 
 
 def _attend_own(vs, s):
-    out, lse = vs.prefix_attention_int4(s["q"], s["k_cache"], s["v_cache"], s["row_off"], s["kv_len"], s["block_table"], scale=s["scale"],
+    out, lse = vs.prefix_attention_packed(s["q"], s["k_cache"], s["v_cache"], s["row_off"], s["kv_len"], s["block_table"], scale=s["scale"],
                                         group_off=s["group_off"], prefix_len=s["prefix_len"], prefix_table=s["prefix_table"], want_lse=True)
     return {"out": out, "lse": lse}
 
