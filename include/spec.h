@@ -611,6 +611,92 @@ int spec_prefix_attention(const spec_prefix_attention_args *args, spec_stream_t 
 /* Workspace of spec_prefix_attention (0 if the sizes are invalid). */
 size_t spec_attention_workspace_bytes(int rows, int R, int Hq, int D);
 
+/* ------------------------------------- head norms and caches in 4 bits ----
+ * A paged cache in 4 bits (SPEC_CACHE_PACKED) holds a token's head in D / 32 groups
+ * of 32 elements: 16 bytes (element j in nibble j, the low one of a byte first)
+ * and a scale byte b, which stands for s = 2^((b >> 3) - 20) (1 + (b & 7) / 8); an
+ * element is s (nibble - 8), exact in bf16.  Written from fp32 values x: s is the
+ * largest |x| of the group / 7, rounded to its four significant bits (halves up;
+ * 2^-20 to 3840), the nibble 8 + x / s to nearest (halves to even), 1 to 15.  So no
+ * element is off by more than s / 2 while |x| < 26880, where elements saturate.  NaN is
+ * stored as 0, an infinity as +-7 s with the largest s.
+ *   data    [n_pages, Hk, D / 32, page_size, 16] bytes, 16-byte aligned
+ *   scales  [n_pages, Hk, page_size, D / 32] bytes
+ * D is a multiple of 32 (SPEC_ERR_UNSUPPORTED).  Slots are those of
+ * spec_cache_reserve: page * page_size + place.
+ *
+ * spec_norm_rope_cache: spec_rope_cache for models that norm each head of queries
+ * and keys first, and for either kind of cache.  With a weight w [D] (f32) a head x is
+ *   x_i * w_i / sqrt(sum_j x_j^2 / D + eps)
+ * in fp32 before its pairs turn (spec_rope_cache's formula, layouts, frequencies and
+ * scale; elements past rot keep the norm's result); values are written as they are.
+ * One rounding at the end, to the stored type or to 4 bits.  A NULL weight leaves its heads
+ * without norm: with both NULL and SPEC_CACHE_DTYPE the results are spec_rope_cache's.
+ * k_cache, v_cache: [n_slots, Hk, D] of dtype, or the packed data, n_slots being n_pages *
+ * page_size then; page_size and the scales are read for SPEC_CACHE_PACKED alone.
+ * Everything else (positions, slots, strides, Hk = 0, Hq = 0, in place) as in
+ * spec_rope_cache.  Sizes: its own, and eps >= 0 and finite.
+ */
+enum spec_cache_kind { SPEC_CACHE_DTYPE = 0, SPEC_CACHE_PACKED = 1 };
+
+typedef struct spec_norm_rope_args {
+  int rows, Hq, Hk, D, rot;
+  int dtype;     /* spec_dtype of q, k, v, q_out and a SPEC_CACHE_DTYPE cache */
+  int layout;    /* spec_rope_layout */
+  int cache;     /* spec_cache_kind  */
+  int page_size; /* SPEC_CACHE_PACKED  */
+  float scale, eps;
+  const void *q, *k, *v;
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head;
+  void *q_out;
+  int64_t q_out_row, q_out_head;
+  void *k_cache, *v_cache;
+  uint8_t *k_scale, *v_scale; /* SPEC_CACHE_PACKED */
+  int64_t n_slots;
+  const float *q_weight, *k_weight; /* [D], each nullable */
+  const double *freq;
+  const int32_t *position, *slot;
+  uint32_t *status;
+} spec_norm_rope_args;
+
+int spec_norm_rope_cache(const spec_norm_rope_args *args, spec_stream_t stream);
+
+/* spec_cache_read_packed: the values of slots of an packed cache, k and v [rows, Hk, D]
+ * dense in dtype (exact in both types); either output may be NULL.  A row with slot < 0 is
+ * left as it is, and so is one with slot >= n_slots (SPEC_STATUS_BAD_PAGE).
+ * Sizes: rows >= 0, 1 <= Hk <= 1024, D <= 512, page_size >= 1 divides n_slots.
+ */
+typedef struct spec_cache_read_packed_args {
+  int rows, Hk, D, page_size;
+  int dtype; /* spec_dtype of k and v */
+  const void *k_cache, *v_cache;
+  const uint8_t *k_scale, *v_scale;
+  int64_t n_slots;
+  const int32_t *slot; /* [rows] */
+  void *k, *v;
+  uint32_t *status;
+} spec_cache_read_packed_args;
+
+int spec_cache_read_packed(const spec_cache_read_packed_args *args, spec_stream_t stream);
+
+/* spec_prefix_attention_packed: spec_prefix_attention over packed caches; k_cache and
+ * v_cache are their data, dtype is q's and out's.  A key's values are what its nibbles
+ * stand for, unrounded; whatever pages hold past a request's keys has no effect.
+ *   workspace  spec_attention_packed_workspace_bytes(rows, R, Hq, D) bytes
+ * bf16 with D 64 or 128, pages of 16, 32, 64 or a multiple of 128 tokens and 16-byte rows
+ * and scales take the tensor-core kernels; everything else the generic ones.
+ * Sizes: spec_prefix_attention's, D a multiple of 32 (SPEC_ERR_UNSUPPORTED).
+ */
+typedef struct spec_prefix_attention_packed_args {
+  spec_prefix_attention_args attention;
+  const uint8_t *k_scale, *v_scale;
+} spec_prefix_attention_packed_args;
+
+int spec_prefix_attention_packed(const spec_prefix_attention_packed_args *args, spec_stream_t stream);
+
+/* Workspace of spec_prefix_attention_packed (0 if the sizes are invalid). */
+size_t spec_attention_packed_workspace_bytes(int rows, int R, int Hq, int D);
+
 /* ------------------------------------------------------ logit adjustments -
  * Penalties for repeated tokens, biases and grammar masks on packed rows of
  * logits, ahead of spec_verify (rows 1 + l_r of a request, spec_schedule's

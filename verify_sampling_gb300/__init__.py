@@ -537,6 +537,6 @@ def run_round_host(draft_in: DraftInputs, tgt: torch.Tensor, tgt_row_off: torch.
 
 # the operators around the target model's forward pass
 from . import target  # noqa: E402
-from .target import (adjust_logits, attention_workspace_bytes, cache_commit,  # noqa: E402,F401
-                     cache_reserve, cache_tables, prefix_attention, rope_cache,
-                     rope_frequencies)
+from .target import (adjust_logits, attention_packed_workspace_bytes, attention_workspace_bytes,  # noqa: E402,F401
+                     cache_commit, cache_read_packed, cache_reserve, cache_tables, packed_cache, norm_rope_cache,
+                     prefix_attention, prefix_attention_packed, rope_cache, rope_frequencies)

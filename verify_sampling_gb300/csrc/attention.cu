@@ -1,5 +1,6 @@
-// Shared-prefix attention for the sizes the tensor-core kernel does not take:
-// fp32, head sizes other than 64 and 128, pages that do not tile 128 keys.
+// Shared-prefix attention for the sizes the tensor-core kernels do not take:
+// fp32, head sizes other than 64 and 128, pages that do not tile 128 keys; over caches of
+// the queries' type or of 4 bits.
 //
 // Mathematics: softmax with a running maximum and sum, out = sum p v / sum p, all in
 // fp32 FMAs on tiles converted to fp32 in shared memory.
@@ -48,13 +49,14 @@ inline size_t tile_bytes(int D) {
   return (size_t)(kRows * padded(D) + kKeys * (padded(D) + 4) + kKeys * padded(D)) * sizeof(float);
 }
 
-template <typename T, int VEC, int SETS>  // SETS: 128 columns each
-__global__ void __launch_bounds__(kThreads) attention_kernel(spec_prefix_attention_args a, int splits,
+template <typename T, int VEC, int SETS, bool PACKED>  // SETS: 128 columns each
+__global__ void __launch_bounds__(kThreads) attention_kernel(spec_prefix_attention_args a, q4::Cache packed, int splits,
                                                              float* part, float2* stat) {
   extern __shared__ __align__(16) float smem[];
   __shared__ __align__(16) float p_s[kWarps][kKeys][kWarpRows];
   __shared__ float row_s[kWarps][kWarpRows];
-  __shared__ int64_t key_s[kKeys];  // first element of each key of the tile, -1: none
+  __shared__ int64_t key_s[kKeys];  // first element (4 bits: byte) of each key of the tile, -1: none
+  __shared__ int64_t scale_s[PACKED ? kKeys : 1];
   using P = Pack<T, VEC>;
   const int D = a.D, Dp = padded(D), per_head = a.Hq / a.Hk;
   float* q_s = smem;
@@ -129,40 +131,78 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(spec_prefix_attenti
           const bool pre = at < shared;
           const int own = pre ? at : at - shared, pi = own / a.page_size;
           const int page = page_of(a, pre ? ptable : table, pi, &bad);
-          o = (((int64_t)page * a.page_size + (own - pi * a.page_size)) * a.Hk + h) * D;
+          const int tok = own - pi * a.page_size;
+          if (PACKED) {
+            o = q4::data_at(page, h, tok, a.Hk, D / q4::kGroup, a.page_size);
+            scale_s[tid] = q4::scale_at(page, h, tok, a.Hk, D / q4::kGroup, a.page_size);
+          } else {
+            o = (((int64_t)page * a.page_size + tok) * a.Hk + h) * D;
+          }
         }
         key_s[tid] = o;
       }
       __syncthreads();  // the keys' places; the last tile's readers are done too
       // kFetch packs of keys and of values a thread are on their way together
-      for (int i = tid; i < kKeys * packs; i += kThreads * kFetch) {
-        P x[kFetch], y[kFetch];
-        int at[kFetch];
+      if (PACKED) {
+        const int words = D / 8;  // of 8 elements
+        for (int i = tid; i < kKeys * words; i += kThreads * kFetch) {
+          uint32_t x[kFetch], y[kFetch];
+          float sx[kFetch], sy[kFetch];
 #pragma unroll
-        for (int f = 0; f < kFetch; ++f) {
-          const int j = i + f * kThreads, key = j / packs, c = (j - key * packs) * VEC;
-          at[f] = -1;
-          if (j >= kKeys * packs) continue;
-          at[f] = key << 16 | c;
-          const int64_t o = key_s[key];
-          if (o >= 0) {
-            x[f] = *reinterpret_cast<const P*>((const T*)a.k_cache + o + c);
-            y[f] = *reinterpret_cast<const P*>((const T*)a.v_cache + o + c);
-          } else {
+          for (int f = 0; f < kFetch; ++f) {
+            const int j = i + f * kThreads, key = j / words, w = j - key * words;
+            x[f] = y[f] = 0x88888888u;  // zeros
+            sx[f] = sy[f] = 0.f;
+            if (j >= kKeys * words || key_s[key] < 0) continue;
+            const int64_t o = key_s[key] + (int64_t)(w >> 2) * 16 * a.page_size + (w & 3) * 4, so = scale_s[key] + (w >> 2);
+            x[f] = *reinterpret_cast<const uint32_t*>(packed.k + o);
+            y[f] = *reinterpret_cast<const uint32_t*>(packed.v + o);
+            sx[f] = q4::scale_of(packed.k_scale[so]);
+            sy[f] = q4::scale_of(packed.v_scale[so]);
+          }
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) put(&x[f].e[e], 0.f), put(&y[f].e[e], 0.f);
+          for (int f = 0; f < kFetch; ++f) {
+            const int j = i + f * kThreads, key = j / words, c = (j - key * words) * 8;
+            if (j >= kKeys * words) continue;
+            float* ks = k_s + key * (Dp + 4) + c;
+            float* vs = v_s + key * Dp + c;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              ks[e] = (float)((int)(x[f] >> 4 * e & 15u) - 8) * sx[f];
+              vs[e] = (float)((int)(y[f] >> 4 * e & 15u) - 8) * sy[f];
+            }
           }
         }
+      } else {
+        for (int i = tid; i < kKeys * packs; i += kThreads * kFetch) {
+          P x[kFetch], y[kFetch];
+          int at[kFetch];
 #pragma unroll
-        for (int f = 0; f < kFetch; ++f) {
-          if (at[f] < 0) continue;
-          const int key = at[f] >> 16, c = at[f] & 0xffff;
-          float* ks = k_s + key * (Dp + 4) + c;
-          float* vs = v_s + key * Dp + c;
+          for (int f = 0; f < kFetch; ++f) {
+            const int j = i + f * kThreads, key = j / packs, c = (j - key * packs) * VEC;
+            at[f] = -1;
+            if (j >= kKeys * packs) continue;
+            at[f] = key << 16 | c;
+            const int64_t o = key_s[key];
+            if (o >= 0) {
+              x[f] = *reinterpret_cast<const P*>((const T*)a.k_cache + o + c);
+              y[f] = *reinterpret_cast<const P*>((const T*)a.v_cache + o + c);
+            } else {
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            ks[e] = to_f(x[f].e[e]);
-            vs[e] = to_f(y[f].e[e]);
+              for (int e = 0; e < VEC; ++e) put(&x[f].e[e], 0.f), put(&y[f].e[e], 0.f);
+            }
+          }
+#pragma unroll
+          for (int f = 0; f < kFetch; ++f) {
+            if (at[f] < 0) continue;
+            const int key = at[f] >> 16, c = at[f] & 0xffff;
+            float* ks = k_s + key * (Dp + 4) + c;
+            float* vs = v_s + key * Dp + c;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+              ks[e] = to_f(x[f].e[e]);
+              vs[e] = to_f(y[f].e[e]);
+            }
           }
         }
       }
@@ -323,8 +363,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(spec_prefix_attention_ar
   if (a.lse && d == 0) a.lse[unit] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
 }
 
-template <typename T, int VEC, int SETS>
-cudaError_t launch(const spec_prefix_attention_args& a, float* part, float2* stat, cudaStream_t stream) {
+template <typename T, int VEC, int SETS, bool PACKED>
+cudaError_t launch(const spec_prefix_attention_args& a, const q4::Cache& packed, float* part, float2* stat, cudaStream_t stream) {
   const long long units = (long long)a.rows * a.Hq;
   // Blocks for the mean request's rows (a longer one's loop), and shares of at least
   // 64 keys, until there are about eight blocks an SM for 152 SMs, within the
@@ -338,19 +378,21 @@ cudaError_t launch(const spec_prefix_attention_args& a, float* part, float2* sta
   const int splits = (int)std::max(1ll, std::min<long long>({kMaxSplits, (152 * 8 + blocks - 1) / blocks, (keys + 63) / 64,
                                                              (long long)(attn_partial_rows(a.rows, a.Hq) / units)}));
   const size_t smem = tile_bytes(a.D);
-  auto kernel = attention_kernel<T, VEC, SETS>;
+  auto kernel = attention_kernel<T, VEC, SETS, PACKED>;
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
-  kernel<<<dim3(a.R, a.Hk, (unsigned)(tiles * splits)), kThreads, smem, stream>>>(a, splits, part, stat);
+  kernel<<<dim3(a.R, a.Hk, (unsigned)(tiles * splits)), kThreads, smem, stream>>>(a, packed, splits, part, stat);
   if ((err = cudaGetLastError()) != cudaSuccess) return err;
   if (splits > 1)
     join_kernel<T><<<dim3((unsigned)((units + kWarps - 1) / kWarps), (a.D + 31) / 32), kThreads, 0, stream>>>(a, splits, part, stat);
   return cudaGetLastError();
 }
 
-template <typename T, int VEC>
-cudaError_t launch(const spec_prefix_attention_args& a, float* part, float2* stat, cudaStream_t stream) {
-  return a.D <= 128 ? launch<T, VEC, 1>(a, part, stat, stream) : launch<T, VEC, 2>(a, part, stat, stream);
+template <typename T, int VEC, bool PACKED = false>
+cudaError_t launch(const spec_prefix_attention_args& a, float* part, float2* stat, cudaStream_t stream,
+                   const q4::Cache& packed = q4::Cache{}) {
+  return a.D <= 128 ? launch<T, VEC, 1, PACKED>(a, packed, part, stat, stream)
+                    : launch<T, VEC, 2, PACKED>(a, packed, part, stat, stream);
 }
 
 }  // namespace
@@ -364,6 +406,12 @@ cudaError_t launch_attention_generic(const spec_prefix_attention_args& a, float*
     return wide ? launch<float, 4>(a, part, stat, stream) : launch<float, 1>(a, part, stat, stream);
   return wide ? launch<__nv_bfloat16, 8>(a, part, stat, stream)
               : launch<__nv_bfloat16, 1>(a, part, stat, stream);
+}
+
+cudaError_t launch_attention_packed_generic(const spec_prefix_attention_args& a, const q4::Cache& packed, float* part,
+                                          float2* stat, cudaStream_t stream) {
+  return a.dtype == SPEC_F32 ? launch<float, 1, true>(a, part, stat, stream, packed)
+                             : launch<__nv_bfloat16, 1, true>(a, part, stat, stream, packed);
 }
 
 }  // namespace spec

@@ -4,6 +4,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "packed.cuh"
 
 namespace spec {
 
@@ -97,5 +98,7 @@ cudaError_t launch_attention_tc(const spec_prefix_attention_args& a, int sms, fl
                                 int64_t* plan, cudaStream_t stream);
 cudaError_t launch_attention_generic(const spec_prefix_attention_args& a, float* part, float2* stat,
                                      cudaStream_t stream);
+cudaError_t launch_attention_packed_generic(const spec_prefix_attention_args& a, const q4::Cache& packed, float* part,
+                                          float2* stat, cudaStream_t stream);
 
 }  // namespace spec

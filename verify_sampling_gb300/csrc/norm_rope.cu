@@ -1,0 +1,316 @@
+// Norms of query and key heads with rotary positions, keys and values written to a paged
+// cache of the inputs' type or of 4 bits; and the read-back of such a cache.
+//
+// Mathematics: y = x w rsqrt(mean x^2 + eps), then pair i of a head turns by the angle
+// position * freq[i] (rotary.cuh), all in fp32 from one read of the head, rounded once at
+// the end: to the stored type, or to the nearest of a group's 15 values (packed.cuh).
+//
+// Layout (norm_rope_kernel): a head lies over a group of lanes, a 16-byte vector each, in
+// the order of its elements, so that a load, a store, a group of 32 elements to code and
+// a head's sum of squares are each a few lanes side by side.  A pair's other half comes from
+// its lane by a shuffle, cosines, sines and weights stay in a lane's registers over all
+// heads of a token, and four steps' loads go out together.  A warp takes a part of a
+// token's heads at a time.  Bound by memory.
+#include "norm_rope.cuh"
+
+#include <algorithm>
+
+#include "packed.cuh"
+#include "rotary.cuh"
+
+namespace spec {
+
+namespace {
+
+using rotary::cos_sin;
+using rotary::in_turns;
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kSteps = 4;  // loads of a lane on their way together
+
+template <typename T, int VEC>
+struct alignas(sizeof(T) * VEC) Pack {
+  T e[VEC];
+};
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void put(float* o, float v) { *o = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* o, float v) { *o = __float2bfloat16_rn(v); }
+
+// Codes a lane's VEC elements of each chunk and writes them to the token's head in the cache.
+// All lanes of the warp call it; `on`: this one's head is written.
+template <int VEC, int CH>
+__device__ __forceinline__ void store_packed(const float (&y)[CH * VEC], int first, int step, int D, bool on, uint8_t* data,
+                                           uint8_t* scale, int P) {
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int d = first + c * step;  // this lane's first element
+    float amax = 0.f;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) amax = fmaxf(amax, fabsf(y[c * VEC + e]));
+#pragma unroll
+    for (int o = 1; o < q4::kGroup / VEC; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const uint32_t code = q4::code_of(amax);
+    const float s = q4::scale_of(code);
+    uint32_t w = 0;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) w |= q4::nibble_of(y[c * VEC + e], s) << (4 * ((d + e) & 7));
+#pragma unroll
+    for (int o = 1; o < 8 / VEC; o <<= 1) w |= __shfl_xor_sync(0xffffffffu, w, o);
+    if (!on || d >= D) continue;
+    const int g = d / q4::kGroup, in_g = d % q4::kGroup;
+    if (in_g % 8 == 0) *reinterpret_cast<uint32_t*>(data + (size_t)g * 16 * P + in_g / 2) = w;
+    if (in_g == 0) scale[g] = (uint8_t)code;
+  }
+}
+
+// A head over `lanes` lanes (a power of two), or over the whole warp in CH chunks of 32 VEC
+// elements.  FAST: pairs lie in whole vectors, in the half layout lanes apart (CH = 1).
+template <typename T, int VEC, int CH, bool FAST, bool PACKED>
+__global__ void __launch_bounds__(kThreads) norm_rope_kernel(spec_norm_rope_args p, int parts, int lanes) {
+  using P = Pack<T, VEC>;
+  extern __shared__ __align__(16) float2 smem[];
+  const int half = p.rot >> 1, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float2* turns = smem;                         // [half]
+  float2* cs = smem + half + warp * half;       // [half] of the warp's token
+  float* buf = reinterpret_cast<float*>(smem + half * (1 + kWarps)) + warp * 32 * VEC * CH;  // !FAST: its heads
+  for (int f = tid; f < half; f += kThreads) turns[f] = in_turns(p.freq[f]);
+  __syncthreads();
+
+  const int at_once = CH == 1 ? 32 / lanes : 1;
+  const int sub = CH == 1 ? lane / lanes : 0, l = CH == 1 ? lane % lanes : lane;
+  const int first = l * VEC, step = 32 * VEC;  // element e of chunk c is first + c * step + e
+  const bool inter = p.layout == SPEC_ROPE_INTERLEAVED;
+  const int q_steps = (p.Hq + at_once - 1) / at_once, k_steps = (p.Hk + at_once - 1) / at_once;
+  const int steps = q_steps + 2 * k_steps, per = (steps + parts - 1) / parts;
+  const float inv_d = 1.f / (float)p.D;
+  const int64_t units = (int64_t)p.rows * parts;
+
+  for (int64_t unit = (int64_t)blockIdx.x * kWarps + warp; unit < units; unit += (int64_t)gridDim.x * kWarps) {
+    const int row = (int)(unit / parts), part = (int)(unit - (int64_t)row * parts);
+    const int begin = part * per, end = min(begin + per, steps);
+    P x[kSteps][CH];
+    // kind 0: queries, 1: keys, 2: values
+    auto kind_of = [&](int st) { return st < q_steps ? 0 : st < q_steps + k_steps ? 1 : 2; };
+    auto head_of = [&](int st, int kind) { return (st - (kind == 0 ? 0 : kind == 1 ? q_steps : q_steps + k_steps)) * at_once + sub; };
+    auto load = [&](int s0) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int st = s0 + i;
+        if (st >= end) break;
+        const int kind = kind_of(st), h = head_of(st, kind);
+        const T* from = kind == 0   ? (const T*)p.q + (int64_t)row * p.q_row + h * p.q_head
+                        : kind == 1 ? (const T*)p.k + (int64_t)row * p.k_row + h * p.k_head
+                                    : (const T*)p.v + (int64_t)row * p.v_row + h * p.v_head;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+          if (h < (kind == 0 ? p.Hq : p.Hk) && first + c * step < p.D) x[i][c] = *reinterpret_cast<const P*>(from + first + c * step);
+      }
+    };
+    load(begin);  // a row that is left out is read all the same: no load waits for a position
+    const int pos = p.position[row];
+    int slot = p.slot ? p.slot[row] : -1;
+    if (part == 0 && lane == 0) {
+      const uint32_t bad = (pos >= (1 << 24) ? SPEC_STATUS_BAD_POSITION : 0u) | (slot >= p.n_slots ? SPEC_STATUS_BAD_PAGE : 0u);
+      if (bad) set_status(p.status, bad);
+    }
+    if (pos < 0) continue;
+    if (slot >= p.n_slots) slot = -1;
+    const float at = (float)min(pos, (1 << 24) - 1);
+    __syncwarp();
+    for (int f = lane; f < half; f += 32) cs[f] = cos_sin(at, turns[f], p.scale);
+    __syncwarp();
+    // FAST: the lane's cosines and its sines with the sign of the other half's part
+    constexpr int kAngles = FAST ? VEC : 1;
+    float co[kAngles], si[kAngles];
+    const bool turning = FAST && first < p.rot;
+    if (turning) {
+#pragma unroll
+      for (int e = 0; e < kAngles; ++e) {
+        const float2 t = cs[inter ? (first + e) / 2 : first < half ? first + e : first + e - half];
+        co[e] = t.x;
+        si[e] = (inter ? e % 2 == 0 : first < half) ? -t.y : t.y;
+      }
+    }
+    const int other = lane + (first < half ? half : -half) / VEC;  // FAST, half layout: where the other half lies
+
+    for (int s0 = begin; s0 < end; s0 += kSteps) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int st = s0 + i;
+        if (st >= end) break;
+        const int kind = kind_of(st), h = head_of(st, kind);
+        const bool on = h < (kind == 0 ? p.Hq : p.Hk) && (kind == 0 || slot >= 0);
+        if (kind == 2 && !PACKED) {
+#pragma unroll
+          for (int c = 0; c < CH; ++c)
+            if (on && first + c * step < p.D)
+              *reinterpret_cast<P*>((T*)p.v_cache + ((int64_t)slot * p.Hk + h) * p.D + first + c * step) = x[i][c];
+          continue;
+        }
+        float y[CH * VEC];
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) y[c * VEC + e] = first + c * step < p.D ? to_f(x[i][c].e[e]) : 0.f;
+        const float* weight = kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr;
+        if (weight) {
+          float sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < CH * VEC; ++e) sum = fmaf(y[e], y[e], sum);
+          for (int o = 1; o < (CH == 1 ? lanes : 32); o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          const float r = rsqrtf(fmaf(sum, inv_d, p.eps));
+#pragma unroll
+          for (int c = 0; c < CH; ++c)
+            if (first + c * step < p.D)
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) y[c * VEC + e] *= r * weight[first + c * step + e];
+        }
+        if (kind < 2 && half > 0) {
+          if (FAST) {
+            float z[VEC];
+            if (inter) {
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) z[e] = y[e ^ 1];
+            } else {
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) z[e] = __shfl_sync(0xffffffffu, y[e], other & 31);
+            }
+            if (turning) {
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) y[e] = fmaf(y[e], co[e % kAngles], __fmul_rn(z[e], si[e % kAngles]));
+            }
+          } else {
+            float* mine = buf + sub * lanes * VEC;
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) mine[first + c * step + e] = y[c * VEC + e];
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) {
+                const int d = first + c * step + e;
+                if (d >= p.rot) continue;
+                const bool low = inter ? d % 2 == 0 : d < half;
+                const float2 t = cs[inter ? d / 2 : low ? d : d - half];
+                const float z = mine[inter ? d ^ 1 : low ? d + half : d - half];
+                y[c * VEC + e] = fmaf(y[c * VEC + e], t.x, __fmul_rn(z, low ? -t.y : t.y));
+              }
+          }
+        }
+        if (PACKED && kind > 0) {
+          const int64_t page = on ? slot / p.page_size : 0;
+          const int tok = on ? (int)(slot - page * p.page_size) : 0, groups = p.D / q4::kGroup, head = on ? h : 0;
+          store_packed<VEC, CH>(y, first, step, p.D, on,
+                              (uint8_t*)(kind == 1 ? p.k_cache : p.v_cache) + q4::data_at(page, head, tok, p.Hk, groups, p.page_size),
+                              (kind == 1 ? p.k_scale : p.v_scale) + q4::scale_at(page, head, tok, p.Hk, groups, p.page_size),
+                              p.page_size);
+          continue;
+        }
+        if (!on) continue;
+        T* to = kind == 0 ? (T*)p.q_out + (int64_t)row * p.q_out_row + h * p.q_out_head
+                          : (T*)p.k_cache + ((int64_t)slot * p.Hk + h) * p.D;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          P o;
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) put(&o.e[e], y[c * VEC + e]);
+          if (first + c * step < p.D) *reinterpret_cast<P*>(to + first + c * step) = o;
+        }
+      }
+      if (s0 + kSteps < end) load(s0 + kSteps);
+    }
+  }
+}
+
+template <typename T, int VEC, int CH, bool FAST, bool PACKED>
+cudaError_t launch(const spec_norm_rope_args& a, cudaStream_t stream) {
+  int lanes = 32;
+  if (CH == 1)
+    for (lanes = 1; lanes * VEC < a.D;) lanes *= 2;
+  if (PACKED) lanes = std::max(lanes, q4::kGroup / VEC);
+  const int at_once = CH == 1 ? 32 / lanes : 1;
+  const int steps = (a.Hq + at_once - 1) / at_once + 2 * ((a.Hk + at_once - 1) / at_once);
+  // warps for eight blocks an SM, as far as a warp keeps four steps
+  const int64_t warps = 152 * 8 * kWarps;
+  const int parts = (int)std::max<int64_t>(1, std::min<int64_t>((steps + kSteps - 1) / kSteps, warps / std::max(a.rows, 1)));
+  const int64_t blocks = ((int64_t)a.rows * parts + kWarps - 1) / kWarps;
+  const size_t smem = (size_t)(a.rot / 2) * (1 + kWarps) * sizeof(float2) + (FAST ? 0 : (size_t)kWarps * 32 * VEC * CH * sizeof(float));
+  norm_rope_kernel<T, VEC, CH, FAST, PACKED><<<(unsigned)std::min<int64_t>(blocks, 152 * 8), kThreads, smem, stream>>>(a, parts, lanes);
+  return cudaGetLastError();
+}
+
+template <typename T, bool PACKED>
+cudaError_t launch(const spec_norm_rope_args& a, bool wide, cudaStream_t stream) {
+  constexpr int VEC = 16 / (int)sizeof(T);
+  if (wide) {
+    const int turn_step = a.layout == SPEC_ROPE_HALF ? a.rot / 2 : a.rot;
+    if (a.D <= 32 * VEC)
+      return turn_step % VEC == 0 ? launch<T, VEC, 1, true, PACKED>(a, stream) : launch<T, VEC, 1, false, PACKED>(a, stream);
+    if (VEC == 8 || a.D <= 64 * VEC) return launch<T, VEC, 2, false, PACKED>(a, stream);
+    return launch<T, VEC, VEC == 8 ? 2 : 4, false, PACKED>(a, stream);
+  }
+  return a.D <= 128 ? launch<T, 1, 4, false, PACKED>(a, stream) : launch<T, 1, 16, false, PACKED>(a, stream);
+}
+
+// ------------------------------------------------------------- read-back ---
+// A thread turns 4 bytes into 8 elements; 4 threads side by side a group.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(spec_cache_read_packed_args p) {
+  const int groups = p.D / q4::kGroup, words = p.Hk * groups * 4;
+  const int which = blockIdx.y;
+  T* out = (T*)(which ? p.v : p.k);
+  if (!out) return;
+  const uint8_t* data = (const uint8_t*)(which ? p.v_cache : p.k_cache);
+  const uint8_t* scales = which ? p.v_scale : p.k_scale;
+  const int64_t n = (int64_t)p.rows * words;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
+    const int row = (int)(i / words), w = (int)(i - (int64_t)row * words);
+    const int h = w / (4 * groups), g = w / 4 - h * groups;
+    const int slot = p.slot[row];
+    if (slot >= p.n_slots) set_status(p.status, SPEC_STATUS_BAD_PAGE);
+    if (slot < 0 || slot >= p.n_slots) continue;
+    const int page = slot / p.page_size, tok = slot - page * p.page_size;
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(data + q4::data_at(page, h, tok, p.Hk, groups, p.page_size) +
+                                                          (size_t)g * 16 * p.page_size + (w & 3) * 4);
+    const float s = q4::scale_of(scales[q4::scale_at(page, h, tok, p.Hk, groups, p.page_size) + g]);
+    constexpr int VEC = 16 / (int)sizeof(T);
+    T* to = out + i * 8;
+#pragma unroll
+    for (int c = 0; c < 8; c += VEC) {
+      Pack<T, VEC> o;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) put(&o.e[e], (float)((int)(v >> (4 * (c + e)) & 15u) - 8) * s);
+      *reinterpret_cast<Pack<T, VEC>*>(to + c) = o;
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_norm_rope(const spec_norm_rope_args& a, cudaStream_t stream) {
+  if (a.rows == 0 || a.Hq + a.Hk == 0) return cudaSuccess;
+  const int vec = a.dtype == SPEC_F32 ? 4 : 8;
+  auto on = [&](const void* p) { return ((uintptr_t)p % 16) == 0; };
+  bool wide = a.D % vec == 0 && a.q_row % vec == 0 && a.q_head % vec == 0 && a.q_out_row % vec == 0 && a.q_out_head % vec == 0 &&
+              a.k_row % vec == 0 && a.k_head % vec == 0 && a.v_row % vec == 0 && a.v_head % vec == 0 && on(a.q) && on(a.k) &&
+              on(a.v) && on(a.q_out) && on(a.k_cache) && on(a.v_cache);
+  const bool packed = a.cache == SPEC_CACHE_PACKED && a.Hk > 0;
+  if (a.dtype == SPEC_F32) return packed ? launch<float, true>(a, wide, stream) : launch<float, false>(a, wide, stream);
+  return packed ? launch<__nv_bfloat16, true>(a, wide, stream) : launch<__nv_bfloat16, false>(a, wide, stream);
+}
+
+cudaError_t launch_cache_read(const spec_cache_read_packed_args& a, cudaStream_t stream) {
+  if (a.rows == 0) return cudaSuccess;
+  const int64_t n = (int64_t)a.rows * a.Hk * (a.D / 8);
+  const dim3 grid((unsigned)std::min<int64_t>((n + kThreads - 1) / kThreads, 152 * 16), 2);
+  if (a.dtype == SPEC_F32) cache_read_kernel<float><<<grid, kThreads, 0, stream>>>(a);
+  else cache_read_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace spec

@@ -1,0 +1,51 @@
+// A paged cache in 4 bits: where a head's elements lie and how they are coded.
+//
+// A token's head is D / 32 groups of 32 elements; a group is 16 bytes (element j in nibble j,
+// the low one of a byte first) and a scale byte b, s = 2^((b >> 3) - 20) (1 + (b & 7) / 8); an
+// element is s (nibble - 8), nibble 1 .. 15.
+//
+// Scales of four significant bits make an element one of seven: exact in bf16, so that what
+// a kernel multiplies is what the cache holds, and its code shifted left by 20 (4) bits and
+// an added exponent are its bits in fp32 (bf16).  s is amax / 7 rounded to nearest, not up:
+// |x / s| <= 7.44, so no element is off by more than s / 2 either way.
+//
+// Data are [pages, Hk, D / 32, P, 16]: a group of 8 tokens is 128 bytes side by side, a
+// conflict-free 8 x 8 matrix of 16-bit words for ldmatrix, and a page's head one copy.
+#pragma once
+
+#include "common.cuh"
+
+namespace spec {
+namespace q4 {
+
+constexpr int kGroup = 32;
+constexpr int kLeastExp = 107;  // fp32 exponent field of code 0
+
+struct Cache {  // data and scales of keys and values
+  const uint8_t *k, *v, *k_scale, *v_scale;
+};
+
+// First byte of group 0 of a token's head (the next group is 16 P bytes on), and of its scales.
+__host__ __device__ __forceinline__ int64_t data_at(int64_t page, int h, int tok, int Hk, int groups, int P) {
+  return ((page * Hk + h) * groups * P + tok) * 16;
+}
+__host__ __device__ __forceinline__ int64_t scale_at(int64_t page, int h, int tok, int Hk, int groups, int P) {
+  return ((page * Hk + h) * P + tok) * groups;
+}
+
+__device__ __forceinline__ float scale_of(uint32_t code) {
+  return __uint_as_float((code << 20) + ((uint32_t)kLeastExp << 23));
+}
+// Code of a group's largest magnitude / 7 (half a step is added to the bits: halves go up).
+__device__ __forceinline__ uint32_t code_of(float amax) {
+  const int bits = __float_as_int(__fdiv_rn(amax, 7.f));
+  return (uint32_t)min(max(((bits + (1 << 19)) >> 20) - 8 * kLeastExp, 0), 255);
+}
+// x / s to the nearest whole number, halves to even, +-7 at most; NaN gives 0.  (A true
+// division: stored 16-bit values meet halves exactly, and a product with 1 / s would miss them.)
+__device__ __forceinline__ uint32_t nibble_of(float x, float s) {
+  return (uint32_t)(min(max(__float2int_rn(__fdiv_rn(x, s)), -7), 7) + 8);
+}
+
+}  // namespace q4
+}  // namespace spec

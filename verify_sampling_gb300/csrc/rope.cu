@@ -3,13 +3,7 @@
 //
 // Mathematics: pair i of a head turns by the angle position * freq[i]:
 //   (x, y) -> scale * (x cos - y sin, y cos + x sin).
-// The angle is reduced in turns, not radians: with f = freq / (2 pi) kept as an
-// fp32 pair hi + lo and the position p < 2^24 exact in fp32, p * hi = t + e with
-// one product and one fma (e exact), t - rint(t) is exact, and the fraction
-// (t - rint(t)) + (e + p * lo) is off by a few 2^-26 turns at any position, where
-// an fp32 product of radians would be off by p * 2^-24.  sincospif takes it from
-// there.  It costs two fmas an angle, where 64-bit products would hold up the
-// heads of small models (the fp64 pipe is 1/64 of the fp32 one).
+// (angles: rotary.cuh)
 //
 // Layout, small batches and strided heads (rope_kernel): a unit is two 16-byte vectors
 // of a head: the two halves of its pairs in the half layout, two vectors next to each
@@ -26,6 +20,7 @@
 // bf16 took 26.0 us (4.0 TB/s) by the first kernel, 19.7 (5.3 TB/s) by the second, 40001
 // rows of 32 + 2 * 4 heads 164 us and 122 (6.7 TB/s).
 #include "rope.cuh"
+#include "rotary.cuh"
 #include "tc.cuh"
 
 #include <algorithm>
@@ -34,6 +29,9 @@
 namespace spec {
 
 namespace {
+
+using rotary::cos_sin;
+using rotary::in_turns;
 
 constexpr int kThreads = 256;     // of the element-wise kernel
 constexpr int kMaxThreads = 320;  // of rope_kernel: two blocks an SM at 96 registers (three spill: 98 us for 26)
@@ -60,24 +58,6 @@ __device__ __forceinline__ void turn(T& x, T& y, float2 cs) {
   // spelled out, so that every kernel rounds alike
   from_f(fmaf(a, cs.x, -__fmul_rn(b, cs.y)), &x);
   from_f(fmaf(b, cs.x, __fmul_rn(a, cs.y)), &y);
-}
-
-// A frequency (radians) in turns, hi + lo.
-__device__ __forceinline__ float2 in_turns(double freq) {
-  const double turns = freq * 0.15915494309189533577;  // 1 / (2 pi)
-  const float hi = (float)turns;
-  return make_float2(hi, (float)(turns - (double)hi));
-}
-// cos and sin, times the scale, of position x times the frequency.
-__device__ __forceinline__ float2 cos_sin(float x, float2 turns, float scale) {
-  const float m = x * turns.x, e = fmaf(x, turns.x, -m);
-  const float frac = (m - rintf(m)) + fmaf(x, turns.y, e);
-  float s, c;
-  sincospif(2.f * frac, &s, &c);
-  return make_float2(c * scale, s * scale);
-}
-__device__ __forceinline__ float2 cos_sin(float x, double freq, float scale) {
-  return cos_sin(x, in_turns(freq), scale);
 }
 
 // Where head h of a row (queries, keys, values in turn) is read and written (null:

@@ -53,6 +53,25 @@ class PrefixAttentionArgs(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t), ("status", _P)]
 
 
+class NormRopeArgs(ctypes.Structure):
+    _fields_ = [("rows", _I), ("Hq", _I), ("Hk", _I), ("D", _I), ("rot", _I), ("dtype", _I),
+                ("layout", _I), ("cache", _I), ("page_size", _I), ("scale", _F), ("eps", _F), ("q", _P), ("k", _P), ("v", _P),
+                ("q_row", _L), ("q_head", _L), ("k_row", _L), ("k_head", _L), ("v_row", _L), ("v_head", _L),
+                ("q_out", _P), ("q_out_row", _L), ("q_out_head", _L), ("k_cache", _P),
+                ("v_cache", _P), ("k_scale", _P), ("v_scale", _P), ("n_slots", _L), ("q_weight", _P), ("k_weight", _P),
+                ("freq", _P), ("position", _P), ("slot", _P), ("status", _P)]
+
+
+class CacheReadPackedArgs(ctypes.Structure):
+    _fields_ = [("rows", _I), ("Hk", _I), ("D", _I), ("page_size", _I), ("dtype", _I), ("k_cache", _P), ("v_cache", _P),
+                ("k_scale", _P), ("v_scale", _P), ("n_slots", _L), ("slot", _P), ("k", _P), ("v", _P), ("status", _P)]
+
+
+class PrefixAttentionPackedArgs(ctypes.Structure):
+    """spec_prefix_attention_packed_args with the fields of its first member in its place."""
+    _fields_ = PrefixAttentionArgs._fields_ + [("k_scale", _P), ("v_scale", _P)]
+
+
 class LogitsArgs(ctypes.Structure):
     _fields_ = [("R", _I), ("V", _I), ("rows", _I), ("rows_per_request", _I), ("dtype", _I),
                 ("logits", _P), ("ld", _L), ("out", _P), ("out_ld", _L), ("row_off", _P),
@@ -95,17 +114,20 @@ _COMMIT = _Call("spec_cache_commit", CacheCommitArgs)
 _ROPE = _Call("spec_rope_cache", RopeCacheArgs)
 _ATTENTION = _Call("spec_prefix_attention", PrefixAttentionArgs)
 _LOGITS = _Call("spec_adjust_logits", LogitsArgs)
+_NORM_ROPE = _Call("spec_norm_rope_cache", NormRopeArgs)
+_READ_PACKED = _Call("spec_cache_read_packed", CacheReadPackedArgs)
+_ATTENTION_PACKED = _Call("spec_prefix_attention_packed", PrefixAttentionPackedArgs)
 
 
 def _bind(L: ctypes.CDLL) -> None:
     """Prototypes of this module's entry points (called once by ``lib``)."""
-    for call in (_RESERVE, _COMMIT, _ROPE, _ATTENTION, _LOGITS):
+    for call in (_RESERVE, _COMMIT, _ROPE, _ATTENTION, _LOGITS, _NORM_ROPE, _READ_PACKED, _ATTENTION_PACKED):
         call.bind(L)
-    L.spec_attention_workspace_bytes.argtypes = [_I] * 4
-    L.spec_attention_workspace_bytes.restype = ctypes.c_size_t
+    for f in (L.spec_attention_workspace_bytes, L.spec_attention_packed_workspace_bytes):
+        f.argtypes, f.restype = [_I] * 4, ctypes.c_size_t
 
 
-_i32, _i64, _f32, _f64 = torch.int32, torch.int64, torch.float32, torch.float64
+_i32, _i64, _f32, _f64, _u8 = torch.int32, torch.int64, torch.float32, torch.float64, torch.uint8
 _Tensor = torch.Tensor
 _codes = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16}
 
@@ -318,10 +340,117 @@ def rope_cache(q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Ten
     return q_out
 
 
+# ------------------------------------------- head norms, caches in 4 bits --
+def packed_cache(n_pages: int, page_size: int, Hk: int, D: int, device="cuda") -> tuple:
+    """An empty cache in 4 bits for keys or values: data [n_pages, Hk, D / 32, page_size, 16] and scales
+    [n_pages, Hk, page_size, D / 32], both uint8, D a multiple of 32 (zeros stand for -8 * 2^-20)."""
+    if D < 1 or D % 32:
+        raise ValueError("D must be a multiple of 32")
+    return (torch.zeros(n_pages, Hk, D // 32, page_size, 16, dtype=_u8, device=device),
+            torch.zeros(n_pages, Hk, page_size, D // 32, dtype=_u8, device=device))
+
+
+def _packed(cache: tuple, name: str, Hk: Optional[int], D: int) -> tuple:
+    """Addresses of an packed cache's data and scales, and its pages, page size and key heads."""
+    data, scale = cache
+    if not isinstance(data, _Tensor) or not isinstance(scale, _Tensor):
+        raise TypeError(f"{name} must be a pair of tensors")
+    if data.dim() != 5 or (Hk is not None and data.shape[1] != Hk):
+        raise ValueError(f"{name} must be the data [pages, Hk, D / 32, page_size, 16] and scales [pages, Hk, page_size, D / 32]")
+    n, heads, groups, P, width = data.shape
+    if groups * 32 != D or width != 16 or scale.shape != (n, heads, P, groups):
+        raise ValueError(f"{name} must be the data [pages, Hk, D / 32, page_size, 16] and scales [pages, Hk, page_size, D / 32]")
+    return _t(data, name, _u8), _t(scale, f"{name} scales", _u8), n, P, heads
+
+
+def norm_rope_cache(q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Tensor],
+                    freq: torch.Tensor, position: torch.Tensor, slot: Optional[torch.Tensor], k_cache, v_cache, *,
+                    q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                    interleaved: bool = False, scale: float = 1.0, q_out: Optional[torch.Tensor] = None,
+                    status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """spec_norm_rope_cache: ``rope_cache`` after a norm of each head of queries and keys (divided by its root mean
+    square, times ``q_weight`` and ``k_weight`` [D] float32; None: no norm).  The caches are tensors [pages, page_size,
+    Hk, D] as there, or both pairs of ``packed_cache``: then keys and values are stored in 4 bits."""
+    rows, Hq, D = shape = q.shape
+    dt = q.dtype
+    qp, qr, qh = _strided(q, "q", dt, shape)
+    if q_out is None:
+        with _made(stream):
+            q_out = torch.empty(shape, dtype=dt, device=q.device)
+        op, orow, oh = q_out.data_ptr(), Hq * D, D
+    else:
+        op, orow, oh = _strided(q_out, "q_out", dt, shape)
+    Hk = P = n_slots = sp = kc = vc = ks = vs = kp = vp = kr = kh = vr = vh = kind = 0
+    if k is not None:
+        Hk = k.shape[1]
+        kp, kr, kh = _strided(k, "k", dt, (rows, Hk, D))
+        vp, vr, vh = _strided(v, "v", dt, (rows, Hk, D))
+        if isinstance(k_cache, tuple) != isinstance(v_cache, tuple):
+            raise ValueError("k_cache and v_cache must be of one kind")
+        if isinstance(k_cache, tuple):
+            kind = 1
+            kc, ks, n, P, _ = _packed(k_cache, "k_cache", Hk, D)
+            vc, vs, n2, P2, _ = _packed(v_cache, "v_cache", Hk, D)
+            if (n, P) != (n2, P2):
+                raise ValueError("k_cache and v_cache must have the same pages")
+            n_slots = n * P
+        else:
+            if k_cache.dim() != 4 or k_cache.shape[2:] != (Hk, D) or v_cache.shape != k_cache.shape:
+                raise ValueError("k_cache and v_cache must both be [pages, page_size, Hk, D]")
+            kc, vc = _t(k_cache, "k_cache", dt), _t(v_cache, "v_cache", dt)
+            n_slots = k_cache.shape[0] * k_cache.shape[1]
+        sp = _t(slot, "slot", _i32, rows)
+    _NORM_ROPE(_on(stream, q), rows, Hq, Hk, D, 2 * freq.numel(), _code(q), int(interleaved), kind, P, scale, eps,
+               qp, kp, vp, qr, qh, kr, kh, vr, vh, op, orow, oh, kc, vc, ks, vs, n_slots,
+               _opt(q_weight, "q_weight", _f32, D), _opt(k_weight, "k_weight", _f32, D), _t(freq, "freq", _f64),
+               _t(position, "position", _i32, rows), sp, _opt(status, "status", _i32, 1))
+    return q_out
+
+
+def cache_read_packed(k_cache: tuple, v_cache: tuple, slot: torch.Tensor, *, dtype: torch.dtype = torch.bfloat16,
+                    out: Optional[tuple] = None, status: Optional[torch.Tensor] = None, stream=None) -> tuple:
+    """spec_cache_read_packed: what the slots of two ``packed_cache`` pairs stand for, (k, v) [rows, Hk, D] of ``dtype``
+    (exact in bfloat16 and float32).  Rows whose slot is negative or past the cache are left as they are in ``out``
+    (zeros in tensors that the call makes)."""
+    rows = slot.numel()
+    D = k_cache[0].shape[2] * 32 if isinstance(k_cache[0], _Tensor) and k_cache[0].dim() == 5 else 0
+    kc, ks, n, P, Hk = _packed(k_cache, "k_cache", None, D)
+    vc, vs, n2, P2, _ = _packed(v_cache, "v_cache", Hk, D)
+    if (n, P) != (n2, P2):
+        raise ValueError("k_cache and v_cache must have the same pages")
+    if out is None:
+        if dtype not in _codes:
+            raise TypeError("dtype must be float32 or bfloat16")
+        with _made(stream):
+            out = tuple(torch.zeros((rows, Hk, D), dtype=dtype, device=slot.device) for _ in range(2))
+    k, v = out
+    if k.dtype is not v.dtype or k.shape != (rows, Hk, D) or v.shape != k.shape:
+        raise ValueError("out must be two tensors [rows, Hk, D] of one dtype")
+    _READ_PACKED(_on(stream, slot), rows, Hk, D, P, _code(k), kc, vc, ks, vs, n * P, _t(slot, "slot", _i32),
+               _t(k, "out k", k.dtype), _t(v, "out v", v.dtype), _opt(status, "status", _i32, 1))
+    return out
+
+
 # -------------------------------------------------- shared-prefix attention --
 def attention_workspace_bytes(rows: int, R: int, Hq: int, D: int) -> int:
     """spec_attention_workspace_bytes: workspace of ``prefix_attention``."""
     return int(lib().spec_attention_workspace_bytes(rows, R, Hq, D))
+
+
+def attention_packed_workspace_bytes(rows: int, R: int, Hq: int, D: int) -> int:
+    """spec_attention_packed_workspace_bytes: workspace of ``prefix_attention_packed``."""
+    return int(lib().spec_attention_packed_workspace_bytes(rows, R, Hq, D))
+
+
+def _prefixes(group_off, prefix_len, prefix_table) -> tuple:
+    """Groups, pages of a prefix table and the addresses of an attention call's prefixes."""
+    if prefix_len is None or prefix_len.numel() == 0:
+        return 0, 0, 0, 0, 0
+    G = prefix_len.numel()
+    if group_off is None or prefix_table is None or prefix_table.dim() != 2 or prefix_table.shape[0] != G:
+        raise ValueError("prefixes need group_off [G + 1], prefix_len [G] and prefix_table [G, pages]")
+    return (G, prefix_table.shape[1], _t(group_off, "group_off", _i32, G + 1), _t(prefix_len, "prefix_len", _i32),
+            _t(prefix_table, "prefix_table", _i32))
 
 
 def prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -343,14 +472,7 @@ def prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
         raise ValueError("k_cache and v_cache must both be [pages, page_size, Hk, D]")
     n_pages, P, Hk, _ = k_cache.shape
     R, width = block_table.shape
-    G = pages = go = pl = pt = 0
-    if prefix_len is not None and prefix_len.numel() > 0:
-        G = prefix_len.numel()
-        if group_off is None or prefix_table is None or prefix_table.dim() != 2 or prefix_table.shape[0] != G:
-            raise ValueError("prefixes need group_off [G + 1], prefix_len [G] and prefix_table [G, pages]")
-        pages = prefix_table.shape[1]
-        go, pl = _t(group_off, "group_off", _i32, G + 1), _t(prefix_len, "prefix_len", _i32)
-        pt = _t(prefix_table, "prefix_table", _i32)
+    G, pages, go, pl, pt = _prefixes(group_off, prefix_len, prefix_table)
     strides = _strided(q, "q", dt, shape)
     dev = q.device
 
@@ -371,6 +493,43 @@ def prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
                *((out.data_ptr(), Hq * D, D) if made else _strided(out, "out", dt, shape)),
                _opt(lse, "lse", _f32, rows * Hq), _dev(workspace, "workspace").data_ptr(),
                workspace.numel() * workspace.element_size(), _opt(status, "status", _i32, 1))
+    return (out, lse) if want_lse else out
+
+
+def prefix_attention_packed(q: torch.Tensor, k_cache: tuple, v_cache: tuple, row_off: torch.Tensor, kv_len: torch.Tensor,
+                          block_table: torch.Tensor, *, scale: Optional[float] = None,
+                          group_off: Optional[torch.Tensor] = None, prefix_len: Optional[torch.Tensor] = None,
+                          prefix_table: Optional[torch.Tensor] = None, want_lse: bool = False,
+                          out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+    """spec_prefix_attention_packed: ``prefix_attention`` over two ``packed_cache`` pairs."""
+    rows, Hq, D = shape = q.shape
+    dt = q.dtype
+    kc, ks, n_pages, P, Hk = _packed(k_cache, "k_cache", None, D)
+    vc, vs, n2, P2, _ = _packed(v_cache, "v_cache", Hk, D)
+    if (n_pages, P) != (n2, P2):
+        raise ValueError("k_cache and v_cache must have the same pages")
+    R, width = block_table.shape
+    prefixes = _prefixes(group_off, prefix_len, prefix_table)
+    strides = _strided(q, "q", dt, shape)
+    dev = q.device
+    if workspace is not None:
+        _here(workspace, "workspace")
+    with _made(stream):
+        made = out is None
+        if made:
+            out = torch.empty(shape, dtype=dt, device=dev)
+        if want_lse and lse is None:
+            lse = torch.empty((rows, Hq), dtype=_f32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(attention_packed_workspace_bytes(rows, R, Hq, D), dtype=torch.uint8, device=dev)
+    G, pages, go, pl, pt = prefixes
+    _ATTENTION_PACKED(_on(stream, q), R, rows, Hq, Hk, D, _code(q), P, n_pages, width, G, pages,
+                    D ** -0.5 if scale is None else scale, *strides, kc, vc, _t(row_off, "row_off", _i32, R + 1),
+                    _t(kv_len, "kv_len", _i32, R), _t(block_table, "block_table", _i32), go, pl, pt,
+                    *((out.data_ptr(), Hq * D, D) if made else _strided(out, "out", dt, shape)),
+                    _opt(lse, "lse", _f32, rows * Hq), _dev(workspace, "workspace").data_ptr(),
+                    workspace.numel() * workspace.element_size(), _opt(status, "status", _i32, 1), ks, vs)
     return (out, lse) if want_lse else out
 
 
