@@ -662,8 +662,8 @@ typedef struct spec_norm_rope_args {
 int spec_norm_rope_cache(const spec_norm_rope_args *args, spec_stream_t stream);
 
 /* spec_cache_read_packed: the values of slots of an packed cache, k and v [rows, Hk, D]
- * dense in dtype (exact in both types); either output may be NULL.  A row with slot < 0 is
- * left as it is, and so is one with slot >= n_slots (SPEC_STATUS_BAD_PAGE).
+ * dense in dtype (exact in both types); either output may be NULL.  A row with slot < 0
+ * gets zeros, and so does one with slot >= n_slots (SPEC_STATUS_BAD_PAGE).
  * Sizes: rows >= 0, 1 <= Hk <= 1024, D <= 512, page_size >= 1 divides n_slots.
  */
 typedef struct spec_cache_read_packed_args {
@@ -683,8 +683,8 @@ int spec_cache_read_packed(const spec_cache_read_packed_args *args, spec_stream_
  * v_cache are their data, dtype is q's and out's.  A key's values are what its nibbles
  * stand for, unrounded; whatever pages hold past a request's keys has no effect.
  *   workspace  spec_attention_packed_workspace_bytes(rows, R, Hq, D) bytes
- * bf16 with D 64 or 128, pages of 16, 32, 64 or a multiple of 128 tokens and 16-byte rows
- * and scales take the tensor-core kernels; everything else the generic ones.
+ * bf16 with D 64 or 128, pages of 8, 16, 32, 64 or a multiple of 128 tokens and 16-byte
+ * rows and scales take the tensor-core kernels; everything else the generic ones.
  * Sizes: spec_prefix_attention's, D a multiple of 32 (SPEC_ERR_UNSUPPORTED).
  */
 typedef struct spec_prefix_attention_packed_args {

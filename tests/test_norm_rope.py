@@ -211,7 +211,7 @@ def test_left_out_rows_bad_slots_and_far_positions(packed):
         out = [torch.full((6, 1, 64), 9.0, device="cuda") for _ in range(2)]
         vs.cache_read_packed(kc, vc, slot, out=tuple(out), status=status)
         assert status.item() == vs.STATUS_BAD_PAGE
-        assert torch.all(out[0][3:5] == 9) and torch.equal(out[1][[0, 2, 5]].double(), values(vc)[slot[[0, 2, 5]].long()])
+        assert torch.all(out[0][3:5] == 0) and torch.all(out[1][3:5] == 0) and torch.equal(out[1][[0, 2, 5]].double(), values(vc)[slot[[0, 2, 5]].long()])
 
 
 @pytest.mark.parametrize("rows", [20, 1300])

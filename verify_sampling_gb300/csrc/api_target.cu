@@ -4,6 +4,7 @@
 #include <cfloat>
 
 #include "attention.cuh"
+#include "attention_packed.cuh"
 #include "cache_tables.cuh"
 #include "checks.cuh"
 #include "logits.cuh"
@@ -35,6 +36,10 @@ size_t attention_part_bytes(int rows, int Hq, int D) {
 size_t attention_stat_bytes(int rows, int Hq) {
   return align256(attn_partial_rows(rows, Hq) * sizeof(float2));
 }
+
+// The same for the narrow kernel over a packed cache.
+size_t narrow_part_bytes(int rows, int Hq, int D) { return align256(attn_narrow_rows(rows, Hq) * D * sizeof(float)); }
+size_t narrow_stat_bytes(int rows, int Hq) { return align256(attn_narrow_rows(rows, Hq) * sizeof(float2)); }
 
 // Everything but the workspace of an attention call; kNothing: there is nothing to do.
 int check_attention(const spec_prefix_attention_args& a, size_t cache_align) {
@@ -120,8 +125,9 @@ int spec_prefix_attention(const spec_prefix_attention_args* args, spec_stream_t 
 }
 
 size_t spec_attention_packed_workspace_bytes(int rows, int R, int Hq, int D) {
-  if (D % q4::kGroup != 0) return 0;
-  return spec_attention_workspace_bytes(rows, R, Hq, D);
+  if (D % q4::kGroup != 0 || !attention_sizes_ok(rows, R, Hq, D)) return 0;
+  return spec_attention_workspace_bytes(rows, R, Hq, D) + narrow_part_bytes(rows, Hq, D) + narrow_stat_bytes(rows, Hq) +
+         align256(attn_plan_bytes(R));
 }
 
 int spec_prefix_attention_packed(const spec_prefix_attention_packed_args* args, spec_stream_t stream) {
@@ -136,9 +142,22 @@ int spec_prefix_attention_packed(const spec_prefix_attention_packed_args* args, 
   if (rc != SPEC_OK) return rc;
   const q4::Cache packed{(const uint8_t*)a.k_cache, (const uint8_t*)a.v_cache, args->k_scale, args->v_scale};
   char* ws = static_cast<char*>(a.workspace);
-  float* part = reinterpret_cast<float*>(ws);
-  float2* stat = reinterpret_cast<float2*>(ws + attention_part_bytes(a.rows, a.Hq, a.D));
-  return status_of(launch_attention_packed_generic(a, packed, part, stat, reinterpret_cast<cudaStream_t>(stream)));
+  auto take = [&](size_t bytes) {
+    char* p = ws;
+    ws += bytes;
+    return p;
+  };
+  PackedWork work;
+  work.part = reinterpret_cast<float*>(take(attention_part_bytes(a.rows, a.Hq, a.D)));
+  work.stat = reinterpret_cast<float2*>(take(attention_stat_bytes(a.rows, a.Hq)));
+  work.plan = reinterpret_cast<int64_t*>(take(align256(attn_plan_bytes(a.R))));
+  work.narrow_part = reinterpret_cast<float*>(take(narrow_part_bytes(a.rows, a.Hq, a.D)));
+  work.narrow_stat = reinterpret_cast<float2*>(take(narrow_stat_bytes(a.rows, a.Hq)));
+  work.narrow_plan = reinterpret_cast<int64_t*>(take(align256(attn_plan_bytes(a.R))));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int sms = 0;
+  return status_of(attn_packed_ok(a, packed, &sms) ? launch_attention_packed(a, packed, sms, work, s)
+                                                   : launch_attention_packed_generic(a, packed, work.part, work.stat, s));
 }
 
 int spec_rope_cache(const spec_rope_cache_args* args, spec_stream_t stream) {

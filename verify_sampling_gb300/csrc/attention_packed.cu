@@ -1,0 +1,613 @@
+// Attention over a cache in 4 bits for few query rows a key head (decoding, short drafts).
+//
+// Mathematics: the pieces of attention_tc.cu (a reference m that follows the running maximum
+// in steps of 8, l = sum 2^(z - m), O = sum 2^(z - m) v).  An element s (n - 8) is made in bf16
+// by one fma: n goes to bits 3-6 under the exponent of 16, which is 16 + n, and (16 + n) s
+// - 24 s is exact (24 s has six significant bits, the result seven at most).
+//
+// Few rows mean that the bytes of the cache bound it, 17 KB a tile of 128 keys, 390 ns of an
+// SM's share of memory: the tensor cores have to be busy for little more than the rows that are
+// there, and what turns 32768 nibbles into operands is most of the work.  So keys lie along
+// the products' M: S^T = K Q^T and O^T = V^T P^T by mma.m16n8k16, 8 rows a product, whose A
+// fragments are made in registers and never stored: ldmatrix on the packed bytes gives a thread 8
+// dimensions of its key (K), or, transposed, 4 dimensions of two keys side by side (V), and the
+// order of dimensions and of rows within a product is free as long as both operands agree.
+// P^T is S^T's accumulator, rounded to bf16 and transposed by movmatrix.  (tcgen05 takes its
+// operands from shared memory or TMEM: the nibbles would go there and back, at M = 128 with
+// 128 rows for 8.  The wide kernel does that where rows are many.)
+//
+// Block: a producer warp walks the block's items (attention_plan.cuh) and loads query rows,
+// pages and scales by bulk copies into a ring of tiles; four warps take 32 keys of each tile, with
+// a maximum, sums and results of their own, and join at an item's end.  Three blocks an SM hide
+// one's item changes behind the others' tiles.
+//
+// Every wait is bounded: on a timeout the block sets SPEC_STATUS_TIMEOUT, waits for its copies
+// in flight and returns.
+#include "attention_packed.cuh"
+
+#include <climits>
+
+#include "attention_plan.cuh"
+
+namespace spec {
+
+namespace {
+
+constexpr int kWarps = 4, kThreads = 32 * (kWarps + 1);
+constexpr int kItemSlots = 2;
+constexpr float kSlack = 8.f;  // log2 units the maximum may grow by before O is rescaled
+
+// NB: blocks of 8 query rows of an item.
+template <int NB>
+struct NarrowCosts {
+  static constexpr int kItemRows = 8 * NB, kLeast = 4;
+  static constexpr bool kShared = true, kWide = false;
+  __device__ static __forceinline__ int tile(int) { return 4; }
+  __device__ static __forceinline__ int start(int) { return 5; }
+  __device__ static __forceinline__ int tiles_before(int x, int) { return (x + 3) >> 2; }
+};
+
+template <int D, int NB>
+struct Sizes {
+  static constexpr int kGroups = D / q4::kGroup;
+  static constexpr int kData = kTile * D / 2, kScales = kTile * kGroups;  // of a tile's keys (or values)
+  static constexpr int kStageBytes = 2 * (kData + kScales);
+  static constexpr int kStages = NB == 1 ? (D == 128 ? 3 : 6) : (D == 128 ? 3 : 6);
+  static constexpr int kQuery = NB * 8 * D * 2;  // an item's query rows
+  static constexpr int kJoin = 2 * NB * 8 * D * 4;
+};
+
+struct Bars {
+  uint64_t full[8], empty[8], item_full[kItemSlots], item_empty[kItemSlots], meet;
+  Item items[kItemSlots];
+  Layout lay;
+  int64_t warp_sum[kThreads / 32];
+  volatile int abort_flag;
+};
+
+template <int D, int NB>
+struct Smem {
+  using S = Sizes<D, NB>;
+  static constexpr int kQ = S::kStages * S::kStageBytes;
+  static constexpr int kJoin = kQ + kItemSlots * S::kQuery;
+  static constexpr int kStat = kJoin + S::kJoin;  // [kWarps][NB * 8] float2
+  static constexpr int kBars = kStat + kWarps * NB * 8 * 8;
+  static constexpr int kBytes = kBars + (int)sizeof(Bars);
+};
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t saddr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(saddr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t saddr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(saddr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t fma_bf16(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+// Scales of a pair of elements in bf16 from their bytes in the halves' low bytes, and -24 times them.
+struct Scale {
+  uint32_t s, z;
+};
+__device__ __forceinline__ Scale scale_pair(uint32_t bytes) {
+  Scale r;
+  r.s = bytes * 16u + ((uint32_t)q4::kLeastExp << 7) * 0x10001u;
+  r.z = fma_bf16(r.s, 0xC1C0C1C0u, 0x80008000u);  // -24 s - 0
+  return r;
+}
+// Elements I and I + 4 of a word's 8 (16-bit halves' I-th nibbles).
+template <int I>
+__device__ __forceinline__ uint32_t element_pair(uint32_t w, const Scale& s) {
+  const uint32_t n = I == 0 ? w << 3 : w >> (4 * I - 3);
+  return fma_bf16((n & 0x00780078u) | 0x41804180u, s.s, s.z);
+}
+
+template <int D, int NB>
+__global__ void __launch_bounds__(kThreads, NB == 1 ? kNarrowBlocks : 2)
+    attention_narrow_kernel(const spec_prefix_attention_args a, const q4::Cache packed, const Window w, float* part, float2* stat,
+                            int64_t* plan) {
+  using S = Sizes<D, NB>;
+  using M = Smem<D, NB>;
+  using C = NarrowCosts<NB>;
+  constexpr int G = S::kGroups;
+  extern __shared__ __align__(128) uint8_t smem[];
+  Bars& bars = *reinterpret_cast<Bars*>(smem + M::kBars);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int per_head = a.Hq / a.Hk;
+  lay_out<C, kThreads>(a, w, &bars.lay, bars.warp_sum, plan, [&] {
+    if (tid == 0) {
+      bars.abort_flag = 0;
+      for (int i = 0; i < S::kStages; ++i) {
+        tc::mbar_init(&bars.full[i], 1);
+        tc::mbar_init(&bars.empty[i], kWarps);
+      }
+      for (int i = 0; i < kItemSlots; ++i) {
+        tc::mbar_init(&bars.item_full[i], 1);
+        tc::mbar_init(&bars.item_empty[i], kWarps);
+      }
+      tc::mbar_init(&bars.meet, kWarps);
+      tc::fence_barrier_init();
+    }
+  });
+  __syncthreads();
+  auto warp_wait = [&](uint64_t* bar, uint32_t phase) {  // all of a warp's lanes go on, or all give up
+    bool got = tc::mbar_try_wait(bar, phase & 1u);
+    if (!__all_sync(0xffffffffu, got)) {
+      got = slow_wait(bar, phase, &bars.abort_flag, a.status);
+      got = __all_sync(0xffffffffu, got);
+    }
+    return got;
+  };
+  const int Pe = min(a.page_size, kTile);  // keys of a page within a tile
+
+  if (warp == kWarps) {
+    // ------------------------------------------------------------ producer --
+    Walker<C> walk(a, w, bars.lay);
+    Item it;
+    uint32_t bad = 0, seq = 0, n_item = 0;
+    bool ok = true;
+    const int pieces = a.page_size > kTile ? G : 1;  // copies of a page's head within a tile
+    const int piece_bytes = Pe * 16 * (G / pieces);
+    for (;; ++n_item) {
+      const bool more = walk.next(it);
+      if (!more) it.rows = 0;  // the end
+      const uint32_t slot = n_item % kItemSlots;
+      ok = warp_wait(&bars.item_empty[slot], (n_item / kItemSlots) ^ 1u);
+      if (!ok) break;
+      if (lane == 0) {
+        bars.items[slot] = it;
+        if (it.rows > 0) tc::mbar_expect_tx(&bars.item_full[slot], (uint32_t)(it.rows * D * 2));
+        else tc::mbar_arrive(&bars.item_full[slot]);
+      }
+      if (it.rows == 0) break;
+      __syncwarp();
+      if (lane < it.rows) {
+        const int m = it.m0 + lane, j = m / per_head;
+        tc::bulk_load(smem + M::kQ + slot * S::kQuery + lane * D * 2,
+                      (const __nv_bfloat16*)a.q + (int64_t)(it.row0 + j) * a.q_row + (int64_t)(it.h * per_head + (m - j * per_head)) * a.q_head,
+                      D * 2, &bars.item_full[slot]);
+      }
+      // page ids, 32 at a time, the next 32 on their way
+      const int pages = (it.keys + a.page_size - 1) / a.page_size;
+      int base = (int)((int64_t)it.lo * kTile / a.page_size);
+      auto fetch = [&](int from) { return from + lane < pages ? page_of(a, it.table, from + lane, &bad) : 0; };
+      int cur = fetch(base), nxt = fetch(base + 32);
+      for (int i = it.lo; i < it.hi; ++i, ++seq) {
+        const int first = (int)((int64_t)i * kTile / a.page_size);  // first page of the tile
+        if (first >= base + 32) {
+          cur = nxt;
+          base += 32;
+          nxt = fetch(base + 32);
+        }
+        const int live = min(kTile, it.keys - i * kTile);
+        const int used = (live + Pe - 1) / Pe;
+        const uint32_t st = seq % S::kStages;
+        // lane c: copy c of the tile, (page, keys or values, data piece or scales)
+        const int copies = used * 2 * (pieces + 1);
+        ok = warp_wait(&bars.empty[st], (seq / S::kStages) ^ 1u);
+        if (!ok) break;
+        if (lane == 0) tc::mbar_expect_tx(&bars.full[st], (uint32_t)(used * 2 * (Pe * 16 * G + Pe * G)));
+        __syncwarp();
+        const int in_page = (int)((int64_t)i * kTile - (int64_t)first * a.page_size);  // pages of more than a tile
+        for (int c0 = 0; c0 < copies; c0 += 32) {
+          const int c = c0 + lane, x = c / (2 * (pieces + 1)), rest = c - x * 2 * (pieces + 1);
+          const int page = __shfl_sync(0xffffffffu, cur, min(first + x - base, 31) & 31);
+          if (c >= copies) continue;
+          const int kv = rest & 1, piece = rest >> 1;
+          uint8_t* to = smem + st * S::kStageBytes + kv * (S::kData + S::kScales);
+          if (piece < pieces)
+            tc::bulk_load(to + (x * G + piece) * Pe * 16,
+                          (kv ? packed.v : packed.k) + q4::data_at(page, it.h, in_page, a.Hk, G, a.page_size) +
+                              (int64_t)piece * 16 * a.page_size,
+                          piece_bytes, &bars.full[st]);
+          else
+            tc::bulk_load(to + S::kData + x * Pe * G,
+                          (kv ? packed.v_scale : packed.k_scale) + q4::scale_at(page, it.h, in_page, a.Hk, G, a.page_size), Pe * G,
+                          &bars.full[st]);
+        }
+      }
+      if (!ok) break;
+    }
+    if (bad) set_status(a.status, bad);
+    if (!ok) {  // the copies in flight land before the block's memory goes
+      const uint32_t from = seq > (uint32_t)S::kStages ? seq - S::kStages : 0u;
+      for (uint32_t s = from; s < seq; ++s) tc::mbar_wait(&bars.full[s % S::kStages], (s / S::kStages) & 1u, kWaitNs);
+      for (uint32_t s = n_item > kItemSlots ? n_item - kItemSlots : 0u; s <= n_item; ++s)
+        tc::mbar_wait(&bars.item_full[s % kItemSlots], (s / kItemSlots) & 1u, kWaitNs / 100);
+    }
+  } else {
+    // ----------------------------------------------------------- consumers --
+    const int g = lane >> 2, t = lane & 3;
+    const float sl = a.scale * kLog2e;
+    const uint32_t sbase = tc::smem_u32(smem);
+    // ldmatrix rows of this lane: blocks of 8 keys 4 warp + 2 b + (lane >> 3 & 1), group (lane >> 4) and then two on
+    uint32_t row_at[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int key = (warp * 4 + 2 * b + (lane >> 3 & 1)) * 8, page = key / Pe;
+      row_at[b] = (uint32_t)((page * G + (lane >> 4)) * Pe * 16 + (key - page * Pe + (lane & 7)) * 16);
+    }
+    const uint32_t two_groups = 2 * Pe * 16;
+    const bool wide_out = ((uintptr_t)a.out & 7) == 0 && a.out_row % 4 == 0 && a.out_head % 4 == 0;
+    float* join = reinterpret_cast<float*>(smem + M::kJoin);
+    float2* row_stat = reinterpret_cast<float2*>(smem + M::kStat);
+    uint32_t seq = 0, met = 0;
+    bool ok = true;
+    auto meet = [&] {  // the four warps (a named barrier's wait would have no limit)
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars.meet);
+      ok = warp_wait(&bars.meet, met++);
+      return ok;
+    };
+    for (uint32_t n_item = 0;; ++n_item) {
+      const uint32_t slot = n_item % kItemSlots;
+      ok = warp_wait(&bars.item_full[slot], n_item / kItemSlots);
+      if (!ok) break;
+      const Item it = bars.items[slot];
+      if (it.rows == 0) break;
+      // query fragments: dimensions 32 c + 8 t + (i, i + 4) of row g
+      const uint8_t* qs = smem + M::kQ + slot * S::kQuery;
+      auto query = [&](int nb, int c, uint32_t (&q)[4]) {
+        const uint4 v = tc::lds128(qs + (nb * 8 + g) * D * 2 + c * 64 + t * 16);
+        q[0] = __byte_perm(v.x, v.z, 0x5410);
+        q[1] = __byte_perm(v.x, v.z, 0x7632);
+        q[2] = __byte_perm(v.y, v.w, 0x5410);
+        q[3] = __byte_perm(v.y, v.w, 0x7632);
+      };
+      constexpr bool kHold = NB <= 2;  // the fragments fit the registers
+      uint32_t q[kHold ? NB : 1][G][4];
+      if (kHold) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int c = 0; c < G; ++c) query(nb, c, q[kHold ? nb : 0][c]);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars.item_empty[slot]);
+      }
+      int limit[NB][2];  // keys of rows 2 t, 2 t + 1 of each block (rows past the item's: any)
+      float ref[NB][2], l[NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int m = min(nb * 8 + 2 * t + e, it.rows - 1);
+          limit[nb][e] = it.prefix ? it.keys : min(it.keys, it.first_own + (it.m0 + m) / per_head);
+          ref[nb][e] = -CUDART_INF_F;
+          l[nb][e] = 0.f;
+        }
+      const int least = it.prefix ? it.keys : min(it.keys, it.first_own + it.m0 / per_head);  // of the first row
+      float o[G][2][NB][4];
+#pragma unroll
+      for (int c = 0; c < G; ++c)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[c][x][nb][e] = 0.f;
+
+      for (int i = it.lo; i < it.hi; ++i, ++seq) {
+        const uint32_t st = seq % S::kStages;
+        ok = warp_wait(&bars.full[st], seq / S::kStages);
+        if (!ok) break;
+        const uint32_t ks = sbase + st * S::kStageBytes, vs = ks + S::kData + S::kScales;
+        const uint8_t* k_scale = smem + st * S::kStageBytes + S::kData;
+        const uint8_t* v_scale = k_scale + S::kData + S::kScales;
+        float s[2][NB][4];  // scores of keys g and g + 8 of 16, rows 2 t and 2 t + 1
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[b][nb][e] = 0.f;
+        uint32_t sc[2][2];  // the groups' scale bytes of keys g and g + 8
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int key = (warp * 4 + 2 * b + x) * 8 + g;
+            sc[b][x] = G == 4 ? *reinterpret_cast<const uint32_t*>(k_scale + key * G)
+                              : (uint32_t)*reinterpret_cast<const uint16_t*>(k_scale + key * G);
+          }
+#pragma unroll
+        for (int c = 0; c < G; c += 2) {
+          uint32_t r[2][4];  // [pair of blocks][block, block + 1 of group c, then of c + 1]
+#pragma unroll
+          for (int b = 0; b < 2; ++b) ldmatrix4(r[b], ks + row_at[b] + (c >> 1) * two_groups);
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            uint32_t f[2][8];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const Scale z = scale_pair(__byte_perm(sc[b][x], 0, 0x4040 | (c + cc) * 0x0101));
+                const uint32_t v = r[b][2 * cc + x];
+                f[b][x] = element_pair<0>(v, z);
+                f[b][2 + x] = element_pair<1>(v, z);
+                f[b][4 + x] = element_pair<2>(v, z);
+                f[b][6 + x] = element_pair<3>(v, z);
+              }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              uint32_t qf[4];
+              if (!kHold) query(nb, c + cc, qf);
+              const uint32_t* qq = kHold ? q[kHold ? nb : 0][c + cc] : qf;
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                mma(s[b][nb], f[b][0], f[b][1], f[b][2], f[b][3], qq[0], qq[1]);
+                mma(s[b][nb], f[b][4], f[b][5], f[b][6], f[b][7], qq[2], qq[3]);
+              }
+            }
+          }
+        }
+        // scores in log2 units, masked
+        const int key0 = i * kTile + warp * 32 + g;
+        if (i * kTile + kTile > least) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (key0 + 16 * b + 8 * (e >> 1) >= limit[nb][e & 1]) s[b][nb][e] = -CUDART_INF_F;
+        }
+        bool grown = false;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float top = fmaxf(fmaxf(s[0][nb][e], s[0][nb][e + 2]), fmaxf(s[1][nb][e], s[1][nb][e + 2]));
+            grown |= top * sl > ref[nb][e] + kSlack;
+          }
+        if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float top = fmaxf(fmaxf(s[0][nb][e], s[0][nb][e + 2]), fmaxf(s[1][nb][e], s[1][nb][e + 2])) * sl;
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+              // each row by its own scores alone: its bits do not depend on its neighbours
+              const float to = top > ref[nb][e] + kSlack ? top : ref[nb][e];
+              const float f = to == ref[nb][e] ? 1.f : tc::ex2(ref[nb][e] - to);  // 0 from -inf
+              ref[nb][e] = to;
+              l[nb][e] *= f;
+#pragma unroll
+              for (int c = 0; c < G; ++c)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  o[c][x][nb][e] *= f;
+                  o[c][x][nb][e + 2] *= f;
+                }
+            }
+        }
+        uint32_t p[2][NB][2];  // weights of keys 2 t, 2 t + 1 (and + 8) of each 16, row g
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const float sub0 = ref[nb][0] == -CUDART_INF_F ? 0.f : ref[nb][0], sub1 = ref[nb][1] == -CUDART_INF_F ? 0.f : ref[nb][1];
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float p0 = tc::ex2(fmaf(s[b][nb][2 * x], sl, -sub0)), p1 = tc::ex2(fmaf(s[b][nb][2 * x + 1], sl, -sub1));
+              l[nb][0] += p0;
+              l[nb][1] += p1;
+              // rounded to bf16: 8 bits of a weight are 8 bits of its share of the result
+              p[b][nb][x] = transposed(pack_bf16(p0, p1));
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          // scale bytes of keys 2 t and 2 t + 1 of both blocks, split by even and odd groups
+          uint32_t even[2][2], odd[2][2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint8_t* at = v_scale + ((warp * 4 + 2 * b + x) * 8 + 2 * t) * G;
+            uint32_t k0, k1;
+            if (G == 4) {
+              const uint2 v = *reinterpret_cast<const uint2*>(at);
+              k0 = v.x, k1 = v.y;
+            } else {
+              k0 = *reinterpret_cast<const uint32_t*>(at);
+              k1 = k0 >> 16;
+            }
+            even[x][0] = k0 & 0x00ff00ffu, even[x][1] = k1 & 0x00ff00ffu;
+            odd[x][0] = k0 >> 8 & 0x00ff00ffu, odd[x][1] = k1 >> 8 & 0x00ff00ffu;
+          }
+#pragma unroll
+          for (int c = 0; c < G; c += 2) {
+            uint32_t r[4];
+            ldmatrix4_trans(r, vs + row_at[b] + (c >> 1) * two_groups);
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+              Scale z[2];
+#pragma unroll
+              for (int x = 0; x < 2; ++x)
+                z[x] = scale_pair(cc == 0 ? __byte_perm(even[x][0], even[x][1], c == 0 ? 0x5410 : 0x7632)
+                                          : __byte_perm(odd[x][0], odd[x][1], c == 0 ? 0x5410 : 0x7632));
+              const uint32_t v0 = r[2 * cc], v1 = r[2 * cc + 1];
+              const uint32_t f0 = element_pair<0>(v0, z[0]), f1 = element_pair<1>(v0, z[0]), f2 = element_pair<0>(v1, z[1]),
+                             f3 = element_pair<1>(v1, z[1]);
+              const uint32_t h0 = element_pair<2>(v0, z[0]), h1 = element_pair<3>(v0, z[0]), h2 = element_pair<2>(v1, z[1]),
+                             h3 = element_pair<3>(v1, z[1]);
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                mma(o[c + cc][0][nb], f0, f1, f2, f3, p[b][nb][0], p[b][nb][1]);
+                mma(o[c + cc][1][nb], h0, h1, h2, h3, p[b][nb][0], p[b][nb][1]);
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars.empty[st]);
+      }
+      if (!ok) break;
+      if (!kHold) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars.item_empty[slot]);
+      }
+      // ---- the warps' results: maxima and sums of all, results pairwise
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], x);
+          if (g == 0) row_stat[warp * NB * 8 + nb * 8 + 2 * t + e] = make_float2(ref[nb][e], l[nb][e]);
+        }
+      if (!meet()) break;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float2 v[kWarps];
+          float top = -CUDART_INF_F, sum = 0.f;
+#pragma unroll
+          for (int x = 0; x < kWarps; ++x) {
+            v[x] = row_stat[x * NB * 8 + nb * 8 + 2 * t + e];
+            top = fmaxf(top, v[x].x);
+          }
+          const float sub = top == -CUDART_INF_F ? 0.f : top;
+#pragma unroll
+          for (int x = 0; x < kWarps; ++x) sum = fmaf(v[x].y, tc::ex2(v[x].x - sub), sum);
+          const float f = tc::ex2(ref[nb][e] - sub);  // 0 from -inf
+          ref[nb][e] = top;
+          l[nb][e] = sum;
+#pragma unroll
+          for (int c = 0; c < G; ++c)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              o[c][x][nb][e] *= f;
+              o[c][x][nb][e + 2] *= f;
+            }
+        }
+      auto give = [&](float* to) {
+#pragma unroll
+        for (int c = 0; c < G; ++c)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              *reinterpret_cast<float4*>(to + (((c * 2 + x) * NB + nb) * 32 + lane) * 4) =
+                  make_float4(o[c][x][nb][0], o[c][x][nb][1], o[c][x][nb][2], o[c][x][nb][3]);
+      };
+      auto take = [&](const float* from) {
+#pragma unroll
+        for (int c = 0; c < G; ++c)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              const float4 v = *reinterpret_cast<const float4*>(from + (((c * 2 + x) * NB + nb) * 32 + lane) * 4);
+              o[c][x][nb][0] += v.x, o[c][x][nb][1] += v.y, o[c][x][nb][2] += v.z, o[c][x][nb][3] += v.w;
+            }
+      };
+      float* mine = join + (warp & 1) * NB * 8 * D;
+      if (warp >= 2) give(mine);
+      if (!meet()) break;
+      if (warp < 2) take(mine);
+      if (warp == 1) give(mine);
+      if (!meet()) break;
+      if (warp > 0) continue;
+      take(join + NB * 8 * D);
+      // row 2 t + e: dimensions 32 c + 4 g .. + 3
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int m = nb * 8 + 2 * t + e;
+          if (m >= it.rows) continue;
+          const float sum = l[nb][e];
+          const int j = (it.m0 + m) / per_head, row = it.row0 + j, hq = it.h * per_head + (it.m0 + m - j * per_head);
+          if (!it.direct) {
+            const size_t at = it.slot + m;
+#pragma unroll
+            for (int c = 0; c < G; ++c)
+              *reinterpret_cast<float4*>(part + at * D + 32 * c + 4 * g) =
+                  make_float4(o[c][0][nb][e], o[c][0][nb][e + 2], o[c][1][nb][e], o[c][1][nb][e + 2]);
+            if (g == 0) stat[at] = make_float2(ref[nb][e], sum);
+            continue;
+          }
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row without keys: zeros
+          __nv_bfloat16* out = (__nv_bfloat16*)a.out + (int64_t)row * a.out_row + (int64_t)hq * a.out_head + 4 * g;
+#pragma unroll
+          for (int c = 0; c < G; ++c) {
+            const uint2 v = make_uint2(pack_bf16(o[c][0][nb][e] * inv, o[c][0][nb][e + 2] * inv),
+                                       pack_bf16(o[c][1][nb][e] * inv, o[c][1][nb][e + 2] * inv));
+            if (wide_out) {
+              *reinterpret_cast<uint2*>(out + 32 * c) = v;
+            } else {
+              *reinterpret_cast<uint32_t*>(out + 32 * c) = v.x;
+              *reinterpret_cast<uint32_t*>(out + 32 * c + 2) = v.y;
+            }
+          }
+          if (a.lse && g == 0) a.lse[(size_t)row * a.Hq + hq] = sum == 0.f ? -CUDART_INF_F : (ref[nb][e] + log2f(sum)) * kLn2;
+        }
+    }
+  }
+  tc::grid_dep_launch();
+}
+
+template <int D, int NB>
+cudaError_t launch(const spec_prefix_attention_args& a, const q4::Cache& packed, int sms, const PackedWork& work, cudaStream_t stream) {
+  using C = NarrowCosts<NB>;
+  constexpr int kBytes = Smem<D, NB>::kBytes;
+  auto kernel = attention_narrow_kernel<D, NB>;
+  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  if (err != cudaSuccess) return err;
+  const int blocks = std::min(NB == 1 ? kNarrowBlocks : 2, 227 * 1024 / (kBytes + 1024));
+  const int most_rows = attn_window_rows(a.Hq), windows = (int)(((int64_t)a.rows + most_rows - 1) / most_rows);
+  const int step = (int)(((int64_t)a.rows + windows - 1) / windows);
+  for (int64_t lo = 0; lo < a.rows; lo += step) {
+    const Window w{(int)lo, (int)std::min<int64_t>(lo + step, a.rows), INT_MAX};
+    kernel<<<sms * blocks, kThreads, kBytes, stream>>>(a, packed, w, work.narrow_part, work.narrow_stat, work.narrow_plan);
+    if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    const Pieces pieces{work.narrow_part, work.narrow_stat, work.narrow_plan};
+    err = launch_join<D, C, C>(a, w, windows, pieces, pieces, stream);
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
+}
+
+template <int D>
+cudaError_t launch(const spec_prefix_attention_args& a, const q4::Cache& packed, int sms, const PackedWork& work, cudaStream_t stream) {
+  const int64_t m = (int64_t)a.rows * (a.Hq / a.Hk);  // query rows of a key head
+  if (m <= 8 * (int64_t)a.R) return launch<D, 1>(a, packed, sms, work, stream);
+  if (m <= 16 * (int64_t)a.R) return launch<D, 2>(a, packed, sms, work, stream);
+  return launch<D, 4>(a, packed, sms, work, stream);
+}
+
+}  // namespace
+
+// bf16 heads of 64 or 128, pages that tile 128 keys, rows, data and scales on 16 bytes.
+bool attn_packed_ok(const spec_prefix_attention_args& a, const q4::Cache& packed, int* sms) {
+  if (((uintptr_t)packed.k_scale | (uintptr_t)packed.v_scale) % 16 != 0) return false;
+  return attn_tc_ok(a, sms);
+}
+
+cudaError_t launch_attention_packed(const spec_prefix_attention_args& a, const q4::Cache& packed, int sms, const PackedWork& work,
+                                    cudaStream_t stream) {
+  return a.D == 128 ? launch<128>(a, packed, sms, work, stream) : launch<64>(a, packed, sms, work, stream);
+}
+
+}  // namespace spec

@@ -37,7 +37,7 @@
 
 #include <cstddef>
 
-#include "attention.cuh"
+#include "attention_plan.cuh"
 #include "fused_tc.cuh"
 #include "tc.cuh"
 
@@ -47,177 +47,26 @@ namespace {
 
 using namespace attn;
 
-constexpr int kTile = 128;  // keys of a tile, rows of a softmax group
+// (kTile: keys of a tile, and rows of a softmax group)
 // Softmax warps: group t (rows 128 t ..) is warps 8 t .. 8 t + 7; warps w and w + 4 of it
 // share 32 rows (TMEM lanes go by the warp's number mod 4), 16 each, and a row has
 // threads i and i + 16 of its warp, each half of its columns.
 constexpr int kSoftWarps = 16, kProducer = 16, kMma = 17, kPlanner = 18, kLoader = 19;
 constexpr int kThreads = 640;
 constexpr int kItemSlots = 4, kItemReaders = 3 + kSoftWarps;  // producer, MMA, loader, softmax warps
-constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kSlack = 8.f;  // log2 units the maximum may grow by before O is rescaled
+
 // Costs, in units of 0.1 us, measured: a tile of an item of both softmax groups (bound
 // by the products), a tile of a smaller one (bound by its 64 KB where all blocks stream,
 // otherwise by its chain of product, softmax and product), and an item's start and end.
-constexpr int kCostPair = 17, kCostSingle = 15, kCostStartPair = 57, kCostStartSingle = 21;
-
-// ------------------------------------------------------------ work layout --
-struct Window {  // the packed rows of a launch: [lo, hi)
-  int lo, hi;
-};
-__device__ __forceinline__ Rows inside(const Rows& rows, const Window& w) {
-  const int lo = max(rows.row0, w.lo), hi = min(rows.row0 + rows.n, w.hi);
-  return Rows{lo, max(hi - lo, 0)};
-}
-
-struct Segment {  // a group's prefix or a request's own keys
-  int row0, n;    // packed rows in the window
-  int keys;
-  int first_own;  // own index of row 0's last key + 1 (prefix: keys)
-  const int32_t* table;
-  bool prefix;
-};
-
-struct Item {
-  int row0, m0, rows;  // query rows m0 .. m0 + rows of the segment's n * heads-per-key-head
-  int h, lo, hi;       // key head, tiles
-  int keys;            // keys the item reads
-  int first_own;
-  bool prefix;
-  bool direct;  // the whole of its rows' keys: the result itself is written
-  const int32_t* table;
-  size_t slot;  // partial row of its row m0
-};
-
-struct Layout {
-  int64_t per;  // cost of a block
-  int64_t x0, x1;
-  int k0;        // first segment and its position
-  int64_t s0;
-};
-
-__device__ __forceinline__ Segment segment(const spec_prefix_attention_args& a, const Window& w, int k, uint32_t* bad) {
-  Segment s;
-  if (k < a.G) {
-    const int2 in = group_requests(a, k, bad);
-    const Rows rows = inside(rows_between(a, in.x, in.y, bad), w);
-    s = Segment{rows.row0, rows.n, prefix_keys(a, k, bad), 0,
-                a.prefix_table + (size_t)k * a.max_prefix_pages, true};
-    s.first_own = s.keys;
-  } else {
-    const int r = k - a.G;
-    const Rows all = rows_between(a, r, r + 1, bad), rows = inside(all, w);
-    const int kv = own_keys(a, r, bad);
-    s = Segment{rows.row0, rows.n, kv, kv - all.n + 1 + (rows.row0 - all.row0),
-                a.block_table + (size_t)r * a.max_pages, false};
-  }
-  return s;
-}
-// The group that request r is in, or -1, and the keys of its prefix.
-__device__ __forceinline__ int group_of(const spec_prefix_attention_args& a, int r, uint32_t* bad) {
-  if (a.G == 0) return -1;
-  const int g = last_at_or_below(a.group_off, a.G, r);
-  const int2 in = group_requests(a, g, bad);
-  return r >= in.x && r < in.y ? g : -1;
-}
-__device__ __forceinline__ int shared_keys(const spec_prefix_attention_args& a, int r, uint32_t* bad) {
-  const int g = group_of(a, r, bad);
-  return g < 0 ? 0 : prefix_keys(a, g, bad);
-}
-// Keys that the item of query rows [256 i, ..) needs: its last row's.
-__device__ __forceinline__ int item_keys(const Segment& s, int i, int per_head) {
-  if (s.prefix) return s.keys;
-  const int j = min(s.n - 1, (i * kItemRows + kItemRows - 1) / per_head);
-  return max(0, min(s.keys, s.first_own + j));
-}
-__device__ __forceinline__ int item_count(const Segment& s, int per_head) {
-  return (int)(((unsigned)s.n * (unsigned)per_head + kItemRows - 1) / kItemRows);  // rows * Hq < 2^31
-}
-__device__ __forceinline__ int tile_cost(int rows) { return rows > kTile ? kCostPair : kCostSingle; }
-__device__ __forceinline__ int start_cost(int rows) { return rows > kTile ? kCostStartPair : kCostStartSingle; }
-// Cost of an item of `rows` query rows (or more: 256 are its own).
-__device__ __forceinline__ int item_cost(int keys, int rows) {
-  const int tiles = (keys + kTile - 1) / kTile;
-  return tiles ? start_cost(rows) + tiles * tile_cost(rows) : 0;
-}
-__device__ __forceinline__ int64_t head_cost(const Segment& s, int per_head) {
-  const int n = item_count(s, per_head);
-  if (n == 0) return 0;
-  int64_t c = item_cost(item_keys(s, n - 1, per_head), s.n * per_head - (n - 1) * kItemRows);
-  if (s.prefix) return c + (int64_t)(n - 1) * item_cost(s.keys, kItemRows);
-#pragma unroll 1
-  for (int i = 0; i < n - 1; ++i) c += item_cost(item_keys(s, i, per_head), kItemRows);
-  return c;
-}
-// x / y rounded up or a little more, by one 32-bit division: the code of a 64-bit one
-// is a good part of what a block with little work has to fetch before it starts.
-__device__ __forceinline__ int64_t share_of(int64_t x, unsigned y) {
-  const int drop = max(0, 32 - __clzll(x));
-  return (int64_t)((unsigned)(x >> drop) / y + 1) << drop;
-}
-
-// Tiles whose costs begin before `x` units of an item's tiles.
-__device__ __forceinline__ int tiles_before(int x, int rows) {
-  return rows > kTile ? (unsigned)(x + kCostPair - 1) / kCostPair : (unsigned)(x + kCostSingle - 1) / kCostSingle;
-}
-
-// The block's items in order.  (One copy of each step: a block's first item waits for
-// this code to be fetched.)
-struct Walker {
-  const spec_prefix_attention_args& a;
-  const Window& w;
-  int64_t pos, x0, x1;
-  int k, h, i, per_head, count;
-  Segment seg;
-  bool alone;  // a request without a prefix
-  uint32_t bad;
-
-  __device__ Walker(const spec_prefix_attention_args& args, const Window& window, const Layout& lay)
-      : a(args), w(window), pos(lay.s0), x0(lay.x0), x1(lay.x1), k(lay.k0 - 1), h(0), i(0),
-        per_head(args.Hq / args.Hk), count(0), alone(false), bad(0) {}
-  __device__ __forceinline__ bool next(Item& it) {
-#pragma unroll 1
-    while (pos < x1) {
-      if (i >= count) {  // next head, or next segment
-        i = 0;
-        if (count == 0 || ++h >= a.Hk) {
-          h = 0;
-          if (++k >= a.G + a.R) return false;
-          seg = segment(a, w, k, &bad);
-          count = item_count(seg, per_head);
-          alone = k >= a.G && (a.G == 0 || shared_keys(a, k - a.G, &bad) == 0);
-          if (count > 0 && pos < x0) {  // the layout starts in this segment: whole heads before it
-            const int64_t c = head_cost(seg, per_head);
-#pragma unroll 1
-            for (; pos + c <= x0 && h + 1 < a.Hk; ++h) pos += c;
-          }
-        }
-        continue;
-      }
-      const int keys = item_keys(seg, i, per_head), m = seg.n * per_head;
-      it.m0 = i * kItemRows;
-      ++i;
-      const int left = m - it.m0;
-      const int cost = item_cost(keys, left), tiles = (keys + kTile - 1) / kTile;
-      const int64_t at = pos + start_cost(left);
-      pos += cost;
-      if (cost == 0 || pos <= x0) continue;
-      it.lo = x0 <= at ? 0 : tiles_before((int)(x0 - at), left);  // x0 - at < cost
-      it.hi = x1 <= at ? 0 : x1 >= pos ? tiles : tiles_before((int)(x1 - at), left);
-      if (it.lo >= it.hi) continue;
-      it.row0 = seg.row0;
-      it.rows = min(kItemRows, left);
-      it.h = h;
-      it.keys = keys;
-      it.first_own = seg.first_own;
-      it.prefix = seg.prefix;
-      it.direct = alone && it.lo == 0 && it.hi == tiles;
-      it.table = seg.table;
-      it.slot = (seg.prefix ? 0 : (size_t)(w.hi - w.lo) * a.Hq) + (size_t)(seg.row0 - w.lo) * a.Hq + (size_t)h * m +
-                it.m0 + (size_t)kItemRows * blockIdx.x;
-      return true;
-    }
-    return false;
+struct Costs {
+  static constexpr int kItemRows = attn::kItemRows, kLeast = 17;
+  static constexpr bool kShared = false, kWide = true;  // takes every segment
+  __device__ static __forceinline__ int tile(int rows) { return rows > kTile ? 17 : 15; }
+  __device__ static __forceinline__ int start(int rows) { return rows > kTile ? 57 : 21; }
+  // Tiles whose costs begin before `x` units of an item's tiles.
+  __device__ static __forceinline__ int tiles_before(int x, int rows) {
+    return rows > kTile ? (unsigned)(x + 16) / 17 : (unsigned)(x + 14) / 15;
   }
 };
 
@@ -342,11 +191,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 // 16 bytes to a shared address, without registers in between.
 __device__ __forceinline__ void copy16(uint32_t saddr, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(saddr), "l"(from) : "memory");
@@ -358,26 +202,6 @@ __device__ __forceinline__ void store32(float* p, const uint32_t* v) {
                "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
-// bf16x2 with `lo` in the low half
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// The rest of a wait whose first look failed.  Gives up when the time limit passes or
-// another warp has given up.  (Out of line: the code of a role that a short item
-// runs once has to fit the instruction cache beside the others'.)
-__device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t phase, volatile int* abort_flag, uint32_t* status) {
-  for (int i = 0; i < 2000; ++i) {
-    if (tc::mbar_wait(bar, phase & 1u, kWaitNs / 2000)) return true;
-    if (*abort_flag) return false;
-  }
-  *abort_flag = 1;
-  set_status(status, SPEC_STATUS_TIMEOUT);
-  return false;
-}
-
 // Everything shared beside the tiles.
 struct Shared {
   uint64_t item_full[kItemSlots], item_empty[kItemSlots];
@@ -420,22 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be uniform
   const int per_head = a.Hq / a.Hk;
 
-  // ---- the work layout: every thread a run of segments, one scan
-  {
-    const int n_seg = a.G + a.R, run = (n_seg + kThreads - 1) / kThreads;
-    const int k0 = min(tid * run, n_seg), k1 = min(k0 + run, n_seg);
-    uint32_t bad = 0;
-    auto cost_of = [&](int k) { return a.Hk * head_cost(segment(a, w, k, &bad), per_head); };
-    int64_t mine = 0;
-#pragma unroll 1
-    for (int k = k0; k < k1; ++k) mine += cost_of(k);
-    int64_t inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t t = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += t;
-    }
-    if (lane == 31) warp_sum[warp] = inc;
+  lay_out<Costs, kThreads>(a, w, &lay, warp_sum, plan, [&] {
     if (warp == kMma) tc::tmem_alloc(&bars.tmem, 512);
     if (warp == kLoader) {
       // arrivals of each barrier, in the order they lie in
@@ -450,40 +259,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == kProducer && lane == 0) {
       abort_flag = 0;
-      lay = Layout{0, 0, 0, 0, 0};
       tc::tma_prefetch_desc(&k_map);
       tc::tma_prefetch_desc(&v_map);
       if (q_box > 0) tc::tma_prefetch_desc(&q_map);
     }
-    __syncthreads();
-    int64_t sum = lane < kThreads / 32 ? warp_sum[lane] : 0;  // every warp scans the warps' sums
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t t = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += t;
-    }
-    const int64_t total = __shfl_sync(0xffffffffu, sum, 31);
-    const int64_t upto = __shfl_sync(0xffffffffu, sum, warp);
-    int64_t at = upto - __shfl_sync(0xffffffffu, inc, 31) + inc - mine;  // the thread's first segment
-    // at least one tile a block, so that every block of an item's range has one
-    const int64_t per = max(share_of(total, gridDim.x), (int64_t)max(kCostPair, kCostSingle));
-    const int64_t x0 = per * blockIdx.x, x1 = min(x0 + per, total);
-    const bool here = x0 < x1 && at <= x0 && x0 < at + mine;
-    if (here || blockIdx.x == 0) {
-#pragma unroll 1
-      for (int k = k0; k < k1; ++k) {
-        const int64_t c = run == 1 ? mine : cost_of(k);
-        if (blockIdx.x == 0) plan[1 + k] = at;
-        if (here && at <= x0 && x0 < at + c) lay = Layout{per, x0, x1, k, at};
-        at += c;
-      }
-    }
-    if (blockIdx.x == 0 && tid == 0) plan[0] = per;
-    if (bad && blockIdx.x == 0) set_status(a.status, bad);
-    tc::fence_before_sync();
-    __syncthreads();
-    tc::fence_after_sync();
-  }
+  });
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem, 0);
   // A wait of a whole warp: all of its lanes go on, or all give up.
   auto warp_wait = [&](uint64_t* bar, uint32_t phase) {
@@ -677,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kPlanner) {
     // ------------------------------------------------------------- planner --
-    Walker walk(a, w, lay);
+    Walker<Costs> walk(a, w, lay);
     Item it;
     for (uint32_t n_item = 0;; ++n_item) {
       if (!walk.next(it)) it.rows = 0;  // the end
@@ -921,173 +704,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMma) tc::tmem_dealloc(tmem, 512);
 }
 
-// ----------------------------------------------------------------- join ----
-constexpr int kJoinThreads = 128;
-constexpr int kJoinBlocks = 152 * 16;
-constexpr int kJoinRows = 64;  // query rows (packed rows x heads of a key head) of a block at a time
-
-constexpr int kJoinLanes = 16;  // threads of a row
-
-// Cost of a head's items before item `upto`, and of all of them; a row's threads add them up.
-__device__ __forceinline__ void costs_of(const Segment& s, int per_head, int upto, int64_t* before, int64_t* all) {
-  const int n = item_count(s, per_head), lane = threadIdx.x % kJoinLanes;
-  const uint32_t lanes = (uint32_t)((1ull << kJoinLanes) - 1) << (threadIdx.x & 31 & ~(kJoinLanes - 1));
-  int64_t x = 0, y = 0;
-  for (int i = lane; i < n; i += kJoinLanes) {
-    const int64_t c = item_cost(item_keys(s, i, per_head), s.n * per_head - i * kItemRows);
-    y += c;
-    if (i < upto) x += c;
-  }
-#pragma unroll
-  for (int o = kJoinLanes / 2; o > 0; o >>= 1) {
-    x += __shfl_xor_sync(lanes, x, o);
-    y += __shfl_xor_sync(lanes, y, o);
-  }
-  *before = x;
-  *all = y;
-}
-
-// Joins the pieces of every row that has more than one.  A block takes a request's
-// rows, tiles of 64 of one key head after the other: what says where their pieces are
-// is a chain of dependent loads, paid once a block.  Half a warp a row: twice the rows in
-// flight (the round of 256 requests behind a prefix 779 us in all, 790 with a warp a row, both in
-// short runs: after half a second the power limit's clock makes it 828).
-template <int D>
-__device__ __forceinline__ void join_request(const spec_prefix_attention_args& a, const Window& w, int r,
-                                             const float* part, const float2* stat, const int64_t* plan) {
-  constexpr int kPer = D / kJoinLanes, kBatch = 4;
-  const int lane = threadIdx.x % kJoinLanes, per_head = a.Hq / a.Hk;
-  uint32_t bad = 0;
-  const Segment own = segment(a, w, a.G + r, &bad);
-  int g = group_of(a, r, &bad);
-  Segment pre{0, 0, 0, 0, nullptr, true};
-  if (g >= 0) pre = segment(a, w, g, &bad);
-  if (own.row0 < pre.row0 || own.row0 + own.n > pre.row0 + pre.n) g = -1;  // rows out of order
-  const int m_own = own.n * per_head;
-  const int m_off = (own.row0 - pre.row0) * per_head;  // the request's first row among the group's
-  tc::grid_dep_wait();  // all of the above is the caller's; the pieces and their layout are ready now
-  const int64_t per = plan[0];
-  const int64_t own_at = plan[1 + a.G + r], pre_at = g >= 0 ? plan[1 + g] : 0;
-
-  const int tiles = (m_own + kJoinRows - 1) / kJoinRows, all_tiles = tiles * a.Hk;
-  int item[2] = {-1, -1}, head = -1;  // own and prefix item, and key head, whose pieces are known
-  int64_t before[2] = {0, 0}, all[2] = {0, 0};
-  int first[2] = {0, 0}, count[2] = {0, 0};
-  auto pieces = [&](int k, const Segment& s, int64_t at, int h, int i) {  // blocks that have pieces of item i
-    if (i == item[k] && h == head) return;
-    const int tiles = (item_keys(s, i, per_head) + kTile - 1) / kTile;
-    count[k] = 0;
-    if (i != item[k]) costs_of(s, per_head, i, &before[k], &all[k]);
-    item[k] = i;
-    if (tiles == 0) return;
-    const int rows = s.n * per_head - i * kItemRows;
-    at += h * all[k] + before[k] + start_cost(rows);
-    first[k] = (int)(at / per);
-    count[k] = (int)((at + (int64_t)(tiles - 1) * tile_cost(rows)) / per) - first[k] + 1;
-  };
-
-  const bool wide_out = ((uintptr_t)a.out & 7) == 0 && a.out_row % 4 == 0 && a.out_head % 4 == 0;
-
-#pragma unroll 1
-  for (int x = blockIdx.y; x < all_tiles; x += gridDim.y) {
-    const int h = x / tiles, m0 = (x - h * tiles) * kJoinRows;
-    const size_t own_slot = ((size_t)(w.hi - w.lo) + (own.row0 - w.lo)) * a.Hq + (size_t)h * m_own;
-    const size_t pre_slot = (size_t)(pre.row0 - w.lo) * a.Hq + (size_t)h * pre.n * per_head + m_off;
-    for (int m = m0 + threadIdx.x / kJoinLanes; m < min(m0 + kJoinRows, m_own); m += kJoinThreads / kJoinLanes) {
-      pieces(0, own, own_at, h, m / kItemRows);
-      if (g >= 0) pieces(1, pre, pre_at, h, (m_off + m) / kItemRows);
-      head = h;
-      const int c0 = count[0], n = c0 + count[1];
-      if (count[1] == 0 && n == 1) continue;  // written by its block
-      // piece p lies at one of two places plus p steps of 256 rows
-      const size_t own_at_row = own_slot + m + (size_t)kItemRows * first[0];
-      const size_t pre_at_row = pre_slot + m + (size_t)kItemRows * first[1] - (size_t)kItemRows * c0;
-      const float* own_part = part + own_at_row * D + lane * kPer;
-      const float* pre_part = part + (ptrdiff_t)pre_at_row * D + lane * kPer;
-      float top = -CUDART_INF_F, sum = 0.f, o[kPer];
-#pragma unroll
-      for (int d = 0; d < kPer; ++d) o[d] = 0.f;
-#pragma unroll 1
-      for (int p0 = 0; p0 < n; p0 += kBatch) {
-        float2 st[kBatch];
-        float v[kBatch][kPer];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int p = p0 + i;
-          st[i] = make_float2(-CUDART_INF_F, 0.f);
-          if (p < n) {
-            st[i] = stat[(p < c0 ? own_at_row : pre_at_row) + (size_t)(p * kItemRows)];
-            const float* src = (p < c0 ? own_part : pre_part) + (size_t)p * (kItemRows * D);
-#pragma unroll
-            for (int d = 0; d < kPer; d += 4) {
-              const float4 y = *reinterpret_cast<const float4*>(src + d);
-              v[i][d] = y.x, v[i][d + 1] = y.y, v[i][d + 2] = y.z, v[i][d + 3] = y.w;
-            }
-          }
-        }
-        const float m_new = fmaxf(max3(st[0].x, st[1].x, st[2].x), fmaxf(st[3].x, top));
-        const float c = top == -CUDART_INF_F ? 0.f : tc::ex2(top - m_new);
-        sum *= c;
-#pragma unroll
-        for (int d = 0; d < kPer; ++d) o[d] *= c;
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          if (p0 + i >= n) break;
-          const float w = st[i].x == -CUDART_INF_F ? 0.f : tc::ex2(st[i].x - m_new);
-          sum = fmaf(st[i].y, w, sum);
-#pragma unroll
-          for (int d = 0; d < kPer; ++d) o[d] = fmaf(v[i][d], w, o[d]);
-        }
-        top = m_new;
-      }
-      const int j = m / per_head, b = own.row0 + j, hq = h * per_head + (m - j * per_head);
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row without keys: zeros
-      __nv_bfloat16* out = (__nv_bfloat16*)a.out + (size_t)b * a.out_row + (size_t)hq * a.out_head + lane * kPer;
-      uint32_t r2[kPer / 2];
-#pragma unroll
-      for (int d = 0; d < kPer; d += 2) r2[d / 2] = pack_bf16(o[d] * inv, o[d + 1] * inv);
-      if (wide_out) {
-#pragma unroll
-        for (int d = 0; d < kPer / 2; d += 2) *reinterpret_cast<uint2*>(out + 2 * d) = make_uint2(r2[d], r2[d + 1]);
-      } else {
-#pragma unroll
-        for (int d = 0; d < kPer / 2; ++d) *reinterpret_cast<uint32_t*>(out + 2 * d) = r2[d];
-      }
-      if (a.lse && lane == 0)
-        a.lse[(size_t)b * a.Hq + hq] = sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * kLn2;
-    }
-  }
-}
-
-// Where the window is a part of the rows (kPart), the blocks share out its requests, from
-// the first to the last that has rows in it; otherwise there is a block for each.
-template <int D, bool kPart>
-__global__ void __launch_bounds__(kJoinThreads, 4)
-    join_tc_kernel(const spec_prefix_attention_args a, const Window w, const float* part, const float2* stat,
-                   const int64_t* plan) {
-  int r = blockIdx.x;
-  if (!kPart) {
-    join_request<D>(a, w, r, part, stat, plan);
-    return;
-  }
-  __shared__ int first_s, last_s;
-  if (threadIdx.x == 0) first_s = a.R, last_s = -1;
-  __syncthreads();
-  int first = a.R, last = -1;
-#pragma unroll 8
-  for (int i = threadIdx.x; i < a.R; i += kJoinThreads) {
-    const int row0 = a.row_off[i], row1 = a.row_off[i + 1];
-    if (row0 < row1 && row0 < w.hi && row1 > w.lo) first = min(first, i), last = max(last, i);
-  }
-  if (last >= 0) {
-    atomicMin(&first_s, first);
-    atomicMax(&last_s, last);
-  }
-  __syncthreads();
-  for (r += first_s; r <= last_s; r += gridDim.x) join_request<D>(a, w, r, part, stat, plan);
-  tc::grid_dep_wait();  // a block without requests, too, ends after the pieces' kernel
-}
-
 template <int D>
 cudaError_t launch(const spec_prefix_attention_args& a, int sms, float* part, float2* stat, int64_t* plan,
                    cudaStream_t stream) {
@@ -1115,25 +731,12 @@ cudaError_t launch(const spec_prefix_attention_args& a, int sms, float* part, fl
   // windows of equal size
   const int most_rows = attn_window_rows(a.Hq), windows = (int)(((int64_t)a.rows + most_rows - 1) / most_rows);
   const int step = (int)(((int64_t)a.rows + windows - 1) / windows);
-  // a block of the join a tile of the mean request, until there are kJoinBlocks of them
-  const int64_t tiles = (((int64_t)a.rows * per_head + (int64_t)kJoinRows * a.R - 1) / ((int64_t)kJoinRows * a.R)) * a.Hk;
-  const int at_once = std::min(a.R, (a.R + windows - 1) / windows + (windows > 1));  // requests of a window
-  const int64_t most = (kJoinBlocks + at_once - 1) / at_once;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(at_once, (unsigned)(tiles < most ? tiles : most));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   for (int64_t lo = 0; lo < a.rows; lo += step) {
-    const Window w{(int)lo, (int)std::min<int64_t>(lo + step, a.rows)};
+    const Window w{(int)lo, (int)std::min<int64_t>(lo + step, a.rows), 0};
     attention_tc_kernel<D><<<sms, kThreads, Smem<D>::kBytes, stream>>>(km, vm, qm, q_box, a, w, part, stat, plan);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
-    err = cudaLaunchKernelEx(&cfg, windows > 1 ? join_tc_kernel<D, true> : join_tc_kernel<D, false>, a, w,
-                             (const float*)part, (const float2*)stat, (const int64_t*)plan);
+    const Pieces pieces{part, stat, plan};
+    err = launch_join<D, Costs, Costs>(a, w, windows, pieces, pieces, stream);
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;

@@ -273,11 +273,14 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(spec_cache_read_pa
     const int h = w / (4 * groups), g = w / 4 - h * groups;
     const int slot = p.slot[row];
     if (slot >= p.n_slots) set_status(p.status, SPEC_STATUS_BAD_PAGE);
-    if (slot < 0 || slot >= p.n_slots) continue;
-    const int page = slot / p.page_size, tok = slot - page * p.page_size;
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(data + q4::data_at(page, h, tok, p.Hk, groups, p.page_size) +
-                                                          (size_t)g * 16 * p.page_size + (w & 3) * 4);
-    const float s = q4::scale_of(scales[q4::scale_at(page, h, tok, p.Hk, groups, p.page_size) + g]);
+    uint32_t v = 0x88888888u;  // zeros
+    float s = 0.f;
+    if (slot >= 0 && slot < p.n_slots) {
+      const int page = slot / p.page_size, tok = slot - page * p.page_size;
+      v = *reinterpret_cast<const uint32_t*>(data + q4::data_at(page, h, tok, p.Hk, groups, p.page_size) +
+                                             (size_t)g * 16 * p.page_size + (w & 3) * 4);
+      s = q4::scale_of(scales[q4::scale_at(page, h, tok, p.Hk, groups, p.page_size) + g]);
+    }
     constexpr int VEC = 16 / (int)sizeof(T);
     T* to = out + i * 8;
 #pragma unroll

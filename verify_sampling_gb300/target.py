@@ -410,8 +410,7 @@ def norm_rope_cache(q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torc
 def cache_read_packed(k_cache: tuple, v_cache: tuple, slot: torch.Tensor, *, dtype: torch.dtype = torch.bfloat16,
                     out: Optional[tuple] = None, status: Optional[torch.Tensor] = None, stream=None) -> tuple:
     """spec_cache_read_packed: what the slots of two ``packed_cache`` pairs stand for, (k, v) [rows, Hk, D] of ``dtype``
-    (exact in bfloat16 and float32).  Rows whose slot is negative or past the cache are left as they are in ``out``
-    (zeros in tensors that the call makes)."""
+    (exact in bfloat16 and float32), zeros where a slot is negative or past the cache."""
     rows = slot.numel()
     D = k_cache[0].shape[2] * 32 if isinstance(k_cache[0], _Tensor) and k_cache[0].dim() == 5 else 0
     kc, ks, n, P, Hk = _packed(k_cache, "k_cache", None, D)
@@ -422,7 +421,7 @@ def cache_read_packed(k_cache: tuple, v_cache: tuple, slot: torch.Tensor, *, dty
         if dtype not in _codes:
             raise TypeError("dtype must be float32 or bfloat16")
         with _made(stream):
-            out = tuple(torch.zeros((rows, Hk, D), dtype=dtype, device=slot.device) for _ in range(2))
+            out = tuple(torch.empty((rows, Hk, D), dtype=dtype, device=slot.device) for _ in range(2))
     k, v = out
     if k.dtype is not v.dtype or k.shape != (rows, Hk, D) or v.shape != k.shape:
         raise ValueError("out must be two tensors [rows, Hk, D] of one dtype")
