@@ -1,9 +1,7 @@
 // Attention over a cache in 4 bits for few query rows a key head (decoding, short drafts).
 //
 // Mathematics: the pieces of attention_tc.cu (a reference m that follows the running maximum
-// in steps of 8, l = sum 2^(z - m), O = sum 2^(z - m) v).  An element s (n - 8) is made in bf16
-// by one fma: n goes to bits 3-6 under the exponent of 16, which is 16 + n, and (16 + n) s
-// - 24 s is exact (24 s has six significant bits, the result seven at most).
+// in steps of 8, l = sum 2^(z - m), O = sum 2^(z - m) v), over elements made in bf16 (packed.cuh).
 //
 // Few rows mean that the bytes of the cache bound it, 17 KB a tile of 128 keys, 390 ns of an
 // SM's share of memory: the tensor cores have to be busy for little more than the rows that are
@@ -33,8 +31,13 @@ namespace spec {
 
 namespace {
 
+using q4::element_pair;
+using q4::Scale;
+using q4::scale_pair;
+
 constexpr int kWarps = 4, kThreads = 32 * (kWarps + 1);
 constexpr int kItemSlots = 2;
+constexpr int kNarrowMost = 32;  // query rows of a segment that is the narrow kernel's where both run
 constexpr float kSlack = 8.f;  // log2 units the maximum may grow by before O is rescaled
 
 // NB: blocks of 8 query rows of an item.
@@ -98,28 +101,6 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t fma_bf16(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
-// Scales of a pair of elements in bf16 from their bytes in the halves' low bytes, and -24 times them.
-struct Scale {
-  uint32_t s, z;
-};
-__device__ __forceinline__ Scale scale_pair(uint32_t bytes) {
-  Scale r;
-  r.s = bytes * 16u + ((uint32_t)q4::kLeastExp << 7) * 0x10001u;
-  r.z = fma_bf16(r.s, 0xC1C0C1C0u, 0x80008000u);  // -24 s - 0
-  return r;
-}
-// Elements I and I + 4 of a word's 8 (16-bit halves' I-th nibbles).
-template <int I>
-__device__ __forceinline__ uint32_t element_pair(uint32_t w, const Scale& s) {
-  const uint32_t n = I == 0 ? w << 3 : w >> (4 * I - 3);
-  return fma_bf16((n & 0x00780078u) | 0x41804180u, s.s, s.z);
-}
-
 template <int D, int NB>
 __global__ void __launch_bounds__(kThreads, NB == 1 ? kNarrowBlocks : 2)
     attention_narrow_kernel(const spec_prefix_attention_args a, const q4::Cache packed, const Window w, float* part, float2* stat,
@@ -569,7 +550,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? kNarrowBlocks : 2)
 }
 
 template <int D, int NB>
-cudaError_t launch(const spec_prefix_attention_args& a, const q4::Cache& packed, int sms, const PackedWork& work, cudaStream_t stream) {
+cudaError_t launch(const spec_prefix_attention_args& a, const q4::Cache& packed, int sms, const PackedWork& work, bool both,
+                   cudaStream_t stream) {
   using C = NarrowCosts<NB>;
   constexpr int kBytes = Smem<D, NB>::kBytes;
   auto kernel = attention_narrow_kernel<D, NB>;
@@ -578,12 +560,13 @@ cudaError_t launch(const spec_prefix_attention_args& a, const q4::Cache& packed,
   const int blocks = std::min(NB == 1 ? kNarrowBlocks : 2, 227 * 1024 / (kBytes + 1024));
   const int most_rows = attn_window_rows(a.Hq), windows = (int)(((int64_t)a.rows + most_rows - 1) / most_rows);
   const int step = (int)(((int64_t)a.rows + windows - 1) / windows);
+  const Pieces narrow{work.narrow_part, work.narrow_stat, work.narrow_plan}, wide{work.part, work.stat, work.plan};
   for (int64_t lo = 0; lo < a.rows; lo += step) {
-    const Window w{(int)lo, (int)std::min<int64_t>(lo + step, a.rows), INT_MAX};
+    const Window w{(int)lo, (int)std::min<int64_t>(lo + step, a.rows), both ? kNarrowMost : INT_MAX};
+    if (both && (err = launch_attention_wide(a, packed, sms, w.lo, w.hi, w.narrow, work, stream)) != cudaSuccess) return err;
     kernel<<<sms * blocks, kThreads, kBytes, stream>>>(a, packed, w, work.narrow_part, work.narrow_stat, work.narrow_plan);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
-    const Pieces pieces{work.narrow_part, work.narrow_stat, work.narrow_plan};
-    err = launch_join<D, C, C>(a, w, windows, pieces, pieces, stream);
+    err = launch_join<D, WideCosts<true>, C>(a, w, windows, wide, narrow, stream);
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;
@@ -591,10 +574,13 @@ cudaError_t launch(const spec_prefix_attention_args& a, const q4::Cache& packed,
 
 template <int D>
 cudaError_t launch(const spec_prefix_attention_args& a, const q4::Cache& packed, int sms, const PackedWork& work, cudaStream_t stream) {
-  const int64_t m = (int64_t)a.rows * (a.Hq / a.Hk);  // query rows of a key head
-  if (m <= 8 * (int64_t)a.R) return launch<D, 1>(a, packed, sms, work, stream);
-  if (m <= 16 * (int64_t)a.R) return launch<D, 2>(a, packed, sms, work, stream);
-  return launch<D, 4>(a, packed, sms, work, stream);
+  const int64_t m = (int64_t)a.rows * (a.Hq / a.Hk), R = a.R;  // query rows of a key head
+  // The narrow kernel alone for requests of few rows without a prefix; otherwise the wide
+  // one takes the segments of more than kNarrowMost rows before it.
+  const bool both = a.G > 0 || m > kNarrowMost * R;
+  if (m <= 8 * R) return launch<D, 1>(a, packed, sms, work, both, stream);
+  if (m <= 16 * R) return launch<D, 2>(a, packed, sms, work, both, stream);
+  return launch<D, 4>(a, packed, sms, work, both, stream);
 }
 
 }  // namespace

@@ -24,6 +24,10 @@ struct PackedWork {
   int64_t *plan, *narrow_plan;
 };
 
+// The tensor-core kernel of attention_tc.cu over a packed cache: the segments of more than `narrow`
+// query rows of the packed rows [lo, hi).
+cudaError_t launch_attention_wide(const spec_prefix_attention_args& a, const q4::Cache& packed, int sms, int lo, int hi, int narrow,
+                                  const PackedWork& work, cudaStream_t stream);
 bool attn_packed_ok(const spec_prefix_attention_args& a, const q4::Cache& packed, int* sms);
 cudaError_t launch_attention_packed(const spec_prefix_attention_args& a, const q4::Cache& packed, int sms, const PackedWork& work,
                                     cudaStream_t stream);

@@ -26,6 +26,21 @@ constexpr int kTile = 128;  // keys of a tile
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 // ------------------------------------------------------------ work layout --
+// Costs, in units of 0.1 us, measured: a tile of an item of both softmax groups (bound
+// by the products), a tile of a smaller one (bound by its 64 KB where all blocks stream,
+// otherwise by its chain of product, softmax and product), and an item's start and end.
+template <bool SHARED>  // with a narrow kernel, over a packed cache
+struct WideCosts {
+  static constexpr int kItemRows = attn::kItemRows, kLeast = 17;
+  static constexpr bool kShared = SHARED, kWide = true;
+  __device__ static __forceinline__ int tile(int rows) { return rows > kTile ? 17 : 15; }
+  __device__ static __forceinline__ int start(int rows) { return rows > kTile ? 57 : 21; }
+  // Tiles whose costs begin before `x` units of an item's tiles.
+  __device__ static __forceinline__ int tiles_before(int x, int rows) {
+    return rows > kTile ? (unsigned)(x + 16) / 17 : (unsigned)(x + 14) / 15;
+  }
+};
+
 struct Window {  // the packed rows of a launch: [lo, hi)
   int lo, hi;
   int narrow;  // where two kernels share the segments: query rows of the largest that the narrow one takes
@@ -238,9 +253,8 @@ __device__ __forceinline__ void lay_out(const spec_prefix_attention_args& a, con
 }
 
 // The rest of a wait whose first look failed.  Gives up when the time limit passes or
-// another warp has given up.  (Out of line: the code of a role that a short item
-// runs once has to fit the instruction cache beside the others'.)
-__device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t phase, volatile int* abort_flag, uint32_t* status) {
+// another warp has given up.
+__device__ __forceinline__ bool slow_wait_here(uint64_t* bar, uint32_t phase, volatile int* abort_flag, uint32_t* status) {
   for (int i = 0; i < 2000; ++i) {
     if (tc::mbar_wait(bar, phase & 1u, kWaitNs / 2000)) return true;
     if (*abort_flag) return false;
@@ -248,6 +262,11 @@ __device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t phase, volatile i
   *abort_flag = 1;
   set_status(status, SPEC_STATUS_TIMEOUT);
   return false;
+}
+// (Out of line: the code of a role that a short item runs once has to fit the instruction
+// cache beside the others'.)
+__device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t phase, volatile int* abort_flag, uint32_t* status) {
+  return slow_wait_here(bar, phase, abort_flag, status);
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {

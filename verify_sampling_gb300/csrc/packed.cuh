@@ -47,5 +47,30 @@ __device__ __forceinline__ uint32_t nibble_of(float x, float s) {
   return (uint32_t)(min(max(__float2int_rn(__fdiv_rn(x, s)), -7), 7) + 8);
 }
 
+// ------------------------------------------------ elements in bf16 pairs --
+__device__ __forceinline__ uint32_t fma_bf16(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+// Scales of a pair of elements from their bytes in the halves' low bytes, and -24 times them.
+struct Scale {
+  uint32_t s, z;
+};
+__device__ __forceinline__ Scale scale_pair(uint32_t bytes) {
+  Scale r;
+  r.s = bytes * 16u + ((uint32_t)kLeastExp << 7) * 0x10001u;
+  r.z = fma_bf16(r.s, 0xC1C0C1C0u, 0x80008000u);  // -24 s - 0
+  return r;
+}
+// Elements I and I + 4 of a word's 8 (its halves' I-th nibbles): n goes to bits 3-6 under the
+// exponent of 16, which is 16 + n, and (16 + n) s - 24 s is exact, as 24 s and the result are
+// numbers of six and seven bits.
+template <int I>
+__device__ __forceinline__ uint32_t element_pair(uint32_t w, const Scale& s) {
+  const uint32_t n = I == 0 ? w << 3 : w >> (4 * I - 3);
+  return fma_bf16((n & 0x00780078u) | 0x41804180u, s.s, s.z);
+}
+
 }  // namespace q4
 }  // namespace spec
