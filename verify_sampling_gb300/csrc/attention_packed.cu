@@ -14,6 +14,12 @@
 // operands from shared memory or TMEM: the nibbles would go there and back, at M = 128 with
 // 128 rows for 8.  The wide kernel does that where rows are many.)
 //
+// Shifts and masks run at half an instruction a clock, which bounds the kernel before memory does,
+// so K's nibbles become whole numbers n - 8 in fp16 (one shift a word where bf16 takes three), and a
+// group's scale goes on its part of the score, in fp32.  The queries in fp16 are exact: a
+// row is taken times a power of two that brings its largest element to 2^13, and what falls below
+// 2^-24 then is 2^-37 of that.  Values keep bf16: fp16 has not the scales' range.
+//
 // Block: a producer warp walks the block's items (attention_plan.cuh) and loads query rows,
 // pages and scales by bulk copies into a ring of tiles; four warps take 32 keys of each tile, with
 // a maximum, sums and results of their own, and join at an item's end.  Three blocks an SM hide
@@ -23,6 +29,7 @@
 // in flight and returns.
 #include "attention_packed.cuh"
 
+#include <cfloat>
 #include <climits>
 
 #include "attention_plan.cuh"
@@ -32,12 +39,12 @@ namespace spec {
 namespace {
 
 using q4::element_pair;
+using q4::number_pair;
 using q4::Scale;
-using q4::scale_pair;
 
 constexpr int kWarps = 4, kThreads = 32 * (kWarps + 1);
 constexpr int kItemSlots = 2;
-constexpr int kNarrowMost = 32;  // query rows of a segment that is the narrow kernel's where both run
+constexpr int kNarrowMost = 16;  // query rows of a segment that is the narrow kernel's where both run
 constexpr float kSlack = 8.f;  // log2 units the maximum may grow by before O is rescaled
 
 // NB: blocks of 8 query rows of an item.
@@ -55,7 +62,7 @@ struct Sizes {
   static constexpr int kGroups = D / q4::kGroup;
   static constexpr int kData = kTile * D / 2, kScales = kTile * kGroups;  // of a tile's keys (or values)
   static constexpr int kStageBytes = 2 * (kData + kScales);
-  static constexpr int kStages = NB == 1 ? (D == 128 ? 3 : 6) : (D == 128 ? 3 : 6);
+  static constexpr int kStages = D == 128 ? 3 : 6;
   static constexpr int kQuery = NB * 8 * D * 2;  // an item's query rows
   static constexpr int kJoin = 2 * NB * 8 * D * 4;
 };
@@ -90,10 +97,29 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t saddr
                : "r"(saddr)
                : "memory");
 }
+// fp16x2 with `lo` in the low half
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
+}
+// fp16 operands: d += a b, and d = a b.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -245,25 +271,40 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? kNarrowBlocks : 2)
       if (!ok) break;
       const Item it = bars.items[slot];
       if (it.rows == 0) break;
-      // query fragments: dimensions 32 c + 8 t + (i, i + 4) of row g
-      const uint8_t* qs = smem + M::kQ + slot * S::kQuery;
-      auto query = [&](int nb, int c, uint32_t (&q)[4]) {
-        const uint4 v = tc::lds128(qs + (nb * 8 + g) * D * 2 + c * 64 + t * 16);
-        q[0] = __byte_perm(v.x, v.z, 0x5410);
-        q[1] = __byte_perm(v.x, v.z, 0x7632);
-        q[2] = __byte_perm(v.y, v.w, 0x5410);
-        q[3] = __byte_perm(v.y, v.w, 0x7632);
-      };
-      constexpr bool kHold = NB <= 2;  // the fragments fit the registers
-      uint32_t q[kHold ? NB : 1][G][4];
-      if (kHold) {
+      // query fragments in fp16: dimensions 32 c + 8 t + (i, i + 4) of row g, times a power of two
+      uint32_t q[NB][G][4];
+      float row_sl[NB][2];  // scores of rows 2 t, 2 t + 1 to log2 units
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+      for (int nb = 0; nb < NB; ++nb) {
+        const uint8_t* qs = smem + M::kQ + slot * S::kQuery + (nb * 8 + g) * D * 2 + t * 16;
+        uint4 v[G];
+        uint32_t most = 0;  // magnitudes' fp32 bits
 #pragma unroll
-          for (int c = 0; c < G; ++c) query(nb, c, q[kHold ? nb : 0][c]);
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bars.item_empty[slot]);
+        for (int c = 0; c < G; ++c) {
+          v[c] = tc::lds128(qs + c * 64);
+          const uint32_t x[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) most = max(most, max(x[e] << 16 & 0x7fff0000u, x[e] & 0x7fff0000u));
+        }
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        const uint32_t e = most >> 23, up = e == 255u ? 127u : min(267u - e, 190u);  // exponent fields (a row with infinities: as it is)
+        const float f = __uint_as_float(up << 23), back = __uint_as_float((254u - up) << 23);
+        auto low = [&](uint32_t x) { return __uint_as_float(x << 16) * f; };
+        auto high = [&](uint32_t x) { return __uint_as_float(x & 0xffff0000u) * f; };
+#pragma unroll
+        for (int c = 0; c < G; ++c) {
+          q[nb][c][0] = pack_f16(low(v[c].x), low(v[c].z));
+          q[nb][c][1] = pack_f16(high(v[c].x), high(v[c].z));
+          q[nb][c][2] = pack_f16(low(v[c].y), low(v[c].w));
+          q[nb][c][3] = pack_f16(high(v[c].y), high(v[c].w));
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x)  // (not 0, which would make NaN of a masked score)
+          row_sl[nb][x] = fmaxf(sl * __shfl_sync(0xffffffffu, back, (2 * t + x) * 4), FLT_MIN);
       }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars.item_empty[slot]);
       int limit[NB][2];  // keys of rows 2 t, 2 t + 1 of each block (rows past the item's: any)
       float ref[NB][2], l[NB][2];
 #pragma unroll
@@ -291,55 +332,30 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? kNarrowBlocks : 2)
         ok = warp_wait(&bars.full[st], seq / S::kStages);
         if (!ok) break;
         const uint32_t ks = sbase + st * S::kStageBytes, vs = ks + S::kData + S::kScales;
-        const uint8_t* k_scale = smem + st * S::kStageBytes + S::kData;
-        const uint8_t* v_scale = k_scale + S::kData + S::kScales;
+        const uint8_t* k_code = smem + st * S::kStageBytes + S::kData + (warp * 32 + g) * G;
+        const uint8_t* v_code = smem + st * S::kStageBytes + 2 * S::kData + S::kScales + (warp * 32 + 2 * t) * G;
         float s[2][NB][4];  // scores of keys g and g + 8 of 16, rows 2 t and 2 t + 1
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[b][nb][e] = 0.f;
-        uint32_t sc[2][2];  // the groups' scale bytes of keys g and g + 8
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int key = (warp * 4 + 2 * b + x) * 8 + g;
-            sc[b][x] = G == 4 ? *reinterpret_cast<const uint32_t*>(k_scale + key * G)
-                              : (uint32_t)*reinterpret_cast<const uint16_t*>(k_scale + key * G);
-          }
 #pragma unroll
         for (int c = 0; c < G; c += 2) {
           uint32_t r[2][4];  // [pair of blocks][block, block + 1 of group c, then of c + 1]
 #pragma unroll
           for (int b = 0; b < 2; ++b) ldmatrix4(r[b], ks + row_at[b] + (c >> 1) * two_groups);
 #pragma unroll
-          for (int cc = 0; cc < 2; ++cc) {
-            uint32_t f[2][8];
+          for (int cc = 0; cc < 2; ++cc)
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < 2; ++b) {
+              const uint32_t w0 = r[b][2 * cc], w1 = r[b][2 * cc + 1], h0 = w0 >> 8, h1 = w1 >> 8;
+              const float z0 = q4::scale_of(k_code[(16 * b) * G + c + cc]), z1 = q4::scale_of(k_code[(16 * b + 8) * G + c + cc]);
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const Scale z = scale_pair(__byte_perm(sc[b][x], 0, 0x4040 | (c + cc) * 0x0101));
-                const uint32_t v = r[b][2 * cc + x];
-                f[b][x] = element_pair<0>(v, z);
-                f[b][2 + x] = element_pair<1>(v, z);
-                f[b][4 + x] = element_pair<2>(v, z);
-                f[b][6 + x] = element_pair<3>(v, z);
-              }
+              for (int nb = 0; nb < NB; ++nb) {
+                float d[4];
+                const uint32_t* qq = q[nb][c + cc];
+                mma_f16_first(d, number_pair<0>(w0, h0), number_pair<0>(w1, h1), number_pair<1>(w0, h0), number_pair<1>(w1, h1), qq[0], qq[1]);
+                mma_f16(d, number_pair<2>(w0, h0), number_pair<2>(w1, h1), number_pair<3>(w0, h0), number_pair<3>(w1, h1), qq[2], qq[3]);
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              uint32_t qf[4];
-              if (!kHold) query(nb, c + cc, qf);
-              const uint32_t* qq = kHold ? q[kHold ? nb : 0][c + cc] : qf;
-#pragma unroll
-              for (int b = 0; b < 2; ++b) {
-                mma(s[b][nb], f[b][0], f[b][1], f[b][2], f[b][3], qq[0], qq[1]);
-                mma(s[b][nb], f[b][4], f[b][5], f[b][6], f[b][7], qq[2], qq[3]);
+                for (int e = 0; e < 4; ++e) s[b][nb][e] = c + cc == 0 ? d[e] * (e < 2 ? z0 : z1) : fmaf(d[e], e < 2 ? z0 : z1, s[b][nb][e]);
               }
             }
-          }
         }
         // scores in log2 units, masked
         const int key0 = i * kTile + warp * 32 + g;
@@ -358,14 +374,14 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? kNarrowBlocks : 2)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float top = fmaxf(fmaxf(s[0][nb][e], s[0][nb][e + 2]), fmaxf(s[1][nb][e], s[1][nb][e + 2]));
-            grown |= top * sl > ref[nb][e] + kSlack;
+            grown |= top * row_sl[nb][e] > ref[nb][e] + kSlack;
           }
         if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float top = fmaxf(fmaxf(s[0][nb][e], s[0][nb][e + 2]), fmaxf(s[1][nb][e], s[1][nb][e + 2])) * sl;
+              float top = fmaxf(fmaxf(s[0][nb][e], s[0][nb][e + 2]), fmaxf(s[1][nb][e], s[1][nb][e + 2])) * row_sl[nb][e];
 #pragma unroll
               for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
               // each row by its own scores alone: its bits do not depend on its neighbours
@@ -390,7 +406,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? kNarrowBlocks : 2)
           for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const float p0 = tc::ex2(fmaf(s[b][nb][2 * x], sl, -sub0)), p1 = tc::ex2(fmaf(s[b][nb][2 * x + 1], sl, -sub1));
+              const float p0 = tc::ex2(fmaf(s[b][nb][2 * x], row_sl[nb][0], -sub0));
+              const float p1 = tc::ex2(fmaf(s[b][nb][2 * x + 1], row_sl[nb][1], -sub1));
               l[nb][0] += p0;
               l[nb][1] += p1;
               // rounded to bf16: 8 bits of a weight are 8 bits of its share of the result
@@ -399,33 +416,18 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? kNarrowBlocks : 2)
         }
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          // scale bytes of keys 2 t and 2 t + 1 of both blocks, split by even and odd groups
-          uint32_t even[2][2], odd[2][2];
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint8_t* at = v_scale + ((warp * 4 + 2 * b + x) * 8 + 2 * t) * G;
-            uint32_t k0, k1;
-            if (G == 4) {
-              const uint2 v = *reinterpret_cast<const uint2*>(at);
-              k0 = v.x, k1 = v.y;
-            } else {
-              k0 = *reinterpret_cast<const uint32_t*>(at);
-              k1 = k0 >> 16;
-            }
-            even[x][0] = k0 & 0x00ff00ffu, even[x][1] = k1 & 0x00ff00ffu;
-            odd[x][0] = k0 >> 8 & 0x00ff00ffu, odd[x][1] = k1 >> 8 & 0x00ff00ffu;
-          }
 #pragma unroll
           for (int c = 0; c < G; c += 2) {
             uint32_t r[4];
             ldmatrix4_trans(r, vs + row_at[b] + (c >> 1) * two_groups);
 #pragma unroll
             for (int cc = 0; cc < 2; ++cc) {
-              Scale z[2];
+              Scale z[2];  // of keys 2 t and 2 t + 1 of both blocks
 #pragma unroll
-              for (int x = 0; x < 2; ++x)
-                z[x] = scale_pair(cc == 0 ? __byte_perm(even[x][0], even[x][1], c == 0 ? 0x5410 : 0x7632)
-                                          : __byte_perm(odd[x][0], odd[x][1], c == 0 ? 0x5410 : 0x7632));
+              for (int x = 0; x < 2; ++x) {
+                const uint8_t* at = v_code + (16 * b + 8 * x) * G + c + cc;
+                z[x] = q4::scale_two(at[0], at[G]);
+              }
               const uint32_t v0 = r[2 * cc], v1 = r[2 * cc + 1];
               const uint32_t f0 = element_pair<0>(v0, z[0]), f1 = element_pair<1>(v0, z[0]), f2 = element_pair<0>(v1, z[1]),
                              f3 = element_pair<1>(v1, z[1]);
@@ -443,10 +445,6 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? kNarrowBlocks : 2)
         if (lane == 0) tc::mbar_arrive(&bars.empty[st]);
       }
       if (!ok) break;
-      if (!kHold) {
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bars.item_empty[slot]);
-      }
       // ---- the warps' results: maxima and sums of all, results pairwise
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
@@ -579,8 +577,7 @@ cudaError_t launch(const spec_prefix_attention_args& a, const q4::Cache& packed,
   // one takes the segments of more than kNarrowMost rows before it.
   const bool both = a.G > 0 || m > kNarrowMost * R;
   if (m <= 8 * R) return launch<D, 1>(a, packed, sms, work, both, stream);
-  if (m <= 16 * R) return launch<D, 2>(a, packed, sms, work, both, stream);
-  return launch<D, 4>(a, packed, sms, work, both, stream);
+  return launch<D, 2>(a, packed, sms, work, both, stream);
 }
 
 }  // namespace

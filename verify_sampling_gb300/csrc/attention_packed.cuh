@@ -7,7 +7,7 @@ namespace spec {
 
 namespace attn {
 
-constexpr int kNarrowRows = 32;    // query rows of the narrow kernel's largest item
+constexpr int kNarrowRows = 16;    // query rows of the narrow kernel's largest item
 constexpr int kNarrowBlocks = 3;   // blocks an SM, at most
 
 }  // namespace attn

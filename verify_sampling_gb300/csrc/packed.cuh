@@ -53,23 +53,35 @@ __device__ __forceinline__ uint32_t fma_bf16(uint32_t a, uint32_t b, uint32_t c)
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
-// Scales of a pair of elements from their bytes in the halves' low bytes, and -24 times them.
+// Scales of a pair of elements in bf16, and -24 times them.
 struct Scale {
   uint32_t s, z;
 };
-__device__ __forceinline__ Scale scale_pair(uint32_t bytes) {
-  Scale r;
-  r.s = bytes * 16u + ((uint32_t)kLeastExp << 7) * 0x10001u;
-  r.z = fma_bf16(r.s, 0xC1C0C1C0u, 0x80008000u);  // -24 s - 0
-  return r;
-}
+__device__ __forceinline__ Scale scale_bits(uint32_t bits) { return Scale{bits, fma_bf16(bits, 0xC1C0C1C0u, 0x80008000u)}; }  // -24 s - 0
+constexpr uint32_t kScaleBits = ((uint32_t)kLeastExp << 7) * 0x10001u;
+// From codes in the halves' low bytes, one code for both, and a code each.
+__device__ __forceinline__ Scale scale_pair(uint32_t codes) { return scale_bits(codes * 16u + kScaleBits); }
+__device__ __forceinline__ Scale scale_one(uint32_t code) { return scale_bits(code * 0x00100010u + kScaleBits); }
+__device__ __forceinline__ Scale scale_two(uint32_t lo, uint32_t hi) { return scale_bits(hi * 0x00100000u + (lo * 16u + kScaleBits)); }
 // Elements I and I + 4 of a word's 8 (its halves' I-th nibbles): n goes to bits 3-6 under the
 // exponent of 16, which is 16 + n, and (16 + n) s - 24 s is exact, as 24 s and the result are
 // numbers of six and seven bits.
 template <int I>
 __device__ __forceinline__ uint32_t element_pair(uint32_t w, const Scale& s) {
-  const uint32_t n = I == 0 ? w << 3 : w >> (4 * I - 3);
+  const uint32_t n = I == 0 ? w * 8u : w >> (4 * I - 3);
   return fma_bf16((n & 0x00780078u) | 0x41804180u, s.s, s.z);
+}
+// n - 8 of elements I and I + 4 in fp16, with `high` the word shifted right by 8: n lies in bits
+// 0-3 under the exponent of 1024 (I even), which is 1024 + n, or in bits 4-7, 1024 + 16 n.
+template <int I>
+__device__ __forceinline__ uint32_t number_pair(uint32_t w, uint32_t high) {
+  const uint32_t v = I < 2 ? w : high;
+  uint32_t r;
+  if (I % 2 == 0)
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"((v & 0x000f000fu) | 0x64006400u), "r"(0x3C003C00u), "r"(0xE408E408u));  // x - 1032
+  else
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"((v & 0x00f000f0u) | 0x64006400u), "r"(0x2C002C00u), "r"(0xD480D480u));  // x / 16 - 72
+  return r;
 }
 
 }  // namespace q4
