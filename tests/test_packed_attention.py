@@ -158,6 +158,10 @@ TENSOR = [
     ([1] * 3, [3000, 20000, 1], 128, 1, 128, 64, ()),
     ([1, 2, 700, 1, 33], [900, 5, 900, 60, 33], 16, 2, 128, 16, ()),
     ([40, 1, 1], [4000, 3, 70], 1, 1, 64, 16, ((3, 200),)),
+    ([3, 1, 60], [1500, 700, 2000], 16, 4, 128, 384, ((2, 800),)),
+    ([1, 2, 30], [1500, 9000, 200], 12, 2, 64, 8, ((1, 3000), (2, 100))),
+    ([1] * 6, [5000, 4097, 129, 1, 70, 12000], 14, 1, 128, 8, ()),
+    ([1, 40], [5000, 9000], 6, 1, 64, 640, ()),
 ]
 
 

@@ -172,8 +172,33 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? kNarrowBlocks : 2)
     Item it;
     uint32_t bad = 0, seq = 0, n_item = 0;
     bool ok = true;
-    const int pieces = a.page_size > kTile ? G : 1;  // copies of a page's head within a tile
-    const int piece_bytes = Pe * 16 * (G / pieces);
+    // A tile's copies, two a lane at most: keys' and values' data (a page's head in one, or a
+    // copy a group where pages are longer than a tile) and scales.  What is the same for every
+    // tile is worked out here: the producer's instructions are all one scheduler's.
+    const int groups_in = a.page_size > kTile ? 1 : G, parts = 2 * (G / groups_in + 1);  // copies of a page
+    const uint32_t page_bytes = (uint32_t)(Pe * (16 * G + G)) * 2;                      // of a page within a tile
+    struct Copy {
+      const uint8_t* from;   // of page 0, head 0
+      uint32_t page, head, tok;  // bytes to the next one's
+      uint32_t to, bytes;
+      int x;  // page of the tile
+    };
+    auto copy_of = [&](int c) {
+      const int x = c / parts, rest = c - x * parts, kv = rest & 1, piece = rest >> 1;
+      const bool data = piece < G / groups_in;
+      const uint32_t unit = data ? 16 : 1;  // bytes of a group
+      Copy r;
+      r.from = (data ? (kv ? packed.v : packed.k) : (kv ? packed.v_scale : packed.k_scale)) + (data ? (size_t)piece * 16 * a.page_size : 0);
+      r.head = unit * G * a.page_size;
+      r.page = r.head * a.Hk;
+      r.tok = data ? 16 : G;
+      r.to = kv * (S::kData + S::kScales) + (data ? (x * G + piece) * Pe * 16 : S::kData + x * Pe * G);
+      r.bytes = unit * Pe * (data ? groups_in : G);
+      r.x = x;
+      return r;
+    };
+    const Copy first_copy = copy_of(lane), second_copy = copy_of(lane + 32);
+    const int tiles_a_page = max(a.page_size / kTile, 1), pages_a_tile = kTile / Pe;
     for (;; ++n_item) {
       const bool more = walk.next(it);
       if (!more) it.rows = 0;  // the end
@@ -195,41 +220,44 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? kNarrowBlocks : 2)
       }
       // page ids, 32 at a time, the next 32 on their way
       const int pages = (it.keys + a.page_size - 1) / a.page_size;
-      int base = (int)((int64_t)it.lo * kTile / a.page_size);
+      int first = it.lo * pages_a_tile, in_page = 0;  // the tile's first page, and its tile of a longer one
+      if (tiles_a_page > 1) {
+        first = it.lo / tiles_a_page;
+        in_page = it.lo - first * tiles_a_page;
+      }
+      int base = first;
       auto fetch = [&](int from) { return from + lane < pages ? page_of(a, it.table, from + lane, &bad) : 0; };
       int cur = fetch(base), nxt = fetch(base + 32);
+      const uint8_t* head1 = first_copy.from + (size_t)first_copy.head * it.h;
+      const uint8_t* head2 = second_copy.from + (size_t)second_copy.head * it.h;
       for (int i = it.lo; i < it.hi; ++i, ++seq) {
-        const int first = (int)((int64_t)i * kTile / a.page_size);  // first page of the tile
         if (first >= base + 32) {
           cur = nxt;
           base += 32;
           nxt = fetch(base + 32);
         }
-        const int live = min(kTile, it.keys - i * kTile);
-        const int used = (live + Pe - 1) / Pe;
+        const int used = min(pages_a_tile, pages - first);  // pages with keys
         const uint32_t st = seq % S::kStages;
-        // lane c: copy c of the tile, (page, keys or values, data piece or scales)
-        const int copies = used * 2 * (pieces + 1);
         ok = warp_wait(&bars.empty[st], (seq / S::kStages) ^ 1u);
         if (!ok) break;
-        if (lane == 0) tc::mbar_expect_tx(&bars.full[st], (uint32_t)(used * 2 * (Pe * 16 * G + Pe * G)));
+        if (lane == 0) tc::mbar_expect_tx(&bars.full[st], used * page_bytes);
         __syncwarp();
-        const int in_page = (int)((int64_t)i * kTile - (int64_t)first * a.page_size);  // pages of more than a tile
-        for (int c0 = 0; c0 < copies; c0 += 32) {
-          const int c = c0 + lane, x = c / (2 * (pieces + 1)), rest = c - x * 2 * (pieces + 1);
-          const int page = __shfl_sync(0xffffffffu, cur, min(first + x - base, 31) & 31);
-          if (c >= copies) continue;
-          const int kv = rest & 1, piece = rest >> 1;
-          uint8_t* to = smem + st * S::kStageBytes + kv * (S::kData + S::kScales);
-          if (piece < pieces)
-            tc::bulk_load(to + (x * G + piece) * Pe * 16,
-                          (kv ? packed.v : packed.k) + q4::data_at(page, it.h, in_page, a.Hk, G, a.page_size) +
-                              (int64_t)piece * 16 * a.page_size,
-                          piece_bytes, &bars.full[st]);
-          else
-            tc::bulk_load(to + S::kData + x * Pe * G,
-                          (kv ? packed.v_scale : packed.k_scale) + q4::scale_at(page, it.h, in_page, a.Hk, G, a.page_size), Pe * G,
+        uint8_t* to = smem + st * S::kStageBytes;
+        const uint32_t skip = in_page * kTile;
+        const int page = __shfl_sync(0xffffffffu, cur, (first - base + first_copy.x) & 31);
+        if (lane < used * parts)
+          tc::bulk_load(to + first_copy.to, head1 + (size_t)first_copy.page * (uint32_t)page + skip * first_copy.tok, first_copy.bytes, &bars.full[st]);
+        if (used * parts > 32) {
+          const int page2 = __shfl_sync(0xffffffffu, cur, (first - base + second_copy.x) & 31);
+          if (lane + 32 < used * parts)
+            tc::bulk_load(to + second_copy.to, head2 + (size_t)second_copy.page * (uint32_t)page2 + skip * second_copy.tok, second_copy.bytes,
                           &bars.full[st]);
+        }
+        if (tiles_a_page == 1) {
+          first += pages_a_tile;
+        } else if (++in_page == tiles_a_page) {
+          in_page = 0;
+          ++first;
         }
       }
       if (!ok) break;
@@ -582,9 +610,10 @@ cudaError_t launch(const spec_prefix_attention_args& a, const q4::Cache& packed,
 
 }  // namespace
 
-// bf16 heads of 64 or 128, pages that tile 128 keys, rows, data and scales on 16 bytes.
+// bf16 heads of 64 or 128, pages that tile 128 keys and are below 2 GB, rows, data and scales on 16 bytes.
 bool attn_packed_ok(const spec_prefix_attention_args& a, const q4::Cache& packed, int* sms) {
   if (((uintptr_t)packed.k_scale | (uintptr_t)packed.v_scale) % 16 != 0) return false;
+  if ((int64_t)a.page_size * a.Hk * a.D / 2 >= ((int64_t)1 << 31)) return false;  // a page's bytes, in 32 bits
   return attn_tc_ok(a, sms);
 }
 
