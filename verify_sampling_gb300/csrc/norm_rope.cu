@@ -17,6 +17,7 @@
 
 #include "packed.cuh"
 #include "rotary.cuh"
+#include "tc.cuh"
 
 namespace spec {
 
@@ -227,12 +228,274 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(spec_norm_rope_args
   }
 }
 
+// ------------------------------------------------------------ long batches --
+// Rows whose heads lie side by side, by bulk copies through a ring of stages in shared
+// memory, a few tokens each: one warp issues loads and stores, one computes the
+// cosines of the stages ahead, the others take heads as above, in place where a bulk store
+// takes them on (queries, and the keys of a cache of the inputs' type).  Every wait is bounded: on
+// a timeout the block sets SPEC_STATUS_TIMEOUT, waits for its copies in flight and returns.
+constexpr int kBulkThreads = kThreads + 64, kBulkBlocks = 2;  // blocks an SM
+constexpr int kMaxStages = 4;
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+struct Ring {
+  uint64_t full[kMaxStages], done[kMaxStages], freed[kMaxStages];
+  int2 at[kMaxStages][kWarps];  // position (-1: left out) and slot (-1: none) of a stage's tokens
+};
+
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t phase) {
+  return tc::mbar_try_wait(bar, phase & 1u) || tc::mbar_wait(bar, phase & 1u, kWaitNs);
+}
+
+// Stage i of the block holds tokens (blockIdx.x + i * gridDim.x) * tokens and on; `tokens`
+// divides the warps.
+template <typename T, bool PACKED>
+__global__ void __launch_bounds__(kBulkThreads, kBulkBlocks)
+    norm_rope_bulk_kernel(spec_norm_rope_args p, int tokens, int stages, int lanes) {
+  constexpr int VEC = 16 / (int)sizeof(T);
+  using P = Pack<T, VEC>;
+  extern __shared__ __align__(128) uint8_t bulk_s[];
+  const int half = p.rot >> 1, turned = p.Hq + p.Hk;
+  const bool inter = p.layout == SPEC_ROPE_INTERLEAVED;
+  const uint32_t head_bytes = p.D * (uint32_t)sizeof(T), row_bytes = (turned + p.Hk) * head_bytes;
+  const uint32_t stage_bytes = tokens * row_bytes;
+  Ring& ring = *reinterpret_cast<Ring*>(bulk_s + stages * stage_bytes);
+  float2* turns = reinterpret_cast<float2*>(&ring + 1);
+  // cosine and signed sine of every element that turns: [stage][token][cosines, sines][VEC / 4][lane] float4
+  float* cs_s = reinterpret_cast<float*>(turns + ((half + 1) & ~1));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int groups = (p.rows + tokens - 1) / tokens;
+  const int n = (groups - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  auto first_row = [&](int i) { return ((int)blockIdx.x + i * (int)gridDim.x) * tokens; };
+  constexpr int kLoader = kWarps, kCosines = kWarps + 1;
+  const int turn_lanes = p.rot / VEC;
+
+  auto load = [&](int i) {  // queries, keys and values of a stage's tokens
+    const int row0 = first_row(i), count = min(tokens, p.rows - row0), st = i % stages;
+    if (lane == 0) tc::mbar_expect_tx(&ring.full[st], count * row_bytes);
+    __syncwarp();
+    if (lane < 3 * count) {
+      const int t = lane / 3, part = lane - 3 * t;
+      const size_t row = (size_t)(row0 + t);
+      const T* from = part == 0   ? (const T*)p.q + row * p.q_row
+                      : part == 1 ? (const T*)p.k + row * p.k_row
+                                  : (const T*)p.v + row * p.v_row;
+      const uint32_t bytes = (part == 0 ? p.Hq : p.Hk) * head_bytes;
+      const uint32_t to = part == 0 ? 0 : part == 1 ? p.Hq * head_bytes : turned * head_bytes;
+      if (bytes) tc::bulk_load(bulk_s + st * stage_bytes + t * row_bytes + to, from, bytes, &ring.full[st]);
+    }
+  };
+
+  if (warp == kLoader) {
+    if (lane < stages) {
+      tc::mbar_init(&ring.full[lane], 2);
+      tc::mbar_init(&ring.done[lane], kWarps);
+      tc::mbar_init(&ring.freed[lane], 1);
+    }
+    tc::fence_barrier_init();
+    __syncwarp();
+    for (int i = 0; i < min(stages, n); ++i) load(i);  // nobody waits for one before the barrier below
+  } else {
+    for (int f = tid; f < half; f += kThreads) turns[f] = in_turns(p.freq[f]);
+  }
+  __syncthreads();
+
+  if (warp == kLoader) {
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const int st = i % stages;
+      ok = __all_sync(0xffffffffu, wait_for(&ring.done[st], i / stages));
+      if (!ok) break;
+      const int row0 = first_row(i), count = min(tokens, p.rows - row0);
+      if (lane < 3 * count) {
+        const int t = lane / 3, part = lane - 3 * t;
+        const int2 at = ring.at[st][t];
+        const uint8_t* from = bulk_s + st * stage_bytes + t * row_bytes;
+        const size_t slot = (size_t)at.y * p.Hk * p.D;
+        if (part == 0 && p.Hq && at.x >= 0)
+          tc::bulk_store((T*)p.q_out + (size_t)(row0 + t) * p.q_out_row, from, p.Hq * head_bytes);
+        if (!PACKED && part == 1 && p.Hk && at.x >= 0 && at.y >= 0)
+          tc::bulk_store((T*)p.k_cache + slot, from + p.Hq * head_bytes, p.Hk * head_bytes);
+        if (!PACKED && part == 2 && p.Hk && at.x >= 0 && at.y >= 0)
+          tc::bulk_store((T*)p.v_cache + slot, from + turned * head_bytes, p.Hk * head_bytes);
+      }
+      tc::bulk_commit();
+      if (i > 0 && i - 1 + stages < n) {  // the stage before this one has been read: its next tokens
+        tc::bulk_wait_read<1>();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&ring.freed[(i - 1) % stages]);
+        load(i - 1 + stages);
+      }
+    }
+    if (!ok) {  // the loads in flight land before the block's memory goes
+      if (lane == 0) set_status(p.status, SPEC_STATUS_TIMEOUT);
+      for (int st = 0; st < stages; ++st) {
+        // the last load of a stage: the phase its barrier is in, or the one before
+        wait_for(&ring.full[st], 0);
+        wait_for(&ring.full[st], 1);
+      }
+    }
+    tc::bulk_wait();
+  } else if (warp == kCosines) {
+    auto read = [&](int i) {  // position and slot of token `lane` of stage i
+      const int row = first_row(i) + lane;
+      if (i >= n || lane >= tokens || row >= p.rows) return make_int2(0, -1);
+      return make_int2(p.position[row], p.slot ? p.slot[row] : -1);
+    };
+    int2 next = read(0);
+    uint32_t bad = 0;
+    for (int i = 0; i < n; ++i) {
+      const int st = i % stages;
+      int2 at = next;
+      next = read(i + 1);
+      if (at.x >= (1 << 24)) bad |= SPEC_STATUS_BAD_POSITION;
+      if (at.y >= p.n_slots) bad |= SPEC_STATUS_BAD_PAGE, at.y = -1;
+      const float x = (float)min(max(at.x, 0), (1 << 24) - 1);
+      if (i >= stages && !__all_sync(0xffffffffu, wait_for(&ring.freed[st], i / stages - 1))) break;
+      if (lane < tokens) ring.at[st][lane] = at;
+      for (int t = 0; t < tokens; ++t) {
+        const float pos = __shfl_sync(0xffffffffu, x, t);
+        float* co = cs_s + (size_t)(st * tokens + t) * 2 * p.rot;
+        for (int f = lane; f < half; f += 32) {
+          const float2 v = cos_sin(pos, turns[f], p.scale);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int d = inter ? 2 * f + k : f + k * half, l = d / VEC, e = d % VEC;
+            float* to = co + ((e >> 2) * turn_lanes + l) * 4 + (e & 3);
+            to[0] = v.x;
+            to[p.rot] = k == 0 ? -v.y : v.y;
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&ring.full[st]);
+    }
+    if (bad) set_status(p.status, bad);
+  } else {
+    const int each = kWarps / tokens, t = warp / each, in_t = warp - t * each;  // a token's warps
+    const int at_once = 32 / lanes, sub = lane / lanes, l = lane % lanes, first = l * VEC;
+    const int q_steps = (p.Hq + at_once - 1) / at_once, k_steps = (p.Hk + at_once - 1) / at_once;
+    const int steps = q_steps + (PACKED ? 2 : 1) * k_steps;
+    const bool live = first < p.D, turning = first < p.rot;
+    const float inv_d = 1.f / (float)p.D;
+    const int other = (lane + (first < half ? half : -half) / VEC) & 31;  // half layout: where the other half lies
+    float qw[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) qw[e] = p.q_weight && live ? p.q_weight[first + e] : 1.f;
+    for (int i = 0; i < n; ++i) {
+      const int st = i % stages;
+      if (!__all_sync(0xffffffffu, wait_for(&ring.full[st], i / stages))) break;
+      const int2 at = ring.at[st][t];
+      if (first_row(i) + t < p.rows && at.x >= 0) {
+        float co[VEC], si[VEC];
+        if (turning) {
+          const float4* c4 = reinterpret_cast<const float4*>(cs_s + (size_t)(st * tokens + t) * 2 * p.rot) + l;
+          const float4* s4 = reinterpret_cast<const float4*>(cs_s + (size_t)(st * tokens + t) * 2 * p.rot + p.rot) + l;
+#pragma unroll
+          for (int j = 0; j < VEC / 4; ++j) {
+            const float4 c = c4[j * turn_lanes], v = s4[j * turn_lanes];
+            co[4 * j] = c.x, co[4 * j + 1] = c.y, co[4 * j + 2] = c.z, co[4 * j + 3] = c.w;
+            si[4 * j] = v.x, si[4 * j + 1] = v.y, si[4 * j + 2] = v.z, si[4 * j + 3] = v.w;
+          }
+        }
+        uint8_t* token = bulk_s + st * stage_bytes + t * row_bytes + first * sizeof(T);
+        const int page = PACKED && at.y >= 0 ? at.y / p.page_size : 0, tok = PACKED && at.y >= 0 ? at.y - page * p.page_size : 0;
+#pragma unroll 2
+        for (int step = in_t; step < steps; step += each) {
+          const int kind = step < q_steps ? 0 : step < q_steps + k_steps ? 1 : 2;
+          const int h = (step - (kind == 0 ? 0 : kind == 1 ? q_steps : q_steps + k_steps)) * at_once + sub;
+          const bool on = h < (kind == 0 ? p.Hq : p.Hk);
+          P* here = reinterpret_cast<P*>(token + (size_t)(h + (kind == 0 ? 0 : kind == 1 ? p.Hq : turned)) * head_bytes);
+          P x;
+          if (on && live) x = *here;
+          float y[VEC];
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) y[e] = on && live ? to_f(x.e[e]) : 0.f;
+          const float* weight = kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr;
+          if (weight) {
+            float sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) sum = fmaf(y[e], y[e], sum);
+            for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            const float r = rsqrtf(fmaf(sum, inv_d, p.eps));
+            if (live) {
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) y[e] *= r * (kind == 0 ? qw[e] : weight[first + e]);
+            }
+          }
+          if (kind < 2 && half > 0) {
+            float z[VEC];
+            if (inter) {
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) z[e] = y[e ^ 1];
+            } else {
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) z[e] = __shfl_sync(0xffffffffu, y[e], other);
+            }
+            if (turning) {
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) y[e] = fmaf(y[e], co[e], __fmul_rn(z[e], si[e]));
+            }
+          }
+          if (PACKED && kind > 0) {
+            const int heads = p.D / q4::kGroup, head = on ? h : 0;
+            store_packed<VEC, 1>(y, first, 32 * VEC, p.D, on && at.y >= 0,
+                                 (uint8_t*)(kind == 1 ? p.k_cache : p.v_cache) + q4::data_at(page, head, tok, p.Hk, heads, p.page_size),
+                                 (kind == 1 ? p.k_scale : p.v_scale) + q4::scale_at(page, head, tok, p.Hk, heads, p.page_size), p.page_size);
+          } else if (on && live) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) put(&x.e[e], y[e]);
+            *here = x;
+          }
+        }
+      }
+      tc::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&ring.done[st]);
+    }
+  }
+}
+
+// Shared memory of a block with `stages` stages.
+template <typename T>
+size_t bulk_bytes(const spec_norm_rope_args& a, int tokens, int stages) {
+  const size_t half = a.rot / 2, row = (size_t)(a.Hq + 2 * a.Hk) * a.D * sizeof(T);
+  return stages * tokens * row + sizeof(Ring) + (half + 1) / 2 * 16 + (size_t)stages * tokens * 2 * a.rot * sizeof(float);
+}
+constexpr size_t kBulkMemory = 222 * 1024, kStageBytes = 26 * 1024;
+constexpr size_t kBulkBytes = 12000000;  // of a batch, from which on
+constexpr int kBulkRows = 608;           // four tokens an SM
+template <typename T, bool PACKED>
+bool launch_bulk(const spec_norm_rope_args& a, int lanes, cudaStream_t stream, cudaError_t* err) {
+  const size_t row = (size_t)(a.Hq + 2 * a.Hk) * a.D * sizeof(T);
+  auto dense = [&](int n, int64_t head) { return n < 2 || head == a.D; };  // heads side by side
+  if (a.rows < kBulkRows || a.rows * row < kBulkBytes || !dense(a.Hq, a.q_head) || !dense(a.Hq, a.q_out_head) || !dense(a.Hk, a.k_head) ||
+      !dense(a.Hk, a.v_head))
+    return false;
+  int tokens = std::min({kWarps, a.rows / kBulkRows, std::max(1, (int)(kStageBytes / row))});
+  while (tokens & (tokens - 1)) tokens &= tokens - 1;
+  int stages = kMaxStages;
+  while (stages > 1 && bulk_bytes<T>(a, tokens, stages) > kBulkMemory / kBulkBlocks) --stages;
+  if (stages < 3) return false;
+  auto kernel = norm_rope_bulk_kernel<T, PACKED>;
+  *err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kBulkMemory / kBulkBlocks));
+  if (*err != cudaSuccess) return true;
+  const int groups = (a.rows + tokens - 1) / tokens;
+  kernel<<<std::min(groups, kBulkBlocks * 152), kBulkThreads, bulk_bytes<T>(a, tokens, stages), stream>>>(a, tokens, stages, lanes);
+  *err = cudaGetLastError();
+  return true;
+}
+
 template <typename T, int VEC, int CH, bool FAST, bool PACKED>
 cudaError_t launch(const spec_norm_rope_args& a, cudaStream_t stream) {
   int lanes = 32;
   if (CH == 1)
     for (lanes = 1; lanes * VEC < a.D;) lanes *= 2;
   if (PACKED) lanes = std::max(lanes, q4::kGroup / VEC);
+  if (FAST) {
+    cudaError_t err;
+    if (launch_bulk<T, PACKED>(a, lanes, stream, &err)) return err;
+  }
   const int at_once = CH == 1 ? 32 / lanes : 1;
   const int steps = (a.Hq + at_once - 1) / at_once + 2 * ((a.Hk + at_once - 1) / at_once);
   // warps for eight blocks an SM, as far as a warp keeps four steps
