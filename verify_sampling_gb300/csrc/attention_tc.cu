@@ -48,6 +48,10 @@ namespace spec {
 namespace {
 
 using namespace attn;
+using tc::add2;
+using tc::fma2;
+using tc::halves;
+using tc::pair;
 
 // (kTile: keys of a tile, and rows of a softmax group)
 // Softmax warps: group t (rows 128 t ..) is warps 8 t .. 8 t + 7; warps w and w + 4 of it
@@ -161,30 +165,6 @@ __device__ __forceinline__ void tmem_st16h(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  return pair(__float_as_uint(lo), __float_as_uint(hi));
-}
-__device__ __forceinline__ float2 halves(uint64_t v) {
-  uint32_t lo, hi;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
-  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
 }
 // 16 bytes to a shared address, without registers in between.
 __device__ __forceinline__ void copy16(uint32_t saddr, const void* from) {

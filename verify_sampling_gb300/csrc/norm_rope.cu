@@ -14,6 +14,7 @@
 #include "norm_rope.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 #include "packed.cuh"
 #include "rotary.cuh"
@@ -38,6 +39,112 @@ __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void put(float* o, float v) { *o = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* o, float v) { *o = __float2bfloat16_rn(v); }
+
+// A lane's 16 bytes of a head, normed and turned.  What an element and the other half of its pair
+// are taken times (the weight's part of it, cosine or signed sine) is the same for all heads of
+// a token and kind: mine[e] and others[e]; the head's 1 / rms comes last.
+template <typename T>
+struct Lane {
+  static constexpr int VEC = 16 / (int)sizeof(T);
+  uint64_t mine[VEC / 2], others[VEC / 2];
+  bool turning;  // the lane's elements are below rot
+};
+__device__ __forceinline__ void unpack(const uint4& v, uint64_t (&x)[4], __nv_bfloat16) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = tc::pair(w[e] << 16, w[e] & 0xffff0000u);
+}
+__device__ __forceinline__ void unpack(const uint4& v, uint64_t (&x)[2], float) {
+  x[0] = tc::pair(v.x, v.y);
+  x[1] = tc::pair(v.z, v.w);
+}
+__device__ __forceinline__ uint4 packed_up(const uint64_t (&y)[4], __nv_bfloat16) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 v = tc::halves(y[e]);
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(v.y), "f"(v.x));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 packed_up(const uint64_t (&y)[2], float) {
+  const float2 a = tc::halves(y[0]), b = tc::halves(y[1]);
+  return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+}
+// The lane's factors from cosines and signed sines (co, si; read where `turning`) and the head's weight.
+template <typename T, bool INTER>
+__device__ __forceinline__ void factors(Lane<T>& f, const float* co, const float* si, const float* weight, int first, int half) {
+  constexpr int VEC = Lane<T>::VEC;
+#pragma unroll
+  for (int e = 0; e < VEC; e += 2) {
+    float m[2], o[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int d = first + e + k, at = INTER ? d ^ 1 : d < half ? d + half : d - half;
+      m[k] = f.turning ? co[e + k] : 1.f;
+      o[k] = f.turning ? si[e + k] : 0.f;
+      if (weight) {
+        m[k] *= weight[d];
+        if (f.turning) o[k] *= weight[at];
+      }
+    }
+    f.mine[e / 2] = tc::pair(m[0], m[1]);
+    f.others[e / 2] = tc::pair(o[0], o[1]);
+  }
+}
+// All lanes of a warp call it; a head is `lanes` of them, `other` the lane of the other halves (half layout).
+template <typename T, bool INTER>
+__device__ __forceinline__ void norm_turn(const uint4& v, uint64_t (&y)[Lane<T>::VEC / 2], const Lane<T>& f, bool norm, int lanes, int other,
+                                          float inv_d, float eps) {
+  constexpr int N = Lane<T>::VEC / 2;
+  uint64_t x[N], z[N];
+  unpack(v, x, T());
+  if (INTER) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const float2 t = tc::halves(x[e]);
+      z[e] = tc::pair(t.y, t.x);
+    }
+  } else {
+    uint4 w;
+    w.x = __shfl_sync(0xffffffffu, v.x, other), w.y = __shfl_sync(0xffffffffu, v.y, other);
+    w.z = __shfl_sync(0xffffffffu, v.z, other), w.w = __shfl_sync(0xffffffffu, v.w, other);
+    unpack(w, z, T());
+  }
+  if (!f.turning) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) z[e] = 0;  // (what is not its pair may be NaN)
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e) y[e] = tc::fma2(x[e], f.mine[e], tc::mul2(z[e], f.others[e]));
+  if (!norm) {
+    if (!f.turning) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) y[e] = x[e];  // (its sign, where it is zero)
+    }
+    return;
+  }
+  uint64_t sum2 = tc::mul2(x[0], x[0]);
+#pragma unroll
+  for (int e = 1; e < N; ++e) sum2 = tc::fma2(x[e], x[e], sum2);
+  const float2 s = tc::halves(sum2);
+  float sum = s.x + s.y;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+    if (o < lanes) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const float r = rsqrtf(fmaf(sum, inv_d, eps));
+#pragma unroll
+  for (int e = 0; e < N; ++e) y[e] = tc::mul2(y[e], tc::pair(r, r));
+}
+template <int N>
+__device__ __forceinline__ void spread(const uint64_t (&y)[N], float (&to)[2 * N]) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const float2 v = tc::halves(y[e]);
+    to[2 * e] = v.x;
+    to[2 * e + 1] = v.y;
+  }
+}
 
 // Codes a lane's VEC elements of each chunk and writes them to the token's head in the cache.
 // All lanes of the warp call it; `on`: this one's head is written.
@@ -66,16 +173,119 @@ __device__ __forceinline__ void store_packed(const float (&y)[CH * VEC], int fir
   }
 }
 
-// A head over `lanes` lanes (a power of two), or over the whole warp in CH chunks of 32 VEC
-// elements.  FAST: pairs lie in whole vectors, in the half layout lanes apart (CH = 1).
-template <typename T, int VEC, int CH, bool FAST, bool PACKED>
+// Whole vectors that turn or do not: a head over `lanes` lanes (a power of two).
+template <typename T, bool INTER, bool PACKED>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(spec_norm_rope_args p, int parts, int lanes) {
+  constexpr int VEC = Lane<T>::VEC, N = VEC / 2;
+  extern __shared__ __align__(16) float2 smem[];
+  const int half = p.rot >> 1, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float2* turns = smem;                    // [half]
+  float2* cs = smem + half + warp * half;  // [half] of the warp's token
+  for (int f = tid; f < half; f += kThreads) turns[f] = in_turns(p.freq[f]);
+  __syncthreads();
+
+  const int at_once = 32 / lanes, sub = lane / lanes, first = (lane % lanes) * VEC;
+  const int q_steps = (p.Hq + at_once - 1) / at_once, k_steps = (p.Hk + at_once - 1) / at_once;
+  const int steps = q_steps + 2 * k_steps, per = (steps + parts - 1) / parts;
+  const float inv_d = 1.f / (float)p.D;
+  const bool live = first < p.D;
+  const int other = (lane + (first < half ? half : -half) / VEC) & 31;  // half layout: where the other halves lie
+  const int64_t units = (int64_t)p.rows * parts;
+  auto kind_of = [&](int st) { return st < q_steps ? 0 : st < q_steps + k_steps ? 1 : 2; };  // queries, keys, values
+  auto head_of = [&](int st, int kind) { return (st - (kind == 0 ? 0 : kind == 1 ? q_steps : q_steps + k_steps)) * at_once + sub; };
+
+  for (int64_t unit = (int64_t)blockIdx.x * kWarps + warp; unit < units; unit += (int64_t)gridDim.x * kWarps) {
+    const int row = (int)(unit / parts), part = (int)(unit - (int64_t)row * parts);
+    const int begin = part * per, end = min(begin + per, steps);
+    uint4 x[kSteps];
+    auto load = [&](int s0) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int st = s0 + i;
+        if (st >= end) break;
+        const int kind = kind_of(st), h = head_of(st, kind);
+        const T* from = kind == 0   ? (const T*)p.q + (int64_t)row * p.q_row + h * p.q_head
+                        : kind == 1 ? (const T*)p.k + (int64_t)row * p.k_row + h * p.k_head
+                                    : (const T*)p.v + (int64_t)row * p.v_row + h * p.v_head;
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (h < (kind == 0 ? p.Hq : p.Hk) && live) x[i] = *reinterpret_cast<const uint4*>(from + first);
+      }
+    };
+    load(begin);  // a row that is left out is read all the same: no load waits for a position
+    const int pos = p.position[row];
+    int slot = p.slot ? p.slot[row] : -1;
+    if (part == 0 && lane == 0) {
+      const uint32_t bad = (pos >= (1 << 24) ? SPEC_STATUS_BAD_POSITION : 0u) | (slot >= p.n_slots ? SPEC_STATUS_BAD_PAGE : 0u);
+      if (bad) set_status(p.status, bad);
+    }
+    if (pos < 0) continue;
+    if (slot >= p.n_slots) slot = -1;
+    const float at = (float)min(pos, (1 << 24) - 1);
+    __syncwarp();
+    for (int f = lane; f < half; f += 32) cs[f] = cos_sin(at, turns[f], p.scale);
+    __syncwarp();
+    Lane<T> lf;
+    lf.turning = first < p.rot;
+    float co[VEC], si[VEC];
+    if (lf.turning) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float2 t = cs[INTER ? (first + e) / 2 : first < half ? first + e : first + e - half];
+        co[e] = t.x;
+        si[e] = (INTER ? e % 2 == 0 : first < half) ? -t.y : t.y;
+      }
+    }
+    int have = -1;  // kind whose factors these are
+    const int64_t page = PACKED && slot >= 0 ? slot / p.page_size : 0;
+    const int tok = PACKED && slot >= 0 ? (int)(slot - page * p.page_size) : 0, groups = p.D / q4::kGroup;
+
+    for (int s0 = begin; s0 < end; s0 += kSteps) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int st = s0 + i;
+        if (st >= end) break;
+        const int kind = kind_of(st), h = head_of(st, kind);
+        const bool on = h < (kind == 0 ? p.Hq : p.Hk) && (kind == 0 || slot >= 0);
+        uint64_t y[N];
+        if (kind == 2) {
+          unpack(x[i], y, T());
+        } else {
+          const float* weight = kind == 0 ? p.q_weight : p.k_weight;
+          if (kind != have) {
+            factors<T, INTER>(lf, co, si, live ? weight : nullptr, first, half);
+            have = kind;
+          }
+          norm_turn<T, INTER>(x[i], y, lf, weight != nullptr, lanes, other, inv_d, p.eps);
+        }
+        if (PACKED && kind > 0) {
+          float yf[VEC];
+          spread(y, yf);
+          const int head = on ? h : 0;
+          store_packed<VEC, 1>(yf, first, 32 * VEC, p.D, on,
+                               (uint8_t*)(kind == 1 ? p.k_cache : p.v_cache) + q4::data_at(page, head, tok, p.Hk, groups, p.page_size),
+                               (kind == 1 ? p.k_scale : p.v_scale) + q4::scale_at(page, head, tok, p.Hk, groups, p.page_size), p.page_size);
+          continue;
+        }
+        if (!on || !live) continue;
+        T* to = kind == 0 ? (T*)p.q_out + (int64_t)row * p.q_out_row + h * p.q_out_head
+                          : (T*)(kind == 1 ? p.k_cache : p.v_cache) + ((int64_t)slot * p.Hk + h) * p.D;
+        *reinterpret_cast<uint4*>(to + first) = kind == 2 ? x[i] : packed_up(y, T());
+      }
+      if (s0 + kSteps < end) load(s0 + kSteps);
+    }
+  }
+}
+
+// Any sizes: a head over `lanes` lanes (a power of two), or over the whole warp in CH chunks of 32 VEC
+// elements; the other halves of pairs come from shared memory.
+template <typename T, int VEC, int CH, bool PACKED>
+__global__ void __launch_bounds__(kThreads) norm_rope_general_kernel(spec_norm_rope_args p, int parts, int lanes) {
   using P = Pack<T, VEC>;
   extern __shared__ __align__(16) float2 smem[];
   const int half = p.rot >> 1, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float2* turns = smem;                         // [half]
   float2* cs = smem + half + warp * half;       // [half] of the warp's token
-  float* buf = reinterpret_cast<float*>(smem + half * (1 + kWarps)) + warp * 32 * VEC * CH;  // !FAST: its heads
+  float* buf = reinterpret_cast<float*>(smem + half * (1 + kWarps)) + warp * 32 * VEC * CH;  // its heads
   for (int f = tid; f < half; f += kThreads) turns[f] = in_turns(p.freq[f]);
   __syncthreads();
 
@@ -122,20 +332,6 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(spec_norm_rope_args
     __syncwarp();
     for (int f = lane; f < half; f += 32) cs[f] = cos_sin(at, turns[f], p.scale);
     __syncwarp();
-    // FAST: the lane's cosines and its sines with the sign of the other half's part
-    constexpr int kAngles = FAST ? VEC : 1;
-    float co[kAngles], si[kAngles];
-    const bool turning = FAST && first < p.rot;
-    if (turning) {
-#pragma unroll
-      for (int e = 0; e < kAngles; ++e) {
-        const float2 t = cs[inter ? (first + e) / 2 : first < half ? first + e : first + e - half];
-        co[e] = t.x;
-        si[e] = (inter ? e % 2 == 0 : first < half) ? -t.y : t.y;
-      }
-    }
-    const int other = lane + (first < half ? half : -half) / VEC;  // FAST, half layout: where the other half lies
-
     for (int s0 = begin; s0 < end; s0 += kSteps) {
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
@@ -169,39 +365,24 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(spec_norm_rope_args
               for (int e = 0; e < VEC; ++e) y[c * VEC + e] *= r * weight[first + c * step + e];
         }
         if (kind < 2 && half > 0) {
-          if (FAST) {
-            float z[VEC];
-            if (inter) {
+          float* mine = buf + sub * lanes * VEC;
+          __syncwarp();
 #pragma unroll
-              for (int e = 0; e < VEC; ++e) z[e] = y[e ^ 1];
-            } else {
+          for (int c = 0; c < CH; ++c)
 #pragma unroll
-              for (int e = 0; e < VEC; ++e) z[e] = __shfl_sync(0xffffffffu, y[e], other & 31);
+            for (int e = 0; e < VEC; ++e) mine[first + c * step + e] = y[c * VEC + e];
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+              const int d = first + c * step + e;
+              if (d >= p.rot) continue;
+              const bool low = inter ? d % 2 == 0 : d < half;
+              const float2 t = cs[inter ? d / 2 : low ? d : d - half];
+              const float z = mine[inter ? d ^ 1 : low ? d + half : d - half];
+              y[c * VEC + e] = fmaf(y[c * VEC + e], t.x, __fmul_rn(z, low ? -t.y : t.y));
             }
-            if (turning) {
-#pragma unroll
-              for (int e = 0; e < VEC; ++e) y[e] = fmaf(y[e], co[e % kAngles], __fmul_rn(z[e], si[e % kAngles]));
-            }
-          } else {
-            float* mine = buf + sub * lanes * VEC;
-            __syncwarp();
-#pragma unroll
-            for (int c = 0; c < CH; ++c)
-#pragma unroll
-              for (int e = 0; e < VEC; ++e) mine[first + c * step + e] = y[c * VEC + e];
-            __syncwarp();
-#pragma unroll
-            for (int c = 0; c < CH; ++c)
-#pragma unroll
-              for (int e = 0; e < VEC; ++e) {
-                const int d = first + c * step + e;
-                if (d >= p.rot) continue;
-                const bool low = inter ? d % 2 == 0 : d < half;
-                const float2 t = cs[inter ? d / 2 : low ? d : d - half];
-                const float z = mine[inter ? d ^ 1 : low ? d + half : d - half];
-                y[c * VEC + e] = fmaf(y[c * VEC + e], t.x, __fmul_rn(z, low ? -t.y : t.y));
-              }
-          }
         }
         if (PACKED && kind > 0) {
           const int64_t page = on ? slot / p.page_size : 0;
@@ -249,26 +430,26 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t phase) {
 
 // Stage i of the block holds tokens (blockIdx.x + i * gridDim.x) * tokens and on; `tokens`
 // divides the warps.
-template <typename T, bool PACKED>
+template <typename T, bool INTER, bool PACKED>
 __global__ void __launch_bounds__(kBulkThreads, kBulkBlocks)
     norm_rope_bulk_kernel(spec_norm_rope_args p, int tokens, int stages, int lanes) {
-  constexpr int VEC = 16 / (int)sizeof(T);
-  using P = Pack<T, VEC>;
+  constexpr int VEC = Lane<T>::VEC, N = VEC / 2;
   extern __shared__ __align__(128) uint8_t bulk_s[];
   const int half = p.rot >> 1, turned = p.Hq + p.Hk;
-  const bool inter = p.layout == SPEC_ROPE_INTERLEAVED;
   const uint32_t head_bytes = p.D * (uint32_t)sizeof(T), row_bytes = (turned + p.Hk) * head_bytes;
   const uint32_t stage_bytes = tokens * row_bytes;
   Ring& ring = *reinterpret_cast<Ring*>(bulk_s + stages * stage_bytes);
   float2* turns = reinterpret_cast<float2*>(&ring + 1);
-  // cosine and signed sine of every element that turns: [stage][token][cosines, sines][VEC / 4][lane] float4
-  float* cs_s = reinterpret_cast<float*>(turns + ((half + 1) & ~1));
+  float* weight_s = reinterpret_cast<float*>(turns + ((half + 1) & ~1));  // [queries, keys][D]
+  // what a lane's elements and the others of their pairs are taken times:
+  // [stage][token][queries, keys][mine, others][VEC / 4][lane] float4
+  float* factor_s = weight_s + 2 * p.D;
+  const int head_lanes = p.D / VEC;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int groups = (p.rows + tokens - 1) / tokens;
   const int n = (groups - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
   auto first_row = [&](int i) { return ((int)blockIdx.x + i * (int)gridDim.x) * tokens; };
   constexpr int kLoader = kWarps, kCosines = kWarps + 1;
-  const int turn_lanes = p.rot / VEC;
 
   auto load = [&](int i) {  // queries, keys and values of a stage's tokens
     const int row0 = first_row(i), count = min(tokens, p.rows - row0), st = i % stages;
@@ -297,6 +478,10 @@ __global__ void __launch_bounds__(kBulkThreads, kBulkBlocks)
     for (int i = 0; i < min(stages, n); ++i) load(i);  // nobody waits for one before the barrier below
   } else {
     for (int f = tid; f < half; f += kThreads) turns[f] = in_turns(p.freq[f]);
+    for (int d = tid; d < 2 * p.D; d += kThreads) {
+      const float* w = d < p.D ? p.q_weight : p.k_weight;
+      weight_s[d] = w ? w[d < p.D ? d : d - p.D] : 1.f;
+    }
   }
   __syncthreads();
 
@@ -342,6 +527,13 @@ __global__ void __launch_bounds__(kBulkThreads, kBulkBlocks)
       if (i >= n || lane >= tokens || row >= p.rows) return make_int2(0, -1);
       return make_int2(p.position[row], p.slot ? p.slot[row] : -1);
     };
+    auto place = [&](int d) { return ((d % VEC >> 2) * head_lanes + d / VEC) * 4 + (d & 3); };
+    for (int d = p.rot + lane; d < p.D; d += 32)  // what does not turn: the same for all
+      for (int x = 0; x < 2 * stages * tokens; ++x) {
+        float* to = factor_s + (size_t)x * 2 * p.D + place(d);
+        to[0] = weight_s[(x & 1) * p.D + d];
+        to[p.D] = 0.f;
+      }
     int2 next = read(0);
     uint32_t bad = 0;
     for (int i = 0; i < n; ++i) {
@@ -355,15 +547,18 @@ __global__ void __launch_bounds__(kBulkThreads, kBulkBlocks)
       if (lane < tokens) ring.at[st][lane] = at;
       for (int t = 0; t < tokens; ++t) {
         const float pos = __shfl_sync(0xffffffffu, x, t);
-        float* co = cs_s + (size_t)(st * tokens + t) * 2 * p.rot;
+        float* of = factor_s + (size_t)(st * tokens + t) * 4 * p.D;
         for (int f = lane; f < half; f += 32) {
           const float2 v = cos_sin(pos, turns[f], p.scale);
+          const int d0 = INTER ? 2 * f : f, d1 = INTER ? d0 + 1 : f + half, p0 = place(d0), p1 = place(d1);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int d = inter ? 2 * f + k : f + k * half, l = d / VEC, e = d % VEC;
-            float* to = co + ((e >> 2) * turn_lanes + l) * 4 + (e & 3);
-            to[0] = v.x;
-            to[p.rot] = k == 0 ? -v.y : v.y;
+            const float w0 = weight_s[k * p.D + d0], w1 = weight_s[k * p.D + d1];
+            float* to = of + k * 2 * p.D;
+            to[p0] = v.x * w0;
+            to[p1] = v.x * w1;
+            to[p.D + p0] = -v.y * w1;
+            to[p.D + p1] = v.y * w0;
           }
         }
       }
@@ -374,80 +569,55 @@ __global__ void __launch_bounds__(kBulkThreads, kBulkBlocks)
   } else {
     const int each = kWarps / tokens, t = warp / each, in_t = warp - t * each;  // a token's warps
     const int at_once = 32 / lanes, sub = lane / lanes, l = lane % lanes, first = l * VEC;
-    const int q_steps = (p.Hq + at_once - 1) / at_once, k_steps = (p.Hk + at_once - 1) / at_once;
-    const int steps = q_steps + (PACKED ? 2 : 1) * k_steps;
-    const bool live = first < p.D, turning = first < p.rot;
+    const bool live = first < p.D;
     const float inv_d = 1.f / (float)p.D;
-    const int other = (lane + (first < half ? half : -half) / VEC) & 31;  // half layout: where the other half lies
-    float qw[VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) qw[e] = p.q_weight && live ? p.q_weight[first + e] : 1.f;
+    const int other = (lane + (first < half ? half : -half) / VEC) & 31;  // half layout: where the other halves lie
     for (int i = 0; i < n; ++i) {
       const int st = i % stages;
       if (!__all_sync(0xffffffffu, wait_for(&ring.full[st], i / stages))) break;
       const int2 at = ring.at[st][t];
       if (first_row(i) + t < p.rows && at.x >= 0) {
-        float co[VEC], si[VEC];
-        if (turning) {
-          const float4* c4 = reinterpret_cast<const float4*>(cs_s + (size_t)(st * tokens + t) * 2 * p.rot) + l;
-          const float4* s4 = reinterpret_cast<const float4*>(cs_s + (size_t)(st * tokens + t) * 2 * p.rot + p.rot) + l;
+        Lane<T> lf;
+        lf.turning = first < p.rot;
+        auto factors_of = [&](int kind) {
+          const float4* f4 = reinterpret_cast<const float4*>(factor_s + (size_t)((st * tokens + t) * 2 + kind) * 2 * p.D) + (live ? l : 0);
 #pragma unroll
           for (int j = 0; j < VEC / 4; ++j) {
-            const float4 c = c4[j * turn_lanes], v = s4[j * turn_lanes];
-            co[4 * j] = c.x, co[4 * j + 1] = c.y, co[4 * j + 2] = c.z, co[4 * j + 3] = c.w;
-            si[4 * j] = v.x, si[4 * j + 1] = v.y, si[4 * j + 2] = v.z, si[4 * j + 3] = v.w;
+            const float4 m = f4[j * head_lanes], o = f4[p.D / 4 + j * head_lanes];
+            lf.mine[2 * j] = tc::pair(m.x, m.y), lf.mine[2 * j + 1] = tc::pair(m.z, m.w);
+            lf.others[2 * j] = tc::pair(o.x, o.y), lf.others[2 * j + 1] = tc::pair(o.z, o.w);
           }
-        }
+        };
         uint8_t* token = bulk_s + st * stage_bytes + t * row_bytes + first * sizeof(T);
+        const uint32_t hop = each * at_once * head_bytes;
         const int page = PACKED && at.y >= 0 ? at.y / p.page_size : 0, tok = PACKED && at.y >= 0 ? at.y - page * p.page_size : 0;
-#pragma unroll 2
-        for (int step = in_t; step < steps; step += each) {
-          const int kind = step < q_steps ? 0 : step < q_steps + k_steps ? 1 : 2;
-          const int h = (step - (kind == 0 ? 0 : kind == 1 ? q_steps : q_steps + k_steps)) * at_once + sub;
-          const bool on = h < (kind == 0 ? p.Hq : p.Hk);
-          P* here = reinterpret_cast<P*>(token + (size_t)(h + (kind == 0 ? 0 : kind == 1 ? p.Hq : turned)) * head_bytes);
-          P x;
-          if (on && live) x = *here;
-          float y[VEC];
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) y[e] = on && live ? to_f(x.e[e]) : 0.f;
-          const float* weight = kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr;
-          if (weight) {
-            float sum = 0.f;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) sum = fmaf(y[e], y[e], sum);
-            for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const float r = rsqrtf(fmaf(sum, inv_d, p.eps));
-            if (live) {
-#pragma unroll
-              for (int e = 0; e < VEC; ++e) y[e] *= r * (kind == 0 ? qw[e] : weight[first + e]);
+        const int groups_of = p.D / q4::kGroup;
+        auto heads = [&](auto kind_v, int begin, int count, const float* weight, void* cache, uint8_t* scales) {
+          constexpr int kind = decltype(kind_v)::value;
+          if (kind < 2) factors_of(kind);
+          uint8_t* from = token + (uint32_t)(begin + in_t * at_once + sub) * head_bytes;
+          for (int h0 = in_t * at_once; h0 < count; h0 += each * at_once, from += hop) {
+            const bool on = h0 + sub < count;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (on && live) v = *reinterpret_cast<const uint4*>(from);
+            uint64_t y[N];
+            if (kind == 2) unpack(v, y, T());
+            else norm_turn<T, INTER>(v, y, lf, weight != nullptr, lanes, other, inv_d, p.eps);
+            if (PACKED && kind > 0) {
+              float yf[VEC];
+              spread(y, yf);
+              const int head = on ? h0 + sub : 0;
+              store_packed<VEC, 1>(yf, first, 32 * VEC, p.D, on && at.y >= 0,
+                                   (uint8_t*)cache + q4::data_at(page, head, tok, p.Hk, groups_of, p.page_size),
+                                   scales + q4::scale_at(page, head, tok, p.Hk, groups_of, p.page_size), p.page_size);
+            } else if (on && live) {
+              *reinterpret_cast<uint4*>(from) = packed_up(y, T());
             }
           }
-          if (kind < 2 && half > 0) {
-            float z[VEC];
-            if (inter) {
-#pragma unroll
-              for (int e = 0; e < VEC; ++e) z[e] = y[e ^ 1];
-            } else {
-#pragma unroll
-              for (int e = 0; e < VEC; ++e) z[e] = __shfl_sync(0xffffffffu, y[e], other);
-            }
-            if (turning) {
-#pragma unroll
-              for (int e = 0; e < VEC; ++e) y[e] = fmaf(y[e], co[e], __fmul_rn(z[e], si[e]));
-            }
-          }
-          if (PACKED && kind > 0) {
-            const int heads = p.D / q4::kGroup, head = on ? h : 0;
-            store_packed<VEC, 1>(y, first, 32 * VEC, p.D, on && at.y >= 0,
-                                 (uint8_t*)(kind == 1 ? p.k_cache : p.v_cache) + q4::data_at(page, head, tok, p.Hk, heads, p.page_size),
-                                 (kind == 1 ? p.k_scale : p.v_scale) + q4::scale_at(page, head, tok, p.Hk, heads, p.page_size), p.page_size);
-          } else if (on && live) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) put(&x.e[e], y[e]);
-            *here = x;
-          }
-        }
+        };
+        heads(std::integral_constant<int, 0>(), 0, p.Hq, p.q_weight, nullptr, nullptr);
+        heads(std::integral_constant<int, 1>(), p.Hq, p.Hk, p.k_weight, p.k_cache, p.k_scale);
+        if (PACKED) heads(std::integral_constant<int, 2>(), turned, p.Hk, nullptr, p.v_cache, p.v_scale);
       }
       tc::fence_proxy_async();
       __syncwarp();
@@ -460,7 +630,7 @@ __global__ void __launch_bounds__(kBulkThreads, kBulkBlocks)
 template <typename T>
 size_t bulk_bytes(const spec_norm_rope_args& a, int tokens, int stages) {
   const size_t half = a.rot / 2, row = (size_t)(a.Hq + 2 * a.Hk) * a.D * sizeof(T);
-  return stages * tokens * row + sizeof(Ring) + (half + 1) / 2 * 16 + (size_t)stages * tokens * 2 * a.rot * sizeof(float);
+  return stages * tokens * row + sizeof(Ring) + (half + 1) / 2 * 16 + (size_t)(2 + stages * tokens * 4) * a.D * sizeof(float);
 }
 constexpr size_t kBulkMemory = 222 * 1024, kStageBytes = 26 * 1024;
 constexpr size_t kBulkBytes = 12000000;  // of a batch, from which on
@@ -477,7 +647,7 @@ bool launch_bulk(const spec_norm_rope_args& a, int lanes, cudaStream_t stream, c
   int stages = kMaxStages;
   while (stages > 1 && bulk_bytes<T>(a, tokens, stages) > kBulkMemory / kBulkBlocks) --stages;
   if (stages < 3) return false;
-  auto kernel = norm_rope_bulk_kernel<T, PACKED>;
+  auto kernel = a.layout == SPEC_ROPE_INTERLEAVED ? norm_rope_bulk_kernel<T, true, PACKED> : norm_rope_bulk_kernel<T, false, PACKED>;
   *err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kBulkMemory / kBulkBlocks));
   if (*err != cudaSuccess) return true;
   const int groups = (a.rows + tokens - 1) / tokens;
@@ -486,38 +656,47 @@ bool launch_bulk(const spec_norm_rope_args& a, int lanes, cudaStream_t stream, c
   return true;
 }
 
-template <typename T, int VEC, int CH, bool FAST, bool PACKED>
-cudaError_t launch(const spec_norm_rope_args& a, cudaStream_t stream) {
-  int lanes = 32;
-  if (CH == 1)
-    for (lanes = 1; lanes * VEC < a.D;) lanes *= 2;
-  if (PACKED) lanes = std::max(lanes, q4::kGroup / VEC);
-  if (FAST) {
-    cudaError_t err;
-    if (launch_bulk<T, PACKED>(a, lanes, stream, &err)) return err;
-  }
-  const int at_once = CH == 1 ? 32 / lanes : 1;
+// Lanes of a head, heads of a warp at a time and what a launch of warps of single heads takes.
+struct Shape {
+  int lanes, parts;
+  unsigned blocks;
+};
+Shape shape_of(const spec_norm_rope_args& a, int vec, bool packed, bool chunks = false) {
+  Shape s;
+  for (s.lanes = chunks ? 32 : 1; s.lanes * vec < a.D && s.lanes < 32;) s.lanes *= 2;
+  if (packed) s.lanes = std::max(s.lanes, q4::kGroup / vec);
+  const int at_once = 32 / s.lanes;
   const int steps = (a.Hq + at_once - 1) / at_once + 2 * ((a.Hk + at_once - 1) / at_once);
   // warps for eight blocks an SM, as far as a warp keeps four steps
   const int64_t warps = 152 * 8 * kWarps;
-  const int parts = (int)std::max<int64_t>(1, std::min<int64_t>((steps + kSteps - 1) / kSteps, warps / std::max(a.rows, 1)));
-  const int64_t blocks = ((int64_t)a.rows * parts + kWarps - 1) / kWarps;
-  const size_t smem = (size_t)(a.rot / 2) * (1 + kWarps) * sizeof(float2) + (FAST ? 0 : (size_t)kWarps * 32 * VEC * CH * sizeof(float));
-  norm_rope_kernel<T, VEC, CH, FAST, PACKED><<<(unsigned)std::min<int64_t>(blocks, 152 * 8), kThreads, smem, stream>>>(a, parts, lanes);
+  s.parts = (int)std::max<int64_t>(1, std::min<int64_t>((steps + kSteps - 1) / kSteps, warps / std::max(a.rows, 1)));
+  s.blocks = (unsigned)std::min<int64_t>(((int64_t)a.rows * s.parts + kWarps - 1) / kWarps, 152 * 8);
+  return s;
+}
+
+template <typename T, int VEC, int CH, bool PACKED>
+cudaError_t launch_general(const spec_norm_rope_args& a, cudaStream_t stream) {
+  const Shape s = shape_of(a, VEC, PACKED, CH > 1);
+  const size_t smem = (size_t)(a.rot / 2) * (1 + kWarps) * sizeof(float2) + (size_t)kWarps * 32 * VEC * CH * sizeof(float);
+  norm_rope_general_kernel<T, VEC, CH, PACKED><<<s.blocks, kThreads, smem, stream>>>(a, s.parts, s.lanes);
   return cudaGetLastError();
 }
 
 template <typename T, bool PACKED>
 cudaError_t launch(const spec_norm_rope_args& a, bool wide, cudaStream_t stream) {
   constexpr int VEC = 16 / (int)sizeof(T);
-  if (wide) {
-    const int turn_step = a.layout == SPEC_ROPE_HALF ? a.rot / 2 : a.rot;
-    if (a.D <= 32 * VEC)
-      return turn_step % VEC == 0 ? launch<T, VEC, 1, true, PACKED>(a, stream) : launch<T, VEC, 1, false, PACKED>(a, stream);
-    if (VEC == 8 || a.D <= 64 * VEC) return launch<T, VEC, 2, false, PACKED>(a, stream);
-    return launch<T, VEC, VEC == 8 ? 2 : 4, false, PACKED>(a, stream);
-  }
-  return a.D <= 128 ? launch<T, 1, 4, false, PACKED>(a, stream) : launch<T, 1, 16, false, PACKED>(a, stream);
+  if (!wide) return a.D <= 128 ? launch_general<T, 1, 4, PACKED>(a, stream) : launch_general<T, 1, 16, PACKED>(a, stream);
+  if (a.D > 64 * VEC) return launch_general<T, VEC, VEC == 8 ? 2 : 4, PACKED>(a, stream);
+  if (a.D > 32 * VEC) return launch_general<T, VEC, 2, PACKED>(a, stream);
+  const bool inter = a.layout == SPEC_ROPE_INTERLEAVED;
+  if ((inter ? a.rot : a.rot / 2) % VEC != 0) return launch_general<T, VEC, 1, PACKED>(a, stream);
+  const Shape s = shape_of(a, VEC, PACKED);
+  cudaError_t err;
+  if (launch_bulk<T, PACKED>(a, s.lanes, stream, &err)) return err;
+  const size_t smem = (size_t)(a.rot / 2) * (1 + kWarps) * sizeof(float2);
+  if (inter) norm_rope_kernel<T, true, PACKED><<<s.blocks, kThreads, smem, stream>>>(a, s.parts, s.lanes);
+  else norm_rope_kernel<T, false, PACKED><<<s.blocks, kThreads, smem, stream>>>(a, s.parts, s.lanes);
+  return cudaGetLastError();
 }
 
 // ------------------------------------------------------------- read-back ---
