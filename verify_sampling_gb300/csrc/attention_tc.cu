@@ -59,7 +59,7 @@ using tc::pair;
 // threads i and i + 16 of its warp, each half of its columns.
 constexpr int kSoftWarps = 16, kProducer = 16, kMma = 17, kPlanner = 18, kLoader = 19, kUnpack = 20;
 constexpr int kItemSlots = 4;
-constexpr int kUnpackWarps = 4;  // a packed cache's: a key each thread
+constexpr int kUnpackWarps = 8;  // a packed cache's: half of a key's groups each thread
 template <bool kPacked>
 struct Roles {
   static constexpr int kThreads = 640 + (kPacked ? 32 * kUnpackWarps : 0);
@@ -265,10 +265,10 @@ __global__ void __launch_bounds__(Roles<kPacked>::kThreads, 1)
     }
     return got;
   };
-  // Over a packed cache softmax threads need more registers than a 768th of the file: the other
-  // two warpgroups give theirs, 512 x 96 + 256 x 48 of the 768 x 80 that the block starts with.
+  // Over a packed cache softmax threads need more registers than an 896th of the file: the other
+  // three warpgroups give theirs, 512 x 96 + 384 x 40 of the 896 x 72 that the block starts with.
   if (warp >= kSoftWarps) {
-    if (kPacked) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (kPacked) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == kProducer) {
       // ------------------------------------------------------------ producer --
       uint32_t seq = 0;  // ring positions used: keys and values in turn
@@ -556,10 +556,11 @@ __global__ void __launch_bounds__(Roles<kPacked>::kThreads, 1)
           if (n[t] > 0) tc::mbar_wait(&bars.q_full[t], (n[t] - 1u) & 1u, kWaitNs);
     } else if (kPacked && warp >= kUnpack) {
       // -------------------------------------------------------------- unpack --
-      // A thread's key or value from the packed ring to its row of the operand tile.
-      constexpr int G = S::kGroups;
-      const int key = (warp - kUnpack) * 32 + lane, box = min(a.page_size, kTile), page = key / box;
-      const uint8_t* from = smem + S::kPackedRing + page * G * box * 16 + (key - page * box) * 16;
+      // Half of a key's (or value's) groups from the packed ring to their row of the operand tile, a thread.
+      constexpr int G = S::kGroups, kMine = G / 2;
+      const int at = (warp - kUnpack) * 32 + lane, key = at % kTile, c0 = at / kTile * kMine;
+      const int box = min(a.page_size, kTile), page = key / box;
+      const uint8_t* from = smem + S::kPackedRing + (page * G + c0) * box * 16 + (key - page * box) * 16;
       uint8_t* to = smem + S::kRing + key * 128;
       const uint32_t turn = (key & 7) << 4;
       uint32_t st = 0, ph = 0, pst = 0, pph = 0;
@@ -575,15 +576,15 @@ __global__ void __launch_bounds__(Roles<kPacked>::kThreads, 1)
           ok = warp_wait(&bars.packed_full[pst], pph) && warp_wait(&bars.empty[st], ph ^ 1u);
           if (!ok) break;
           const uint8_t* src = from + pst * S::kPackedBytes;
-          const uint8_t* sp = smem + S::kPackedRing + pst * S::kPackedBytes + S::kPackedData + key * G;
-          const uint32_t scales = G == 4 ? *reinterpret_cast<const uint32_t*>(sp) : *reinterpret_cast<const uint16_t*>(sp);
-          uint4 v[G];
+          const uint8_t* sp = smem + S::kPackedRing + pst * S::kPackedBytes + S::kPackedData + key * G + c0;
+          const uint32_t scales = G == 4 ? *reinterpret_cast<const uint16_t*>(sp) : *sp;
+          uint4 v[kMine];
 #pragma unroll
-          for (int c = 0; c < G; ++c) v[c] = tc::lds128(src + c * box * 16);
+          for (int c = 0; c < kMine; ++c) v[c] = tc::lds128(src + c * box * 16);
           uint8_t* dst = to + st * S::kTileBytes;
           auto words = [&](auto is_key) {
 #pragma unroll
-            for (int c = 0; c < G; ++c) {
+            for (int c = 0; c < kMine; ++c) {
               const q4::Scale z = q4::scale_pair(__byte_perm(scales, 0, 0x4040 | c * 0x0101));
               const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(Roles<kPacked>::kThreads, 1)
                                     ? make_uint4(__byte_perm(p0, p1, 0x5410), __byte_perm(p2, p3, 0x5410), __byte_perm(p0, p1, 0x7632),
                                                  __byte_perm(p2, p3, 0x7632))
                                     : make_uint4(p0, p1, p2, p3);
-                const int chunk = c * 4 + x;
+                const int chunk = (c0 + c) * 4 + x;
                 *reinterpret_cast<uint4*>(dst + (chunk >> 3) * kHalfBytes + (((chunk & 7) << 4) ^ turn)) = o;
               }
             }
