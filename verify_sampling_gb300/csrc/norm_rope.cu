@@ -146,24 +146,51 @@ __device__ __forceinline__ void spread(const uint64_t (&y)[N], float (&to)[2 * N
   }
 }
 
+// The larger magnitude, NaN where either is one.
+__device__ __forceinline__ float larger(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+
 // Codes a lane's VEC elements of each chunk and writes them to the token's head in the cache.
 // All lanes of the warp call it; `on`: this one's head is written.
 template <int VEC, int CH>
-__device__ __forceinline__ void store_packed(const float (&y)[CH * VEC], int first, int step, int D, bool on, uint8_t* data,
-                                           uint8_t* scale, int P) {
+__device__ __forceinline__ void store_packed(const float (&from)[CH * VEC], int first, int step, int D, bool on, uint8_t* data,
+                                             uint8_t* scale, int P) {
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int d = first + c * step;  // this lane's first element
-    float amax = 0.f;
+    float y[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) amax = fmaxf(amax, fabsf(y[c * VEC + e]));
+    for (int e = 0; e < VEC; ++e) y[e] = from[c * VEC + e];
+    auto largest = [&] {
+      float m = fabsf(y[0]);
 #pragma unroll
-    for (int o = 1; o < q4::kGroup / VEC; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      for (int e = 1; e < VEC; ++e) m = larger(m, y[e]);
+#pragma unroll
+      for (int o = 1; o < q4::kGroup / VEC; o <<= 1) m = larger(m, __shfl_xor_sync(0xffffffffu, m, o));
+      return m;
+    };
+    float amax = largest();
+    if (__any_sync(0xffffffffu, amax != amax)) {  // NaN is stored as 0
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (y[e] != y[e]) y[e] = 0.f;
+      amax = largest();
+    }
     const uint32_t code = q4::code_of(amax);
     const float s = q4::scale_of(code);
+    if (__any_sync(0xffffffffu, code == 255)) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) y[e] = fminf(fmaxf(y[e], -7.f * s), 7.f * s);
+    }
+    const float inv = __fdividef(1.f, s);
     uint32_t w = 0;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) w |= q4::nibble_of(y[c * VEC + e], s) << (4 * ((d + e) & 7));
+    for (int e = VEC - 1; e >= 0; --e) w = w * 16u + (q4::number_of(y[e], s, inv) & 15u);
+    w ^= VEC == 8 ? 0x88888888u : VEC == 4 ? 0x8888u : 8u;  // n + 8
+    if (VEC < 8) w <<= 4 * (d & 7);
 #pragma unroll
     for (int o = 1; o < 8 / VEC; o <<= 1) w |= __shfl_xor_sync(0xffffffffu, w, o);
     if (!on || d >= D) continue;
@@ -700,37 +727,41 @@ cudaError_t launch(const spec_norm_rope_args& a, bool wide, cudaStream_t stream)
 }
 
 // ------------------------------------------------------------- read-back ---
-// A thread turns 4 bytes into 8 elements; 4 threads side by side a group.
+// A thread turns 4 bytes into 8 elements, 4 threads side by side a group; it keeps its word of a row
+// and steps over rows.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(spec_cache_read_packed_args p) {
-  const int groups = p.D / q4::kGroup, words = p.Hk * groups * 4;
-  const int which = blockIdx.y;
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(spec_cache_read_packed_args p, int at_once) {
+  const int groups = p.D / q4::kGroup, words = p.Hk * groups * 4, wide = min(words, kThreads);
+  const int which = blockIdx.y, r0 = threadIdx.x / wide;
   T* out = (T*)(which ? p.v : p.k);
-  if (!out) return;
+  if (!out || r0 >= at_once) return;
   const uint8_t* data = (const uint8_t*)(which ? p.v_cache : p.k_cache);
   const uint8_t* scales = which ? p.v_scale : p.k_scale;
-  const int64_t n = (int64_t)p.rows * words;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
-    const int row = (int)(i / words), w = (int)(i - (int64_t)row * words);
+  for (int w = threadIdx.x - r0 * wide; w < words; w += wide) {
     const int h = w / (4 * groups), g = w / 4 - h * groups;
-    const int slot = p.slot[row];
-    if (slot >= p.n_slots) set_status(p.status, SPEC_STATUS_BAD_PAGE);
-    uint32_t v = 0x88888888u;  // zeros
-    float s = 0.f;
-    if (slot >= 0 && slot < p.n_slots) {
-      const int page = slot / p.page_size, tok = slot - page * p.page_size;
-      v = *reinterpret_cast<const uint32_t*>(data + q4::data_at(page, h, tok, p.Hk, groups, p.page_size) +
-                                             (size_t)g * 16 * p.page_size + (w & 3) * 4);
-      s = q4::scale_of(scales[q4::scale_at(page, h, tok, p.Hk, groups, p.page_size) + g]);
-    }
-    constexpr int VEC = 16 / (int)sizeof(T);
-    T* to = out + i * 8;
-#pragma unroll
-    for (int c = 0; c < 8; c += VEC) {
-      Pack<T, VEC> o;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) put(&o.e[e], (float)((int)(v >> (4 * (c + e)) & 15u) - 8) * s);
-      *reinterpret_cast<Pack<T, VEC>*>(to + c) = o;
+    const uint8_t* word = data + q4::data_at(0, h, 0, p.Hk, groups, p.page_size) + (size_t)g * 16 * p.page_size + (w & 3) * 4;
+    const uint8_t* code = scales + q4::scale_at(0, h, 0, p.Hk, groups, p.page_size) + g;
+    const int64_t page_bytes = q4::data_at(1, 0, 0, p.Hk, groups, p.page_size), page_codes = q4::scale_at(1, 0, 0, p.Hk, groups, p.page_size);
+#pragma unroll 4
+    for (int64_t row = (int64_t)blockIdx.x * at_once + r0; row < p.rows; row += (int64_t)gridDim.x * at_once) {
+      const int slot = p.slot[row];
+      uint32_t v = 0x88888888u, b = 0;  // zeros
+      if (slot >= p.n_slots) set_status(p.status, SPEC_STATUS_BAD_PAGE);
+      if (slot >= 0 && slot < p.n_slots) {
+        const uint32_t page = (uint32_t)slot / (uint32_t)p.page_size, tok = slot - page * p.page_size;
+        v = *reinterpret_cast<const uint32_t*>(word + page * page_bytes + (size_t)tok * 16);
+        b = code[page * page_codes + (size_t)tok * groups];
+      }
+      const q4::Scale s = q4::scale_pair(b * 0x10001u);
+      const uint32_t p0 = q4::element_pair<0>(v, s), p1 = q4::element_pair<1>(v, s), p2 = q4::element_pair<2>(v, s), p3 = q4::element_pair<3>(v, s);
+      const uint32_t x[4] = {__byte_perm(p0, p1, 0x5410), __byte_perm(p2, p3, 0x5410), __byte_perm(p0, p1, 0x7632), __byte_perm(p2, p3, 0x7632)};
+      uint4* to = reinterpret_cast<uint4*>(out + ((size_t)row * words + w) * 8);
+      if (sizeof(T) == 2) {
+        *to = make_uint4(x[0], x[1], x[2], x[3]);
+      } else {
+        to[0] = make_uint4(x[0] << 16, x[0] & 0xffff0000u, x[1] << 16, x[1] & 0xffff0000u);
+        to[1] = make_uint4(x[2] << 16, x[2] & 0xffff0000u, x[3] << 16, x[3] & 0xffff0000u);
+      }
     }
   }
 }
@@ -751,10 +782,10 @@ cudaError_t launch_norm_rope(const spec_norm_rope_args& a, cudaStream_t stream) 
 
 cudaError_t launch_cache_read(const spec_cache_read_packed_args& a, cudaStream_t stream) {
   if (a.rows == 0) return cudaSuccess;
-  const int64_t n = (int64_t)a.rows * a.Hk * (a.D / 8);
-  const dim3 grid((unsigned)std::min<int64_t>((n + kThreads - 1) / kThreads, 152 * 16), 2);
-  if (a.dtype == SPEC_F32) cache_read_kernel<float><<<grid, kThreads, 0, stream>>>(a);
-  else cache_read_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(a);
+  const int words = a.Hk * (a.D / 8), at_once = std::max(1, kThreads / words);
+  const dim3 grid((unsigned)std::min<int64_t>(((int64_t)a.rows + at_once - 1) / at_once, 152 * 8), 2);
+  if (a.dtype == SPEC_F32) cache_read_kernel<float><<<grid, kThreads, 0, stream>>>(a, at_once);
+  else cache_read_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(a, at_once);
   return cudaGetLastError();
 }
 

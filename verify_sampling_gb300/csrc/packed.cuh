@@ -41,10 +41,14 @@ __device__ __forceinline__ uint32_t code_of(float amax) {
   const int bits = __float_as_int(__fdiv_rn(amax, 7.f));
   return (uint32_t)min(max(((bits + (1 << 19)) >> 20) - 8 * kLeastExp, 0), 255);
 }
-// x / s to the nearest whole number, halves to even, +-7 at most; NaN gives 0.  (A true
-// division: stored 16-bit values meet halves exactly, and a product with 1 / s would miss them.)
-__device__ __forceinline__ uint32_t nibble_of(float x, float s) {
-  return (uint32_t)(min(max(__float2int_rn(__fdiv_rn(x, s)), -7), 7) + 8);
+// x / s to the nearest whole number, halves to even, in the low four bits, for |x| < 7.5 s; `inv` is 1 / s
+// within an ulp or two.  The product with it may miss a half that the quotient meets exactly
+// (16-bit values often do), so it is made a little small, and x - n s, which is exact, decides.
+__device__ __forceinline__ uint32_t number_of(float x, float s, float inv) {
+  const float t = fmaf(x, inv, -0x1p-18f) + 12582912.f;  // 1.5 2^23: the sum's low bits are the whole number
+  const float rest = fmaf(-(t - 12582912.f), s, x);
+  const int odd = __float_as_int(t) & 1;
+  return __float_as_uint(t) + (__float_as_int(rest) + odd > __float_as_int(0.5f * s));  // (below 0: a negative int)
 }
 
 // ------------------------------------------------ elements in bf16 pairs --
