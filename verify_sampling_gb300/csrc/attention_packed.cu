@@ -57,6 +57,9 @@ struct NarrowCosts {
   __device__ static __forceinline__ int tiles_before(int x, int) { return (x + 3) >> 2; }
 };
 
+// Blocks an SM: as many as hold the results of two row blocks of 128 dimensions in registers, or of less.
+constexpr int narrow_blocks(int D, int NB) { return D * NB == 256 ? 2 : kNarrowBlocks; }
+
 template <int D, int NB>
 struct Sizes {
   static constexpr int kGroups = D / q4::kGroup;
@@ -128,7 +131,7 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 template <int D, int NB>
-__global__ void __launch_bounds__(kThreads, NB == 1 ? kNarrowBlocks : 2)
+__global__ void __launch_bounds__(kThreads, narrow_blocks(D, NB))
     attention_narrow_kernel(const spec_prefix_attention_args a, const q4::Cache packed, const Window w, float* part, float2* stat,
                             int64_t* plan) {
   using S = Sizes<D, NB>;
@@ -285,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? kNarrowBlocks : 2)
     const bool wide_out = ((uintptr_t)a.out & 7) == 0 && a.out_row % 4 == 0 && a.out_head % 4 == 0;
     float* join = reinterpret_cast<float*>(smem + M::kJoin);
     float2* row_stat = reinterpret_cast<float2*>(smem + M::kStat);
-    uint32_t seq = 0, met = 0;
+    uint32_t st = 0, st_phase = 0, met = 0;
     bool ok = true;
     auto meet = [&] {  // the four warps (a named barrier's wait would have no limit)
       __syncwarp();
@@ -355,9 +358,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? kNarrowBlocks : 2)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[c][x][nb][e] = 0.f;
 
-      for (int i = it.lo; i < it.hi; ++i, ++seq) {
-        const uint32_t st = seq % S::kStages;
-        ok = warp_wait(&bars.full[st], seq / S::kStages);
+      for (int i = it.lo; i < it.hi; ++i) {
+        ok = warp_wait(&bars.full[st], st_phase);
         if (!ok) break;
         const uint32_t ks = sbase + st * S::kStageBytes, vs = ks + S::kData + S::kScales;
         const uint8_t* k_code = smem + st * S::kStageBytes + S::kData + (warp * 32 + g) * G;
@@ -471,6 +473,10 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? kNarrowBlocks : 2)
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&bars.empty[st]);
+        if (++st == S::kStages) {
+          st = 0;
+          st_phase ^= 1u;
+        }
       }
       if (!ok) break;
       // ---- the warps' results: maxima and sums of all, results pairwise
@@ -583,7 +589,7 @@ cudaError_t launch(const spec_prefix_attention_args& a, const q4::Cache& packed,
   auto kernel = attention_narrow_kernel<D, NB>;
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
   if (err != cudaSuccess) return err;
-  const int blocks = std::min(NB == 1 ? kNarrowBlocks : 2, 227 * 1024 / (kBytes + 1024));
+  const int blocks = std::min(narrow_blocks(D, NB), 227 * 1024 / (kBytes + 1024));
   const int most_rows = attn_window_rows(a.Hq), windows = (int)(((int64_t)a.rows + most_rows - 1) / most_rows);
   const int step = (int)(((int64_t)a.rows + windows - 1) / windows);
   const Pieces narrow{work.narrow_part, work.narrow_stat, work.narrow_plan}, wide{work.part, work.stat, work.plan};
@@ -604,7 +610,11 @@ cudaError_t launch(const spec_prefix_attention_args& a, const q4::Cache& packed,
   // The narrow kernel alone for requests of few rows without a prefix; otherwise the wide
   // one takes the segments of more than kNarrowMost rows before it.
   const bool both = a.G > 0 || m > kNarrowMost * R;
-  if (m <= 8 * R) return launch<D, 1>(a, packed, sms, work, both, stream);
+  // 16 rows an item cost 1.45 times 8 (D = 128: 256 requests of 4096 keys 461 us and 318) or 1.22 times (D = 64: 101
+  // requests of 1500 keys 54 us and 44), but read the keys of a request of 9 to 16 rows once: where a
+  // request has several rows, some have more than the mean.
+  const int64_t most = D == 64 && a.rows > a.R ? 6 : 8;
+  if (m <= most * R) return launch<D, 1>(a, packed, sms, work, both, stream);
   return launch<D, 2>(a, packed, sms, work, both, stream);
 }
 

@@ -442,7 +442,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_general_kernel(spec_norm_r
 // cosines of the stages ahead, the others take heads as above, in place where a bulk store
 // takes them on (queries, and the keys of a cache of the inputs' type).  Every wait is bounded: on
 // a timeout the block sets SPEC_STATUS_TIMEOUT, waits for its copies in flight and returns.
-constexpr int kBulkThreads = kThreads + 64, kBulkBlocks = 2;  // blocks an SM
+constexpr int kBulkThreads = kThreads + 64;
+constexpr int bulk_blocks(bool packed) { return packed ? 2 : 3; }  // an SM
 constexpr int kMaxStages = 4;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
@@ -458,7 +459,7 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t phase) {
 // Stage i of the block holds tokens (blockIdx.x + i * gridDim.x) * tokens and on; `tokens`
 // divides the warps.
 template <typename T, bool INTER, bool PACKED>
-__global__ void __launch_bounds__(kBulkThreads, kBulkBlocks)
+__global__ void __launch_bounds__(kBulkThreads, bulk_blocks(PACKED))
     norm_rope_bulk_kernel(spec_norm_rope_args p, int tokens, int stages, int lanes) {
   constexpr int VEC = Lane<T>::VEC, N = VEC / 2;
   extern __shared__ __align__(128) uint8_t bulk_s[];
@@ -659,7 +660,7 @@ size_t bulk_bytes(const spec_norm_rope_args& a, int tokens, int stages) {
   const size_t half = a.rot / 2, row = (size_t)(a.Hq + 2 * a.Hk) * a.D * sizeof(T);
   return stages * tokens * row + sizeof(Ring) + (half + 1) / 2 * 16 + (size_t)(2 + stages * tokens * 4) * a.D * sizeof(float);
 }
-constexpr size_t kBulkMemory = 222 * 1024, kStageBytes = 26 * 1024;
+constexpr size_t kBulkMemory = 222 * 1024, kStageBytes = 20 * 1024;
 constexpr size_t kBulkBytes = 12000000;  // of a batch, from which on
 constexpr int kBulkRows = 608;           // four tokens an SM
 template <typename T, bool PACKED>
@@ -671,14 +672,15 @@ bool launch_bulk(const spec_norm_rope_args& a, int lanes, cudaStream_t stream, c
     return false;
   int tokens = std::min({kWarps, a.rows / kBulkRows, std::max(1, (int)(kStageBytes / row))});
   while (tokens & (tokens - 1)) tokens &= tokens - 1;
+  constexpr int kBlocks = bulk_blocks(PACKED);
   int stages = kMaxStages;
-  while (stages > 1 && bulk_bytes<T>(a, tokens, stages) > kBulkMemory / kBulkBlocks) --stages;
+  while (stages > 1 && bulk_bytes<T>(a, tokens, stages) > kBulkMemory / kBlocks) --stages;
   if (stages < 3) return false;
   auto kernel = a.layout == SPEC_ROPE_INTERLEAVED ? norm_rope_bulk_kernel<T, true, PACKED> : norm_rope_bulk_kernel<T, false, PACKED>;
-  *err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kBulkMemory / kBulkBlocks));
+  *err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kBulkMemory / kBlocks));
   if (*err != cudaSuccess) return true;
   const int groups = (a.rows + tokens - 1) / tokens;
-  kernel<<<std::min(groups, kBulkBlocks * 152), kBulkThreads, bulk_bytes<T>(a, tokens, stages), stream>>>(a, tokens, stages, lanes);
+  kernel<<<std::min(groups, kBlocks * 152), kBulkThreads, bulk_bytes<T>(a, tokens, stages), stream>>>(a, tokens, stages, lanes);
   *err = cudaGetLastError();
   return true;
 }
@@ -783,7 +785,7 @@ cudaError_t launch_norm_rope(const spec_norm_rope_args& a, cudaStream_t stream) 
 cudaError_t launch_cache_read(const spec_cache_read_packed_args& a, cudaStream_t stream) {
   if (a.rows == 0) return cudaSuccess;
   const int words = a.Hk * (a.D / 8), at_once = std::max(1, kThreads / words);
-  const dim3 grid((unsigned)std::min<int64_t>(((int64_t)a.rows + at_once - 1) / at_once, 152 * 8), 2);
+  const dim3 grid((unsigned)std::min<int64_t>(((int64_t)a.rows + at_once - 1) / at_once, 152 * 2), 2);
   if (a.dtype == SPEC_F32) cache_read_kernel<float><<<grid, kThreads, 0, stream>>>(a, at_once);
   else cache_read_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(a, at_once);
   return cudaGetLastError();

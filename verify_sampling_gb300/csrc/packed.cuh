@@ -67,13 +67,19 @@ constexpr uint32_t kScaleBits = ((uint32_t)kLeastExp << 7) * 0x10001u;
 __device__ __forceinline__ Scale scale_pair(uint32_t codes) { return scale_bits(codes * 16u + kScaleBits); }
 __device__ __forceinline__ Scale scale_one(uint32_t code) { return scale_bits(code * 0x00100010u + kScaleBits); }
 __device__ __forceinline__ Scale scale_two(uint32_t lo, uint32_t hi) { return scale_bits(hi * 0x00100000u + (lo * 16u + kScaleBits)); }
+// (x & mask) | bits in one instruction, which two constants alone may become two.
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(mask), "r"(bits));
+  return r;
+}
 // Elements I and I + 4 of a word's 8 (its halves' I-th nibbles): n goes to bits 3-6 under the
 // exponent of 16, which is 16 + n, and (16 + n) s - 24 s is exact, as 24 s and the result are
 // numbers of six and seven bits.
 template <int I>
 __device__ __forceinline__ uint32_t element_pair(uint32_t w, const Scale& s) {
   const uint32_t n = I == 0 ? w * 8u : w >> (4 * I - 3);
-  return fma_bf16((n & 0x00780078u) | 0x41804180u, s.s, s.z);
+  return fma_bf16(and_or(n, 0x00780078u, 0x41804180u), s.s, s.z);
 }
 // n - 8 of elements I and I + 4 in fp16, with `high` the word shifted right by 8: n lies in bits
 // 0-3 under the exponent of 1024 (I even), which is 1024 + n, or in bits 4-7, 1024 + 16 n.
@@ -82,9 +88,9 @@ __device__ __forceinline__ uint32_t number_pair(uint32_t w, uint32_t high) {
   const uint32_t v = I < 2 ? w : high;
   uint32_t r;
   if (I % 2 == 0)
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"((v & 0x000f000fu) | 0x64006400u), "r"(0x3C003C00u), "r"(0xE408E408u));  // x - 1032
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(and_or(v, 0x000f000fu, 0x64006400u)), "r"(0x3C003C00u), "r"(0xE408E408u));  // x - 1032
   else
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"((v & 0x00f000f0u) | 0x64006400u), "r"(0x2C002C00u), "r"(0xD480D480u));  // x / 16 - 72
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(and_or(v, 0x00f000f0u, 0x64006400u)), "r"(0x2C002C00u), "r"(0xD480D480u));  // x / 16 - 72
   return r;
 }
 
