@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, narrow_blocks(D, NB))
         const uint32_t ks = sbase + st * S::kStageBytes, vs = ks + S::kData + S::kScales;
         const uint8_t* k_code = smem + st * S::kStageBytes + S::kData + (warp * 32 + g) * G;
         const uint8_t* v_code = smem + st * S::kStageBytes + 2 * S::kData + S::kScales + (warp * 32 + 2 * t) * G;
-        float s[2][NB][4];  // scores of keys g and g + 8 of 16, rows 2 t and 2 t + 1
+        uint64_t s2[2][NB][2];  // scores of keys g and g + 8 of 16, rows 2 t and 2 t + 1
 #pragma unroll
         for (int c = 0; c < G; c += 2) {
           uint32_t r[2][4];  // [pair of blocks][block, block + 1 of group c, then of c + 1]
@@ -382,12 +382,25 @@ __global__ void __launch_bounds__(kThreads, narrow_blocks(D, NB))
                 const uint32_t* qq = q[nb][c + cc];
                 mma_f16_first(d, number_pair<0>(w0, h0), number_pair<0>(w1, h1), number_pair<1>(w0, h0), number_pair<1>(w1, h1), qq[0], qq[1]);
                 mma_f16(d, number_pair<2>(w0, h0), number_pair<2>(w1, h1), number_pair<3>(w0, h0), number_pair<3>(w1, h1), qq[2], qq[3]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[b][nb][e] = c + cc == 0 ? d[e] * (e < 2 ? z0 : z1) : fmaf(d[e], e < 2 ? z0 : z1, s[b][nb][e]);
+                const uint64_t lo = tc::pair(d[0], d[1]), hi = tc::pair(d[2], d[3]);
+                uint64_t* sp = s2[b][nb];
+                sp[0] = c + cc == 0 ? tc::mul2(lo, tc::pair(z0, z0)) : tc::fma2(lo, tc::pair(z0, z0), sp[0]);
+                sp[1] = c + cc == 0 ? tc::mul2(hi, tc::pair(z1, z1)) : tc::fma2(hi, tc::pair(z1, z1), sp[1]);
               }
             }
         }
-        // scores in log2 units, masked
+        float s[2][NB][4];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float2 v = tc::halves(s2[b][nb][x]);
+              s[b][nb][2 * x] = v.x;
+              s[b][nb][2 * x + 1] = v.y;
+            }
+        // keys behind a row's last
         const int key0 = i * kTile + warp * 32 + g;
         if (i * kTile + kTile > least) {
 #pragma unroll
