@@ -29,15 +29,19 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 // Costs, in units of 0.1 us, measured: a tile of an item of both softmax groups (bound
 // by the products), a tile of a smaller one (bound by its 64 KB where all blocks stream,
 // otherwise by its chain of product, softmax and product), and an item's start and end.
-template <bool SHARED>  // with a narrow kernel, over a packed cache
+// Over a packed cache (SHARED: a narrow kernel takes the segments of few rows) both kinds of tile cost
+// what their unpacking does, 2 us: with the other kernel's costs the round of 256 requests behind a
+// prefix took 911 us, with these 839.
+template <bool SHARED>
 struct WideCosts {
-  static constexpr int kItemRows = attn::kItemRows, kLeast = 17;
+  static constexpr int kItemRows = attn::kItemRows;
   static constexpr bool kShared = SHARED, kWide = true;
-  __device__ static __forceinline__ int tile(int rows) { return rows > kTile ? 17 : 15; }
-  __device__ static __forceinline__ int start(int rows) { return rows > kTile ? 57 : 21; }
+  static constexpr int kPair = SHARED ? 20 : 17, kSingle = SHARED ? 20 : 15, kLeast = kPair;
+  __device__ static __forceinline__ int tile(int rows) { return rows > kTile ? kPair : kSingle; }
+  __device__ static __forceinline__ int start(int rows) { return rows > kTile ? (SHARED ? 30 : 57) : (SHARED ? 20 : 21); }
   // Tiles whose costs begin before `x` units of an item's tiles.
   __device__ static __forceinline__ int tiles_before(int x, int rows) {
-    return rows > kTile ? (unsigned)(x + 16) / 17 : (unsigned)(x + 14) / 15;
+    return rows > kTile ? (unsigned)(x + kPair - 1) / kPair : (unsigned)(x + kSingle - 1) / kSingle;
   }
 };
 
