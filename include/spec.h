@@ -633,7 +633,10 @@ size_t spec_attention_workspace_bytes(int rows, int R, int Hq, int D);
  * One rounding at the end, to the stored type or to 4 bits.  A NULL weight leaves its heads
  * without norm: with both NULL and SPEC_CACHE_DTYPE the results are spec_rope_cache's.
  * k_cache, v_cache: [n_slots, Hk, D] of dtype, or the packed data, n_slots being n_pages *
- * page_size then; page_size and the scales are read for SPEC_CACHE_PACKED alone.
+ * page_size then; page_size and the scales are read for SPEC_CACHE_PACKED alone.  Rows
+ * with equal slots leave data and scales of different rows there.
+ * Squares are summed in fp32: a head of zeros with eps = 0 gives NaN, one whose sum of
+ * squares passes fp32 (elements of 10^19) zeros.
  * Everything else (positions, slots, strides, Hk = 0, Hq = 0, in place) as in
  * spec_rope_cache.  Sizes: its own, and eps >= 0 and finite.
  */

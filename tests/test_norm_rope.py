@@ -113,6 +113,35 @@ def test_without_weights_it_is_rope_cache(rows, Hq, Hk, D, rot, interleaved, dt)
     assert torch.equal(a, b) and torch.equal(caches[0][0], caches[1][0]) and torch.equal(caches[0][1], caches[1][1])
 
 
+@pytest.mark.parametrize("rows", [30, 1300])
+@pytest.mark.parametrize("which", ["q", "k"])
+def test_a_norm_of_one_kind_alone(which, rows):
+    qkv, position, slot, pages, (qw, kw) = _inputs(rows, 40, 8, 64, BF)
+    q, k, v = qkv[:, :40], qkv[:, 40:48], qkv[:, 48:]
+    caches = [[torch.zeros(pages, 8, 8, 64, dtype=BF, device="cuda") for _ in range(2)] for _ in range(3)]
+    both = vs.norm_rope_cache(q, k, v, _freq(64), position, slot, *caches[0], q_weight=qw, k_weight=kw)
+    none = vs.norm_rope_cache(q, k, v, _freq(64), position, slot, *caches[1])
+    one = vs.norm_rope_cache(q, k, v, _freq(64), position, slot, *caches[2], **{f"{which}_weight": qw if which == "q" else kw})
+    assert torch.equal(one, both if which == "q" else none)
+    assert torch.equal(caches[2][0], caches[1 if which == "q" else 0][0])
+
+
+def test_the_batch_does_not_change_a_row():
+    """Rows alone, in a few and in a long batch come out with the same bits."""
+    qkv, position, slot, pages, (qw, kw) = _inputs(1500, 40, 8, 128, BF)
+    q, k, v = qkv[:, :40], qkv[:, 40:48], qkv[:, 48:]
+    freq = _freq(128)
+
+    def call(n):
+        kc, vc = vs.packed_cache(pages, 8, 8, 128), vs.packed_cache(pages, 8, 8, 128)
+        out = vs.norm_rope_cache(q[:n], k[:n], v[:n], freq, position[:n].contiguous(), slot[:n].contiguous(), kc, vc, q_weight=qw, k_weight=kw)
+        return out, *vs.cache_read_packed(kc, vc, slot[:n].contiguous())
+
+    long = call(1500)
+    for n in (1, 7, 400):
+        assert all(torch.equal(a, b[:n]) for a, b in zip(call(n), long))
+
+
 PACKED = [(1, 32, 8, 128, 128, 16), (1, 1, 1, 32, 2, 1), (7, 4, 2, 96, 32, 8), (33, 6, 3, 64, 22, 5), (2, 8, 8, 512, 512, 16),
           (311, 40, 8, 128, 64, 64), (700, 4, 1, 64, 32, 16), (9, 5, 5, 32, 0, 3), (64, 7, 1, 160, 24, 24), (40, 3, 2, 256, 256, 32),
           (700, 40, 8, 128, 128, 64), (2100, 32, 4, 128, 64, 16), (1500, 70, 5, 64, 64, 16), (1111, 9, 3, 256, 192, 16)]

@@ -185,6 +185,43 @@ def test_far_scales():
     _run(c)
 
 
+@pytest.mark.parametrize("n", [[2, 1], [30, 1]])
+@pytest.mark.parametrize("power", [-90, -30, 30, 90])
+def test_far_queries(n, power):
+    """Queries of any size, with the scale that makes their scores ordinary; rows of zeros among them."""
+    c = Case(n, [300, 700], 8, 2, 128, 16, BF, ((1, 100),))
+    c.q = c.q * 2.0 ** power
+    c.q[1] = 0
+    c.scale = c.scale * 2.0 ** -power if power > -90 else 1e26  # (2^90 / 11 is 1.1e26)
+    _run(c)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("n", [[3, 2], [30, 2]])
+def test_a_row_of_nan_stays_alone(n, bad):
+    c = Case(n, [300, 70], 8, 2, 128, 16, BF, ((2, 140),))
+    want, lse = _run(c)
+    c.q[1, 3, 5] = bad
+    got = c.call()
+    live = torch.ones(c.off[-1], 8, dtype=torch.bool, device="cuda")
+    live[1, 3] = False
+    assert torch.equal(got[:c.off[-1]][live], want[:c.off[-1]][live]) and bool(torch.isnan(got[1, 3]).any())
+
+
+@pytest.mark.parametrize("each,Hq,Hk", [(4, 64, 8), (1, 256, 2), (9, 64, 16)])
+def test_calls_of_many_rows_run_in_windows(each, Hq, Hk):
+    """More than 2^20 query rows: by the narrow kernel in several items a segment, or by both."""
+    R = (1 << 20) // Hq // each + 700
+    kv = [each + (i * 37) % 90 for i in range(R)]
+    c = Case([each] * R, kv, Hq, Hk, 64, 16, BF, ((R // 2, 130),) if each == 9 else ())
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got, lse = c.call(want_lse=True, status=st)
+    assert st.item() == 0
+    pick = sorted({0, 1, R // 3, R // 2 - 1, R // 2, R - 2, R - 1} | {(i * 7919) % R for i in range(60)} | {(1 << 19) // Hq // each + i for i in range(-3, 4)})
+    c.check(got, lse, pick)
+    assert bool(torch.isfinite(got[:c.off[-1]].float()).all())
+
+
 def test_rows_ahead_of_the_first_request():
     _run(Case([3, 2], [300, 40], 8, 2, 128, 16, BF, ((2, 150),), row0=5))
 

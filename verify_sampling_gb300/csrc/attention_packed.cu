@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, narrow_blocks(D, NB))
         }
         most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
         most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
-        const uint32_t e = most >> 23, up = e == 255u ? 127u : min(267u - e, 190u);  // exponent fields (a row with infinities: as it is)
+        const uint32_t e = most >> 23, up = e == 255u ? 127u : min(267u - e, 253u);  // exponent fields (a row with infinities: as it is)
         const float f = __uint_as_float(up << 23), back = __uint_as_float((254u - up) << 23);
         auto low = [&](uint32_t x) { return __uint_as_float(x << 16) * f; };
         auto high = [&](uint32_t x) { return __uint_as_float(x & 0xffff0000u) * f; };
@@ -620,9 +620,11 @@ cudaError_t launch(const spec_prefix_attention_args& a, const q4::Cache& packed,
 template <int D>
 cudaError_t launch(const spec_prefix_attention_args& a, const q4::Cache& packed, int sms, const PackedWork& work, cudaStream_t stream) {
   const int64_t m = (int64_t)a.rows * (a.Hq / a.Hk), R = a.R;  // query rows of a key head
-  // The narrow kernel alone for requests of few rows without a prefix; otherwise the wide
-  // one takes the segments of more than kNarrowMost rows before it.
-  const bool both = a.G > 0 || m > kNarrowMost * R;
+  // The narrow kernel alone where no segment has more than kNarrowMost query rows, or where requests without
+  // a prefix have few; otherwise the wide one takes the segments of more before it.  (256 requests of
+  // 1024 keys, 8 heads a key head: 1 or 2 rows a request 162 us by the narrow kernel alone, 170 by
+  // both; 1 to 4 rows 246 and 224; 1 to 12 rows 541 and 253, with 32 rows for 16 as the border 261.)
+  const bool both = m > kNarrowMost && (a.G > 0 || m > kNarrowMost * R);
   // 16 rows an item cost 1.45 times 8 (D = 128: 256 requests of 4096 keys 461 us and 318) or 1.22 times (D = 64: 101
   // requests of 1500 keys 54 us and 44), but read the keys of a request of 9 to 16 rows once: where a
   // request has several rows, some have more than the mean.
