@@ -1,12 +1,14 @@
 """Rounds of speculative decoding around a small target model with a paged cache.
 
-    python examples/target_step.py [rounds]
+    python examples/target_step.py [rounds] [--packed]
 
 Each round, without a host synchronisation: draft, schedule, cache slots for the
 scheduled rows (cache_reserve), rotary positions and the cache write (rope_cache),
 attention over a system prompt that all requests share and each request's own pages
 (prefix_attention), penalties and a grammar mask on the packed logits
 (adjust_logits), verification, and the kept lengths and freed pages (cache_commit).
+With --packed the target norms its heads of queries and keys and its cache is held in 4 bits
+(norm_rope_cache, prefix_attention_packed).
 The target is one attention layer between random embeddings and a random output
 matrix: it stands in for a real one, whose other layers change nothing here.
 """
@@ -29,8 +31,9 @@ class TargetStep:
     """R requests behind one shared prefix; ``tokens`` are each request's own tokens so far (``length`` of them,
     ``prompt_len`` of those the prompt).  All but a request's last token are in the cache, which has pages for
     ``room`` tokens a request: one whose next rows do not fit is refused by cache_reserve and stays as it is."""
+    packed = False  # head norms and a cache in 4 bits
 
-    def __init__(self, R=6, gamma=4, V=1000, Hq=8, Hk=2, D=64, page_size=16, prefix=75, prompt=9, room=400, seed=0):
+    def __init__(self, R=6, gamma=4, V=1000, Hq=8, Hk=2, D=64, page_size=16, prefix=75, prompt=9, room=400, seed=0, packed=False):
         dev, g = "cuda", torch.Generator("cuda").manual_seed(seed)
         self.R, self.gamma, self.V, self.Hq, self.Hk, self.D, self.P = R, gamma, V, Hq, Hk, D, page_size
         wl = synth.WORKLOADS["tiny"].scaled(R=R, gamma=gamma, V=V)
@@ -50,8 +53,13 @@ class TargetStep:
         own = -(-room // page_size)
         self.prefix_pages = -(-prefix // page_size)
         n_pages = self.prefix_pages + R * own
-        self.k_cache = torch.zeros(n_pages, page_size, Hk, D, dtype=BF16, device=dev)
-        self.v_cache = torch.zeros_like(self.k_cache)
+        self.packed = packed
+        if packed:
+            self.k_cache, self.v_cache = (vs.packed_cache(n_pages, page_size, Hk, D, dev) for _ in range(2))
+            self.q_weight, self.k_weight = (1 + 0.2 * torch.randn(D, generator=g, device=dev) for _ in range(2))
+        else:
+            self.k_cache = torch.zeros(n_pages, page_size, Hk, D, dtype=BF16, device=dev)
+            self.v_cache = torch.zeros_like(self.k_cache)
         self.cache = vs.cache_tables(R, n_pages, page_size, own, dev)
         self.cache["ring_pos"][0] = self.prefix_pages
         self.prefix_tokens = torch.randint(0, V, (prefix,), generator=g, device=dev, dtype=I32)
@@ -87,10 +95,18 @@ class TargetStep:
         go to the cache."""
         h = self.embed[tokens.long()]
         qkv = (h @ self.w_qkv).view(len(h), self.Hq + 2 * self.Hk, self.D)
-        q = vs.rope_cache(qkv[:, :self.Hq], qkv[:, self.Hq:self.Hq + self.Hk], qkv[:, self.Hq + self.Hk:], self.freq, position,
-                          slot, self.k_cache, self.v_cache, scale=self.rope_scale, status=self.status,
-                          q_out=torch.zeros(len(h), self.Hq, self.D, dtype=BF16, device=h.device))
-        return h, q
+        args = (qkv[:, :self.Hq], qkv[:, self.Hq:self.Hq + self.Hk], qkv[:, self.Hq + self.Hk:], self.freq, position, slot,
+                self.k_cache, self.v_cache)
+        more = dict(scale=self.rope_scale, status=self.status, q_out=torch.zeros(len(h), self.Hq, self.D, dtype=BF16, device=h.device))
+        if self.packed:
+            return h, vs.norm_rope_cache(*args, q_weight=self.q_weight, k_weight=self.k_weight, **more)
+        return h, vs.rope_cache(*args, **more)
+
+    def _attend(self, q, row_off, new_len):
+        """The rows' attention over the shared prefix and their requests' own pages."""
+        attention = vs.prefix_attention_packed if self.packed else vs.prefix_attention
+        return attention(q, self.k_cache, self.v_cache, row_off, new_len, self.cache["block_table"], group_off=self.group_off,
+                         prefix_len=self.prefix_len, prefix_table=self.prefix_table, status=self.status)
 
     def round(self, seed: int) -> dict:
         R, G1 = self.R, self.gamma + 1
@@ -104,8 +120,7 @@ class TargetStep:
         j = torch.arange(rows, device=req.device) - s["row_off"].long()[req]
         fed = torch.cat([self.x0[:, None], d["x"]], 1)[req, j.clamp(0, self.gamma)]
         h, q = self._project(fed, r["position"], r["slot"])
-        o = vs.prefix_attention(q, self.k_cache, self.v_cache, s["row_off"], r["new_len"], self.cache["block_table"],
-                                group_off=self.group_off, prefix_len=self.prefix_len, prefix_table=self.prefix_table, status=self.status)
+        o = self._attend(q, s["row_off"], r["new_len"])
         raw = ((h + o.flatten(1) @ self.w_out) @ self.w_head).float()
         logits = vs.adjust_logits(raw, self.tokens, self.prompt_len, self.length, row_off=s["row_off"], x=d["x"], mask=self.mask,
                                   mask_row=self.mask_row, status=self.status, **self.penalty)
@@ -125,8 +140,9 @@ class TargetStep:
 
 
 def main() -> None:
-    rounds = int(sys.argv[1]) if len(sys.argv) > 1 else 20
-    step = TargetStep()
+    numbers = [int(a) for a in sys.argv[1:] if a != "--packed"]
+    rounds = numbers[0] if numbers else 20
+    step = TargetStep(packed="--packed" in sys.argv)
     for t in range(rounds):
         step.round(t)
     torch.cuda.synchronize()
