@@ -145,10 +145,11 @@ def _here(t: torch.Tensor, name: str) -> None:
         raise ValueError(f"{name} must lie on the current device")
 
 
-def _t(t: torch.Tensor, name: str, dtype: torch.dtype, numel: int = 0) -> int:
-    """Address of a contiguous tensor of the current device, of this dtype (and at least numel entries)."""
+def _t(t: torch.Tensor, name: str, dtype: torch.dtype, numel: int = 0, dev: Optional[int] = None) -> int:
+    """Address of a contiguous tensor of the current device (``dev``, where the caller has asked for it), of this dtype
+    (and at least numel entries)."""
     # (a host tensor's device is -1)
-    if isinstance(t, _Tensor) and t.get_device() == _device() and t.dtype is dtype and t.is_contiguous():
+    if isinstance(t, _Tensor) and t.get_device() == (_device() if dev is None else dev) and t.dtype is dtype and t.is_contiguous():
         if not numel or t.numel() >= numel:
             return t.data_ptr()
     _here(t, name)
@@ -158,8 +159,8 @@ def _t(t: torch.Tensor, name: str, dtype: torch.dtype, numel: int = 0) -> int:
     raise ValueError(f"{name} must have {numel} entries")
 
 
-def _opt(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, numel: int = 0) -> int:
-    return 0 if t is None else _t(t, name, dtype, numel)
+def _opt(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, numel: int = 0, dev: Optional[int] = None) -> int:
+    return 0 if t is None else _t(t, name, dtype, numel, dev)
 
 
 def _code(t: torch.Tensor) -> int:
@@ -292,9 +293,9 @@ def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: str = "none", 
     return f.to(device), scale
 
 
-def _strided(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) -> tuple:
+def _strided(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: Optional[int] = None) -> tuple:
     """Address and the row and head strides of [rows, heads, D] whose last dimension is dense."""
-    if not isinstance(t, _Tensor) or t.get_device() != _device():
+    if not isinstance(t, _Tensor) or t.get_device() != (_device() if dev is None else dev):
         _here(t, name)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
@@ -350,17 +351,17 @@ def packed_cache(n_pages: int, page_size: int, Hk: int, D: int, device="cuda") -
             torch.zeros(n_pages, Hk, page_size, D // 32, dtype=_u8, device=device))
 
 
-def _packed(cache: tuple, name: str, Hk: Optional[int], D: int) -> tuple:
-    """Addresses of an packed cache's data and scales, and its pages, page size and key heads."""
+def _packed(cache: tuple, name: str, Hk: Optional[int], D: int, dev: int) -> tuple:
+    """Addresses of a packed cache's data and scales, and its pages, page size and key heads."""
     data, scale = cache
     if not isinstance(data, _Tensor) or not isinstance(scale, _Tensor):
         raise TypeError(f"{name} must be a pair of tensors")
-    if data.dim() != 5 or (Hk is not None and data.shape[1] != Hk):
-        raise ValueError(f"{name} must be the data [pages, Hk, D / 32, page_size, 16] and scales [pages, Hk, page_size, D / 32]")
-    n, heads, groups, P, width = data.shape
-    if groups * 32 != D or width != 16 or scale.shape != (n, heads, P, groups):
-        raise ValueError(f"{name} must be the data [pages, Hk, D / 32, page_size, 16] and scales [pages, Hk, page_size, D / 32]")
-    return _t(data, name, _u8), _t(scale, f"{name} scales", _u8), n, P, heads
+    shape = data.shape
+    if len(shape) == 5:
+        n, heads, groups, P, width = shape
+        if groups * 32 == D and width == 16 and (Hk is None or heads == Hk) and scale.shape == (n, heads, P, groups):
+            return _t(data, name, _u8, 0, dev), _t(scale, f"{name} scales", _u8, 0, dev), n, P, heads
+    raise ValueError(f"{name} must be the data [pages, Hk, D / 32, page_size, 16] and scales [pages, Hk, page_size, D / 32]")
 
 
 def norm_rope_cache(q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Tensor],
@@ -372,38 +373,38 @@ def norm_rope_cache(q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torc
     square, times ``q_weight`` and ``k_weight`` [D] float32; None: no norm).  The caches are tensors [pages, page_size,
     Hk, D] as there, or both pairs of ``packed_cache``: then keys and values are stored in 4 bits."""
     rows, Hq, D = shape = q.shape
-    dt = q.dtype
-    qp, qr, qh = _strided(q, "q", dt, shape)
+    dt, dev = q.dtype, _device()
+    qp, qr, qh = _strided(q, "q", dt, shape, dev)
     if q_out is None:
         with _made(stream):
             q_out = torch.empty(shape, dtype=dt, device=q.device)
         op, orow, oh = q_out.data_ptr(), Hq * D, D
     else:
-        op, orow, oh = _strided(q_out, "q_out", dt, shape)
+        op, orow, oh = _strided(q_out, "q_out", dt, shape, dev)
     Hk = P = n_slots = sp = kc = vc = ks = vs = kp = vp = kr = kh = vr = vh = kind = 0
     if k is not None:
         Hk = k.shape[1]
-        kp, kr, kh = _strided(k, "k", dt, (rows, Hk, D))
-        vp, vr, vh = _strided(v, "v", dt, (rows, Hk, D))
+        kp, kr, kh = _strided(k, "k", dt, (rows, Hk, D), dev)
+        vp, vr, vh = _strided(v, "v", dt, (rows, Hk, D), dev)
         if isinstance(k_cache, tuple) != isinstance(v_cache, tuple):
             raise ValueError("k_cache and v_cache must be of one kind")
         if isinstance(k_cache, tuple):
             kind = 1
-            kc, ks, n, P, _ = _packed(k_cache, "k_cache", Hk, D)
-            vc, vs, n2, P2, _ = _packed(v_cache, "v_cache", Hk, D)
+            kc, ks, n, P, _ = _packed(k_cache, "k_cache", Hk, D, dev)
+            vc, vs, n2, P2, _ = _packed(v_cache, "v_cache", Hk, D, dev)
             if (n, P) != (n2, P2):
                 raise ValueError("k_cache and v_cache must have the same pages")
             n_slots = n * P
         else:
             if k_cache.dim() != 4 or k_cache.shape[2:] != (Hk, D) or v_cache.shape != k_cache.shape:
                 raise ValueError("k_cache and v_cache must both be [pages, page_size, Hk, D]")
-            kc, vc = _t(k_cache, "k_cache", dt), _t(v_cache, "v_cache", dt)
+            kc, vc = _t(k_cache, "k_cache", dt, 0, dev), _t(v_cache, "v_cache", dt, 0, dev)
             n_slots = k_cache.shape[0] * k_cache.shape[1]
-        sp = _t(slot, "slot", _i32, rows)
+        sp = _t(slot, "slot", _i32, rows, dev)
     _NORM_ROPE(_on(stream, q), rows, Hq, Hk, D, 2 * freq.numel(), _code(q), int(interleaved), kind, P, scale, eps,
                qp, kp, vp, qr, qh, kr, kh, vr, vh, op, orow, oh, kc, vc, ks, vs, n_slots,
-               _opt(q_weight, "q_weight", _f32, D), _opt(k_weight, "k_weight", _f32, D), _t(freq, "freq", _f64),
-               _t(position, "position", _i32, rows), sp, _opt(status, "status", _i32, 1))
+               _opt(q_weight, "q_weight", _f32, D, dev), _opt(k_weight, "k_weight", _f32, D, dev), _t(freq, "freq", _f64, 0, dev),
+               _t(position, "position", _i32, rows, dev), sp, _opt(status, "status", _i32, 1, dev))
     return q_out
 
 
@@ -411,23 +412,27 @@ def cache_read_packed(k_cache: tuple, v_cache: tuple, slot: torch.Tensor, *, dty
                     out: Optional[tuple] = None, status: Optional[torch.Tensor] = None, stream=None) -> tuple:
     """spec_cache_read_packed: what the slots of two ``packed_cache`` pairs stand for, (k, v) [rows, Hk, D] of ``dtype``
     (exact in bfloat16 and float32), zeros where a slot is negative or past the cache."""
-    rows = slot.numel()
+    rows, dev = slot.numel(), _device()
     D = k_cache[0].shape[2] * 32 if isinstance(k_cache[0], _Tensor) and k_cache[0].dim() == 5 else 0
-    kc, ks, n, P, Hk = _packed(k_cache, "k_cache", None, D)
-    vc, vs, n2, P2, _ = _packed(v_cache, "v_cache", Hk, D)
+    kc, ks, n, P, Hk = _packed(k_cache, "k_cache", None, D, dev)
+    vc, vs, n2, P2, _ = _packed(v_cache, "v_cache", Hk, D, dev)
     if (n, P) != (n2, P2):
         raise ValueError("k_cache and v_cache must have the same pages")
+    at = _t(slot, "slot", _i32, 0, dev)
     if out is None:
         if dtype not in _codes:
             raise TypeError("dtype must be float32 or bfloat16")
         with _made(stream):
-            out = tuple(torch.empty((rows, Hk, D), dtype=dtype, device=slot.device) for _ in range(2))
-    k, v = out
-    if k.dtype is not v.dtype or k.shape != (rows, Hk, D) or v.shape != k.shape:
-        raise ValueError("out must be two tensors [rows, Hk, D] of one dtype")
-    _READ_PACKED(_on(stream, slot), rows, Hk, D, P, _code(k), kc, vc, ks, vs, n * P, _t(slot, "slot", _i32),
-               _t(k, "out k", k.dtype), _t(v, "out v", v.dtype), _opt(status, "status", _i32, 1))
-    return out
+            k = torch.empty((rows, Hk, D), dtype=dtype, device=slot.device)
+            v = torch.empty((rows, Hk, D), dtype=dtype, device=slot.device)
+        kp, vp = k.data_ptr(), v.data_ptr()
+    else:
+        k, v = out
+        if k.dtype is not v.dtype or k.shape != (rows, Hk, D) or v.shape != k.shape:
+            raise ValueError("out must be two tensors [rows, Hk, D] of one dtype")
+        kp, vp = _t(k, "out k", k.dtype, 0, dev), _t(v, "out v", v.dtype, 0, dev)
+    _READ_PACKED(_on(stream, slot), rows, Hk, D, P, _code(k), kc, vc, ks, vs, n * P, at, kp, vp, _opt(status, "status", _i32, 1, dev))
+    return k, v
 
 
 # -------------------------------------------------- shared-prefix attention --
@@ -503,32 +508,30 @@ def prefix_attention_packed(q: torch.Tensor, k_cache: tuple, v_cache: tuple, row
                           workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
     """spec_prefix_attention_packed: ``prefix_attention`` over two ``packed_cache`` pairs."""
     rows, Hq, D = shape = q.shape
-    dt = q.dtype
-    kc, ks, n_pages, P, Hk = _packed(k_cache, "k_cache", None, D)
-    vc, vs, n2, P2, _ = _packed(v_cache, "v_cache", Hk, D)
+    dt, dev = q.dtype, _device()
+    kc, ks, n_pages, P, Hk = _packed(k_cache, "k_cache", None, D, dev)
+    vc, vs, n2, P2, _ = _packed(v_cache, "v_cache", Hk, D, dev)
     if (n_pages, P) != (n2, P2):
         raise ValueError("k_cache and v_cache must have the same pages")
     R, width = block_table.shape
-    prefixes = _prefixes(group_off, prefix_len, prefix_table)
-    strides = _strided(q, "q", dt, shape)
-    dev = q.device
+    G, pages, go, pl, pt = _prefixes(group_off, prefix_len, prefix_table)
+    strides = _strided(q, "q", dt, shape, dev)
     if workspace is not None:
         _here(workspace, "workspace")
     with _made(stream):
         made = out is None
         if made:
-            out = torch.empty(shape, dtype=dt, device=dev)
+            out = torch.empty(shape, dtype=dt, device=q.device)
         if want_lse and lse is None:
-            lse = torch.empty((rows, Hq), dtype=_f32, device=dev)
+            lse = torch.empty((rows, Hq), dtype=_f32, device=q.device)
         if workspace is None:
-            workspace = torch.empty(attention_packed_workspace_bytes(rows, R, Hq, D), dtype=torch.uint8, device=dev)
-    G, pages, go, pl, pt = prefixes
+            workspace = torch.empty(attention_packed_workspace_bytes(rows, R, Hq, D), dtype=_u8, device=q.device)
     _ATTENTION_PACKED(_on(stream, q), R, rows, Hq, Hk, D, _code(q), P, n_pages, width, G, pages,
-                    D ** -0.5 if scale is None else scale, *strides, kc, vc, _t(row_off, "row_off", _i32, R + 1),
-                    _t(kv_len, "kv_len", _i32, R), _t(block_table, "block_table", _i32), go, pl, pt,
-                    *((out.data_ptr(), Hq * D, D) if made else _strided(out, "out", dt, shape)),
-                    _opt(lse, "lse", _f32, rows * Hq), _dev(workspace, "workspace").data_ptr(),
-                    workspace.numel() * workspace.element_size(), _opt(status, "status", _i32, 1), ks, vs)
+                      D ** -0.5 if scale is None else scale, *strides, kc, vc, _t(row_off, "row_off", _i32, R + 1, dev),
+                      _t(kv_len, "kv_len", _i32, R, dev), _t(block_table, "block_table", _i32, 0, dev), go, pl, pt,
+                      *((out.data_ptr(), Hq * D, D) if made else _strided(out, "out", dt, shape, dev)),
+                      _opt(lse, "lse", _f32, rows * Hq, dev), _dev(workspace, "workspace").data_ptr(),
+                      workspace.numel() * workspace.element_size(), _opt(status, "status", _i32, 1, dev), ks, vs)
     return (out, lse) if want_lse else out
 
 
