@@ -287,10 +287,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 // ----------------------------------------------------------------- join ----
 constexpr int kJoinThreads = 128;
+constexpr int kFewRows = 152 * 8;  // query rows of a call whose join has a block for each
 constexpr int kJoinBlocks = 152 * 16;
 constexpr int kJoinRows = 64;  // query rows (packed rows x heads of a key head) of a block at a time
 
 constexpr int kJoinLanes = 16;  // threads of a row
+constexpr int join_rows(int share) { return share > 1 ? 1 : kJoinRows; }  // of a block at a time
 
 // Cost of a head's items before item `upto`, and of all of them; a row's threads add them up.
 template <class C>
@@ -322,11 +324,15 @@ struct Pieces {  // what a kernel leaves
   const float2* stat;
   const int64_t* plan;
 };
-template <int D, class C, class N>
+// kShare: half-warps that share a row's pieces (all of a block's or one).
+template <int D, int kShare, class C, class N>
 __device__ __forceinline__ void join_request(const spec_prefix_attention_args& a, const Window& w, int r, const Pieces& wide,
                                              const Pieces& narrow) {
-  constexpr int kPer = D / kJoinLanes, kBatch = 4;
+  constexpr int kPer = D / kJoinLanes, kBatch = 4, kHalves = kJoinThreads / kJoinLanes;
+  constexpr int kTileRows = join_rows(kShare);
+  static_assert(kShare == 1 || kShare == kHalves, "a block's half-warps");
   const int lane = threadIdx.x % kJoinLanes, per_head = a.Hq / a.Hk;
+  const int share = kShare > 1 ? threadIdx.x / kJoinLanes : 0;
   uint32_t bad = 0;
   const Segment own = segment(a, w, a.G + r, &bad);
   int g = group_of(a, r, &bad);
@@ -344,7 +350,7 @@ __device__ __forceinline__ void join_request(const spec_prefix_attention_args& a
   const int64_t own_per = from_own.plan[0], pre_per = from_pre.plan[0];
   const int64_t own_at = from_own.plan[1 + a.G + r], pre_at = g >= 0 ? from_pre.plan[1 + g] : 0;
 
-  const int tiles = (m_own + kJoinRows - 1) / kJoinRows, all_tiles = tiles * a.Hk;
+  const int tiles = (m_own + kTileRows - 1) / kTileRows, all_tiles = tiles * a.Hk;
   int item[2] = {-1, -1}, head = -1;  // own and prefix item, and key head, whose pieces are known
   int64_t before[2] = {0, 0}, all[2] = {0, 0};
   int first[2] = {0, 0}, count[2] = {0, 0};
@@ -370,10 +376,10 @@ __device__ __forceinline__ void join_request(const spec_prefix_attention_args& a
 
 #pragma unroll 1
   for (int x = blockIdx.y; x < all_tiles; x += gridDim.y) {
-    const int h = x / tiles, m0 = (x - h * tiles) * kJoinRows;
+    const int h = x / tiles, m0 = (x - h * tiles) * kTileRows;
     const size_t own_slot = ((size_t)(w.hi - w.lo) + (own.row0 - w.lo)) * a.Hq + (size_t)h * m_own;
     const size_t pre_slot = (size_t)(pre.row0 - w.lo) * a.Hq + (size_t)h * pre.n * per_head + m_off;
-    for (int m = m0 + threadIdx.x / kJoinLanes; m < min(m0 + kJoinRows, m_own); m += kJoinThreads / kJoinLanes) {
+    for (int m = m0 + (kShare > 1 ? 0 : threadIdx.x / kJoinLanes); m < min(m0 + kTileRows, m_own); m += kHalves / kShare) {
       find(own_n, 0, own, own_at, own_per, h, m);
       if (g >= 0) find(pre_n, 1, pre, pre_at, pre_per, h, m_off + m);
       head = h;
@@ -388,7 +394,7 @@ __device__ __forceinline__ void join_request(const spec_prefix_attention_args& a
 #pragma unroll
       for (int d = 0; d < kPer; ++d) o[d] = 0.f;
 #pragma unroll 1
-      for (int p0 = 0; p0 < n; p0 += kBatch) {
+      for (int p0 = share * kBatch; p0 < n; p0 += kShare * kBatch) {
         float2 st[kBatch];
         float v[kBatch][kPer];
 #pragma unroll
@@ -421,6 +427,31 @@ __device__ __forceinline__ void join_request(const spec_prefix_attention_args& a
         }
         top = m_new;
       }
+      if (kShare > 1) {  // the half-warps' sums, by the first of them
+        __shared__ __align__(16) float o_s[kHalves][D];
+        __shared__ float2 stat_s[kHalves];
+        __syncthreads();  // the last row's are read
+#pragma unroll
+        for (int d = 0; d < kPer; ++d) o_s[share][lane * kPer + d] = o[d];
+        if (lane == 0) stat_s[share] = make_float2(top, sum);
+        __syncthreads();
+        if (share > 0) continue;
+        float m_all = top;
+#pragma unroll
+        for (int x = 1; x < kHalves; ++x) m_all = fmaxf(m_all, stat_s[x].x);
+        const float c = top == -CUDART_INF_F ? 0.f : tc::ex2(top - m_all);
+        sum *= c;
+#pragma unroll
+        for (int d = 0; d < kPer; ++d) o[d] *= c;
+#pragma unroll
+        for (int x = 1; x < kHalves; ++x) {
+          const float w = stat_s[x].x == -CUDART_INF_F ? 0.f : tc::ex2(stat_s[x].x - m_all);
+          sum = fmaf(stat_s[x].y, w, sum);
+#pragma unroll
+          for (int d = 0; d < kPer; ++d) o[d] = fmaf(o_s[x][lane * kPer + d], w, o[d]);
+        }
+        top = m_all;
+      }
       const int j = m / per_head, b = own.row0 + j, hq = h * per_head + (m - j * per_head);
       const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row without keys: zeros
       __nv_bfloat16* out = (__nv_bfloat16*)a.out + (size_t)b * a.out_row + (size_t)hq * a.out_head + lane * kPer;
@@ -442,12 +473,12 @@ __device__ __forceinline__ void join_request(const spec_prefix_attention_args& a
 
 // Where the window is a part of the rows (kPart), the blocks share out its requests, from
 // the first to the last that has rows in it; otherwise there is a block for each.
-template <int D, bool kPart, class C, class N>
+template <int D, bool kPart, int kShare, class C, class N>
 __global__ void __launch_bounds__(kJoinThreads, 4)
     join_pieces_kernel(const spec_prefix_attention_args a, const Window w, const Pieces wide, const Pieces narrow) {
   int r = blockIdx.x;
   if (!kPart) {
-    join_request<D, C, N>(a, w, r, wide, narrow);
+    join_request<D, kShare, C, N>(a, w, r, wide, narrow);
     return;
   }
   __shared__ int first_s, last_s;
@@ -464,15 +495,15 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
     atomicMax(&last_s, last);
   }
   __syncthreads();
-  for (r += first_s; r <= last_s; r += gridDim.x) join_request<D, C, N>(a, w, r, wide, narrow);
+  for (r += first_s; r <= last_s; r += gridDim.x) join_request<D, kShare, C, N>(a, w, r, wide, narrow);
   tc::grid_dep_wait();  // a block without requests, too, ends after the pieces' kernel
 }
 
 // Blocks of the join for a call's rows in `windows` windows.
-inline dim3 join_grid(const spec_prefix_attention_args& a, int windows) {
+inline dim3 join_grid(const spec_prefix_attention_args& a, int windows, int tile_rows) {
   // a block a tile of the mean request, until there are kJoinBlocks of them
   const int per_head = a.Hq / a.Hk;
-  const int64_t tiles = (((int64_t)a.rows * per_head + (int64_t)kJoinRows * a.R - 1) / ((int64_t)kJoinRows * a.R)) * a.Hk;
+  const int64_t tiles = (((int64_t)a.rows * per_head + (int64_t)tile_rows * a.R - 1) / ((int64_t)tile_rows * a.R)) * a.Hk;
   const int at_once = std::min(a.R, (a.R + windows - 1) / windows + (windows > 1));  // requests of a window
   const int64_t most = (kJoinBlocks + at_once - 1) / at_once;
   return dim3(at_once, (unsigned)(tiles < most ? tiles : most));
@@ -482,7 +513,11 @@ template <int D, class C, class N>
 cudaError_t launch_join(const spec_prefix_attention_args& a, const Window& w, int windows, const Pieces& wide, const Pieces& narrow,
                         cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = join_grid(a, windows);
+  // Few rows over a packed cache have many pieces each: a block shares them (one row of 20001 keys, 32 heads on 8:
+  // 57 pieces a row, 21.4 us with a row a half-warp, 15.8 with a row a block).
+  const bool few = C::kShared && windows == 1 && (int64_t)a.rows * a.Hq <= kFewRows;
+  constexpr int kHalves = C::kShared ? kJoinThreads / kJoinLanes : 1;
+  cfg.gridDim = join_grid(a, windows, join_rows(few ? kHalves : 1));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -490,7 +525,11 @@ cudaError_t launch_join(const spec_prefix_attention_args& a, const Window& w, in
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, windows > 1 ? join_pieces_kernel<D, true, C, N> : join_pieces_kernel<D, false, C, N>, a, w, wide, narrow);
+  return cudaLaunchKernelEx(&cfg,
+                            windows > 1 ? join_pieces_kernel<D, true, 1, C, N>
+                            : few       ? join_pieces_kernel<D, false, kHalves, C, N>
+                                        : join_pieces_kernel<D, false, 1, C, N>,
+                            a, w, wide, narrow);
 }
 
 }  // namespace
