@@ -622,8 +622,8 @@ size_t spec_attention_workspace_bytes(int rows, int R, int Hq, int D);
  * stored as 0, an infinity as +-7 s with the largest s.
  *   data    [n_pages, Hk, D / 32, page_size, 16] bytes, 16-byte aligned
  *   scales  [n_pages, Hk, page_size, D / 32] bytes
- * D is a multiple of 32 (SPEC_ERR_UNSUPPORTED).  Slots are those of
- * spec_cache_reserve: page * page_size + place.
+ * D is a multiple of 32 and a page's data, page_size * Hk * D / 2 bytes, are below 2^31
+ * (SPEC_ERR_UNSUPPORTED).  Slots are those of spec_cache_reserve: page * page_size + place.
  *
  * spec_norm_rope_cache: spec_rope_cache for models that norm each head of queries
  * and keys first, and for either kind of cache.  With a weight w [D] (f32) a head x is

@@ -73,14 +73,14 @@ def test_norm_rope_refuses(lib):
               ({"q": 4096, "q_out": 4096, "q_row": 512, "q_out_row": 1024}, BAD), ({"rows": 0}, vs.SPEC_OK), ({"Hq": 0, "Hk": 0}, vs.SPEC_OK)]
     _refusals(lib.spec_norm_rope_cache, NORM, sizes, common)
     _refusals(lib.spec_norm_rope_cache, NORM, {**sizes, "cache": 1, "page_size": 16}, common + [
-        ({"D": 80, "rot": 80}, UNSUP), ({"page_size": 0}, BAD), ({"page_size": 17}, BAD), ({"k_scale": None}, BAD), ({"v_scale": None}, BAD),
+        ({"D": 80, "rot": 80}, UNSUP), ({"page_size": 1 << 25, "n_slots": 1 << 26}, UNSUP), ({"page_size": 0}, BAD), ({"page_size": 17}, BAD), ({"k_scale": None}, BAD), ({"v_scale": None}, BAD),
         ({"k_cache": 4104}, ALIGN), ({"v_cache": 4097}, ALIGN)])
 
 
 def test_cache_read_refuses(lib):
     _refusals(lib.spec_cache_read_packed, READ, dict(rows=4, Hk=2, D=64, page_size=16, n_slots=96), [
         ({"rows": -1}, BAD), ({"Hk": 0}, BAD), ({"Hk": 1025}, BAD), ({"D": 0}, BAD), ({"D": 80}, UNSUP), ({"D": 544}, UNSUP), ({"page_size": 0}, BAD),
-        ({"page_size": 7}, BAD), ({"n_slots": -16}, BAD), ({"dtype": 2}, BAD), ({"slot": None}, BAD), ({"k_cache": None}, BAD),
+        ({"page_size": 1 << 25, "n_slots": 1 << 26}, UNSUP), ({"page_size": 7}, BAD), ({"n_slots": -16}, BAD), ({"dtype": 2}, BAD), ({"slot": None}, BAD), ({"k_cache": None}, BAD),
         ({"v_scale": None}, BAD), ({"k_cache": 4104}, ALIGN), ({"slot": 4098}, ALIGN), ({"v": 4100}, ALIGN), ({"status": 4098}, ALIGN),
         ({"rows": 0}, vs.SPEC_OK), ({"k": None, "v": None}, vs.SPEC_OK)])
 
@@ -94,7 +94,7 @@ def test_attention_refuses(lib):
                  workspace_bytes=need)
     _refusals(lib.spec_prefix_attention_packed, ATTN, sizes, [
         ({"R": -1}, BAD), ({"R": 65536}, BAD), ({"rows": -1}, BAD), ({"Hq": 0}, BAD), ({"Hq": 7}, BAD), ({"Hk": 0}, BAD), ({"Hq": 1026}, BAD),
-        ({"D": 0}, BAD), ({"D": 257}, UNSUP), ({"D": 80}, UNSUP), ({"dtype": 3}, BAD), ({"page_size": 0}, BAD), ({"n_pages": 0}, BAD),
+        ({"D": 0}, BAD), ({"D": 257}, UNSUP), ({"D": 80}, UNSUP), ({"page_size": 1 << 25, "n_pages": 2}, UNSUP), ({"dtype": 3}, BAD), ({"page_size": 0}, BAD), ({"n_pages": 0}, BAD),
         ({"max_pages": 0}, BAD), ({"G": -1}, BAD), ({"G": 5}, BAD), ({"max_prefix_pages": 0}, BAD), ({"scale": 0.0}, BAD),
         ({"scale": float("nan")}, BAD), ({"q": None}, BAD), ({"k_cache": None}, BAD), ({"out": None}, BAD), ({"row_off": None}, BAD),
         ({"kv_len": None}, BAD), ({"block_table": None}, BAD), ({"group_off": None}, BAD), ({"k_scale": None}, BAD), ({"v_scale": None}, BAD),

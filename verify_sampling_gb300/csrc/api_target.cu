@@ -135,7 +135,7 @@ int spec_prefix_attention_packed(const spec_prefix_attention_packed_args* args, 
   spec_prefix_attention_args a = args->attention;
   int rc = check_attention(a, 16);
   if (rc != SPEC_OK && rc != kNothing) return rc;
-  if (a.D % q4::kGroup != 0) return SPEC_ERR_UNSUPPORTED;
+  if (a.D % q4::kGroup != 0 || !q4::page_fits(a.page_size, a.Hk, a.D)) return SPEC_ERR_UNSUPPORTED;
   if (rc == kNothing) return SPEC_OK;
   if (!args->k_scale || !args->v_scale) return SPEC_ERR_INVALID_ARG;
   rc = check_workspace(a.workspace, a.workspace_bytes, spec_attention_packed_workspace_bytes(a.rows, a.R, a.Hq, a.D));
@@ -205,7 +205,7 @@ int spec_norm_rope_cache(const spec_norm_rope_args* args, spec_stream_t stream) 
       (a.cache != SPEC_CACHE_DTYPE && a.cache != SPEC_CACHE_PACKED) || !(a.eps >= 0.f) || !(a.eps <= FLT_MAX))
     return SPEC_ERR_INVALID_ARG;
   const bool packed = a.cache == SPEC_CACHE_PACKED;
-  if (a.D > kNormRopeMaxDim || (packed && a.D % q4::kGroup != 0)) return SPEC_ERR_UNSUPPORTED;
+  if (a.D > kNormRopeMaxDim || (packed && (a.D % q4::kGroup != 0 || !q4::page_fits(a.page_size, a.Hk, a.D)))) return SPEC_ERR_UNSUPPORTED;
   if (a.Hk == 0) {
     a.k = a.v = nullptr;
     a.k_cache = a.v_cache = nullptr;
@@ -244,7 +244,7 @@ int spec_cache_read_packed(const spec_cache_read_packed_args* args, spec_stream_
   if (a.rows < 0 || a.Hk < 1 || a.Hk > 1024 || a.D < 1 || a.page_size < 1 || !valid_dtype(a.dtype) || a.n_slots < 0 ||
       a.n_slots % a.page_size != 0)
     return SPEC_ERR_INVALID_ARG;
-  if (a.D > kNormRopeMaxDim || a.D % q4::kGroup != 0) return SPEC_ERR_UNSUPPORTED;
+  if (a.D > kNormRopeMaxDim || a.D % q4::kGroup != 0 || !q4::page_fits(a.page_size, a.Hk, a.D)) return SPEC_ERR_UNSUPPORTED;
   if (a.rows == 0 || (!a.k && !a.v)) return SPEC_OK;
   if (!a.slot || (a.k && (!a.k_cache || !a.k_scale)) || (a.v && (!a.v_cache || !a.v_scale))) return SPEC_ERR_INVALID_ARG;
   if (!aligned(a.k_cache, 16) || !aligned(a.v_cache, 16) || !aligned(a.slot, 4) || !aligned(a.k, 16) || !aligned(a.v, 16) ||

@@ -635,10 +635,9 @@ cudaError_t launch(const spec_prefix_attention_args& a, const q4::Cache& packed,
 
 }  // namespace
 
-// bf16 heads of 64 or 128, pages that tile 128 keys and are below 2 GB, rows, data and scales on 16 bytes.
+// bf16 heads of 64 or 128, pages that tile 128 keys, rows, data and scales on 16 bytes.
 bool attn_packed_ok(const spec_prefix_attention_args& a, const q4::Cache& packed, int* sms) {
   if (((uintptr_t)packed.k_scale | (uintptr_t)packed.v_scale) % 16 != 0) return false;
-  if ((int64_t)a.page_size * a.Hk * a.D / 2 >= ((int64_t)1 << 31)) return false;  // a page's bytes, in 32 bits
   return attn_tc_ok(a, sms);
 }
 

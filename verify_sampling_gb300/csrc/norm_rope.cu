@@ -730,9 +730,9 @@ cudaError_t launch(const spec_norm_rope_args& a, bool wide, cudaStream_t stream)
 
 // ------------------------------------------------------------- read-back ---
 // A thread turns 4 bytes into 8 elements, 4 threads side by side a group; it keeps its word of a row
-// and steps over rows.
+// and steps over rows.  `shift`: the page size's logarithm, or -1.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(spec_cache_read_packed_args p, int at_once) {
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(spec_cache_read_packed_args p, int at_once, int shift) {
   const int groups = p.D / q4::kGroup, words = p.Hk * groups * 4, wide = min(words, kThreads);
   const int which = blockIdx.y, r0 = threadIdx.x / wide;
   T* out = (T*)(which ? p.v : p.k);
@@ -743,21 +743,23 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(spec_cache_read_pa
     const int h = w / (4 * groups), g = w / 4 - h * groups;
     const uint8_t* word = data + q4::data_at(0, h, 0, p.Hk, groups, p.page_size) + (size_t)g * 16 * p.page_size + (w & 3) * 4;
     const uint8_t* code = scales + q4::scale_at(0, h, 0, p.Hk, groups, p.page_size) + g;
-    const int64_t page_bytes = q4::data_at(1, 0, 0, p.Hk, groups, p.page_size), page_codes = q4::scale_at(1, 0, 0, p.Hk, groups, p.page_size);
+    const uint32_t page_bytes = (uint32_t)q4::data_at(1, 0, 0, p.Hk, groups, p.page_size), page_codes = page_bytes / 16;  // (below 2^31)
+    const int64_t step = (int64_t)gridDim.x * at_once;
+    uint4* to = reinterpret_cast<uint4*>(out + ((blockIdx.x * (int64_t)at_once + r0) * words + w) * 8);
 #pragma unroll 4
-    for (int64_t row = (int64_t)blockIdx.x * at_once + r0; row < p.rows; row += (int64_t)gridDim.x * at_once) {
+    for (int64_t row = (int64_t)blockIdx.x * at_once + r0; row < p.rows; row += step, to += step * words * (int)sizeof(T) / 2) {
       const int slot = p.slot[row];
       uint32_t v = 0x88888888u, b = 0;  // zeros
       if (slot >= p.n_slots) set_status(p.status, SPEC_STATUS_BAD_PAGE);
       if (slot >= 0 && slot < p.n_slots) {
-        const uint32_t page = (uint32_t)slot / (uint32_t)p.page_size, tok = slot - page * p.page_size;
-        v = *reinterpret_cast<const uint32_t*>(word + page * page_bytes + (size_t)tok * 16);
-        b = code[page * page_codes + (size_t)tok * groups];
+        const uint32_t page = shift >= 0 ? (uint32_t)slot >> shift : (uint32_t)slot / (uint32_t)p.page_size;
+        const uint32_t tok = slot - page * p.page_size;
+        v = *reinterpret_cast<const uint32_t*>(word + (size_t)page * page_bytes + tok * 16);
+        b = code[(size_t)page * page_codes + tok * groups];
       }
       const q4::Scale s = q4::scale_pair(b * 0x10001u);
       const uint32_t p0 = q4::element_pair<0>(v, s), p1 = q4::element_pair<1>(v, s), p2 = q4::element_pair<2>(v, s), p3 = q4::element_pair<3>(v, s);
       const uint32_t x[4] = {__byte_perm(p0, p1, 0x5410), __byte_perm(p2, p3, 0x5410), __byte_perm(p0, p1, 0x7632), __byte_perm(p2, p3, 0x7632)};
-      uint4* to = reinterpret_cast<uint4*>(out + ((size_t)row * words + w) * 8);
       if (sizeof(T) == 2) {
         *to = make_uint4(x[0], x[1], x[2], x[3]);
       } else {
@@ -785,9 +787,12 @@ cudaError_t launch_norm_rope(const spec_norm_rope_args& a, cudaStream_t stream) 
 cudaError_t launch_cache_read(const spec_cache_read_packed_args& a, cudaStream_t stream) {
   if (a.rows == 0) return cudaSuccess;
   const int words = a.Hk * (a.D / 8), at_once = std::max(1, kThreads / words);
+  int shift = 0;  // of a page size that is a power of two, or -1
+  while ((1 << shift) < a.page_size && shift < 30) ++shift;
+  if (1 << shift != a.page_size) shift = -1;
   const dim3 grid((unsigned)std::min<int64_t>(((int64_t)a.rows + at_once - 1) / at_once, 152 * 2), 2);
-  if (a.dtype == SPEC_F32) cache_read_kernel<float><<<grid, kThreads, 0, stream>>>(a, at_once);
-  else cache_read_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(a, at_once);
+  if (a.dtype == SPEC_F32) cache_read_kernel<float><<<grid, kThreads, 0, stream>>>(a, at_once, shift);
+  else cache_read_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(a, at_once, shift);
   return cudaGetLastError();
 }
 

@@ -25,6 +25,9 @@ struct Cache {  // data and scales of keys and values
   const uint8_t *k, *v, *k_scale, *v_scale;
 };
 
+// Whether a page's bytes are below 2^31.
+inline bool page_fits(int64_t page_size, int Hk, int D) { return page_size * Hk < ((int64_t)1 << 32) / D; }
+
 // First byte of group 0 of a token's head (the next group is 16 P bytes on), and of its scales.
 __host__ __device__ __forceinline__ int64_t data_at(int64_t page, int h, int tok, int Hk, int groups, int P) {
   return ((page * Hk + h) * groups * P + tok) * 16;
