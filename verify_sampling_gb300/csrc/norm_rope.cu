@@ -623,6 +623,12 @@ __global__ void __launch_bounds__(kBulkThreads, bulk_blocks(PACKED))
         auto heads = [&](auto kind_v, int begin, int count, const float* weight, void* cache, uint8_t* scales) {
           constexpr int kind = decltype(kind_v)::value;
           if (kind < 2) factors_of(kind);
+          uint8_t *data = nullptr, *codes = nullptr;  // of the token's head 0
+          if (PACKED && kind > 0) {
+            data = (uint8_t*)cache + q4::data_at(page, 0, tok, p.Hk, groups_of, p.page_size);
+            codes = scales + q4::scale_at(page, 0, tok, p.Hk, groups_of, p.page_size);
+          }
+          const uint32_t head_codes = groups_of * p.page_size;
           uint8_t* from = token + (uint32_t)(begin + in_t * at_once + sub) * head_bytes;
           for (int h0 = in_t * at_once; h0 < count; h0 += each * at_once, from += hop) {
             const bool on = h0 + sub < count;
@@ -634,10 +640,8 @@ __global__ void __launch_bounds__(kBulkThreads, bulk_blocks(PACKED))
             if (PACKED && kind > 0) {
               float yf[VEC];
               spread(y, yf);
-              const int head = on ? h0 + sub : 0;
-              store_packed<VEC, 1>(yf, first, 32 * VEC, p.D, on && at.y >= 0,
-                                   (uint8_t*)cache + q4::data_at(page, head, tok, p.Hk, groups_of, p.page_size),
-                                   scales + q4::scale_at(page, head, tok, p.Hk, groups_of, p.page_size), p.page_size);
+              const uint32_t at_head = (on ? h0 + sub : 0) * head_codes;  // (a page's bytes are below 2^31)
+              store_packed<VEC, 1>(yf, first, 32 * VEC, p.D, on && at.y >= 0, data + (size_t)at_head * 16, codes + at_head, p.page_size);
             } else if (on && live) {
               *reinterpret_cast<uint4*>(from) = packed_up(y, T());
             }
