@@ -259,13 +259,16 @@ __device__ __forceinline__ void lay_out(const spec_prefix_attention_args& a, con
 // The rest of a wait whose first look failed.  Gives up when the time limit passes or
 // another warp has given up.
 __device__ __forceinline__ bool slow_wait_here(uint64_t* bar, uint32_t phase, volatile int* abort_flag, uint32_t* status) {
-  for (int i = 0; i < 2000; ++i) {
-    if (tc::mbar_wait(bar, phase & 1u, kWaitNs / 2000)) return true;
+  const uint64_t t0 = tc::globaltimer_ns();
+  while (!tc::mbar_try_wait_suspend(bar, phase & 1u, 1000000u)) {
     if (*abort_flag) return false;
+    if (tc::globaltimer_ns() - t0 > kWaitNs) {
+      *abort_flag = 1;
+      set_status(status, SPEC_STATUS_TIMEOUT);
+      return false;
+    }
   }
-  *abort_flag = 1;
-  set_status(status, SPEC_STATUS_TIMEOUT);
-  return false;
+  return true;
 }
 // (Out of line: the code of a role that a short item runs once has to fit the instruction
 // cache beside the others'.)

@@ -265,364 +265,363 @@ __global__ void __launch_bounds__(Roles<kPacked>::kThreads, 1)
     }
     return got;
   };
-  // Over a packed cache softmax threads need more registers than an 896th of the file: the other
-  // three warpgroups give theirs, 512 x 96 + 384 x 40 of the 896 x 72 that the block starts with.
-  if (warp >= kSoftWarps) {
-    if (kPacked) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == kProducer) {
-      // ------------------------------------------------------------ producer --
-      uint32_t seq = 0;  // ring positions used: keys and values in turn
-      uint32_t bad = 0, ph = 0;
-      int st = 0;
-      bool ok = true;
-      const int box = min(a.page_size, kTile), boxes = kTile / box;  // keys of a box, boxes of a tile
-      for (uint32_t n_item = 0;; ++n_item) {
-        const Item& posted = items[n_item % kItemSlots];
-        ok = warp_wait(&bars.item_full[n_item % kItemSlots], n_item / kItemSlots);
-        if (!ok || posted.rows == 0) break;
-        const Item it = posted;
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bars.item_empty[n_item % kItemSlots]);
-        if (kPacked) {  // pages' heads and their scales, by bulk copies
-          constexpr int G = S::kGroups;
-          const int pieces = a.page_size > kTile ? G : 1;  // copies of a page's data within a tile
-          for (int i = it.lo; ok && i < it.hi; ++i) {
-            const int live = min(kTile, it.keys - i * kTile);
-            const int used = (live + box - 1) / box, copies = used * (pieces + 1);
-            const int x = lane / (pieces + 1), piece = lane - x * (pieces + 1);
-            int page = 0, tok = 0;
-            if (lane < copies) {
-              const int key = i * kTile + x * box, pi = key / a.page_size;
-              page = page_of(a, it.table, pi, &bad);
-              tok = key - pi * a.page_size;
-            }
-            for (int kv = 0; kv < 2; ++kv, ++seq) {
-              ok = warp_wait(&bars.packed_empty[st], ph ^ 1u);
-              if (!ok) break;
-              if (lane == 0) tc::mbar_expect_tx(&bars.packed_full[st], (uint32_t)(used * box * (D / 2 + G)));
-              __syncwarp();
-              if (lane < copies) {
-                uint8_t* to = smem + S::kPackedRing + st * S::kPackedBytes;
-                if (piece < pieces)
-                  tc::bulk_load(to + (x * G + piece) * box * 16,
-                                (kv ? packed.v : packed.k) + q4::data_at(page, it.h, tok, a.Hk, G, a.page_size) +
-                                    (int64_t)piece * 16 * a.page_size,
-                                (uint32_t)(box * 16 * (G / pieces)), &bars.packed_full[st]);
-                else
-                  tc::bulk_load(to + S::kPackedData + x * box * G,
-                                (kv ? packed.v_scale : packed.k_scale) + q4::scale_at(page, it.h, tok, a.Hk, G, a.page_size),
-                                (uint32_t)(box * G), &bars.packed_full[st]);
-              }
-              if (++st == S::kPackedStages) {
-                st = 0;
-                ph ^= 1u;
-              }
-            }
+  auto producer = [&] {
+    // ------------------------------------------------------------ producer --
+    uint32_t seq = 0;  // ring positions used: keys and values in turn
+    uint32_t bad = 0, ph = 0;
+    int st = 0;
+    bool ok = true;
+    const int box = min(a.page_size, kTile), boxes = kTile / box;  // keys of a box, boxes of a tile
+    for (uint32_t n_item = 0;; ++n_item) {
+      const Item& posted = items[n_item % kItemSlots];
+      ok = warp_wait(&bars.item_full[n_item % kItemSlots], n_item / kItemSlots);
+      if (!ok || posted.rows == 0) break;
+      const Item it = posted;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars.item_empty[n_item % kItemSlots]);
+      if (kPacked) {  // pages' heads and their scales, by bulk copies
+        constexpr int G = S::kGroups;
+        const int pieces = a.page_size > kTile ? G : 1;  // copies of a page's data within a tile
+        for (int i = it.lo; ok && i < it.hi; ++i) {
+          const int live = min(kTile, it.keys - i * kTile);
+          const int used = (live + box - 1) / box, copies = used * (pieces + 1);
+          const int x = lane / (pieces + 1), piece = lane - x * (pieces + 1);
+          int page = 0, tok = 0;
+          if (lane < copies) {
+            const int key = i * kTile + x * box, pi = key / a.page_size;
+            page = page_of(a, it.table, pi, &bad);
+            tok = key - pi * a.page_size;
           }
-        } else {
-          for (int i = it.lo; ok && i < it.hi; ++i) {
-            const int live = min(kTile, it.keys - i * kTile);
-            const int used = (live + box - 1) / box;  // pages (or parts of one) that have keys
-            int row = 0;
-            const int which = lane / kHalves;
-            if (which < used) {
-              const int key = i * kTile + which * box, pi = key / a.page_size;
-              row = page_of(a, it.table, pi, &bad) * a.page_size + (key - pi * a.page_size);
+          for (int kv = 0; kv < 2; ++kv, ++seq) {
+            ok = warp_wait(&bars.packed_empty[st], ph ^ 1u);
+            if (!ok) break;
+            if (lane == 0) tc::mbar_expect_tx(&bars.packed_full[st], (uint32_t)(used * box * (D / 2 + G)));
+            __syncwarp();
+            if (lane < copies) {
+              uint8_t* to = smem + S::kPackedRing + st * S::kPackedBytes;
+              if (piece < pieces)
+                tc::bulk_load(to + (x * G + piece) * box * 16,
+                              (kv ? packed.v : packed.k) + q4::data_at(page, it.h, tok, a.Hk, G, a.page_size) +
+                                  (int64_t)piece * 16 * a.page_size,
+                              (uint32_t)(box * 16 * (G / pieces)), &bars.packed_full[st]);
+              else
+                tc::bulk_load(to + S::kPackedData + x * box * G,
+                              (kv ? packed.v_scale : packed.k_scale) + q4::scale_at(page, it.h, tok, a.Hk, G, a.page_size),
+                              (uint32_t)(box * G), &bars.packed_full[st]);
             }
-            for (int kv = 0; kv < 2; ++kv, ++seq) {
-              ok = warp_wait(&bars.empty[st], ph ^ 1u);
-              if (!ok) break;
-              if (lane == 0) tc::mbar_expect_tx(&bars.full[st], (uint32_t)(used * box * D * 2));
-              __syncwarp();
-              if (which < used && which < boxes) {
-                const int half = lane % kHalves;
-                tc::tma_load_3d(smem + S::kRing + st * S::kTileBytes + half * kHalfBytes + which * box * 128,
-                                kv ? &v_map : &k_map, &bars.full[st], half * 64, it.h, row);
-              }
-              if (++st == S::kStages) {
-                st = 0;
-                ph ^= 1u;
-              }
+            if (++st == S::kPackedStages) {
+              st = 0;
+              ph ^= 1u;
             }
           }
         }
-        if (!ok) break;
+      } else {
+        for (int i = it.lo; ok && i < it.hi; ++i) {
+          const int live = min(kTile, it.keys - i * kTile);
+          const int used = (live + box - 1) / box;  // pages (or parts of one) that have keys
+          int row = 0;
+          const int which = lane / kHalves;
+          if (which < used) {
+            const int key = i * kTile + which * box, pi = key / a.page_size;
+            row = page_of(a, it.table, pi, &bad) * a.page_size + (key - pi * a.page_size);
+          }
+          for (int kv = 0; kv < 2; ++kv, ++seq) {
+            ok = warp_wait(&bars.empty[st], ph ^ 1u);
+            if (!ok) break;
+            if (lane == 0) tc::mbar_expect_tx(&bars.full[st], (uint32_t)(used * box * D * 2));
+            __syncwarp();
+            if (which < used && which < boxes) {
+              const int half = lane % kHalves;
+              tc::tma_load_3d(smem + S::kRing + st * S::kTileBytes + half * kHalfBytes + which * box * 128,
+                              kv ? &v_map : &k_map, &bars.full[st], half * 64, it.h, row);
+            }
+            if (++st == S::kStages) {
+              st = 0;
+              ph ^= 1u;
+            }
+          }
+        }
       }
-      if (bad) set_status(a.status, bad);
-      if (!ok) {  // the copies in flight land before the block's memory goes
-        constexpr uint32_t kLoaded = kPacked ? S::kPackedStages : S::kStages;
-        uint64_t* loaded = kPacked ? bars.packed_full : bars.full;
-        const uint32_t from = seq > kLoaded ? seq - kLoaded : 0u;
-        for (uint32_t s = from; s < seq; ++s) tc::mbar_wait(&loaded[s % kLoaded], (s / kLoaded) & 1u, kWaitNs);
+      if (!ok) break;
+    }
+    if (bad) set_status(a.status, bad);
+    if (!ok) {  // the copies in flight land before the block's memory goes
+      constexpr uint32_t kLoaded = kPacked ? S::kPackedStages : S::kStages;
+      uint64_t* loaded = kPacked ? bars.packed_full : bars.full;
+      const uint32_t from = seq > kLoaded ? seq - kLoaded : 0u;
+      for (uint32_t s = from; s < seq; ++s) tc::mbar_wait(&loaded[s % kLoaded], (s / kLoaded) & 1u, kWaitNs);
+    }
+  };
+  auto products = [&] {
+    // ------------------------------------------------------------ products --
+    {
+      const uint32_t lead = elected();
+      int rows = 0, tiles = 0, n_rows = 0, n_tiles = 0;  // of the current and the next item
+      uint32_t n_item = 0;
+      uint32_t q_n[2] = {0, 0}, p_n[2] = {0, 0};
+      int turn = 0;  // softmax group of the next small item
+      bool ok = true;
+      constexpr uint32_t kDescS = tc::bf16_idesc(128, kTile);
+      constexpr uint32_t kDescO = tc::bf16_idesc(128, D) | (1u << 16);  // values: keys down, head across
+      const uint32_t q_lo = desc_k(tc::smem_u32(smem));
+      const uint32_t k_lo = desc_k(tc::smem_u32(smem + S::kRing));
+      const uint32_t v_lo = desc_mn(tc::smem_u32(smem + S::kRing), kHalfBytes);
+      struct Place {  // a ring position: its stage and the parity of its barriers
+        uint32_t stage, phase;
+        __device__ __forceinline__ Place next() const {
+          return stage + 1 == S::kStages ? Place{0, phase ^ 1u} : Place{stage + 1, phase};
+        }
+      };
+      auto wait = [&](uint64_t* bar, uint32_t phase) {
+        if (ok) ok = warp_wait(bar, phase);
+      };
+      auto scores = [&](int t, const Place& k, bool last) {  // S_t = Q_t K^T
+        const uint32_t kb = k_lo + k.stage * (S::kTileBytes >> 4), qb = q_lo + t * (S::kTileBytes >> 4);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          constexpr uint32_t kStep = 32 >> 4;
+          const uint32_t off = (c >> 2) * (kHalfBytes >> 4) + (c & 3) * kStep;
+          mma_ss(lead, tmem + t * kTile, qb + off, kb + off, kDescS, c > 0);
+        }
+        commit_if(lead, &bars.s_full[t]);
+        if (last) commit_if(lead, &bars.q_empty[t]);
+      };
+      // O_t (+)= P_t V, the keys of one half of each thread's weights at a time: keys 0-31
+      // and 64-95 of the tile, then the others
+      auto values = [&](int t, const Place& v, bool first, int part) {
+        const uint32_t vb = v_lo + v.stage * (S::kTileBytes >> 4);
+#pragma unroll
+        for (int x = 0; x < kTile / 32; ++x) {
+          const int c = (x >> 1) * 4 + part * 2 + (x & 1);
+          mma_ts(lead, tmem + 2 * kTile + t * kTile, tmem + t * kTile + c * 8, vb + c * (2048 >> 4), kDescO,
+                 x > 0 || part > 0 || !first);
+        }
+      };
+      auto begin = [&](int l0, int l1, const Place& k, int tiles) {  // an item's first scores
+        wait(&bars.full[k.stage], k.phase);
+        for (int t = l0; t <= l1 && ok; ++t) {
+          wait(&bars.q_full[t], q_n[t]++);
+          if (!ok) break;
+          tc::fence_after_sync();
+          scores(t, k, tiles == 1);
+        }
+        if (ok) commit_if(lead, &bars.empty[k.stage]);
+      };
+      auto next = [&](int& r, int& n) {  // the next item's rows and tiles; false after the last
+        const uint32_t slot = n_item % kItemSlots;
+        wait(&bars.item_full[slot], n_item / kItemSlots);
+        ++n_item;
+        if (!ok) return false;
+        // (from one lane, so that what follows is uniform)
+        r = __shfl_sync(0xffffffffu, items[slot].rows, 0);
+        n = __shfl_sync(0xffffffffu, items[slot].hi - items[slot].lo, 0);
+        if (r == 0) return false;
+        if (lane == 0) tc::mbar_arrive(&bars.item_empty[slot]);
+        return true;
+      };
+      auto lanes = [&](int r, int& p, int& q) {  // the softmax groups of an item
+        if (r > kTile) {
+          p = 0;
+          q = 1;
+        } else {
+          p = q = turn;
+          turn ^= 1;
+        }
+      };
+      int l0 = 0, l1 = 0;
+      Place key{0, 0};  // the current tile's keys; its values follow
+      bool more = next(rows, tiles);
+      if (more) {
+        lanes(rows, l0, l1);
+        begin(l0, l1, key, tiles);
       }
-    } else if (warp == kMma) {
-      // ------------------------------------------------------------ products --
-      {
-        const uint32_t lead = elected();
-        int rows = 0, tiles = 0, n_rows = 0, n_tiles = 0;  // of the current and the next item
-        uint32_t n_item = 0;
-        uint32_t q_n[2] = {0, 0}, p_n[2] = {0, 0};
-        int turn = 0;  // softmax group of the next small item
-        bool ok = true;
-        constexpr uint32_t kDescS = tc::bf16_idesc(128, kTile);
-        constexpr uint32_t kDescO = tc::bf16_idesc(128, D) | (1u << 16);  // values: keys down, head across
-        const uint32_t q_lo = desc_k(tc::smem_u32(smem));
-        const uint32_t k_lo = desc_k(tc::smem_u32(smem + S::kRing));
-        const uint32_t v_lo = desc_mn(tc::smem_u32(smem + S::kRing), kHalfBytes);
-        struct Place {  // a ring position: its stage and the parity of its barriers
-          uint32_t stage, phase;
-          __device__ __forceinline__ Place next() const {
-            return stage + 1 == S::kStages ? Place{0, phase ^ 1u} : Place{stage + 1, phase};
+      while (more && ok) {
+        bool more_next = false, early = false;
+        int n0 = 0, n1 = 0;
+        for (int i = 0; i < tiles && ok; ++i) {
+          const bool last = i + 1 == tiles;
+          const Place val = key.next(), then = val.next();
+          if (last) {
+            more_next = next(n_rows, n_tiles);
+            if (more_next) {
+              lanes(n_rows, n0, n1);
+              // ahead of the current item's last values, if all is there: the other
+              // group may still be busy with the item before
+              early = l0 == l1 && n0 == n1 && n0 != l0 &&
+                      __all_sync(0xffffffffu, tc::mbar_try_wait(&bars.q_full[n0], q_n[n0] & 1u) &&
+                                                  tc::mbar_try_wait(&bars.full[then.stage], then.phase));
+              if (early) begin(n0, n1, then, n_tiles);
+            }
           }
-        };
-        auto wait = [&](uint64_t* bar, uint32_t phase) {
-          if (ok) ok = warp_wait(bar, phase);
-        };
-        auto scores = [&](int t, const Place& k, bool last) {  // S_t = Q_t K^T
-          const uint32_t kb = k_lo + k.stage * (S::kTileBytes >> 4), qb = q_lo + t * (S::kTileBytes >> 4);
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            constexpr uint32_t kStep = 32 >> 4;
-            const uint32_t off = (c >> 2) * (kHalfBytes >> 4) + (c & 3) * kStep;
-            mma_ss(lead, tmem + t * kTile, qb + off, kb + off, kDescS, c > 0);
-          }
-          commit_if(lead, &bars.s_full[t]);
-          if (last) commit_if(lead, &bars.q_empty[t]);
-        };
-        // O_t (+)= P_t V, the keys of one half of each thread's weights at a time: keys 0-31
-        // and 64-95 of the tile, then the others
-        auto values = [&](int t, const Place& v, bool first, int part) {
-          const uint32_t vb = v_lo + v.stage * (S::kTileBytes >> 4);
-#pragma unroll
-          for (int x = 0; x < kTile / 32; ++x) {
-            const int c = (x >> 1) * 4 + part * 2 + (x & 1);
-            mma_ts(lead, tmem + 2 * kTile + t * kTile, tmem + t * kTile + c * 8, vb + c * (2048 >> 4), kDescO,
-                   x > 0 || part > 0 || !first);
-          }
-        };
-        auto begin = [&](int l0, int l1, const Place& k, int tiles) {  // an item's first scores
-          wait(&bars.full[k.stage], k.phase);
+          wait(&bars.full[val.stage], val.phase);
+          if (!last) wait(&bars.full[then.stage], then.phase);
           for (int t = l0; t <= l1 && ok; ++t) {
-            wait(&bars.q_full[t], q_n[t]++);
+            wait(&bars.p_half[t], p_n[t]);
             if (!ok) break;
             tc::fence_after_sync();
-            scores(t, k, tiles == 1);
-          }
-          if (ok) commit_if(lead, &bars.empty[k.stage]);
-        };
-        auto next = [&](int& r, int& n) {  // the next item's rows and tiles; false after the last
-          const uint32_t slot = n_item % kItemSlots;
-          wait(&bars.item_full[slot], n_item / kItemSlots);
-          ++n_item;
-          if (!ok) return false;
-          // (from one lane, so that what follows is uniform)
-          r = __shfl_sync(0xffffffffu, items[slot].rows, 0);
-          n = __shfl_sync(0xffffffffu, items[slot].hi - items[slot].lo, 0);
-          if (r == 0) return false;
-          if (lane == 0) tc::mbar_arrive(&bars.item_empty[slot]);
-          return true;
-        };
-        auto lanes = [&](int r, int& p, int& q) {  // the softmax groups of an item
-          if (r > kTile) {
-            p = 0;
-            q = 1;
-          } else {
-            p = q = turn;
-            turn ^= 1;
-          }
-        };
-        int l0 = 0, l1 = 0;
-        Place key{0, 0};  // the current tile's keys; its values follow
-        bool more = next(rows, tiles);
-        if (more) {
-          lanes(rows, l0, l1);
-          begin(l0, l1, key, tiles);
-        }
-        while (more && ok) {
-          bool more_next = false, early = false;
-          int n0 = 0, n1 = 0;
-          for (int i = 0; i < tiles && ok; ++i) {
-            const bool last = i + 1 == tiles;
-            const Place val = key.next(), then = val.next();
-            if (last) {
-              more_next = next(n_rows, n_tiles);
-              if (more_next) {
-                lanes(n_rows, n0, n1);
-                // ahead of the current item's last values, if all is there: the other
-                // group may still be busy with the item before
-                early = l0 == l1 && n0 == n1 && n0 != l0 &&
-                        __all_sync(0xffffffffu, tc::mbar_try_wait(&bars.q_full[n0], q_n[n0] & 1u) &&
-                                                    tc::mbar_try_wait(&bars.full[then.stage], then.phase));
-                if (early) begin(n0, n1, then, n_tiles);
-              }
-            }
-            wait(&bars.full[val.stage], val.phase);
-            if (!last) wait(&bars.full[then.stage], then.phase);
-            for (int t = l0; t <= l1 && ok; ++t) {
-              wait(&bars.p_half[t], p_n[t]);
-              if (!ok) break;
-              tc::fence_after_sync();
-              values(t, val, i == 0, 0);
-              wait(&bars.p_full[t], p_n[t]++);
-              if (!ok) break;
-              tc::fence_after_sync();
-              values(t, val, i == 0, 1);
-              if (last) commit_if(lead, &bars.o_full[t]);
-              else scores(t, then, i + 2 == tiles);
-            }
+            values(t, val, i == 0, 0);
+            wait(&bars.p_full[t], p_n[t]++);
             if (!ok) break;
-            commit_if(lead, &bars.empty[val.stage]);
-            if (!last) commit_if(lead, &bars.empty[then.stage]);
-            key = then;
+            tc::fence_after_sync();
+            values(t, val, i == 0, 1);
+            if (last) commit_if(lead, &bars.o_full[t]);
+            else scores(t, then, i + 2 == tiles);
           }
           if (!ok) break;
-          more = more_next;
-          rows = n_rows;
-          tiles = n_tiles;
-          l0 = n0;
-          l1 = n1;
-          if (more && !early) begin(l0, l1, key, tiles);
+          commit_if(lead, &bars.empty[val.stage]);
+          if (!last) commit_if(lead, &bars.empty[then.stage]);
+          key = then;
         }
-        if (!ok) {  // the products in flight end before TMEM is freed
-          commit_if(lead, &bars.drain);
-          tc::mbar_wait(&bars.drain, 0, kWaitNs);
-        }
+        if (!ok) break;
+        more = more_next;
+        rows = n_rows;
+        tiles = n_tiles;
+        l0 = n0;
+        l1 = n1;
+        if (more && !early) begin(l0, l1, key, tiles);
       }
+      if (!ok) {  // the products in flight end before TMEM is freed
+        commit_if(lead, &bars.drain);
+        tc::mbar_wait(&bars.drain, 0, kWaitNs);
+      }
+    }
+    __syncwarp();
+  };
+  auto planner = [&] {
+    // ------------------------------------------------------------- planner --
+    Walker<WideCosts<kPacked>> walk(a, w, lay);
+    Item it;
+    for (uint32_t n_item = 0;; ++n_item) {
+      if (!walk.next(it)) it.rows = 0;  // the end
+      const uint32_t slot = n_item % kItemSlots;
+      if (!warp_wait(&bars.item_empty[slot], (n_item / kItemSlots) ^ 1u)) break;
+      if (lane == 0) {
+        items[slot] = it;
+        tc::mbar_arrive(&bars.item_full[slot]);
+      }
+      if (it.rows == 0) break;
+    }
+  };
+  auto loader = [&] {
+    // -------------------------------------------------------------- loader --
+    uint32_t n[2] = {0, 0};  // query tiles taken
+    int turn = 0;
+    bool ok = true;
+    for (uint32_t n_item = 0; ok; ++n_item) {
+      const Item& posted = items[n_item % kItemSlots];
+      ok = warp_wait(&bars.item_full[n_item % kItemSlots], n_item / kItemSlots);
+      if (!ok || posted.rows == 0) break;
+      const int row0 = posted.row0, m0 = posted.m0, rows = posted.rows, h = posted.h;
       __syncwarp();
-    } else if (warp == kPlanner) {
-      // ------------------------------------------------------------- planner --
-      Walker<WideCosts<kPacked>> walk(a, w, lay);
-      Item it;
-      for (uint32_t n_item = 0;; ++n_item) {
-        if (!walk.next(it)) it.rows = 0;  // the end
-        const uint32_t slot = n_item % kItemSlots;
-        if (!warp_wait(&bars.item_empty[slot], (n_item / kItemSlots) ^ 1u)) break;
-        if (lane == 0) {
-          items[slot] = it;
-          tc::mbar_arrive(&bars.item_full[slot]);
+      if (lane == 0) tc::mbar_arrive(&bars.item_empty[n_item % kItemSlots]);
+      const bool both = rows > kTile;
+      const int t0 = both ? 0 : turn, t1 = both ? 1 : turn;
+      if (!both) turn ^= 1;
+      for (int t = t0; ok && t <= t1; ++t) {
+        ok = warp_wait(&bars.q_empty[t], n[t] ^ 1u);
+        if (!ok) break;
+        ++n[t];
+        // rows past the item's keep what was there: their results are not read
+        const int first = both ? t * kTile : 0, live = min(kTile, rows - first);
+        if (q_box > 0) {  // boxes of q_box query rows: whole packed rows of one key head
+          const int boxes = (live + q_box - 1) / q_box;
+          if (lane == 0) tc::mbar_expect_tx(&bars.q_full[t], (uint32_t)(boxes * q_box * D * 2));
+          __syncwarp();
+          const int half = lane % kHalves, x = lane / kHalves;
+          if (x < boxes)
+            tc::tma_load_3d(smem + t * S::kTileBytes + half * kHalfBytes + x * q_box * 128, &q_map,
+                            &bars.q_full[t], half * 64, h * per_head, row0 + (m0 + first + x * q_box) / per_head);
+          continue;
         }
-        if (it.rows == 0) break;
+        const uint32_t to = tc::smem_u32(smem) + t * S::kTileBytes;
+        constexpr int kChunks = D / 8;  // 16-byte pieces of a row
+        const int c = lane % kChunks;
+        for (int r = lane / kChunks; r < live; r += 32 / kChunks) {
+          const int qrow = m0 + first + r, j = qrow / per_head;
+          const __nv_bfloat16* q = (const __nv_bfloat16*)a.q + (size_t)(row0 + j) * a.q_row +
+                                   (size_t)(h * per_head + (qrow - j * per_head)) * a.q_head + c * 8;
+          copy16(to + r * 128 + (c >> 3) * kHalfBytes + (((c & 7) ^ (r & 7)) << 4), q);
+        }
       }
-    } else if (warp == kLoader) {
-      // -------------------------------------------------------------- loader --
-      uint32_t n[2] = {0, 0};  // query tiles taken
-      int turn = 0;
-      bool ok = true;
-      for (uint32_t n_item = 0; ok; ++n_item) {
-        const Item& posted = items[n_item % kItemSlots];
-        ok = warp_wait(&bars.item_full[n_item % kItemSlots], n_item / kItemSlots);
-        if (!ok || posted.rows == 0) break;
-        const int row0 = posted.row0, m0 = posted.m0, rows = posted.rows, h = posted.h;
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bars.item_empty[n_item % kItemSlots]);
-        const bool both = rows > kTile;
-        const int t0 = both ? 0 : turn, t1 = both ? 1 : turn;
-        if (!both) turn ^= 1;
-        for (int t = t0; ok && t <= t1; ++t) {
-          ok = warp_wait(&bars.q_empty[t], n[t] ^ 1u);
-          if (!ok) break;
-          ++n[t];
-          // rows past the item's keep what was there: their results are not read
-          const int first = both ? t * kTile : 0, live = min(kTile, rows - first);
-          if (q_box > 0) {  // boxes of q_box query rows: whole packed rows of one key head
-            const int boxes = (live + q_box - 1) / q_box;
-            if (lane == 0) tc::mbar_expect_tx(&bars.q_full[t], (uint32_t)(boxes * q_box * D * 2));
-            __syncwarp();
-            const int half = lane % kHalves, x = lane / kHalves;
-            if (x < boxes)
-              tc::tma_load_3d(smem + t * S::kTileBytes + half * kHalfBytes + x * q_box * 128, &q_map,
-                              &bars.q_full[t], half * 64, h * per_head, row0 + (m0 + first + x * q_box) / per_head);
-            continue;
+      if (q_box > 0) continue;
+      copies_wait();
+      tc::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0 && ok)
+        for (int t = t0; t <= t1; ++t) tc::mbar_arrive(&bars.q_full[t]);
+    }
+    if (abort_flag && q_box > 0)
+      for (int t = 0; t < 2; ++t)
+        if (n[t] > 0) tc::mbar_wait(&bars.q_full[t], (n[t] - 1u) & 1u, kWaitNs);
+  };
+  auto unpack = [&] {
+    // -------------------------------------------------------------- unpack --
+    // Half of a key's (or value's) groups from the packed ring to their row of the operand tile, a thread.
+    constexpr int G = S::kGroups, kMine = G / 2;
+    const int at = (warp - kUnpack) * 32 + lane, key = at % kTile, c0 = at / kTile * kMine;
+    const int box = min(a.page_size, kTile), page = key / box;
+    const uint8_t* from = smem + S::kPackedRing + (page * G + c0) * box * 16 + (key - page * box) * 16;
+    uint8_t* to = smem + S::kRing + key * 128;
+    const uint32_t turn = (key & 7) << 4;
+    uint32_t st = 0, ph = 0, pst = 0, pph = 0;
+    bool ok = true;
+    for (uint32_t n_item = 0; ok; ++n_item) {
+      const Item& posted = items[n_item % kItemSlots];
+      ok = warp_wait(&bars.item_full[n_item % kItemSlots], n_item / kItemSlots);
+      if (!ok || posted.rows == 0) break;
+      const int tiles = 2 * (posted.hi - posted.lo);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars.item_empty[n_item % kItemSlots]);
+      for (int i = 0; i < tiles; ++i) {
+        ok = warp_wait(&bars.packed_full[pst], pph) && warp_wait(&bars.empty[st], ph ^ 1u);
+        if (!ok) break;
+        const uint8_t* src = from + pst * S::kPackedBytes;
+        const uint8_t* sp = smem + S::kPackedRing + pst * S::kPackedBytes + S::kPackedData + key * G + c0;
+        const uint32_t scales = G == 4 ? *reinterpret_cast<const uint16_t*>(sp) : *sp;
+        uint4 v[kMine];
+#pragma unroll
+        for (int c = 0; c < kMine; ++c) v[c] = tc::lds128(src + c * box * 16);
+        uint8_t* dst = to + st * S::kTileBytes;
+        auto words = [&](auto is_key) {
+#pragma unroll
+          for (int c = 0; c < kMine; ++c) {
+            const q4::Scale z = q4::scale_pair(__byte_perm(scales, 0, 0x4040 | c * 0x0101));
+            const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t p0 = q4::element_pair<0>(w[x], z), p1 = q4::element_pair<1>(w[x], z);
+              const uint32_t p2 = q4::element_pair<2>(w[x], z), p3 = q4::element_pair<3>(w[x], z);
+              // keys in the queries' order; values' columns as they come (8 elements e lie at
+              // 2 (e mod 4) + e / 4), for which the results' columns are put in order
+              const uint4 o = decltype(is_key)::value
+                                  ? make_uint4(__byte_perm(p0, p1, 0x5410), __byte_perm(p2, p3, 0x5410), __byte_perm(p0, p1, 0x7632),
+                                               __byte_perm(p2, p3, 0x7632))
+                                  : make_uint4(p0, p1, p2, p3);
+              const int chunk = (c0 + c) * 4 + x;
+              *reinterpret_cast<uint4*>(dst + (chunk >> 3) * kHalfBytes + (((chunk & 7) << 4) ^ turn)) = o;
+            }
           }
-          const uint32_t to = tc::smem_u32(smem) + t * S::kTileBytes;
-          constexpr int kChunks = D / 8;  // 16-byte pieces of a row
-          const int c = lane % kChunks;
-          for (int r = lane / kChunks; r < live; r += 32 / kChunks) {
-            const int qrow = m0 + first + r, j = qrow / per_head;
-            const __nv_bfloat16* q = (const __nv_bfloat16*)a.q + (size_t)(row0 + j) * a.q_row +
-                                     (size_t)(h * per_head + (qrow - j * per_head)) * a.q_head + c * 8;
-            copy16(to + r * 128 + (c >> 3) * kHalfBytes + (((c & 7) ^ (r & 7)) << 4), q);
-          }
-        }
-        if (q_box > 0) continue;
-        copies_wait();
+        };
+        if (i % 2 == 0) words(std::true_type{});
+        else words(std::false_type{});
         tc::fence_proxy_async();
         __syncwarp();
-        if (lane == 0 && ok)
-          for (int t = t0; t <= t1; ++t) tc::mbar_arrive(&bars.q_full[t]);
-      }
-      if (abort_flag && q_box > 0)
-        for (int t = 0; t < 2; ++t)
-          if (n[t] > 0) tc::mbar_wait(&bars.q_full[t], (n[t] - 1u) & 1u, kWaitNs);
-    } else if (kPacked && warp >= kUnpack) {
-      // -------------------------------------------------------------- unpack --
-      // Half of a key's (or value's) groups from the packed ring to their row of the operand tile, a thread.
-      constexpr int G = S::kGroups, kMine = G / 2;
-      const int at = (warp - kUnpack) * 32 + lane, key = at % kTile, c0 = at / kTile * kMine;
-      const int box = min(a.page_size, kTile), page = key / box;
-      const uint8_t* from = smem + S::kPackedRing + (page * G + c0) * box * 16 + (key - page * box) * 16;
-      uint8_t* to = smem + S::kRing + key * 128;
-      const uint32_t turn = (key & 7) << 4;
-      uint32_t st = 0, ph = 0, pst = 0, pph = 0;
-      bool ok = true;
-      for (uint32_t n_item = 0; ok; ++n_item) {
-        const Item& posted = items[n_item % kItemSlots];
-        ok = warp_wait(&bars.item_full[n_item % kItemSlots], n_item / kItemSlots);
-        if (!ok || posted.rows == 0) break;
-        const int tiles = 2 * (posted.hi - posted.lo);
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bars.item_empty[n_item % kItemSlots]);
-        for (int i = 0; i < tiles; ++i) {
-          ok = warp_wait(&bars.packed_full[pst], pph) && warp_wait(&bars.empty[st], ph ^ 1u);
-          if (!ok) break;
-          const uint8_t* src = from + pst * S::kPackedBytes;
-          const uint8_t* sp = smem + S::kPackedRing + pst * S::kPackedBytes + S::kPackedData + key * G + c0;
-          const uint32_t scales = G == 4 ? *reinterpret_cast<const uint16_t*>(sp) : *sp;
-          uint4 v[kMine];
-#pragma unroll
-          for (int c = 0; c < kMine; ++c) v[c] = tc::lds128(src + c * box * 16);
-          uint8_t* dst = to + st * S::kTileBytes;
-          auto words = [&](auto is_key) {
-#pragma unroll
-            for (int c = 0; c < kMine; ++c) {
-              const q4::Scale z = q4::scale_pair(__byte_perm(scales, 0, 0x4040 | c * 0x0101));
-              const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const uint32_t p0 = q4::element_pair<0>(w[x], z), p1 = q4::element_pair<1>(w[x], z);
-                const uint32_t p2 = q4::element_pair<2>(w[x], z), p3 = q4::element_pair<3>(w[x], z);
-                // keys in the queries' order; values' columns as they come (8 elements e lie at
-                // 2 (e mod 4) + e / 4), for which the results' columns are put in order
-                const uint4 o = decltype(is_key)::value
-                                    ? make_uint4(__byte_perm(p0, p1, 0x5410), __byte_perm(p2, p3, 0x5410), __byte_perm(p0, p1, 0x7632),
-                                                 __byte_perm(p2, p3, 0x7632))
-                                    : make_uint4(p0, p1, p2, p3);
-                const int chunk = (c0 + c) * 4 + x;
-                *reinterpret_cast<uint4*>(dst + (chunk >> 3) * kHalfBytes + (((chunk & 7) << 4) ^ turn)) = o;
-              }
-            }
-          };
-          if (i % 2 == 0) words(std::true_type{});
-          else words(std::false_type{});
-          tc::fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) {
-            tc::mbar_arrive(&bars.full[st]);
-            tc::mbar_arrive(&bars.packed_empty[pst]);
-          }
-          if (++st == S::kStages) {
-            st = 0;
-            ph ^= 1u;
-          }
-          if (++pst == S::kPackedStages) {
-            pst = 0;
-            pph ^= 1u;
-          }
+        if (lane == 0) {
+          tc::mbar_arrive(&bars.full[st]);
+          tc::mbar_arrive(&bars.packed_empty[pst]);
+        }
+        if (++st == S::kStages) {
+          st = 0;
+          ph ^= 1u;
+        }
+        if (++pst == S::kPackedStages) {
+          pst = 0;
+          pph ^= 1u;
         }
       }
     }
-  } else {
-    if (kPacked) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+  };
+  auto softmax = [&] {
     // ------------------------------------------------------------- softmax --
     constexpr int kCols = kTile / 2, kDims = D / 2;  // scores and result columns of a thread
     const int t = warp >> 3, half = lane >> 4;
@@ -808,6 +807,28 @@ __global__ void __launch_bounds__(Roles<kPacked>::kThreads, 1)
       }
       more = next(it, seq0);
     }
+  };
+
+  if (kPacked) {
+    // Softmax threads need more registers than an 896th of the file: the other three warpgroups
+    // give theirs, 512 x 96 + 384 x 40 of the 896 x 72 that the block starts with.
+    if (warp >= kSoftWarps) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+      if (warp == kProducer) producer();
+      else if (warp == kMma) products();
+      else if (warp == kPlanner) planner();
+      else if (warp == kLoader) loader();
+      else unpack();
+    } else {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+      softmax();
+    }
+  } else {  // (in this order: with the softmax warps' branch first the round of 256 requests took 816 us for 795)
+    if (warp == kProducer) producer();
+    else if (warp == kMma) products();
+    else if (warp == kPlanner) planner();
+    else if (warp == kLoader) loader();
+    else softmax();
   }
   tc::grid_dep_launch();
   tc::fence_before_sync();
