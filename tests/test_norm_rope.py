@@ -126,20 +126,24 @@ def test_a_norm_of_one_kind_alone(which, rows):
     assert torch.equal(caches[2][0], caches[1 if which == "q" else 0][0])
 
 
-def test_the_batch_does_not_change_a_row():
-    """Rows alone, in a few and in a long batch come out with the same bits."""
-    qkv, position, slot, pages, (qw, kw) = _inputs(1500, 40, 8, 128, BF)
-    q, k, v = qkv[:, :40], qkv[:, 40:48], qkv[:, 48:]
-    freq = _freq(128)
+@pytest.mark.parametrize("rows,Hq,Hk,D", [(1500, 40, 8, 128), (4500, 8, 1, 64)])
+def test_the_batch_does_not_change_a_row(rows, Hq, Hk, D):
+    """Rows alone, in a few and in a long batch, and of heads that lie apart, come out with the same bits."""
+    qkv, position, slot, pages, (qw, kw) = _inputs(rows, Hq, Hk, D, BF)
+    q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hk], qkv[:, Hq + Hk:]
+    freq = _freq(D)
 
-    def call(n):
-        kc, vc = vs.packed_cache(pages, 8, 8, 128), vs.packed_cache(pages, 8, 8, 128)
+    def call(n, q=q):
+        kc, vc = vs.packed_cache(pages, 8, Hk, D), vs.packed_cache(pages, 8, Hk, D)
         out = vs.norm_rope_cache(q[:n], k[:n], v[:n], freq, position[:n].contiguous(), slot[:n].contiguous(), kc, vc, q_weight=qw, k_weight=kw)
         return out, *vs.cache_read_packed(kc, vc, slot[:n].contiguous())
 
-    long = call(1500)
+    long = call(rows)
     for n in (1, 7, 400):
         assert all(torch.equal(a, b[:n]) for a, b in zip(call(n), long))
+    apart = torch.zeros(rows, 2 * Hq, D, dtype=BF, device="cuda")[:, ::2]
+    apart.copy_(q)
+    assert all(torch.equal(a, b) for a, b in zip(call(rows, apart), long))
 
 
 PACKED = [(1, 32, 8, 128, 128, 16), (1, 1, 1, 32, 2, 1), (7, 4, 2, 96, 32, 8), (33, 6, 3, 64, 22, 5), (2, 8, 8, 512, 512, 16),

@@ -5,12 +5,23 @@
 // position * freq[i] (rotary.cuh), all in fp32 from one read of the head, rounded once at
 // the end: to the stored type, or to the nearest of a group's 15 values (packed.cuh).
 //
-// Layout (norm_rope_kernel): a head lies over a group of lanes, a 16-byte vector each, in
-// the order of its elements, so that a load, a store, a group of 32 elements to code and
-// a head's sum of squares are each a few lanes side by side.  A pair's other half comes from
-// its lane by a shuffle, cosines, sines and weights stay in a lane's registers over all
-// heads of a token, and four steps' loads go out together.  A warp takes a part of a
-// token's heads at a time.  Bound by memory.
+// Layout: a head lies over a group of lanes, a 16-byte vector each, in the order of its
+// elements, so that a load, a store, a group of 32 elements to code and a head's sum of
+// squares are each a few lanes side by side.  A pair's other half comes from its lane by a shuffle, and
+// what a lane's elements are taken times (weights, cosines, sines) stays in its registers over
+// a token's heads.
+//
+// Heads that lie side by side (norm_rope_bulk_kernel): bulk copies through a ring of tokens in
+// shared memory.  Strided heads and small batches of small rows (norm_rope_kernel): a warp takes a
+// part of a token's heads, four steps' loads together.  Pairs that are not whole vectors,
+// larger heads and odd strides (norm_rope_general_kernel): other halves from shared memory.
+// The first two give a row the same bits.
+// Bound by memory in long batches: 40001 rows of 40 heads of 128 in bf16 135 us (6.05 TB/s; the
+// ring without arithmetic 126), 2560 rows of 80 heads 25.2 (21.1), where the second kernel takes
+// 391 and 76.  Rows of 20 KB: one row 4.8 and 5.6 us, 456 rows 8.2 and 13.0; rows of 5 KB: 76 rows
+// 3.9 and 5.5, 2432 rows 11.2 and 18.1; rows of 1.2 KB: 2432 rows 6.8 and 6.4, 4864 rows 10.7
+// and 12.8, hence kBulkRow and kBulkBytes.  Three blocks an SM for two: 24.9 and 26.5 us at 2560
+// rows; the coding's registers allow two.
 #include "norm_rope.cuh"
 
 #include <algorithm>
@@ -658,6 +669,9 @@ __global__ void __launch_bounds__(kBulkThreads, bulk_blocks(PACKED))
   }
 }
 
+// Rows of 4 KB or more, or batches of 4 MB (measured at the top).
+constexpr size_t kBulkRow = 4096, kBulkBytes = 4000000;
+
 // Shared memory of a block with `stages` stages.
 template <typename T>
 size_t bulk_bytes(const spec_norm_rope_args& a, int tokens, int stages) {
@@ -665,26 +679,31 @@ size_t bulk_bytes(const spec_norm_rope_args& a, int tokens, int stages) {
   return stages * tokens * row + sizeof(Ring) + (half + 1) / 2 * 16 + (size_t)(2 + stages * tokens * 4) * a.D * sizeof(float);
 }
 constexpr size_t kBulkMemory = 222 * 1024, kStageBytes = 20 * 1024;
-constexpr size_t kBulkBytes = 12000000;  // of a batch, from which on
-constexpr int kBulkRows = 608;           // four tokens an SM
 template <typename T, bool PACKED>
 bool launch_bulk(const spec_norm_rope_args& a, int lanes, cudaStream_t stream, cudaError_t* err) {
   const size_t row = (size_t)(a.Hq + 2 * a.Hk) * a.D * sizeof(T);
   auto dense = [&](int n, int64_t head) { return n < 2 || head == a.D; };  // heads side by side
-  if (a.rows < kBulkRows || a.rows * row < kBulkBytes || !dense(a.Hq, a.q_head) || !dense(a.Hq, a.q_out_head) || !dense(a.Hk, a.k_head) ||
-      !dense(a.Hk, a.v_head))
-    return false;
-  int tokens = std::min({kWarps, a.rows / kBulkRows, std::max(1, (int)(kStageBytes / row))});
-  while (tokens & (tokens - 1)) tokens &= tokens - 1;
-  constexpr int kBlocks = bulk_blocks(PACKED);
-  int stages = kMaxStages;
-  while (stages > 1 && bulk_bytes<T>(a, tokens, stages) > kBulkMemory / kBlocks) --stages;
-  if (stages < 3) return false;
+  if (!dense(a.Hq, a.q_head) || !dense(a.Hq, a.q_out_head) || !dense(a.Hk, a.k_head) || !dense(a.Hk, a.v_head)) return false;
+  if (row < kBulkRow && a.rows * row < kBulkBytes) return false;
+  // Stages of up to 20 KB, one token each until every block has one; three stages at least, with fewer tokens or
+  // blocks an SM where they do not fit.
+  int tokens = 0, stages = 0, blocks = bulk_blocks(PACKED);
+  for (;; --blocks) {
+    if (blocks == 0) return false;
+    tokens = std::max(1, std::min({kWarps, a.rows / (152 * blocks), (int)(kStageBytes / row)}));
+    while (tokens & (tokens - 1)) tokens &= tokens - 1;
+    auto fit = [&] {
+      for (stages = kMaxStages; stages > 0 && bulk_bytes<T>(a, tokens, stages) > kBulkMemory / blocks;) --stages;
+      return stages >= 3;
+    };
+    while (!fit() && tokens > 1) tokens /= 2;
+    if (stages >= 3) break;
+  }
   auto kernel = a.layout == SPEC_ROPE_INTERLEAVED ? norm_rope_bulk_kernel<T, true, PACKED> : norm_rope_bulk_kernel<T, false, PACKED>;
-  *err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kBulkMemory / kBlocks));
+  *err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBulkMemory);
   if (*err != cudaSuccess) return true;
   const int groups = (a.rows + tokens - 1) / tokens;
-  kernel<<<std::min(groups, kBlocks * 152), kBulkThreads, bulk_bytes<T>(a, tokens, stages), stream>>>(a, tokens, stages, lanes);
+  kernel<<<std::min(groups, blocks * 152), kBulkThreads, bulk_bytes<T>(a, tokens, stages), stream>>>(a, tokens, stages, lanes);
   *err = cudaGetLastError();
   return true;
 }
