@@ -286,7 +286,7 @@ def test_refusals():
                                 ((kc, vc), dict(k_weight=kw.cpu()), TypeError), ((kc, pv), {}, ValueError), ((pk, vc), {}, ValueError),
                                 ((pk, (pv[0][:1], pv[1][:1])), {}, ValueError), ((pk, (pv[0], pv[1][..., :1])), {}, ValueError),
                                 (((pk[0].float(), pk[1]), pv), {}, TypeError), ((pk, (pv[0].transpose(1, 2), pv[1])), {}, ValueError),
-                                ((kc.bfloat16(), vc), {}, TypeError), ((kc, vc), dict(eps=-1.0), vs.SpecError),
+                                ((None, vc), {}, TypeError), ((list(pk), pv), {}, TypeError), ((kc.bfloat16(), vc), {}, TypeError), ((kc, vc), dict(eps=-1.0), vs.SpecError),
                                 ((kc, vc), dict(eps=math.nan), vs.SpecError), ((kc[:1], vc), {}, ValueError)):
         with pytest.raises(err):
             vs.norm_rope_cache(*ok, *caches, **kwargs)

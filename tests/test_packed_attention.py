@@ -162,6 +162,9 @@ TENSOR = [
     ([1, 2, 30], [1500, 9000, 200], 12, 2, 64, 8, ((1, 3000), (2, 100))),
     ([1] * 6, [5000, 4097, 129, 1, 70, 12000], 14, 1, 128, 8, ()),
     ([1, 40], [5000, 9000], 6, 1, 64, 640, ()),
+    ([1] * 30 + [200], [40 + 31 * i for i in range(31)], 2, 1, 128, 16, ()),
+    ([1] * 60 + [150], [1 + 17 * i for i in range(61)], 1, 1, 128, 32, ()),
+    ([1] * 20 + [90], [200] * 20 + [95], 6, 3, 64, 64, ()),
 ]
 
 
@@ -208,9 +211,9 @@ def test_a_row_of_nan_stays_alone(n, bad):
     assert torch.equal(got[:c.off[-1]][live], want[:c.off[-1]][live]) and bool(torch.isnan(got[1, 3]).any())
 
 
-@pytest.mark.parametrize("each,Hq,Hk", [(4, 64, 8), (1, 256, 2), (9, 64, 16)])
+@pytest.mark.parametrize("each,Hq,Hk", [(4, 64, 8), (1, 256, 2), (9, 64, 16), (4, 16, 4)])
 def test_calls_of_many_rows_run_in_windows(each, Hq, Hk):
-    """More than 2^20 query rows: by the narrow kernel in several items a segment, or by both."""
+    """More than 2^20 query rows: by the narrow kernel alone (16 rows a segment), or by both."""
     R = (1 << 20) // Hq // each + 700
     kv = [each + (i * 37) % 90 for i in range(R)]
     c = Case([each] * R, kv, Hq, Hk, 64, 16, BF, ((R // 2, 130),) if each == 9 else ())
@@ -323,6 +326,30 @@ def test_refusals():
     a = args()
     a[0], a[3] = c.q[:0], _i32([0, 0])
     assert vs.prefix_attention_packed(*a).shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("dt,n", [(BF, 1), (BF, 9), (F32, 2)])
+def test_pages_past_two_gigabytes(dt, n):
+    """Keys at the end of caches of 2.3 GB give the bits that they give in small ones."""
+    Hq, Hk, D, P, R, kv = 16, 8, 128, 64, 3, 150
+    many, few = 70001, 3 * R
+    g = torch.Generator("cuda").manual_seed(5)
+    x = torch.randn(R * kv, Hq + 2 * Hk, D, generator=g, device="cuda").to(dt)
+    pos = torch.arange(R * kv, dtype=torch.int32, device="cuda")
+    freq, _ = vs.rope_frequencies(D)
+    q = x[:R * n, :Hq].contiguous()
+    place = np.arange(kv)
+    outs = []
+    for pages in (many, few):
+        kc, vc = vs.packed_cache(pages, P, Hk, D), vs.packed_cache(pages, P, Hk, D)
+        table = pages - few + np.arange(few).reshape(R, 3)
+        slot = _i32(np.concatenate([table[r][place // P] * P + place % P for r in range(R)]))
+        turned = vs.norm_rope_cache(x[:, :Hq], x[:, Hq:Hq + Hk], x[:, Hq + Hk:], freq, pos, slot, kc, vc)
+        k, v = vs.cache_read_packed(kc, vc, slot)
+        o = vs.prefix_attention_packed(q, kc, vc, _i32(np.arange(R + 1) * n), _i32([kv] * R), _i32(table))
+        outs.append((turned, k, v, o))
+        del kc, vc
+    assert all(torch.equal(a, b) for a, b in zip(*outs)) and float(outs[0][3].float().abs().max()) > 0
 
 
 @pytest.mark.parametrize("dt,Hq,Hk,D,P", [(BF, 16, 2, 128, 16), (F32, 6, 2, 96, 24)])

@@ -386,6 +386,8 @@ def norm_rope_cache(q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torc
         Hk = k.shape[1]
         kp, kr, kh = _strided(k, "k", dt, (rows, Hk, D), dev)
         vp, vr, vh = _strided(v, "v", dt, (rows, Hk, D), dev)
+        if not isinstance(k_cache, (tuple, _Tensor)) or not isinstance(v_cache, (tuple, _Tensor)):
+            raise TypeError("k_cache and v_cache must be tensors or pairs of packed_cache")
         if isinstance(k_cache, tuple) != isinstance(v_cache, tuple):
             raise ValueError("k_cache and v_cache must be of one kind")
         if isinstance(k_cache, tuple):
