@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_general_kernel(spec_norm_r
   }
 }
 
-// ------------------------------------------------------------ long batches --
+// ---------------------------------------------------------------- bulk rows --
 // Rows whose heads lie side by side, by bulk copies through a ring of stages in shared
 // memory, a few tokens each: one warp issues loads and stores, one computes the
 // cosines of the stages ahead, the others take heads as above, in place where a bulk store
