@@ -298,3 +298,22 @@ def test_refusals():
     with pytest.raises(ValueError):
         vs.packed_cache(1, 8, 1, 48)
     assert vs.cache_read_packed(pk, pv, slot[:0])[0].shape == (0, 1, 64)
+
+
+def test_scales_on_both_sides_of_their_borders():
+    """A group whose largest magnitude is 7 h, h half way between two scales, takes the larger one; the next smaller number
+    the smaller one."""
+    D, P = 32, 5
+    code = torch.arange(1, 255, dtype=torch.float64)
+    scale = lambda c: torch.exp2((c // 8) - 20) * (1 + c % 8 / 8)  # noqa: E731
+    border = (7 * (scale(code - 1) + scale(code)) / 2).float()
+    v = torch.zeros(2 * len(code), 1, D)
+    v[:len(code), 0, 3] = border
+    v[len(code):, 0, 3] = torch.nextafter(border, torch.zeros(()))
+    v[::2] *= -1
+    pages = -(-len(v) // P)
+    kc, vc = vs.packed_cache(pages, P, 1, D), vs.packed_cache(pages, P, 1, D)
+    slot = torch.arange(len(v), dtype=torch.int32, device="cuda")
+    vs.norm_rope_cache(v.cuda(), torch.zeros_like(v).cuda(), v.cuda(), _freq(0), torch.zeros_like(slot), slot, kc, vc)
+    got = vc[1].flatten().cpu().long()[:len(v)]
+    assert torch.equal(got, torch.cat([code, code - 1]).long())

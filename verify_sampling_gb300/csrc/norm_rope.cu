@@ -25,7 +25,6 @@
 #include "norm_rope.cuh"
 
 #include <algorithm>
-#include <type_traits>
 
 #include "packed.cuh"
 #include "rotary.cuh"
@@ -164,6 +163,53 @@ __device__ __forceinline__ float larger(float a, float b) {
   return r;
 }
 
+__device__ __forceinline__ float larger(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
+  return r;
+}
+
+// Codes of M groups' scales and a lane's VEC elements of each as nibbles, for all lanes of the
+// warp; side by side, as each is a chain of dependent steps.
+template <int VEC, int M>
+__device__ __forceinline__ void code_groups(float (&y)[M][VEC], uint32_t (&w)[M], uint32_t (&code)[M]) {
+  auto codes = [&] {
+    float most[M];
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      most[m] = fabsf(y[m][0]);
+#pragma unroll
+      for (int e = 1; e + 1 < VEC; e += 2) most[m] = larger(most[m], y[m][e], y[m][e + 1]);
+      if (VEC % 2 == 0) most[m] = larger(most[m], y[m][VEC - 1]);
+    }
+#pragma unroll
+    for (int o = 1; o < q4::kGroup / VEC; o <<= 1)
+#pragma unroll
+      for (int m = 0; m < M; ++m) most[m] = larger(most[m], __shfl_xor_sync(0xffffffffu, most[m], o));
+    uint32_t largest = 0;
+#pragma unroll
+    for (int m = 0; m < M; ++m) largest = max(largest, code[m] = q4::code_of(most[m]));
+    return largest;
+  };
+  if (__any_sync(0xffffffffu, codes() == 255)) {  // NaN is stored as 0, what is past the largest scale as 7 of it
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (y[m][e] != y[m][e]) y[m][e] = 0.f;
+    codes();
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) y[m][e] = fminf(fmaxf(y[m][e], -7.f * q4::scale_of(code[m])), 7.f * q4::scale_of(code[m]));
+  }
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    const float s = q4::scale_of(code[m]);
+    w[m] = q4::nibbles_of(y[m], s, q4::reciprocal(s));
+  }
+}
+
 // Codes a lane's VEC elements of each chunk and writes them to the token's head in the cache.
 // All lanes of the warp call it; `on`: this one's head is written.
 template <int VEC, int CH>
@@ -172,42 +218,19 @@ __device__ __forceinline__ void store_packed(const float (&from)[CH * VEC], int 
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int d = first + c * step;  // this lane's first element
-    float y[VEC];
+    float y[1][VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) y[e] = from[c * VEC + e];
-    auto largest = [&] {
-      float m = fabsf(y[0]);
-#pragma unroll
-      for (int e = 1; e < VEC; ++e) m = larger(m, y[e]);
-#pragma unroll
-      for (int o = 1; o < q4::kGroup / VEC; o <<= 1) m = larger(m, __shfl_xor_sync(0xffffffffu, m, o));
-      return m;
-    };
-    float amax = largest();
-    if (__any_sync(0xffffffffu, amax != amax)) {  // NaN is stored as 0
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        if (y[e] != y[e]) y[e] = 0.f;
-      amax = largest();
-    }
-    const uint32_t code = q4::code_of(amax);
-    const float s = q4::scale_of(code);
-    if (__any_sync(0xffffffffu, code == 255)) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) y[e] = fminf(fmaxf(y[e], -7.f * s), 7.f * s);
-    }
-    const float inv = __fdividef(1.f, s);
-    uint32_t w = 0;
-#pragma unroll
-    for (int e = VEC - 1; e >= 0; --e) w = w * 16u + (q4::number_of(y[e], s, inv) & 15u);
-    w ^= VEC == 8 ? 0x88888888u : VEC == 4 ? 0x8888u : 8u;  // n + 8
+    for (int e = 0; e < VEC; ++e) y[0][e] = from[c * VEC + e];
+    uint32_t words[1], code[1];
+    code_groups<VEC, 1>(y, words, code);
+    uint32_t w = words[0];
     if (VEC < 8) w <<= 4 * (d & 7);
 #pragma unroll
     for (int o = 1; o < 8 / VEC; o <<= 1) w |= __shfl_xor_sync(0xffffffffu, w, o);
     if (!on || d >= D) continue;
     const int g = d / q4::kGroup, in_g = d % q4::kGroup;
     if (in_g % 8 == 0) *reinterpret_cast<uint32_t*>(data + (size_t)g * 16 * P + in_g / 2) = w;
-    if (in_g == 0) scale[g] = (uint8_t)code;
+    if (in_g == 0) scale[g] = (uint8_t)code[0];
   }
 }
 
@@ -458,9 +481,11 @@ constexpr int bulk_blocks(bool packed) { return packed ? 2 : 3; }  // an SM
 constexpr int kMaxStages = 4;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
+template <bool PACKED>
 struct Ring {
   uint64_t full[kMaxStages], done[kMaxStages], freed[kMaxStages];
   int2 at[kMaxStages][kWarps];  // position (-1: left out) and slot (-1: none) of a stage's tokens
+  longlong2 packed_at[PACKED ? kMaxStages : 1][kWarps];  // first bytes of the slots' data and scales in a cache of 4 bits
 };
 
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t phase) {
@@ -477,7 +502,7 @@ __global__ void __launch_bounds__(kBulkThreads, bulk_blocks(PACKED))
   const int half = p.rot >> 1, turned = p.Hq + p.Hk;
   const uint32_t head_bytes = p.D * (uint32_t)sizeof(T), row_bytes = (turned + p.Hk) * head_bytes;
   const uint32_t stage_bytes = tokens * row_bytes;
-  Ring& ring = *reinterpret_cast<Ring*>(bulk_s + stages * stage_bytes);
+  Ring<PACKED>& ring = *reinterpret_cast<Ring<PACKED>*>(bulk_s + stages * stage_bytes);
   float2* turns = reinterpret_cast<float2*>(&ring + 1);
   float* weight_s = reinterpret_cast<float*>(turns + ((half + 1) & ~1));  // [queries, keys][D]
   // what a lane's elements and the others of their pairs are taken times:
@@ -583,7 +608,14 @@ __global__ void __launch_bounds__(kBulkThreads, bulk_blocks(PACKED))
       if (at.y >= p.n_slots) bad |= SPEC_STATUS_BAD_PAGE, at.y = -1;
       const float x = (float)min(max(at.x, 0), (1 << 24) - 1);
       if (i >= stages && !__all_sync(0xffffffffu, wait_for(&ring.freed[st], i / stages - 1))) break;
-      if (lane < tokens) ring.at[st][lane] = at;
+      if (lane < tokens) {
+        ring.at[st][lane] = at;
+        if (PACKED && at.y >= 0) {
+          const int page = at.y / p.page_size, tok = at.y - page * p.page_size, groups_of = p.D / q4::kGroup;
+          ring.packed_at[st][lane] = make_longlong2(q4::data_at(page, 0, tok, p.Hk, groups_of, p.page_size),
+                                                    q4::scale_at(page, 0, tok, p.Hk, groups_of, p.page_size));
+        }
+      }
       for (int t = 0; t < tokens; ++t) {
         const float pos = __shfl_sync(0xffffffffu, x, t);
         float* of = factor_s + (size_t)(st * tokens + t) * 4 * p.D;
@@ -611,9 +643,12 @@ __global__ void __launch_bounds__(kBulkThreads, bulk_blocks(PACKED))
     const bool live = first < p.D;
     const float inv_d = 1.f / (float)p.D;
     const int other = (lane + (first < half ? half : -half) / VEC) & 31;  // half layout: where the other halves lie
-    for (int i = 0; i < n; ++i) {
-      const int st = i % stages;
-      if (!__all_sync(0xffffffffu, wait_for(&ring.full[st], i / stages))) break;
+    const uint32_t hop = each * at_once * head_bytes, head_codes = p.D / q4::kGroup * p.page_size;
+    const int group = first / q4::kGroup;  // the lane's, and its bytes from a head's first
+    const int64_t in_group = (int64_t)group * 16 * p.page_size + first % q4::kGroup / 2;
+    uint32_t phase = 0;
+    for (int i = 0, st = 0; i < n; ++i, st = st + 1 < stages ? st + 1 : (phase ^= 1u, 0)) {
+      if (!__all_sync(0xffffffffu, wait_for(&ring.full[st], phase))) break;
       const int2 at = ring.at[st][t];
       if (first_row(i) + t < p.rows && at.x >= 0) {
         Lane<T> lf;
@@ -628,39 +663,53 @@ __global__ void __launch_bounds__(kBulkThreads, bulk_blocks(PACKED))
           }
         };
         uint8_t* token = bulk_s + st * stage_bytes + t * row_bytes + first * sizeof(T);
-        const uint32_t hop = each * at_once * head_bytes;
-        const int page = PACKED && at.y >= 0 ? at.y / p.page_size : 0, tok = PACKED && at.y >= 0 ? at.y - page * p.page_size : 0;
-        const int groups_of = p.D / q4::kGroup;
-        auto heads = [&](auto kind_v, int begin, int count, const float* weight, void* cache, uint8_t* scales) {
-          constexpr int kind = decltype(kind_v)::value;
-          if (kind < 2) factors_of(kind);
-          uint8_t *data = nullptr, *codes = nullptr;  // of the token's head 0
-          if (PACKED && kind > 0) {
-            data = (uint8_t*)cache + q4::data_at(page, 0, tok, p.Hk, groups_of, p.page_size);
-            codes = scales + q4::scale_at(page, 0, tok, p.Hk, groups_of, p.page_size);
-          }
-          const uint32_t head_codes = groups_of * p.page_size;
+        auto heads = [&](int kind, int begin, int count, const float* weight) {  // in place
+          factors_of(kind);
           uint8_t* from = token + (uint32_t)(begin + in_t * at_once + sub) * head_bytes;
           for (int h0 = in_t * at_once; h0 < count; h0 += each * at_once, from += hop) {
-            const bool on = h0 + sub < count;
+            const bool on = h0 + sub < count && live;
             uint4 v = make_uint4(0, 0, 0, 0);
-            if (on && live) v = *reinterpret_cast<const uint4*>(from);
+            if (on) v = *reinterpret_cast<const uint4*>(from);
             uint64_t y[N];
-            if (kind == 2) unpack(v, y, T());
-            else norm_turn<T, INTER>(v, y, lf, weight != nullptr, lanes, other, inv_d, p.eps);
-            if (PACKED && kind > 0) {
-              float yf[VEC];
-              spread(y, yf);
-              const uint32_t at_head = (on ? h0 + sub : 0) * head_codes;  // (a page's bytes are below 2^31)
-              store_packed<VEC, 1>(yf, first, 32 * VEC, p.D, on && at.y >= 0, data + (size_t)at_head * 16, codes + at_head, p.page_size);
-            } else if (on && live) {
-              *reinterpret_cast<uint4*>(from) = packed_up(y, T());
-            }
+            norm_turn<T, INTER>(v, y, lf, weight != nullptr, lanes, other, inv_d, p.eps);
+            if (on) *reinterpret_cast<uint4*>(from) = packed_up(y, T());
           }
         };
-        heads(std::integral_constant<int, 0>(), 0, p.Hq, p.q_weight, nullptr, nullptr);
-        heads(std::integral_constant<int, 1>(), p.Hq, p.Hk, p.k_weight, p.k_cache, p.k_scale);
-        if (PACKED) heads(std::integral_constant<int, 2>(), turned, p.Hk, nullptr, p.v_cache, p.v_scale);
+        heads(0, 0, p.Hq, p.q_weight);
+        if (!PACKED) {
+          heads(1, p.Hq, p.Hk, p.k_weight);
+        } else {  // a head of keys and its values together
+          factors_of(1);
+          const longlong2 to = at.y >= 0 ? ring.packed_at[st][t] : make_longlong2(0, 0);
+          const uint8_t* from = token + (uint32_t)(p.Hq + in_t * at_once + sub) * head_bytes;
+          const int64_t data_at = to.x + in_group, scale_at = to.y + group;
+          for (int h0 = in_t * at_once; h0 < p.Hk; h0 += each * at_once, from += hop) {
+            const bool on = h0 + sub < p.Hk && live;
+            uint4 k = make_uint4(0, 0, 0, 0), v = k;
+            if (on) k = *reinterpret_cast<const uint4*>(from), v = *reinterpret_cast<const uint4*>(from + p.Hk * head_bytes);
+            uint64_t y[N];
+            float both[2][VEC];
+            norm_turn<T, INTER>(k, y, lf, p.k_weight != nullptr, lanes, other, inv_d, p.eps);
+            spread(y, both[0]);
+            unpack(v, y, T());
+            spread(y, both[1]);
+            uint32_t w[2], code[2];
+            code_groups<VEC, 2>(both, w, code);
+#pragma unroll
+            for (int m = 0; m < 2 && VEC < 8; ++m) {
+              w[m] <<= 4 * (first & 7);
+              w[m] |= __shfl_xor_sync(0xffffffffu, w[m], 1);
+            }
+            if (!on || at.y < 0) continue;
+            const uint32_t head = (h0 + sub) * head_codes;  // (a page's bytes are below 2^31)
+            const int64_t d_at = data_at + head * (size_t)16, s_at = scale_at + head;
+            if (first % 8 == 0) {
+              *reinterpret_cast<uint32_t*>((uint8_t*)p.k_cache + d_at) = w[0];
+              *reinterpret_cast<uint32_t*>((uint8_t*)p.v_cache + d_at) = w[1];
+            }
+            if (first % q4::kGroup == 0) p.k_scale[s_at] = (uint8_t)code[0], p.v_scale[s_at] = (uint8_t)code[1];
+          }
+        }
       }
       tc::fence_proxy_async();
       __syncwarp();
@@ -673,10 +722,10 @@ __global__ void __launch_bounds__(kBulkThreads, bulk_blocks(PACKED))
 constexpr size_t kBulkRow = 4096, kBulkBytes = 4000000;
 
 // Shared memory of a block with `stages` stages.
-template <typename T>
+template <typename T, bool PACKED>
 size_t bulk_bytes(const spec_norm_rope_args& a, int tokens, int stages) {
   const size_t half = a.rot / 2, row = (size_t)(a.Hq + 2 * a.Hk) * a.D * sizeof(T);
-  return stages * tokens * row + sizeof(Ring) + (half + 1) / 2 * 16 + (size_t)(2 + stages * tokens * 4) * a.D * sizeof(float);
+  return stages * tokens * row + sizeof(Ring<PACKED>) + (half + 1) / 2 * 16 + (size_t)(2 + stages * tokens * 4) * a.D * sizeof(float);
 }
 constexpr size_t kBulkMemory = 222 * 1024, kStageBytes = 20 * 1024;
 template <typename T, bool PACKED>
@@ -693,7 +742,7 @@ bool launch_bulk(const spec_norm_rope_args& a, int lanes, cudaStream_t stream, c
     tokens = std::max(1, std::min({kWarps, a.rows / (152 * blocks), (int)(kStageBytes / row)}));
     while (tokens & (tokens - 1)) tokens &= tokens - 1;
     auto fit = [&] {
-      for (stages = kMaxStages; stages > 0 && bulk_bytes<T>(a, tokens, stages) > kBulkMemory / blocks;) --stages;
+      for (stages = kMaxStages; stages > 0 && bulk_bytes<T, PACKED>(a, tokens, stages) > kBulkMemory / blocks;) --stages;
       return stages >= 3;
     };
     while (!fit() && tokens > 1) tokens /= 2;
@@ -703,7 +752,7 @@ bool launch_bulk(const spec_norm_rope_args& a, int lanes, cudaStream_t stream, c
   *err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBulkMemory);
   if (*err != cudaSuccess) return true;
   const int groups = (a.rows + tokens - 1) / tokens;
-  kernel<<<std::min(groups, blocks * 152), kBulkThreads, bulk_bytes<T>(a, tokens, stages), stream>>>(a, tokens, stages, lanes);
+  kernel<<<std::min(groups, blocks * 152), kBulkThreads, bulk_bytes<T, PACKED>(a, tokens, stages), stream>>>(a, tokens, stages, lanes);
   *err = cudaGetLastError();
   return true;
 }

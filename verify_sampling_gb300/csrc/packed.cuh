@@ -14,6 +14,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "tc.cuh"
 
 namespace spec {
 namespace q4 {
@@ -39,19 +40,52 @@ __host__ __device__ __forceinline__ int64_t scale_at(int64_t page, int h, int to
 __device__ __forceinline__ float scale_of(uint32_t code) {
   return __uint_as_float((code << 20) + ((uint32_t)kLeastExp << 23));
 }
-// Code of a group's largest magnitude / 7 (half a step is added to the bits: halves go up).
+// Code of a group's largest magnitude / 7, 255 for NaN (half a step is added to the bits: halves go up).
+// The product with 1 / 7, whose nearest fp32 is 0.75 2^-24 too large, is rounded down: for a half
+// way point h, 7 h is a number of 8 bits and its product (1 + 0.75 2^-24) h or h, and the number
+// below 7 h is at least 4/7 of h's last place below after division, its product below h.  So
+// this is the code of the rounded quotient, for every magnitude.
 __device__ __forceinline__ uint32_t code_of(float amax) {
-  const int bits = __float_as_int(__fdiv_rn(amax, 7.f));
-  return (uint32_t)min(max(((bits + (1 << 19)) >> 20) - 8 * kLeastExp, 0), 255);
+  const uint32_t bits = __float_as_uint(__fmul_rz(amax, 1.f / 7.f));  // (below 2^31, the sum of a NaN's not)
+  return (uint32_t)min(max((int)((bits + (1u << 19)) >> 20) - 8 * kLeastExp, 0), 255);
 }
-// x / s to the nearest whole number, halves to even, in the low four bits, for |x| < 7.5 s; `inv` is 1 / s
-// within an ulp or two.  The product with it may miss a half that the quotient meets exactly
+__device__ __forceinline__ float reciprocal(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
+}
+// N x / s to the nearest whole numbers, halves to even, for |x| < 7.5 s, as nibbles n + 8, the first
+// lowest; `inv` is 1 / s within an ulp or two.
+// The product with it may miss a half that the quotient meets exactly
 // (16-bit values often do), so it is made a little small, and x - n s, which is exact, decides.
-__device__ __forceinline__ uint32_t number_of(float x, float s, float inv) {
-  const float t = fmaf(x, inv, -0x1p-18f) + 12582912.f;  // 1.5 2^23: the sum's low bits are the whole number
-  const float rest = fmaf(-(t - 12582912.f), s, x);
-  const int odd = __float_as_int(t) & 1;
-  return __float_as_uint(t) + (__float_as_int(rest) + odd > __float_as_int(0.5f * s));  // (below 0: a negative int)
+// The sum with 1.5 2^23 has the whole number in its low bits; what lies above them is the same for
+// all and taken off the word at its end.
+template <int N>
+__device__ __forceinline__ uint32_t nibbles_of(const float (&x)[N], float s, float inv) {
+  constexpr float kWhole = 12582912.f;
+  constexpr uint32_t kWholeBits = 0x4B400000u, kOnes = 0x11111111u >> (32 - 4 * N);
+  const int half = __float_as_int(0.5f * s);
+  uint32_t w = 0;
+  auto join = [&](float t, float rest) {
+    const int odd = __float_as_int(t) & 1;
+    w = w * 16u + __float_as_uint(t) + (__float_as_int(rest) + odd > half);  // (below 0: a negative int)
+  };
+  if constexpr (N == 1) {
+    const float t = fmaf(x[0], inv, -0x1p-18f) + kWhole;
+    join(t, fmaf(-(t - kWhole), s, x[0]));
+  } else {
+    const uint64_t inv2 = tc::pair(inv, inv), less = tc::pair(-s, -s);
+#pragma unroll
+    for (int e = N - 2; e >= 0; e -= 2) {
+      const uint64_t x2 = tc::pair(x[e], x[e + 1]);
+      const uint64_t t2 = tc::add2(tc::fma2(x2, inv2, tc::pair(-0x1p-18f, -0x1p-18f)), tc::pair(kWhole, kWhole));
+      const float2 t = tc::halves(t2), rest = tc::halves(tc::fma2(tc::add2(t2, tc::pair(-kWhole, -kWhole)), less, x2));
+      join(t.y, rest.y);
+      join(t.x, rest.x);
+    }
+  }
+  w += 8u * kOnes - kWholeBits * kOnes;
+  return N == 8 ? w : w & (0xffffffffu >> (32 - 4 * N));
 }
 
 // ------------------------------------------------ elements in bf16 pairs --
