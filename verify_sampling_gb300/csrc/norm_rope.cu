@@ -16,12 +16,14 @@
 // part of a token's heads, four steps' loads together.  Pairs that are not whole vectors,
 // larger heads and odd strides (norm_rope_general_kernel): other halves from shared memory.
 // The first two give a row the same bits.
-// Bound by memory in long batches: 40001 rows of 40 heads of 128 in bf16 135 us (6.05 TB/s; the
-// ring without arithmetic 126), 2560 rows of 80 heads 25.2 (21.1), where the second kernel takes
-// 391 and 76.  Rows of 20 KB: one row 4.8 and 5.6 us, 456 rows 8.2 and 13.0; rows of 5 KB: 76 rows
-// 3.9 and 5.5, 2432 rows 11.2 and 18.1; rows of 1.2 KB: 2432 rows 6.8 and 6.4, 4864 rows 10.7
+// Bound by memory in long batches: 40001 rows of 40 heads of 128 in bf16 132 us (6.20 TB/s; the
+// ring without arithmetic 126), 2560 rows of 80 heads 24.7 (21.1), where the second kernel takes
+// 391 and 76.  Rows of 20 KB: one row 4.6 and 5.6 us, 456 rows 8.2 and 13.0; rows of 5 KB: 76 rows
+// 3.9 and 5.5, 2432 rows 10.9 and 18.1; rows of 1.2 KB: 2432 rows 6.8 and 6.4, 4864 rows 10.4
 // and 12.8, hence kBulkRow and kBulkBytes.  Three blocks an SM for two: 24.9 and 26.5 us at 2560
-// rows; the coding's registers allow two.
+// rows.  Into 4 bits the arithmetic of the coding counts as well (0.6 instructions a clock and
+// scheduler): 2560 rows 27 us, 30011 rows of 4 KB 53.  Three blocks of 64 registers took 37 us for
+// 37.7 and, with smaller stages, 88 for 82 (both with the read-back), so these have two.
 #include "norm_rope.cuh"
 
 #include <algorithm>
