@@ -635,8 +635,10 @@ size_t spec_attention_workspace_bytes(int rows, int R, int Hq, int D);
  * k_cache, v_cache: [n_slots, Hk, D] of dtype, or the packed data, n_slots being n_pages *
  * page_size then; page_size and the scales are read for SPEC_CACHE_PACKED alone.  Rows
  * with equal slots leave data and scales of different rows there.
- * Squares are summed in fp32: a head of zeros with eps = 0 gives NaN, one whose sum of
- * squares passes fp32 (elements of 10^19) zeros.
+ * Heads of any size are normed: one whose mean square + eps leaves [2^-90, 2^90] is taken
+ * times a power of two first (weights times scale to 2^77 keep its products in fp32).  A head of
+ * zeros with eps = 0 gives NaN; an infinity gives NaN in its place and zeros beside it, and
+ * the pair that it turns with is NaN.
  * Everything else (positions, slots, strides, Hk = 0, Hq = 0, in place) as in
  * spec_rope_cache.  Sizes: its own, and eps >= 0 and finite.
  */

@@ -4,6 +4,10 @@
 // Mathematics: y = x w rsqrt(mean x^2 + eps), then pair i of a head turns by the angle
 // position * freq[i] (rotary.cuh), all in fp32 from one read of the head, rounded once at
 // the end: to the stored type, or to the nearest of a group's 15 values (packed.cuh).
+// A head whose mean square + eps is outside [2^-90, 2^90] is computed again, times a power of two
+// (norm_turn).  Asking for that costs every head a comparison and a vote, 1 to 3.5%: 2560 rows of 80 heads
+// 25.3 and 25.8 us, 40001 rows of 40 heads 133.8 and 138.2.  (A pass over all of a token's heads, and
+// another where one was not in range: 26.4 and 136, and 31.5 us for 30.8 at 2560 rows into 4 bits.)
 //
 // Layout: a head lies over a group of lanes, a 16-byte vector each, in the order of its
 // elements, so that a load, a store, a group of 32 elements to code and a head's sum of
@@ -27,6 +31,7 @@
 #include "norm_rope.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 #include "packed.cuh"
 #include "rotary.cuh"
@@ -104,31 +109,67 @@ __device__ __forceinline__ void factors(Lane<T>& f, const float* co, const float
     f.others[e / 2] = tc::pair(o[0], o[1]);
   }
 }
+// 1 / sqrt(x) of a normal number, 0 or infinity.
+__device__ __forceinline__ float rsqrt_of(float x) {
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// A mean square + eps in the middle of fp32's range: squares that vanished beside it, and its products with elements and weights to 2^77, do no harm.
+__device__ __forceinline__ bool in_range(float square) {
+  constexpr uint32_t kLeast = (127u - 90) << 23, kMost = (127u + 90) << 23;
+  return __float_as_uint(square) - kLeast <= kMost - kLeast;  // (a NaN's bits lie past them)
+}
+// The power of two that brings the larger of a head's largest magnitude (its bits) and sqrt(eps) to [1/4, 1/2): the head
+// times it has the same norm, with eps times its square, and squares, sums and products of ordinary size.
+__device__ __forceinline__ float unit_of(uint32_t most, float eps) {
+  const int f = 252 - (int)min(max(most, __float_as_uint(sqrtf(eps))) >> 23, 254u);
+  return __uint_as_float(f > 0 ? (uint32_t)f << 23 : 0x400000u >> -f);
+}
 // All lanes of a warp call it; a head is `lanes` of them, `other` the lane of the other halves (half layout).
-template <typename T, bool INTER>
-__device__ __forceinline__ void norm_turn(const uint4& v, uint64_t (&y)[Lane<T>::VEC / 2], const Lane<T>& f, bool norm, int lanes, int other,
+// `load(again)` gives the lane's elements; a head out of range asks for them again (kept, they would take registers of all).
+template <typename T, bool INTER, class Load>
+__device__ __forceinline__ void norm_turn(Load load, uint64_t (&y)[Lane<T>::VEC / 2], const Lane<T>& f, bool norm, int lanes, int other,
                                           float inv_d, float eps) {
   constexpr int N = Lane<T>::VEC / 2;
   uint64_t x[N], z[N];
-  unpack(v, x, T());
-  if (INTER) {
+  auto elements = [&](auto again) {
+    const uint4 v = load(again);
+    unpack(v, x, T());
+    if (INTER) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const float2 t = tc::halves(x[e]);
-      z[e] = tc::pair(t.y, t.x);
+      for (int e = 0; e < N; ++e) {
+        const float2 t = tc::halves(x[e]);
+        z[e] = tc::pair(t.y, t.x);
+      }
+    } else {
+      uint4 w;
+      w.x = __shfl_sync(0xffffffffu, v.x, other), w.y = __shfl_sync(0xffffffffu, v.y, other);
+      w.z = __shfl_sync(0xffffffffu, v.z, other), w.w = __shfl_sync(0xffffffffu, v.w, other);
+      unpack(w, z, T());
     }
-  } else {
-    uint4 w;
-    w.x = __shfl_sync(0xffffffffu, v.x, other), w.y = __shfl_sync(0xffffffffu, v.y, other);
-    w.z = __shfl_sync(0xffffffffu, v.z, other), w.w = __shfl_sync(0xffffffffu, v.w, other);
-    unpack(w, z, T());
-  }
-  if (!f.turning) {
+    if (!f.turning) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) z[e] = 0;  // (what is not its pair may be NaN)
-  }
+      for (int e = 0; e < N; ++e) z[e] = 0;  // (what is not its pair may be NaN)
+    }
+  };
+  auto turned = [&] {
 #pragma unroll
-  for (int e = 0; e < N; ++e) y[e] = tc::fma2(x[e], f.mine[e], tc::mul2(z[e], f.others[e]));
+    for (int e = 0; e < N; ++e) y[e] = tc::fma2(x[e], f.mine[e], tc::mul2(z[e], f.others[e]));
+  };
+  auto squares = [&] {
+    uint64_t sum2 = tc::mul2(x[0], x[0]);
+#pragma unroll
+    for (int e = 1; e < N; ++e) sum2 = tc::fma2(x[e], x[e], sum2);
+    const float2 s = tc::halves(sum2);
+    float sum = s.x + s.y;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+      if (o < lanes) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+  };
+  elements(std::false_type{});
+  turned();
   if (!norm) {
     if (!f.turning) {
 #pragma unroll
@@ -136,15 +177,26 @@ __device__ __forceinline__ void norm_turn(const uint4& v, uint64_t (&y)[Lane<T>:
     }
     return;
   }
-  uint64_t sum2 = tc::mul2(x[0], x[0]);
+  float square = fmaf(squares(), inv_d, eps);
+  if (!__all_sync(0xffffffffu, in_range(square))) {
+    elements(std::true_type{});
+    uint32_t most = 0;
 #pragma unroll
-  for (int e = 1; e < N; ++e) sum2 = tc::fma2(x[e], x[e], sum2);
-  const float2 s = tc::halves(sum2);
-  float sum = s.x + s.y;
+    for (int e = 0; e < N; ++e) {
+      const float2 t = tc::halves(x[e]);
+      most = max(most, max(__float_as_uint(fabsf(t.x)), __float_as_uint(fabsf(t.y))));
+    }
+    for (int o = 1; o < lanes; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    const float unit = in_range(square) ? 1.f : unit_of(most, eps);  // each head by itself: its bits do not depend on its neighbours
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1)
-    if (o < lanes) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const float r = rsqrtf(fmaf(sum, inv_d, eps));
+    for (int e = 0; e < N; ++e) {
+      x[e] = tc::mul2(x[e], tc::pair(unit, unit));
+      z[e] = tc::mul2(z[e], tc::pair(unit, unit));
+    }
+    turned();
+    square = fmaf(squares(), inv_d, eps * unit * unit);
+  }
+  const float r = rsqrt_of(square);
 #pragma unroll
   for (int e = 0; e < N; ++e) y[e] = tc::mul2(y[e], tc::pair(r, r));
 }
@@ -318,7 +370,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(spec_norm_rope_args
             factors<T, INTER>(lf, co, si, live ? weight : nullptr, first, half);
             have = kind;
           }
-          norm_turn<T, INTER>(x[i], y, lf, weight != nullptr, lanes, other, inv_d, p.eps);
+          norm_turn<T, INTER>([&](auto) { return x[i]; }, y, lf, weight != nullptr, lanes, other, inv_d, p.eps);
         }
         if (PACKED && kind > 0) {
           float yf[VEC];
@@ -416,11 +468,25 @@ __global__ void __launch_bounds__(kThreads) norm_rope_general_kernel(spec_norm_r
           for (int e = 0; e < VEC; ++e) y[c * VEC + e] = first + c * step < p.D ? to_f(x[i][c].e[e]) : 0.f;
         const float* weight = kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr;
         if (weight) {
-          float sum = 0.f;
+          auto squares = [&] {
+            float sum = 0.f;
 #pragma unroll
-          for (int e = 0; e < CH * VEC; ++e) sum = fmaf(y[e], y[e], sum);
-          for (int o = 1; o < (CH == 1 ? lanes : 32); o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          const float r = rsqrtf(fmaf(sum, inv_d, p.eps));
+            for (int e = 0; e < CH * VEC; ++e) sum = fmaf(y[e], y[e], sum);
+            for (int o = 1; o < (CH == 1 ? lanes : 32); o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            return sum;
+          };
+          float square = fmaf(squares(), inv_d, p.eps);
+          if (!__all_sync(0xffffffffu, in_range(square))) {  // as norm_turn
+            uint32_t most = 0;
+#pragma unroll
+            for (int e = 0; e < CH * VEC; ++e) most = max(most, __float_as_uint(fabsf(y[e])));
+            for (int o = 1; o < (CH == 1 ? lanes : 32); o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+            const float unit = in_range(square) ? 1.f : unit_of(most, p.eps);
+#pragma unroll
+            for (int e = 0; e < CH * VEC; ++e) y[e] *= unit;
+            square = fmaf(squares(), inv_d, p.eps * unit * unit);
+          }
+          const float r = rsqrt_of(square);
 #pragma unroll
           for (int c = 0; c < CH; ++c)
             if (first + c * step < p.D)
@@ -665,15 +731,18 @@ __global__ void __launch_bounds__(kBulkThreads, bulk_blocks(PACKED))
           }
         };
         uint8_t* token = bulk_s + st * stage_bytes + t * row_bytes + first * sizeof(T);
+        auto elements = [](const uint8_t* from, bool on, auto again) {  // from shared memory
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (on) v = again.value ? tc::lds128(from) : *reinterpret_cast<const uint4*>(from);
+          return v;
+        };
         auto heads = [&](int kind, int begin, int count, const float* weight) {  // in place
           factors_of(kind);
           uint8_t* from = token + (uint32_t)(begin + in_t * at_once + sub) * head_bytes;
           for (int h0 = in_t * at_once; h0 < count; h0 += each * at_once, from += hop) {
             const bool on = h0 + sub < count && live;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (on) v = *reinterpret_cast<const uint4*>(from);
             uint64_t y[N];
-            norm_turn<T, INTER>(v, y, lf, weight != nullptr, lanes, other, inv_d, p.eps);
+            norm_turn<T, INTER>([&](auto again) { return elements(from, on, again); }, y, lf, weight != nullptr, lanes, other, inv_d, p.eps);
             if (on) *reinterpret_cast<uint4*>(from) = packed_up(y, T());
           }
         };
@@ -687,11 +756,10 @@ __global__ void __launch_bounds__(kBulkThreads, bulk_blocks(PACKED))
           const int64_t data_at = to.x + in_group, scale_at = to.y + group;
           for (int h0 = in_t * at_once; h0 < p.Hk; h0 += each * at_once, from += hop) {
             const bool on = h0 + sub < p.Hk && live;
-            uint4 k = make_uint4(0, 0, 0, 0), v = k;
-            if (on) k = *reinterpret_cast<const uint4*>(from), v = *reinterpret_cast<const uint4*>(from + p.Hk * head_bytes);
+            const uint4 v = elements(from + p.Hk * head_bytes, on, std::false_type{});
             uint64_t y[N];
             float both[2][VEC];
-            norm_turn<T, INTER>(k, y, lf, p.k_weight != nullptr, lanes, other, inv_d, p.eps);
+            norm_turn<T, INTER>([&](auto again) { return elements(from, on, again); }, y, lf, p.k_weight != nullptr, lanes, other, inv_d, p.eps);
             spread(y, both[0]);
             unpack(v, y, T());
             spread(y, both[1]);
