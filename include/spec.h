@@ -666,7 +666,7 @@ typedef struct spec_norm_rope_args {
 
 int spec_norm_rope_cache(const spec_norm_rope_args *args, spec_stream_t stream);
 
-/* spec_cache_read_packed: the values of slots of an packed cache, k and v [rows, Hk, D]
+/* spec_cache_read_packed: the values of slots of a packed cache, k and v [rows, Hk, D]
  * dense in dtype (exact in both types); either output may be NULL.  A row with slot < 0
  * gets zeros, and so does one with slot >= n_slots (SPEC_STATUS_BAD_PAGE).
  * Sizes: rows >= 0, 1 <= Hk <= 1024, D <= 512, page_size >= 1 divides n_slots.

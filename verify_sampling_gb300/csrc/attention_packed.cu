@@ -51,7 +51,8 @@ constexpr float kSlack = 8.f;  // log2 units the maximum may grow by before O is
 
 // NB: blocks of 8 query rows of an item.  An item's start and end cost a little over two tiles: with 0, 5, 9 and 14
 // quarters of a tile 256 requests of one row take 73, 64.7, 61.7 and 62.9 us (500 keys in the mean), 268.8, 256.6,
-// 254.4 and 258.5 us (4096 keys).
+// 254.4 and 258.5 us (4096 keys).  Heads of 64 with 4, 6, 9 and 14: 101 requests of up to 4 rows (16 rows an item) 52.2, 50.0, 45.7 and
+// 46.5 us, 256 of one row (8) over 500 keys 46.1, 45.3, 46.4 and 47.9; heads of 128 and 100 requests of 2 rows (16) 81, 74.5, 69.0 and 69.3.
 template <int NB>
 struct NarrowCosts {
   static constexpr int kItemRows = 8 * NB, kLeast = 4;
@@ -627,11 +628,16 @@ cudaError_t launch(const spec_prefix_attention_args& a, const q4::Cache& packed,
   // The narrow kernel alone where no segment has more than kNarrowMost query rows, or where requests without
   // a prefix have few; otherwise the wide one takes the segments of more before it.  (256 requests of
   // 1024 keys, 8 heads a key head: 1 or 2 rows a request 162 us by the narrow kernel alone, 170 by
-  // both; 1 to 4 rows 246 and 224; 1 to 12 rows 541 and 253, with 32 rows for 16 as the border 261.)
+  // both; 1 to 4 rows 246 and 224; 1 to 12 rows 541 and 253, with 32 rows for 16 as the border 261.)  The
+  // mean knows nothing of one long request among single rows: 255 rows and a request of 256 over 8000 keys, 8 heads a key head,
+  // 859 us by the narrow kernel alone and 711 by both, 255 and 700 at 4 heads 1074 and 821, 2000 and 4000 19.4 ms and 3.9; but 31 rows and
+  // a request of 30 over 8000 keys 125 us and 206.
   const bool both = m > kNarrowMost && (a.G > 0 || m > kNarrowMost * R);
   // 16 rows an item cost 1.45 times 8 (D = 128: 256 requests of 4096 keys 461 us and 318) or 1.22 times (D = 64: 101
   // requests of 1500 keys 54 us and 44), but read the keys of a request of 9 to 16 rows once: where a
-  // request has several rows, some have more than the mean.
+  // request has several rows, some have more than the mean.  250 requests of up to 1500 keys, 8 rows an item and 16: heads of 64, a
+  // mean of 4.4 rows 58 and 67 us, 5.9 55 and 64, 6.0 (some of 9) 71 and 68, 7.5 76 and 66, 10 76 and 66; heads of 128, 7.5 98 and
+  // 110, and past 8 neither is ahead everywhere: 8.3 95 and 114, 9.2 110 and 114, 101 requests of up to 3000 keys 9.4 80 and 77.
   const int64_t most = D == 64 && a.rows > a.R ? 6 : 8;
   if (m <= most * R) return launch<D, 1>(a, packed, sms, work, both, stream);
   return launch<D, 2>(a, packed, sms, work, both, stream);

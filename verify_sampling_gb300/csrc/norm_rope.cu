@@ -20,14 +20,17 @@
 // part of a token's heads, four steps' loads together.  Pairs that are not whole vectors,
 // larger heads and odd strides (norm_rope_general_kernel): other halves from shared memory.
 // The first two give a row the same bits.
-// Bound by memory in long batches: 40001 rows of 40 heads of 128 in bf16 132 us (6.20 TB/s; the
-// ring without arithmetic 126), 2560 rows of 80 heads 24.7 (21.1), where the second kernel takes
-// 391 and 76.  Rows of 20 KB: one row 4.6 and 5.6 us, 456 rows 8.2 and 13.0; rows of 5 KB: 76 rows
-// 3.9 and 5.5, 2432 rows 10.9 and 18.1; rows of 1.2 KB: 2432 rows 6.8 and 6.4, 4864 rows 10.4
-// and 12.8, hence kBulkRow and kBulkBytes.  Three blocks an SM for two: 24.9 and 26.5 us at 2560
-// rows.  Into 4 bits the arithmetic of the coding counts as well (0.6 instructions a clock and
-// scheduler): 2560 rows 27 us, 30011 rows of 4 KB 53.  Three blocks of 64 registers took 37 us for
-// 37.7 and, with smaller stages, 88 for 82 (both with the read-back), so these have two.
+// Figures are of launches one after another over 400 MB of inputs.  Bound by memory in long batches: 40001
+// rows of 40 heads of 128 in bf16, half of a head turned, 138 us (5.9 TB/s; this ring without arithmetic 126), 2560 rows of
+// 80 heads 25.8 (21; the rotary kernel's ring, two blocks an SM of four stages, moves and turns them in 18.5), where the second
+// kernel takes 274 and 55.  Rows of 20 KB: one row 4.9 and 5.6 us, 456 rows 8.3 and 13.5; rows of 5 KB: 76
+// rows 3.8 and 5.7, 2432 rows 11.6 and 18.6; rows of 1.2 KB: 2432 rows 8.4 and 7.8, 4864 rows 12.4
+// and 13.9, hence kBulkRow and kBulkBytes.  fp32: 2560 rows of 48 heads 27.8 us (36.4; at the copy rate 18.5), 40001 of 24
+// 152 (209; 145).  Three blocks an SM for two: 24.9 and 26.5 us at 2560 rows.  Into 4 bits the arithmetic
+// of the coding counts as well (0.6 instructions a clock and scheduler): 2560 rows 30 us (the second kernel 55), 9000 rows of
+// 48 heads 63 (94).  Three blocks of 64 registers took 37 us for 37.7 and, with smaller stages, 88 for 82 (both with the
+// read-back), so these have two.  The third kernel serves what is rare: 2560 rows of 40 heads of 80, 74 of them turned,
+// 56 us (4.8 at the copy rate), of 24 heads of 512 180 (18.5), of 32 heads of 256 in fp32 65 (24.7).
 #include "norm_rope.cuh"
 
 #include <algorithm>
@@ -115,7 +118,8 @@ __device__ __forceinline__ float rsqrt_of(float x) {
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// A mean square + eps in the middle of fp32's range: squares that vanished beside it, and its products with elements and weights to 2^77, do no harm.
+// A mean square + eps in the middle of fp32's range: squares that vanished beside it do no harm, nor do its elements'
+// products with weights to 2^77.
 __device__ __forceinline__ bool in_range(float square) {
   constexpr uint32_t kLeast = (127u - 90) << 23, kMost = (127u + 90) << 23;
   return __float_as_uint(square) - kLeast <= kMost - kLeast;  // (a NaN's bits lie past them)
@@ -932,7 +936,9 @@ cudaError_t launch_cache_read(const spec_cache_read_packed_args& a, cudaStream_t
   int shift = 0;  // of a page size that is a power of two, or -1
   while ((1 << shift) < a.page_size && shift < 30) ++shift;
   if (1 << shift != a.page_size) shift = -1;
-  // Two blocks an SM and kind for 2560 rows of 1 KB (328k words) 8.2 us, four 8.5; for 30011 of 512 B (1.9M) 23.3 and 21.3.
+  // Two blocks an SM and kind, and four: 128k words 4.2 and 4.7 us, 328k (2560 rows of 8 heads of 128) 6.6 and 6.5, 640k 10.3 and
+  // 9.7, 1.02M 14.8 and 13.4, 1.9M (30011 rows of 8 heads of 64) 25.9 and 23.6; over rows that lie in L2 328k 8.2 and 8.5 and 1.9M
+  // 23.3 and 21.3.  (Three: 4.2, 5.6, 8.3, 11.5 and 21.0.)
   const int blocks = 152 * ((int64_t)a.rows * words < (1 << 20) ? 2 : 4);
   const dim3 grid((unsigned)std::min<int64_t>(((int64_t)a.rows + at_once - 1) / at_once, blocks), 2);
   if (a.dtype == SPEC_F32) cache_read_kernel<float><<<grid, kThreads, 0, stream>>>(a, at_once, shift);

@@ -118,7 +118,9 @@ __device__ __forceinline__ uint32_t element_pair(uint32_t w, const Scale& s) {
   const uint32_t n = I == 0 ? w * 8u : w >> (4 * I - 3);
   return fma_bf16(and_or(n, 0x00780078u, 0x41804180u), s.s, s.z);
 }
-// n - 8 of elements I and I + 4 in fp16, with `high` the word shifted right by 8: n lies in bits
+// n - 8 of elements I and I + 4 in fp16 by the published conversion of small integers (Kim et al., "Who Says Elephants Can't
+// Run", 2022): an integer's bits under the exponent whose unit they are, and the exponent taken off by one fma, as above in bf16
+// with the scale in the same fma.  `high` is the word shifted right by 8: n lies in bits
 // 0-3 under the exponent of 1024 (I even), which is 1024 + n, or in bits 4-7, 1024 + 16 n.
 template <int I>
 __device__ __forceinline__ uint32_t number_pair(uint32_t w, uint32_t high) {
